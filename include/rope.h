@@ -23,6 +23,12 @@
  *                     README), with QK-RMSNorm first (the pull request's
  *                     Qwen3 Architecture), and with M-RoPE.
  *   rope_apply_no_alloc  rope_apply for callers that cannot allocate.
+ *   rope_apply_qkv_fp8   rope_apply_qkv with key/value caches held in 8 bits.
+ *   kv_attention, kv_attention_fp8
+ *                     grouped-query attention over the caches that the Q/K
+ *                     operators append to ("com.microsoft.SparseAttention"
+ *                     README), with capped scores, a bias by distance, document
+ *                     and prefix masks.
  *
  * Conventions shared by every entry point
  *   - All tensors are dense, contiguous, row-major. Tensor pointers are DEVICE
@@ -55,7 +61,7 @@
  *     kernel gave up on one of its waits (each is bounded by 2 s of device
  *     time) and returned early, so the output is incomplete; not expected in
  *     normal operation. Bit 2 (Q/K entry points): some cache row was outside
- *     the cache and was not stored.
+ *     the cache and was not stored (kv_attention: some query's row is outside).
  */
 #ifndef ROPE_GB300_H
 #define ROPE_GB300_H
@@ -438,6 +444,125 @@ rope_status rope_apply_no_alloc(rope_dtype dtype, int32_t x_rank, const int64_t*
                                 int32_t interleaved, int32_t rotary_embedding_dim,
                                 int32_t num_heads, int32_t* oor_flag, rope_stream_t stream);
 
+/*
+ * rope_apply_qkv_fp8 -- rope_apply_qkv (or, with both norm weights,
+ * rope_apply_qkv_rmsnorm) in cache mode with caches held in 8 bits. No
+ * counterpart on the pages, like ROPE_BF16. Q and K heads are computed exactly
+ * as by those calls, rounded to T; q_out has their bits, and the rows of K and
+ * V are then rounded once more, to e4m3 (sign, 4 exponent and 3 mantissa bits,
+ * largest 448) with one scale for each block of ROPE_KV_SCALE_BLOCK cache rows
+ * of one head:
+ *   cache row j of (b, n) stands for code[b, n, j, :] * scale[b, n, j / 16].
+ *
+ * k_cache, v_cache  device e4m3 codes (B, kv_num_heads, max_cache_len, H), one
+ *           byte each, updated in place: token s of batch b goes to row
+ *           past_seq_lens[b] + s; rows outside [0, max_cache_len) are not
+ *           stored (status bit 2).
+ * k_scale, v_scale  device float32 (B, kv_num_heads, ceil(max_cache_len / 16)),
+ *           updated in place with the caches. Always powers of two: with amax
+ *           the largest finite magnitude of the block's new rows, the block
+ *           needs 2^ceil(log2(amax / 448)), at least 2^-120. A block whose first
+ *           row is new gets that. A block that starts with older rows (row
+ *           numbers below past_seq_lens[b]) gets it or its present scale,
+ *           whichever is larger, and where the scale grows the codes of the
+ *           older rows are rounded again: code' = e4m3(code * old / new),
+ *           exact unless code' is subnormal. Scales of other blocks and codes
+ *           of rows from past_seq_lens[b] + S on stay as they are. A block's
+ *           scale needs no value before its first row is appended.
+ * Codes are rounded to nearest even. An infinity becomes +-448, a NaN stays
+ * one; neither counts for a scale.
+ * query .. value, positions, past_seq_lens (required), interleaved,
+ * rotary_embedding_dim, norm weights (both or neither), epsilon, q_out,
+ * status_flags, ownership and errors as rope_apply_qkv in cache mode and
+ * rope_apply_qkv_rmsnorm; no scratch. max_cache_len is limited to 2^31 - 1.
+ */
+#define ROPE_KV_SCALE_BLOCK 16
+rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
+                               int32_t kv_num_heads, int64_t head_size, const void* query,
+                               const void* key, const void* value, const void* q_norm_weight,
+                               const void* k_norm_weight, float epsilon, const void* cos_cache,
+                               const void* sin_cache, int64_t cache_rows, const int64_t* position_ids,
+                               const int32_t* past_seq_lens, int32_t interleaved,
+                               int32_t rotary_embedding_dim, void* q_out, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, int64_t max_cache_len,
+                               int32_t* status_flags, rope_stream_t stream);
+
+/*
+ * kv_attention -- attention of the S newest tokens of each sequence over the
+ * caches that rope_apply_qkv, rope_apply_qkv_rmsnorm and mrope_apply_qkv
+ * append to, after such a call with the same past_seq_lens ([SparseAttention
+ * README, Description: grouped-query attention over past and new keys, scale;
+ * Inputs] with its causal mask, without its sparsity; the cap, the bias and
+ * the two masks have no counterpart on the pages).
+ *
+ * Token s of batch b is at cache row i = past_seq_lens[b] + s. With total =
+ * past_seq_lens[b] + S (within [0, max_cache_len]), query head h reads key/value
+ * head n = h / (num_heads / kv_num_heads), and key row j < total is visible if
+ *   j <= i, or j < prefix_lens[b]             (causal, the prefix open to all)
+ *   and document_ids[b, j] == document_ids[b, i]          (if documents given).
+ *   x_j = c(scale * q . k_j) - alibi_slopes[h] * |i - j|,
+ *   c(y) = softcap * tanh(y / softcap), or y where softcap is 0,
+ *   out = sum_j softmax(x)_j v_j over the visible j.
+ * A row that sees no key (or whose largest score is -inf) gives 0. Keys and
+ * values that a row does not see, and cache rows from total on, may hold
+ * anything, NaN included. Products of 16-bit types are exact and summed in
+ * float32, as are the softmax statistics; the weights are rounded to T (to
+ * float16 over 8-bit caches) for the product with V. float32 keeps float32
+ * products.
+ *
+ * query     device T (B, S, num_heads*H): the q_out of the Q/K operators.
+ * k_cache, v_cache  device T (B, kv_num_heads, max_cache_len, H), read only.
+ * past_seq_lens device int32 (B). A query whose row i is outside the cache sets
+ *           status bit 2; it sees the rows that its formula says (with
+ *           documents: none).
+ * scale     finite; usually 1 / sqrt(H). softcap finite, >= 0; 0: no cap.
+ * alibi_slopes  NULL or device float32 (num_heads).
+ * document_ids  NULL or device int32 (B, max_cache_len), by cache row.
+ * prefix_lens   NULL or device int32 (B).
+ * out       device T (B, S, num_heads*H); must not overlap an input.
+ * status_flags  NULL or the status word (bits 1 and 2).
+ * workspace NULL or workspace_bytes of device memory, 16-byte aligned, any
+ *           contents: where there are few rows the keys are split over more
+ *           CTAs, whose partial results meet here. kv_attention_workspace says
+ *           how much the planned split takes; less (or NULL) splits less. Calls
+ *           that may run at the same time need workspaces of their own. Nothing
+ *           is kept in it between calls.
+ * The result of a call does not depend on timing (no atomics); the number of
+ * splits, which follows from the sizes and the workspace, changes roundings.
+ * Errors (before any launch): ROPE_ERR_INVALID_ARG for bad sizes, head counts,
+ * scale or softcap, NULL or misaligned pointers; ROPE_ERR_UNSUPPORTED for
+ * another dtype, head_size above 256, batch, seq or max_cache_len above
+ * 2^31 - 1. B*S == 0 launches nothing.
+ */
+rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
+                         int32_t kv_num_heads, int64_t head_size, const void* query,
+                         const void* k_cache, const void* v_cache, int64_t max_cache_len,
+                         const int32_t* past_seq_lens, float scale, float softcap,
+                         const float* alibi_slopes, const int32_t* document_ids,
+                         const int32_t* prefix_lens, void* out, int32_t* status_flags,
+                         void* workspace, int64_t workspace_bytes, rope_stream_t stream);
+
+/*
+ * kv_attention_fp8 -- kv_attention over the caches that rope_apply_qkv_fp8
+ * appends to: k_cache, v_cache hold e4m3 codes, k_scale, v_scale the scales
+ * (powers of two, as written there) of each block of ROPE_KV_SCALE_BLOCK rows,
+ * and key or value row j is code * scale. Everything else as kv_attention.
+ */
+rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
+                             int32_t kv_num_heads, int64_t head_size, const void* query,
+                             const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, int64_t max_cache_len,
+                             const int32_t* past_seq_lens, float scale, float softcap,
+                             const float* alibi_slopes, const int32_t* document_ids,
+                             const int32_t* prefix_lens, void* out, int32_t* status_flags,
+                             void* workspace, int64_t workspace_bytes, rope_stream_t stream);
+
+/* Bytes of workspace with which kv_attention and kv_attention_fp8 split the keys
+   of such a call as planned; 0 where nothing is split, -1 for sizes that they
+   refuse. A host function: no CUDA call. */
+int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
+                               int64_t head_size, int64_t max_cache_len);
+
 /* Static name of a status code. */
 const char* rope_status_string(rope_status status);
 
@@ -450,7 +575,8 @@ const char* rope_last_error(void);
    per thread), "rope_tma_kernel" (TMA pipeline),
    "rope_fused_kernel", "rope_qkv_kernel" (SIMT, one head per thread),
    "rope_qkv_heads_kernel" (SIMT Q/K, several heads of one role per thread),
-   "rope_qkv_tma_kernel" (TMA pipeline) or "rope_cache_build_kernel"; "" before the first
+   "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
+   (8-bit append) or "kv_simple_kernel" (attention on CUDA cores); "" before the first
    launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.
    The string is static; never free it. */

@@ -18,7 +18,8 @@ from .build import LIB_PATH, build_library  # noqa: F401
 __all__ = [
     "RopeError", "load_library", "build_library", "rope_apply", "mrope_apply",
     "mrope_apply_stream_map", "mrope_stream_map", "rope_apply_fused", "rope_cache_build",
-    "rope_apply_qkv", "mrope_apply_qkv",
+    "rope_apply_qkv", "mrope_apply_qkv", "rope_apply_qkv_fp8", "kv_attention", "kv_attention_fp8",
+    "kv_attention_workspace", "kv_cache_fp8",
     "set_variant", "get_variant", "variant",
     "ROPE_OK", "ROPE_ERR_INVALID_ARG", "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_CUDA",
 ]
@@ -26,6 +27,7 @@ __all__ = [
 ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA = 0, 1, 2, 3
 ROPE_F32, ROPE_F16, ROPE_BF16 = 0, 1, 2
 ROPE_SCRATCH_BYTES = 64
+ROPE_KV_SCALE_BLOCK = 16
 VARIANTS = {"auto": 0, "simt": 1, "tma": 2}
 _UNSUPPORTED_DTYPE = 99  # passed through so the library reports ROPE_ERR_UNSUPPORTED
 
@@ -60,6 +62,13 @@ SIGNATURES = {
                         _i32p, _i32, _f32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp],
     "rope_apply_no_alloc": [_i32, _i32, _i64p, _vp, _vp, _i32, _i64p, _vp, _vp, _vp, _i32, _i32, _i32, _vp,
                             _vp],
+    "rope_apply_qkv_fp8": [_i32, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _i64,
+                           _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
+    "kv_attention": [_i32, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _i64, _vp, _f32, _f32, _vp, _vp, _vp,
+                     _vp, _vp, _vp, _i64, _vp],
+    "kv_attention_fp8": [_i32, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _f32, _f32, _vp,
+                         _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+    "kv_attention_workspace": [_i64, _i64, _i32, _i32, _i64, _i64],
     "rope_set_variant": [_i32],
     "rope_get_variant": [],
     "rope_status_string": [_i32],
@@ -67,7 +76,7 @@ SIGNATURES = {
     "rope_last_kernel": [],
 }
 _RESTYPES = {"rope_status_string": ctypes.c_char_p, "rope_last_error": ctypes.c_char_p,
-             "rope_last_kernel": ctypes.c_char_p}
+             "rope_last_kernel": ctypes.c_char_p, "kv_attention_workspace": _i64}
 
 
 class RopeError(RuntimeError):
@@ -428,6 +437,202 @@ def rope_cache_build(inv_freq, rows, dtype=None, *, attention_scaling=1.0, cos_o
                                   _ptr(cos_out), _ptr(sin_out), _stream(inv_freq, stream))
     _check("rope_cache_build", st)
     return cos_out, sin_out
+
+
+# --------------------------------------------------------------------------
+# 8-bit caches and attention over the caches
+# --------------------------------------------------------------------------
+
+def _shaped(name, t, like, shape, *dtypes):
+    """``t`` checked: contiguous, on the device of ``like``, of one of the dtypes and of the shape."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must have dtype {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """The device of ``x`` current and, where the caller names one, ``stream`` too (so that what is
+    allocated belongs to the stream that the launch runs on). Free where nothing has to change."""
+
+    def __init__(self, x, stream):
+        import torch
+
+        self.handle = (stream or torch.cuda.current_stream(x.device)).cuda_stream
+        self.was = []
+        if stream is not None:
+            self.was.append(torch.cuda.stream(stream))
+        if x.device.index != torch.cuda.current_device():
+            self.was.append(torch.cuda.device(x.device))
+
+    def __enter__(self):
+        for c in self.was:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.was):
+            c.__exit__(*exc)
+
+
+def kv_cache_fp8(batch, kv_num_heads, max_cache_len, head_size, device=None):
+    """Empty 8-bit caches for rope_apply_qkv_fp8: (k_cache, v_cache, k_scale, v_scale). Codes are
+    float8_e4m3fn (batch, kv_num_heads, max_cache_len, head_size), scales float32 with one value for
+    ROPE_KV_SCALE_BLOCK rows of a head."""
+    import torch
+
+    device = torch.device("cuda") if device is None else device
+    blocks = -(-max_cache_len // ROPE_KV_SCALE_BLOCK)
+    codes = [torch.zeros((batch, kv_num_heads, max_cache_len, head_size), dtype=torch.uint8,
+                         device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((batch, kv_num_heads, blocks), dtype=torch.float32, device=device) for _ in range(2)]
+    return codes[0], codes[1], scales[0], scales[1]
+
+
+def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_heads, kv_num_heads, k_cache, v_cache,
+                       k_scale, v_scale, past_seq_lens, key=None, value=None, interleaved=0, rotary_embedding_dim=0,
+                       q_out=None, status=None, q_norm_weight=None, k_norm_weight=None, epsilon=1e-6, stream=None):
+    """rope_apply_qkv in cache mode with caches held in 8 bits (see ``rope_apply_qkv_fp8`` in include/rope.h).
+
+    k_cache and v_cache are float8_e4m3fn (or uint8 codes) (B, kv_num_heads, max_len, H), k_scale and v_scale
+    float32 (B, kv_num_heads, ceil(max_len / 16)), all updated in place (``kv_cache_fp8`` makes them). With
+    q_norm_weight and k_norm_weight each Q and K head is RMS-normalised first. Returns q_out."""
+    import torch
+
+    lib = load_library()
+    T = query.dtype
+    if query.dim() != 3:
+        raise ValueError("query must be (B, S, hidden)")
+    B, S, hidden = query.shape
+    packed = key is None and value is None
+    rows_per_tok = num_heads + (2 * kv_num_heads if packed else 0)
+    if rows_per_tok < 1 or hidden % rows_per_tok:
+        raise ValueError(f"query hidden size {hidden} is not a multiple of {rows_per_tok} heads")
+    H = hidden // rows_per_tok
+    if k_cache.dim() != 4 or cos_cache.dim() != 2:
+        raise ValueError("k_cache must be (B, kv_num_heads, max_len, H) and cos_cache (rows, rd/2)")
+    L = k_cache.shape[2]
+    plane = (B, kv_num_heads, L, H)
+    blocks = (B, kv_num_heads, -(-L // ROPE_KV_SCALE_BLOCK))
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    table = (cos_cache.shape[0], (rotary_embedding_dim or H) // 2)
+    _shaped("query", query, query, query.shape, T)
+    _shaped("key", key, query, (B, S, kv_num_heads * H), T)
+    _shaped("value", value, query, (B, S, kv_num_heads * H), T)
+    _shaped("cos_cache", cos_cache, query, table, T)
+    _shaped("sin_cache", sin_cache, query, table, T)
+    _shaped("position_ids", position_ids, query, (B, S), torch.int64)
+    _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
+    _shaped("k_cache", k_cache, query, plane, *codes)
+    _shaped("v_cache", v_cache, query, plane, *codes)
+    _shaped("k_scale", k_scale, query, blocks, torch.float32)
+    _shaped("v_scale", v_scale, query, blocks, torch.float32)
+    _shaped("q_norm_weight", q_norm_weight, query, (H,), T)
+    _shaped("k_norm_weight", k_norm_weight, query, (H,), T)
+    _shaped("q_out", q_out, query, (B, S, num_heads * H), T)
+    if status is not None:
+        _shaped("status", status, query, status.shape, torch.int32)
+    with _on(query, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty((B, S, num_heads * H), dtype=T, device=query.device)
+        st = lib.rope_apply_qkv_fp8(
+            _dtype_code(query), B, S, num_heads, kv_num_heads, H, _address(query), _address(key), _address(value),
+            _address(q_norm_weight), _address(k_norm_weight), epsilon, _address(cos_cache), _address(sin_cache),
+            table[0], _address(position_ids), _address(past_seq_lens), int(interleaved), rotary_embedding_dim,
+            _address(q_out), _address(k_cache), _address(v_cache), _address(k_scale), _address(v_scale), L,
+            _address(status), handle)
+    _check("rope_apply_qkv_fp8", st)
+    return q_out
+
+
+def kv_attention_workspace(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len):
+    """Bytes of workspace that kv_attention and kv_attention_fp8 use for such a call."""
+    n = load_library().kv_attention_workspace(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len)
+    if n < 0:
+        _check("kv_attention_workspace", ROPE_ERR_INVALID_ARG)
+    return n
+
+
+def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap, alibi_slopes,
+               document_ids, prefix_lens, out, status, workspace, stream):
+    import torch
+
+    lib = load_library()
+    T = query.dtype
+    if query.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("query must be (B, S, num_heads*H) and k_cache (B, kv_num_heads, max_len, H)")
+    B, S, hidden = query.shape
+    _, N, L, H = k_cache.shape
+    plane = (B, N, L, H)
+    _shaped("query", query, query, (B, S, num_heads * H), T)
+    kinds = (T,) if scales is None else (torch.float8_e4m3fn, torch.uint8)
+    _shaped("k_cache", k_cache, query, plane, *kinds)
+    _shaped("v_cache", v_cache, query, plane, *kinds)
+    _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
+    _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), torch.float32)
+    _shaped("document_ids", document_ids, query, (B, L), torch.int32)
+    _shaped("prefix_lens", prefix_lens, query, (B,), torch.int32)
+    _shaped("out", out, query, (B, S, hidden), T)
+    if status is not None:
+        _shaped("status", status, query, status.shape, torch.int32)
+    if workspace is not None:
+        _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
+    scale = H ** -0.5 if scale is None else scale
+    with _on(query, stream) as handle:
+        if out is None:
+            out = torch.empty_like(query)
+        if workspace is None:
+            need = lib.kv_attention_workspace(B, S, num_heads, N, H, L)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+        room = 0 if workspace is None else workspace.numel()
+        code = _dtype_code(query)
+        if scales is None:
+            st = lib.kv_attention(code, B, S, num_heads, N, H, _address(query), _address(k_cache), _address(v_cache),
+                                  L, _address(past_seq_lens), scale, softcap, _address(alibi_slopes),
+                                  _address(document_ids), _address(prefix_lens), _address(out), _address(status),
+                                  _address(workspace), room, handle)
+        else:
+            blocks = (B, N, -(-L // ROPE_KV_SCALE_BLOCK))
+            ks = _shaped("k_scale", scales[0], query, blocks, torch.float32)
+            vs = _shaped("v_scale", scales[1], query, blocks, torch.float32)
+            st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, _address(query), _address(k_cache),
+                                      _address(v_cache), _address(ks), _address(vs), L, _address(past_seq_lens),
+                                      scale, softcap, _address(alibi_slopes), _address(document_ids),
+                                      _address(prefix_lens), _address(out), _address(status), _address(workspace),
+                                      room, handle)
+    _check(name, st)
+    return out
+
+
+def kv_attention(query, k_cache, v_cache, past_seq_lens, *, num_heads, scale=None, softcap=0.0, alibi_slopes=None,
+                 document_ids=None, prefix_lens=None, out=None, status=None, workspace=None, stream=None):
+    """Attention of the S newest tokens over the caches that the Q/K operators append to (see
+    ``kv_attention`` in include/rope.h): query (B, S, num_heads*H) as rope_apply_qkv returns it, caches
+    (B, kv_num_heads, max_len, H) after its append, past_seq_lens the lengths before it. scale: 1/sqrt(H)
+    if None. workspace: uint8 device memory of ``kv_attention_workspace`` bytes, or None to take it from
+    PyTorch's allocator for the call. Returns out."""
+    return _attention("kv_attention", query, k_cache, v_cache, None, past_seq_lens, num_heads, scale, softcap,
+                      alibi_slopes, document_ids, prefix_lens, out, status, workspace, stream)
+
+
+def kv_attention_fp8(query, k_cache, v_cache, k_scale, v_scale, past_seq_lens, *, num_heads, scale=None, softcap=0.0,
+                     alibi_slopes=None, document_ids=None, prefix_lens=None, out=None, status=None, workspace=None,
+                     stream=None):
+    """kv_attention over the 8-bit caches and scales of rope_apply_qkv_fp8."""
+    return _attention("kv_attention_fp8", query, k_cache, v_cache, (k_scale, v_scale), past_seq_lens, num_heads,
+                      scale, softcap, alibi_slopes, document_ids, prefix_lens, out, status, workspace, stream)
 
 
 def set_variant(name):

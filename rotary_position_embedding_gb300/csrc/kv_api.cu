@@ -1,0 +1,415 @@
+// C ABI of the cache operators: rope_apply_qkv_fp8, kv_attention and
+// kv_attention_fp8 (include/rope.h). Argument checks, choice of kernel, launch
+// geometry. As in rope_api.cu nothing is allocated or kept, nothing waits, and
+// every check comes before any CUDA call.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+#include <initializer_list>
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "kv_internal.h"
+#include "rope.h"
+#include "rope_internal.h"
+
+using namespace rope_gb300;
+
+static_assert(ROPE_KV_SCALE_BLOCK == kKvBlock, "rope.h and the kernels agree on the rows of a scale");
+
+#define KV_TRY(expr)              \
+  do {                            \
+    rope_status _s = (expr);      \
+    if (_s != ROPE_OK) return _s; \
+  } while (0)
+
+namespace {
+
+constexpr int kSms = 152;  // GB300
+constexpr int64_t kWorkspaceSlack = 16;  // aligns the part behind the partial outputs
+
+rope_status fail(rope_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  set_last_error(buf);
+  return st;
+}
+
+rope_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(ROPE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+rope_status check_ptr(const void* p, const char* name, size_t align) {
+  if (!p) return fail(ROPE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(p, align)) return fail(ROPE_ERR_INVALID_ARG, "%s is not aligned to %zu bytes", name, align);
+  return ROPE_OK;
+}
+
+rope_status check_optional(const void* p, const char* name, size_t align) {
+  return p ? check_ptr(p, name, align) : ROPE_OK;
+}
+
+rope_status check_dtype(rope_dtype dt) {
+  if (dt != ROPE_F32 && dt != ROPE_F16 && dt != ROPE_BF16)
+    return fail(ROPE_ERR_UNSUPPORTED, "dtype %d: only float32 (0), float16 (1) and bfloat16 (2) are implemented",
+                (int)dt);
+  return ROPE_OK;
+}
+
+// The product of non-negative sizes stays below 2^62 (bytes of every tensor fit int64).
+bool sizes_fit(std::initializer_list<int64_t> v) {
+  int64_t n = 1;
+  for (int64_t x : v) {
+    if (x == 0) return true;
+    if (n > ((int64_t)1 << 62) / x) return false;
+    n *= x;
+  }
+  return true;
+}
+
+int pow2_at_least(int64_t n) {
+  int p = 1;
+  while (p < n) p *= 2;
+  return p;
+}
+
+// A kernel with more than 48 KB of dynamic shared memory is allowed the
+// device's most, once for each device.
+std::mutex g_mu;
+std::set<std::pair<int, const void*>> g_raised;
+
+rope_status allow_smem(const void* fn, size_t smem) {
+  if (smem <= 48 * 1024) return ROPE_OK;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_raised.count(std::make_pair(dev, fn))) return ROPE_OK;
+  int most = 0;
+  e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(shared memory opt-in)");
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, fn);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+  most -= (int)fa.sharedSizeBytes;  // what the kernel holds statically
+  if (most < (int)smem) return fail(ROPE_ERR_UNSUPPORTED, "needs %zu bytes of shared memory", smem);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+  g_raised.insert(std::make_pair(dev, fn));
+  return ROPE_OK;
+}
+
+// Launched as a programmatic dependent, as every kernel of the library.
+rope_status launch(const void* fn, dim3 grid, int threads, size_t smem, rope_stream_t stream, void** args,
+                   const char* what) {
+  KV_TRY(allow_smem(fn, smem));
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return ROPE_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+struct Plan {
+  int64_t tiles = 0;  // row tiles of a (b, kvh)
+  int splits = 1;
+  int64_t split_bytes = 0;  // workspace of one split of every row
+};
+
+// Splits from the sizes alone: the lengths are on the device. The keys are
+// split where the row tiles leave SMs without a CTA, up to the cache's length
+// over 256 keys a split.
+Plan plan_attention(int64_t B, int64_t S, int64_t Nq, int64_t Nkv, int64_t H, int64_t max_len) {
+  Plan pl;
+  const int64_t R = S * (Nq / Nkv);
+  pl.tiles = (R + kKvSimpleRows - 1) / kKvSimpleRows;
+  const int64_t ctas = pl.tiles * Nkv * B;
+  int64_t n = (2 * kSms + ctas - 1) / ctas;
+  if (n > (max_len + 255) / 256) n = (max_len + 255) / 256;
+  if (n > 64) n = 64;
+  pl.splits = n < 1 ? 1 : (int)n;
+  pl.split_bytes = B * Nkv * R * (H * 4 + 8);
+  return pl;
+}
+
+rope_status check_attention_sizes(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
+                                  int64_t head_size, int64_t max_cache_len) {
+  if (batch < 0 || seq < 0) return fail(ROPE_ERR_INVALID_ARG, "batch and seq must be >= 0");
+  if (num_heads < 1 || kv_num_heads < 1)
+    return fail(ROPE_ERR_INVALID_ARG, "num_heads (%d) and kv_num_heads (%d) must be >= 1", num_heads, kv_num_heads);
+  if (num_heads % kv_num_heads)
+    return fail(ROPE_ERR_INVALID_ARG, "kv_num_heads %d does not divide num_heads %d", kv_num_heads, num_heads);
+  if (head_size < 1) return fail(ROPE_ERR_INVALID_ARG, "head_size must be >= 1");
+  if (max_cache_len < 1) return fail(ROPE_ERR_INVALID_ARG, "max_cache_len must be >= 1");
+  if (head_size > kKvMaxHead)
+    return fail(ROPE_ERR_UNSUPPORTED, "head_size %lld exceeds %d", (long long)head_size, kKvMaxHead);
+  if (batch > INT32_MAX || seq > INT32_MAX || max_cache_len > INT32_MAX || kv_num_heads > 65535)
+    return fail(ROPE_ERR_UNSUPPORTED, "batch, seq and max_cache_len are limited to 2^31 - 1, kv_num_heads to 65535");
+  if (!sizes_fit({batch, seq, num_heads, head_size, 1024}) ||
+      !sizes_fit({batch, kv_num_heads, max_cache_len, head_size, 8}))
+    return fail(ROPE_ERR_INVALID_ARG, "Q has more than 2^52 or the caches more than 2^59 elements");
+  return ROPE_OK;
+}
+
+rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t seq, int32_t num_heads,
+                           int32_t kv_num_heads, int64_t head_size, const void* query, const void* k_cache,
+                           const void* v_cache, const float* k_scale, const float* v_scale,
+                           int64_t max_cache_len, const int32_t* past_seq_lens, float scale, float softcap,
+                           const float* alibi_slopes, const int32_t* document_ids, const int32_t* prefix_lens,
+                           void* out, int32_t* status_flags, void* workspace, int64_t workspace_bytes,
+                           rope_stream_t stream) {
+  set_last_error("");
+  KV_TRY(check_dtype(dtype));
+  KV_TRY(check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len));
+  if (!std::isfinite(scale)) return fail(ROPE_ERR_INVALID_ARG, "scale must be finite");
+  if (!(softcap >= 0.0f && softcap < INFINITY))
+    return fail(ROPE_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
+  if (workspace_bytes < 0) return fail(ROPE_ERR_INVALID_ARG, "workspace_bytes is negative");
+  if (batch == 0 || seq == 0) return ROPE_OK;
+  const size_t es = dtype == ROPE_F32 ? 4 : 2;
+  KV_TRY(check_ptr(query, "query", es));
+  KV_TRY(check_ptr(k_cache, "k_cache", fp8 ? 1 : es));
+  KV_TRY(check_ptr(v_cache, "v_cache", fp8 ? 1 : es));
+  if (fp8) {
+    KV_TRY(check_ptr(k_scale, "k_scale", 4));
+    KV_TRY(check_ptr(v_scale, "v_scale", 4));
+  }
+  KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
+  KV_TRY(check_ptr(out, "out", es));
+  KV_TRY(check_optional(alibi_slopes, "alibi_slopes", 4));
+  KV_TRY(check_optional(document_ids, "document_ids", 4));
+  KV_TRY(check_optional(prefix_lens, "prefix_lens", 4));
+  KV_TRY(check_optional(status_flags, "status_flags", 4));
+  KV_TRY(check_optional(workspace, "workspace", 16));
+
+  Plan pl = plan_attention(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+  const int64_t fits =
+      workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
+  if (pl.splits > fits) pl.splits = fits > 1 ? (int)fits : 1;
+
+  KvParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = query;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.out = out;
+  p.past = past_seq_lens;
+  p.slopes = alibi_slopes;
+  p.docs = document_ids;
+  p.prefix = prefix_lens;
+  p.status = status_flags;
+  p.G = num_heads / kv_num_heads;
+  p.S = seq;
+  p.R = seq * p.G;
+  p.max_len = max_cache_len;
+  p.nblk = (max_cache_len + kKvBlock - 1) / kKvBlock;
+  p.B = (int32_t)batch;
+  p.Nq = num_heads;
+  p.Nkv = kv_num_heads;
+  p.H = (int32_t)head_size;
+  p.splits = pl.splits;
+  if (pl.splits > 1) {
+    const int64_t rows = batch * kv_num_heads * pl.splits * p.R;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
+  }
+  p.vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) &&
+          aligned(out, 16);
+  p.scale = scale;
+  p.cap = softcap;
+
+  void* args[] = {&p};
+  const int64_t gx = pl.tiles * pl.splits;
+  if (gx > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
+  KV_TRY(launch(kv_simple_kernel(dtype, fp8), dim3((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535)),
+                kKvSimpleThreads, kv_simple_smem((int)head_size), stream, args, "kv_attention launch"));
+  set_last_kernel("kv_simple_kernel");
+  if (pl.splits > 1) {
+    const int64_t rows = batch * kv_num_heads * p.R;
+    int64_t grid = (rows + kKvCombineThreads / 32 - 1) / (kKvCombineThreads / 32);
+    if (grid > INT32_MAX) grid = INT32_MAX;
+    KV_TRY(launch(kv_combine_kernel(dtype), dim3((unsigned)grid), kKvCombineThreads, 0, stream, args,
+                  "kv_attention launch (joining the splits)"));
+  }
+  return ROPE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
+                               int64_t head_size, int64_t max_cache_len) {
+  set_last_error("");
+  if (check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len) != ROPE_OK) return -1;
+  if (batch == 0 || seq == 0) return 0;
+  const Plan pl = plan_attention(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+  return pl.splits > 1 ? pl.splits * pl.split_bytes + kWorkspaceSlack : 0;
+}
+
+rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
+                         int64_t head_size, const void* query, const void* k_cache, const void* v_cache,
+                         int64_t max_cache_len, const int32_t* past_seq_lens, float scale, float softcap,
+                         const float* alibi_slopes, const int32_t* document_ids, const int32_t* prefix_lens,
+                         void* out, int32_t* status_flags, void* workspace, int64_t workspace_bytes,
+                         rope_stream_t stream) {
+  return attention_impl(dtype, false, batch, seq, num_heads, kv_num_heads, head_size, query, k_cache, v_cache,
+                        nullptr, nullptr, max_cache_len, past_seq_lens, scale, softcap, alibi_slopes, document_ids,
+                        prefix_lens, out, status_flags, workspace, workspace_bytes, stream);
+}
+
+rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
+                             int32_t kv_num_heads, int64_t head_size, const void* query, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             int64_t max_cache_len, const int32_t* past_seq_lens, float scale, float softcap,
+                             const float* alibi_slopes, const int32_t* document_ids, const int32_t* prefix_lens,
+                             void* out, int32_t* status_flags, void* workspace, int64_t workspace_bytes,
+                             rope_stream_t stream) {
+  return attention_impl(dtype, true, batch, seq, num_heads, kv_num_heads, head_size, query, k_cache, v_cache,
+                        k_scale, v_scale, max_cache_len, past_seq_lens, scale, softcap, alibi_slopes, document_ids,
+                        prefix_lens, out, status_flags, workspace, workspace_bytes, stream);
+}
+
+rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
+                               int32_t kv_num_heads, int64_t head_size, const void* query, const void* key,
+                               const void* value, const void* q_norm_weight, const void* k_norm_weight,
+                               float epsilon, const void* cos_cache, const void* sin_cache, int64_t cache_rows,
+                               const int64_t* position_ids, const int32_t* past_seq_lens, int32_t interleaved,
+                               int32_t rotary_embedding_dim, void* q_out, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, int64_t max_cache_len, int32_t* status_flags,
+                               rope_stream_t stream) {
+  set_last_error("");
+  KV_TRY(check_dtype(dtype));
+  const bool norm = q_norm_weight || k_norm_weight;
+  if (norm && (!q_norm_weight || !k_norm_weight))
+    return fail(ROPE_ERR_INVALID_ARG, "RMSNorm needs both q_norm_weight and k_norm_weight");
+  if (norm && !(epsilon >= 0.0f && epsilon < INFINITY))
+    return fail(ROPE_ERR_INVALID_ARG, "epsilon must be finite and >= 0");
+  if (batch < 0 || seq < 0) return fail(ROPE_ERR_INVALID_ARG, "batch and seq must be >= 0");
+  if (num_heads < 1 || kv_num_heads < 1)
+    return fail(ROPE_ERR_INVALID_ARG, "num_heads (%d) and kv_num_heads (%d) must be >= 1", num_heads, kv_num_heads);
+  if (num_heads % kv_num_heads)
+    return fail(ROPE_ERR_INVALID_ARG, "kv_num_heads %d does not divide num_heads %d", kv_num_heads, num_heads);
+  if (head_size < 2 || head_size % 2) return fail(ROPE_ERR_INVALID_ARG, "head_size must be even and >= 2");
+  if (head_size > INT32_MAX / 4) return fail(ROPE_ERR_UNSUPPORTED, "head_size exceeds 2^29");
+  if (interleaved != 0 && interleaved != 1)
+    return fail(ROPE_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", interleaved);
+  if (cache_rows < 0) return fail(ROPE_ERR_INVALID_ARG, "cache_rows is negative");
+  const int64_t rd = rotary_embedding_dim ? rotary_embedding_dim : head_size;
+  if (rd < 2 || rd % 2 || rd > head_size)
+    return fail(ROPE_ERR_INVALID_ARG, "rotary_embedding_dim %d must be 0 or even, 0 < rd <= head size %lld",
+                rotary_embedding_dim, (long long)head_size);
+  if (max_cache_len < 1) return fail(ROPE_ERR_INVALID_ARG, "max_cache_len must be >= 1");
+  if (max_cache_len > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "max_cache_len is limited to 2^31 - 1");
+  if (!sizes_fit({batch, seq, (int64_t)num_heads + 2 * (int64_t)kv_num_heads, head_size, 8}) ||
+      !sizes_fit({batch, kv_num_heads, max_cache_len, head_size, 8}) || !sizes_fit({cache_rows, rd, 8}))
+    return fail(ROPE_ERR_INVALID_ARG, "Q/K/V, the caches or the tables have more than 2^59 elements");
+  if (batch == 0 || seq == 0) return ROPE_OK;
+  const bool packed = !key && !value;
+  if (!packed && (!key || !value)) return fail(ROPE_ERR_INVALID_ARG, "key and value come together (or packed in query)");
+  const size_t es = dtype == ROPE_F32 ? 4 : 2;
+  KV_TRY(check_ptr(query, "query", es));
+  if (!packed) {
+    KV_TRY(check_ptr(key, "key", es));
+    KV_TRY(check_ptr(value, "value", es));
+  }
+  KV_TRY(check_ptr(q_out, "q_out", es));
+  if (packed && q_out == query)
+    return fail(ROPE_ERR_INVALID_ARG, "q_out cannot alias a packed query (different row strides)");
+  KV_TRY(check_ptr(k_cache, "k_cache", 1));
+  KV_TRY(check_ptr(v_cache, "v_cache", 1));
+  KV_TRY(check_ptr(k_scale, "k_scale", 4));
+  KV_TRY(check_ptr(v_scale, "v_scale", 4));
+  KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
+  if (cache_rows > 0) {
+    KV_TRY(check_ptr(cos_cache, "cos_cache", es));
+    KV_TRY(check_ptr(sin_cache, "sin_cache", es));
+  }
+  KV_TRY(check_optional(position_ids, "position_ids", 8));
+  KV_TRY(check_optional(status_flags, "status_flags", 4));
+  if (norm) {
+    KV_TRY(check_ptr(q_norm_weight, "q_norm_weight", es));
+    KV_TRY(check_ptr(k_norm_weight, "k_norm_weight", es));
+  }
+
+  const int V16 = 16 / (int)es;
+  bool vec = head_size % V16 == 0 && (rd / 2) % V16 == 0 && aligned(k_cache, V16) && aligned(v_cache, V16);
+  for (const void* x : {query, key, value, (const void*)q_out, cos_cache, sin_cache, q_norm_weight, k_norm_weight})
+    vec = vec && aligned(x, 16);
+  const int V = vec ? V16 : 1;
+  KvAppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = query;
+  p.k = key;
+  p.v = value;
+  p.cos = cos_cache;
+  p.sin = sin_cache;
+  p.pos = position_ids;
+  p.past = past_seq_lens;
+  p.qw = q_norm_weight;
+  p.kw = k_norm_weight;
+  p.q_out = q_out;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = status_flags;
+  p.B = batch;
+  p.S = seq;
+  p.max_len = max_cache_len;
+  p.nblk = (max_cache_len + kKvBlock - 1) / kKvBlock;
+  p.cache_rows = cache_rows;
+  p.H = head_size;
+  p.Nq = num_heads;
+  p.Nkv = kv_num_heads;
+  p.packed = packed;
+  p.h = (int32_t)(rd / 2);
+  p.rd = (int32_t)rd;
+  p.nP = p.h / V;
+  p.U = p.nP + (int32_t)((head_size - rd) / V);
+  p.eps = epsilon;
+  if (norm && p.U > 32)
+    return fail(ROPE_ERR_UNSUPPORTED, "RMSNorm: a head has %d units, at most 32 are implemented", p.U);
+  p.lanes = p.U >= 32 ? 32 : pow2_at_least(p.U);
+  p.rows = pow2_at_least(seq < kKvBlock ? seq : kKvBlock);
+  while (p.lanes * p.rows > kKvAppendThreads) p.rows /= 2;
+  p.wide = head_size % 16 == 0 && aligned(k_cache, 16) && aligned(v_cache, 16);
+  p.blocks = (seq + kKvBlock - 2) / kKvBlock + 1;
+  if (!sizes_fit({4, batch, kv_num_heads, p.blocks}))
+    return fail(ROPE_ERR_INVALID_ARG, "more than 2^60 cache blocks");
+  p.kv_tasks = 2 * batch * kv_num_heads * p.blocks;
+  p.q_tasks = (batch * seq * num_heads + p.rows - 1) / p.rows;
+  const int per_cta = kKvAppendThreads / (p.lanes * p.rows);
+  int64_t grid = (p.kv_tasks + p.q_tasks + per_cta - 1) / per_cta;
+  if (grid > INT32_MAX) grid = INT32_MAX;
+  void* args[] = {&p};
+  KV_TRY(launch(kv_append_kernel(dtype, vec, interleaved != 0, norm), dim3((unsigned)grid), kKvAppendThreads, 0, stream,
+                args, "rope_apply_qkv_fp8 launch"));
+  set_last_kernel("kv_append_kernel");
+  return ROPE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,81 @@
+// Internal interface between the C-ABI layer of the cache operators (kv_api.cu)
+// and their kernels. Not installed; not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace rope_gb300 {
+
+// Rows of an 8-bit cache that share a scale (ROPE_KV_SCALE_BLOCK in rope.h).
+constexpr int kKvBlock = 16;
+// Largest head size of the attention kernels.
+constexpr int kKvMaxHead = 256;
+
+// Attention over a key/value cache. The Nq / Nkv = G query heads of a key/value
+// head and the S new tokens of a sequence are the R = S * G rows of one problem
+// (b, kvh): row r is token r / G, query head kvh * G + r % G, so its Q and its
+// output are H consecutive elements of a (B, S, Nq, H) tensor.
+struct KvParams {
+  const void* q;           // (B, S, Nq*H)
+  const void* k;           // (B, Nkv, max_len, H): T, or e4m3 codes
+  const void* v;
+  const float* ks;         // (B, Nkv, nblk) scales of the 8-bit caches, or null
+  const float* vs;
+  void* out;               // (B, S, Nq*H)
+  const int32_t* past;     // (B)
+  const float* slopes;     // (Nq), or null
+  const int32_t* docs;     // (B, max_len), or null
+  const int32_t* prefix;   // (B), or null
+  int32_t* status;
+  float* ws_o;             // splits > 1: partial outputs (B*Nkv, splits, R, H)
+  float2* ws_ml;           // and their (maximum, sum) (B*Nkv, splits, R)
+  int64_t S, R, max_len, nblk;
+  int32_t B, Nq, Nkv, G, H;
+  int32_t splits;
+  int32_t vec;             // 16-byte loads of Q, K and V are aligned
+  float scale;             // factor of q.k
+  float cap;               // 0: no cap
+};
+
+// Kernel entry points for cudaLaunchKernel; each launch takes (KvParams).
+const void* kv_simple_kernel(int dtype, bool fp8);
+size_t kv_simple_smem(int H);
+const void* kv_combine_kernel(int dtype);
+
+constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
+constexpr int kKvCombineThreads = 128;  // one warp a row
+
+// Q and K rotation with the append to 8-bit caches.
+struct KvAppendParams {
+  const void* q;           // (B, S, Nq*H), or packed (B, S, (Nq + 2 Nkv)*H)
+  const void* k;           // (B, S, Nkv*H), or null when packed
+  const void* v;
+  const void* cos;         // (cache_rows, h)
+  const void* sin;
+  const int64_t* pos;      // (B, S), or null: past + s
+  const int32_t* past;     // (B)
+  const void* qw;          // RMSNorm weights (H), or null
+  const void* kw;
+  void* q_out;             // (B, S, Nq*H)
+  uint8_t* k_cache;        // (B, Nkv, max_len, H) e4m3 codes
+  uint8_t* v_cache;
+  float* k_scale;          // (B, Nkv, nblk)
+  float* v_scale;
+  int32_t* status;
+  int64_t B, S, max_len, nblk, cache_rows;
+  int64_t H;
+  int32_t Nq, Nkv, packed;
+  int32_t h, rd;           // half rotary width, rotary width
+  int32_t U, nP;           // units of a row, pair units among them
+  int32_t lanes;           // lanes that share a row (a power of two)
+  int32_t rows;            // rows of a group (a power of two <= 16)
+  int32_t wide;            // the caches take 16-byte accesses
+  int64_t blocks;          // most blocks that the S rows of a sequence touch
+  int64_t kv_tasks, q_tasks;
+  float eps;
+};
+constexpr int kKvAppendThreads = 256;
+const void* kv_append_kernel(int dtype, bool vec, bool interleaved, bool rms_norm);
+
+}  // namespace rope_gb300

@@ -949,6 +949,7 @@ rope_status mrope_common(rope_dtype dtype, int32_t x_rank, const int64_t* x_shap
 }  // namespace
 
 void rope_gb300::set_last_error(const char* msg) { g_last_error = msg; }
+void rope_gb300::set_last_kernel(const char* name) { g_last_kernel = name; }
 
 extern "C" {
 

@@ -93,6 +93,8 @@ const void* mrope_qkv_kernel(int dtype, bool vec, bool interleaved, bool rms_nor
 const void* qkv_heads_kernel(int dtype, bool interleaved, bool implicit_pos, bool rms_norm, int hpt, bool ragged);
 // Records the message rope_last_error() returns on the calling thread.
 void set_last_error(const char* msg);
+// Records the (static) name rope_last_kernel() returns on the calling thread.
+void set_last_kernel(const char* name);
 
 // TMA-pipelined variant (vector path, head size <= 256 elements); its launch
 // takes (KParams, TParams, CUtensorMap x, CUtensorMap y).
