@@ -474,7 +474,7 @@ rope_status rope_apply_no_alloc(rope_dtype dtype, int32_t x_rank, const int64_t*
  * query .. value, positions, past_seq_lens (required), interleaved,
  * rotary_embedding_dim, norm weights (both or neither), epsilon, q_out,
  * status_flags, ownership and errors as rope_apply_qkv in cache mode and
- * rope_apply_qkv_rmsnorm; no scratch. max_cache_len is limited to 2^31 - 1.
+ * rope_apply_qkv_rmsnorm; no scratch. max_cache_len is limited to 2^30.
  */
 #define ROPE_KV_SCALE_BLOCK 16
 rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
@@ -532,7 +532,7 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
  * Errors (before any launch): ROPE_ERR_INVALID_ARG for bad sizes, head counts,
  * scale or softcap, NULL or misaligned pointers; ROPE_ERR_UNSUPPORTED for
  * another dtype, head_size above 256, batch, seq or max_cache_len above
- * 2^31 - 1. B*S == 0 launches nothing.
+ * 2^30. B*S == 0 launches nothing.
  */
 rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
                          int32_t kv_num_heads, int64_t head_size, const void* query,
@@ -576,8 +576,8 @@ const char* rope_last_error(void);
    "rope_fused_kernel", "rope_qkv_kernel" (SIMT, one head per thread),
    "rope_qkv_heads_kernel" (SIMT Q/K, several heads of one role per thread),
    "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
-   (8-bit append) or "kv_simple_kernel" (attention on CUDA cores); "" before the first
-   launch. Calls that fail or launch nothing (empty X) leave it unchanged.
+   (8-bit append), "kv_token_kernel" (attention, few rows) or "kv_simple_kernel"
+   (attention on CUDA cores); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.
    The string is static; never free it. */
 const char* rope_last_kernel(void);

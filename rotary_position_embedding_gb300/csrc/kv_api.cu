@@ -30,6 +30,7 @@ static_assert(ROPE_KV_SCALE_BLOCK == kKvBlock, "rope.h and the kernels agree on 
 namespace {
 
 constexpr int kSms = 152;  // GB300
+constexpr int64_t kMaxLen = 1 << 30;     // positions and offsets between them stay in 32 bits
 constexpr int64_t kWorkspaceSlack = 16;  // aligns the part behind the partial outputs
 
 rope_status fail(rope_status st, const char* fmt, ...) {
@@ -131,23 +132,33 @@ rope_status launch(const void* fn, dim3 grid, int threads, size_t smem, rope_str
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
+enum class Family { kSimple, kToken };
+
 struct Plan {
+  Family family = Family::kSimple;
   int64_t tiles = 0;  // row tiles of a (b, kvh)
   int splits = 1;
   int64_t split_bytes = 0;  // workspace of one split of every row
 };
 
-// Splits from the sizes alone: the lengths are on the device. The keys are
-// split where the row tiles leave SMs without a CTA, up to the cache's length
-// over 256 keys a split.
-Plan plan_attention(int64_t B, int64_t S, int64_t Nq, int64_t Nkv, int64_t H, int64_t max_len) {
+// Kernel family and splits from the sizes alone: the lengths are on the device.
+// The keys are split where the row tiles leave SMs without a CTA, and a long
+// cache also so that sequences of other lengths even out.
+Plan plan_attention(Family family, int64_t B, int64_t S, int64_t Nq, int64_t Nkv, int64_t H, int64_t max_len) {
   Plan pl;
+  pl.family = family;
   const int64_t R = S * (Nq / Nkv);
-  pl.tiles = (R + kKvSimpleRows - 1) / kKvSimpleRows;
+  const int64_t rows = family == Family::kToken ? (R > 8 ? 16 : 8) : kKvSimpleRows;
+  pl.tiles = (R + rows - 1) / rows;
   const int64_t ctas = pl.tiles * Nkv * B;
   int64_t n = (2 * kSms + ctas - 1) / ctas;
-  if (n > (max_len + 255) / 256) n = (max_len + 255) / 256;
-  if (n > 64) n = 64;
+  if (family == Family::kToken) {
+    n = (4 * kSms + ctas - 1) / ctas;
+    if (n < (max_len + 1023) / 1024 && ctas < 16 * kSms) n = (max_len + 1023) / 1024;
+  }
+  const int64_t least = family == Family::kToken ? 64 : 256;
+  if (n > (max_len + least - 1) / least) n = (max_len + least - 1) / least;
+  if (n > 128) n = 128;
   pl.splits = n < 1 ? 1 : (int)n;
   pl.split_bytes = B * Nkv * R * (H * 4 + 8);
   return pl;
@@ -164,8 +175,8 @@ rope_status check_attention_sizes(int64_t batch, int64_t seq, int32_t num_heads,
   if (max_cache_len < 1) return fail(ROPE_ERR_INVALID_ARG, "max_cache_len must be >= 1");
   if (head_size > kKvMaxHead)
     return fail(ROPE_ERR_UNSUPPORTED, "head_size %lld exceeds %d", (long long)head_size, kKvMaxHead);
-  if (batch > INT32_MAX || seq > INT32_MAX || max_cache_len > INT32_MAX || kv_num_heads > 65535)
-    return fail(ROPE_ERR_UNSUPPORTED, "batch, seq and max_cache_len are limited to 2^31 - 1, kv_num_heads to 65535");
+  if (batch > kMaxLen || seq > kMaxLen || max_cache_len > kMaxLen || kv_num_heads > 65535)
+    return fail(ROPE_ERR_UNSUPPORTED, "batch, seq and max_cache_len are limited to 2^30, kv_num_heads to 65535");
   if (!sizes_fit({batch, seq, num_heads, head_size, 1024}) ||
       !sizes_fit({batch, kv_num_heads, max_cache_len, head_size, 8}))
     return fail(ROPE_ERR_INVALID_ARG, "Q has more than 2^52 or the caches more than 2^59 elements");
@@ -203,7 +214,11 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   KV_TRY(check_optional(status_flags, "status_flags", 4));
   KV_TRY(check_optional(workspace, "workspace", 16));
 
-  Plan pl = plan_attention(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+  const bool vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) &&
+                   aligned(v_cache, 16) && aligned(out, 16);
+  const Family family =
+      vec && dtype != ROPE_F32 && rope_get_variant() != ROPE_VARIANT_SIMT ? Family::kToken : Family::kSimple;
+  Plan pl = plan_attention(family, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
   const int64_t fits =
       workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
   if (pl.splits > fits) pl.splits = fits > 1 ? (int)fits : 1;
@@ -236,22 +251,28 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     p.ws_o = static_cast<float*>(workspace);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
   }
-  p.vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) && aligned(v_cache, 16) &&
-          aligned(out, 16);
+  p.vec = vec;
   p.scale = scale;
   p.cap = softcap;
 
   void* args[] = {&p};
   const int64_t gx = pl.tiles * pl.splits;
   if (gx > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
-  KV_TRY(launch(kv_simple_kernel(dtype, fp8), dim3((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535)),
-                kKvSimpleThreads, kv_simple_smem((int)head_size), stream, args, "kv_attention launch"));
-  set_last_kernel("kv_simple_kernel");
+  const dim3 grid((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
+  if (family == Family::kToken) {
+    const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.R > 8);
+    KV_TRY(launch(k.fn, grid, kKvTokenThreads, k.smem, stream, args, "kv_attention launch (few rows)"));
+    set_last_kernel("kv_token_kernel");
+  } else {
+    KV_TRY(launch(kv_simple_kernel(dtype, fp8), grid, kKvSimpleThreads, kv_simple_smem((int)head_size), stream, args,
+                  "kv_attention launch"));
+    set_last_kernel("kv_simple_kernel");
+  }
   if (pl.splits > 1) {
     const int64_t rows = batch * kv_num_heads * p.R;
-    int64_t grid = (rows + kKvCombineThreads / 32 - 1) / (kKvCombineThreads / 32);
-    if (grid > INT32_MAX) grid = INT32_MAX;
-    KV_TRY(launch(kv_combine_kernel(dtype), dim3((unsigned)grid), kKvCombineThreads, 0, stream, args,
+    int64_t gc = (rows + kKvCombineThreads / 32 - 1) / (kKvCombineThreads / 32);
+    if (gc > INT32_MAX) gc = INT32_MAX;
+    KV_TRY(launch(kv_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
                   "kv_attention launch (joining the splits)"));
   }
   return ROPE_OK;
@@ -266,8 +287,13 @@ int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, in
   set_last_error("");
   if (check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len) != ROPE_OK) return -1;
   if (batch == 0 || seq == 0) return 0;
-  const Plan pl = plan_attention(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
-  return pl.splits > 1 ? pl.splits * pl.split_bytes + kWorkspaceSlack : 0;
+  int64_t most = 0;
+  for (Family f : {Family::kSimple, Family::kToken}) {  // whichever kernel the call turns out to take
+    const Plan pl = plan_attention(f, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+    if (pl.splits > 1 && pl.splits * pl.split_bytes + kWorkspaceSlack > most)
+      most = pl.splits * pl.split_bytes + kWorkspaceSlack;
+  }
+  return most;
 }
 
 rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
@@ -323,7 +349,7 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
     return fail(ROPE_ERR_INVALID_ARG, "rotary_embedding_dim %d must be 0 or even, 0 < rd <= head size %lld",
                 rotary_embedding_dim, (long long)head_size);
   if (max_cache_len < 1) return fail(ROPE_ERR_INVALID_ARG, "max_cache_len must be >= 1");
-  if (max_cache_len > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "max_cache_len is limited to 2^31 - 1");
+  if (max_cache_len > kMaxLen) return fail(ROPE_ERR_UNSUPPORTED, "max_cache_len is limited to 2^30");
   if (!sizes_fit({batch, seq, (int64_t)num_heads + 2 * (int64_t)kv_num_heads, head_size, 8}) ||
       !sizes_fit({batch, kv_num_heads, max_cache_len, head_size, 8}) || !sizes_fit({cache_rows, rd, 8}))
     return fail(ROPE_ERR_INVALID_ARG, "Q/K/V, the caches or the tables have more than 2^59 elements");

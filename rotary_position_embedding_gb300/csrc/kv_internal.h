@@ -43,6 +43,15 @@ const void* kv_simple_kernel(int dtype, bool fp8);
 size_t kv_simple_smem(int H);
 const void* kv_combine_kernel(int dtype);
 
+// Few rows, 16-bit T, KvParams.vec: `rows` rows of a (b, kvh) a CTA.
+struct KvTokenKernel {
+  const void* fn;
+  size_t smem;
+  int rows;
+};
+constexpr int kKvTokenThreads = 128;
+KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
+
 constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;  // one warp a row
 

@@ -1,0 +1,576 @@
+// Attention over a key/value cache for few rows (single tokens, short drafts):
+// R = S * G rows of a (b, kvh), 8 or 16 of them a CTA, 16-bit T.
+//
+// Every cached byte is used once per 8 or 16 rows, so the cache's bandwidth is
+// the bound and the arithmetic has to stay out of its way. Both products run
+// on mma.m16n8k16 with the keys on the 16-row side, so that a group of up to 8
+// query heads fills the 8-column side:
+//   S^T = K Q^T   (16 tokens x 8 rows),   O^T += V^T P^T   (16 dims x 8 rows).
+// A warp walks units of 16 tokens by itself: no barrier until its keys are done.
+//
+// Loads. A lane copies exactly the 16-byte pieces of K and V that it will feed
+// to its own fragments (cp.async into a ring of its own in shared memory,
+// 32 lanes x 16 bytes side by side), so a wait for its own copies is all the
+// synchronisation there is, the reads back have no bank conflicts, and the bytes
+// in flight do not depend on registers. Any order of the head's dimensions
+// serves S as long as K and Q share it, and any order serves O as long as the
+// output undoes it; the orders are chosen so that the pieces are 64 and 128
+// contiguous bytes of a cache row:
+//   K: lane (g = lane / 4, c = lane % 4) takes tokens g and g + 8, bytes
+//      q * 64 + c * 16 .. + 15 of the row for each q;
+//   V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims v * 8 * VD + g * VD .. + VD - 1;
+//      two tokens' words are interleaved in registers into V^T fragments.
+// 8-bit caches: codes become float16 exactly on the way into the fragments; the
+// key scale of a unit (a block of 16 rows has one) multiplies its scores, the
+// value scale its weights, relative to the largest seen so far (a power of two,
+// so nothing is rounded). Q is float16 too, for bfloat16 after scaling each row
+// by a power of two; the scores undo it.
+//
+// Softmax: the running maximum moves only where a score passes it by 8 (in
+// log2), so weights stay below 2^8 (exact in float32, far from float16's end) and
+// the common unit costs one vote. P^T fragments come from S^T by movmatrix.
+//
+// A value that no row sees is zeroed before the product. Where one that only
+// some rows see is not finite, its zero weight in the others would make a NaN
+// of it: the CTA then does its rows over again one by one (kv_careful_row).
+#pragma once
+
+#include "kv_careful.cuh"
+
+namespace rope_gb300 {
+
+constexpr int kTokWarps = kKvTokenThreads / 32;
+
+template <class T>
+constexpr bool kIsBf16 = false;
+template <>
+constexpr bool kIsBf16<__nv_bfloat16> = true;
+
+__device__ __forceinline__ uint32_t kv_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 (or 8, 4) bytes global -> shared; zeros where `on` is false.
+template <int BYTES>
+__device__ __forceinline__ void kv_cp(uint32_t dst, const void* src, bool on) {
+  const int n = on ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void kv_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void kv_cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 kv_lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 kv_lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t kv_lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ float kv_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float kv_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh(y) = 1 - 2 / (1 + e^(2y)) from y2 = 2 * log2(e) * y. Absolute error a
+// few 2^-24 (the score needs an absolute one: it goes into an exponent).
+__device__ __forceinline__ float kv_tanh_of(float y2) { return fmaf(-2.0f, kv_rcp(1.0f + kv_exp2(y2)), 1.0f); }
+
+template <bool BF16>
+__device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t kv_transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two e4m3 codes (the low 16 bits) to float16x2, exactly.
+__device__ __forceinline__ uint32_t kv_codes2(uint32_t two) {
+  uint32_t y;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(y) : "r"(two));
+  return y;
+}
+__device__ __forceinline__ uint32_t kv_codes2_high(uint32_t two) {
+  uint32_t y;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(y) : "r"(two));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t kv_pack2(float lo, float hi) {
+  uint32_t y;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+
+// Whether either 16-bit half of x is an infinity or a NaN.
+template <bool BF16>
+__device__ __forceinline__ bool kv_odd2(uint32_t x) {
+  constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
+  return (x & E) == E || ((x >> 16) & E) == E;
+}
+
+// Whether one of four e4m3 codes is NaN (all bits but the sign set).
+__device__ __forceinline__ bool kv_nan4(uint32_t x) { return ((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)) != 0; }
+
+// A row of bfloat16 values as float16: scaled by the power of two that brings
+// its largest magnitude to 2^8..2^9. Returns what undoes it. `amax` is the
+// row's; rows that are 0 or not finite stay unscaled.
+__device__ __forceinline__ float kv_row_shift(float amax, float* factor) {
+  const int e = (int)(__float_as_uint(amax) >> 23);  // biased exponent of amax >= 0
+  *factor = 1.0f;
+  if (e == 0 || e >= 255) return 1.0f;
+  int s = 127 + 8 - e;  // factor 2^s
+  if (s > 120) s = 120;
+  if (s < -120) s = -120;
+  *factor = __uint_as_float((uint32_t)(127 + s) << 23);
+  return __uint_as_float((uint32_t)(127 - s) << 23);
+}
+
+template <class T, bool FP8, int HD, int NB>
+struct TokenCfg {
+  static constexpr int ES = FP8 ? 1 : 2;
+  static constexpr int KQ = HD * ES / 64;               // 16-byte pieces of K per lane and token
+  static constexpr int VD = FP8 ? (HD >= 128 ? 16 : 8) : 8;  // dims of a V piece
+  static constexpr int VB = VD * ES;                    // bytes of a V piece
+  static constexpr int VQ = HD / (8 * VD);              // V pieces per lane and token
+  static constexpr int kK = 2 * KQ * 512;
+  static constexpr int kV = 4 * VQ * 32 * VB;
+  static constexpr int kStage = kK + kV + 128;          // and 16 documents, 2 scales
+  static constexpr int kStages = kStage * 4 * kTokWarps <= 112 * 1024 ? (kStage * 6 * kTokWarps <= 112 * 1024 ? 6 : 4) : 3;
+  static constexpr int kMerge = kTokWarps * NB * 8 * (HD + 4) * 4;
+  static constexpr int kRing = kStage * kStages * kTokWarps;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+};
+
+template <class T, bool FP8, int HD, int NB>
+__global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvParams p) {
+  using C = TokenCfg<T, FP8, HD, NB>;
+  using bits = typename Elem<T>::bits;
+  constexpr bool BF = !FP8 && kIsBf16<T>;  // type of the matrix operands
+  constexpr int OT = HD / 16;                                   // 16-dim tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kTokWarps][NB * 8], s_l[kTokWarps][NB * 8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t rows0 = (int64_t)(blockIdx.x / p.splits) * (NB * 8);
+  const int split = blockIdx.x % p.splits;
+  const int kvh = blockIdx.y;
+  const uint32_t ring = kv_smem(smem) + warp * (C::kStage * C::kStages);
+  for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
+    const KvSeq seq = kv_seq(p, b);
+    if (blockIdx.x == 0 && kvh == 0 && tid == 0) kv_flag_rows(p, seq);
+    const int64_t rlast = (rows0 + NB * 8 < p.R ? rows0 + NB * 8 : p.R) - 1;
+    int64_t end = kv_limit(seq, seq.past + rlast / p.G);
+    if (end < 0) end = 0;
+    int64_t lo64, hi64;
+    kv_split(end, p.splits, split, 16 * kTokWarps, &lo64, &hi64);
+    const int lo = (int)lo64, hi = (int)hi64;
+    const int64_t plane = (int64_t)b * p.Nkv + kvh;
+    const int HB = p.H * C::ES;  // bytes of a cache row
+    const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + plane * p.max_len * HB;
+    const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + plane * p.max_len * HB;
+    const int32_t* dbase = p.docs ? p.docs + (int64_t)b * p.max_len : nullptr;
+
+    auto copy_unit = [&](int j0, int stage) {
+      const uint32_t at = ring + stage * C::kStage;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = j0 + g + 8 * h;
+        const uint8_t* src = kbase + (int64_t)(j < hi ? j : lo) * HB;
+#pragma unroll
+        for (int q = 0; q < C::KQ; ++q) {
+          const int off = q * 64 + c * 16;
+          const bool on = j < hi && off < HB;
+          kv_cp<16>(at + (h * C::KQ + q) * 512 + lane * 16, src + (on ? off : 0), on);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int j = j0 + 2 * c + (t & 1) + 8 * (t >> 1);
+        const uint8_t* src = vbase + (int64_t)(j < hi ? j : lo) * HB;
+#pragma unroll
+        for (int v = 0; v < C::VQ; ++v) {
+          const int off = (v * 8 + g) * C::VB;
+          const bool on = j < hi && off < HB;
+          kv_cp<C::VB>(at + C::kK + ((t * C::VQ + v) * 32 + lane) * C::VB, src + (on ? off : 0), on);
+        }
+      }
+      const uint32_t meta = at + C::kK + C::kV;
+      if (dbase && lane < 16) kv_cp<4>(meta + lane * 4, dbase + (j0 + lane < hi ? j0 + lane : lo), j0 + lane < hi);
+      if (FP8 && lane >= 16 && lane < 18)
+        kv_cp<4>(meta + lane * 4, (lane == 16 ? p.ks : p.vs) + plane * p.nblk + j0 / kKvBlock, j0 < hi);
+    };
+    auto row_of = [&](int64_t r) {  // element offset of a row of Q or of the output
+      return (((int64_t)b * p.S + r / p.G) * p.Nq + (int64_t)kvh * p.G + r % p.G) * p.H;
+    };
+
+    const int first = lo + warp * 16, step = 16 * kTokWarps;
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      if (first + s * step < hi) copy_unit(first + s * step, s);
+      kv_cp_commit();
+    }
+
+    // Q fragments: row g of each column tile, in the order of K's pieces
+    uint32_t qf[NB][HD / 16][2];
+    float undo[NB] = {};
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int64_t r = rows0 + n * 8 + g;
+      const bool live = r < p.R;
+      const bits* src = static_cast<const bits*>(p.q) + (live ? row_of(r) : 0);
+      undo[n] = 1.0f;
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int q = 0; q < C::KQ; ++q) {
+          const int d = q * 32 + c * 8;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (live && d < p.H) w = __ldg(reinterpret_cast<const uint4*>(src + d));
+          qf[n][2 * q][0] = w.x, qf[n][2 * q][1] = w.y, qf[n][2 * q + 1][0] = w.z, qf[n][2 * q + 1][1] = w.w;
+        }
+      } else {
+        // 16 dims a piece; bfloat16 rows become float16 after scaling by a power of two
+        uint32_t raw[C::KQ][8];
+        float amax = 0.0f;
+#pragma unroll
+        for (int q = 0; q < C::KQ; ++q)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int d = q * 64 + c * 16 + i * 8;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live && d < p.H) w = __ldg(reinterpret_cast<const uint4*>(src + d));
+            raw[q][4 * i] = w.x, raw[q][4 * i + 1] = w.y, raw[q][4 * i + 2] = w.z, raw[q][4 * i + 3] = w.w;
+          }
+        if constexpr (kIsBf16<T>) {
+#pragma unroll
+          for (int q = 0; q < C::KQ; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = fabsf(Elem<T>::tof((bits)raw[q][i])), d = fabsf(Elem<T>::tof((bits)(raw[q][i] >> 16)));
+              amax = fmaxf(amax, fmaxf(a, d));
+            }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          float f;
+          undo[n] = kv_row_shift(amax, &f);
+#pragma unroll
+          for (int q = 0; q < C::KQ; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              raw[q][i] = kv_pack2<false>(Elem<T>::tof((bits)raw[q][i]) * f, Elem<T>::tof((bits)(raw[q][i] >> 16)) * f);
+        }
+#pragma unroll
+        for (int q = 0; q < C::KQ; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[n][4 * q + i][0] = raw[q][2 * i], qf[n][4 * q + i][1] = raw[q][2 * i + 1];
+      }
+    }
+
+    // the rows whose scores this lane holds: 2c and 2c + 1 of each column tile
+    float mult[NB][2], slope[NB][2], m[NB][2], l[NB][2];
+    int64_t pos[NB][2];
+    int lim[NB][2], doc[NB][2];
+    const float c1 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    const float c2 = p.cap * kLog2e;
+    int full = 0x7fffffff;  // keys below this are seen by every row
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t r = rows0 + n * 8 + 2 * c + e;
+        const bool live = r < p.R;
+        mult[n][e] = c1 * __shfl_sync(0xffffffffu, undo[n], 4 * (2 * c + e));
+        pos[n][e] = seq.past + (live ? r : 0) / p.G;
+        int64_t k = live ? kv_limit(seq, pos[n][e]) : 0;
+        doc[n][e] = 0;
+        if (p.docs && live && !kv_document(p, b, pos[n][e], &doc[n][e])) k = 0;
+        lim[n][e] = k > 0 ? (int)k : 0;
+        slope[n][e] = p.slopes && live ? __ldg(p.slopes + kvh * p.G + r % p.G) * kLog2e : 0.0f;
+        if (live && lim[n][e] < full) full = lim[n][e];
+        m[n][e] = -CUDART_INF_F;
+        l[n][e] = 0.0f;
+      }
+#pragma unroll
+    for (int o = 1; o <= 2; o *= 2) {
+      const int x = __shfl_xor_sync(0xffffffffu, full, o);
+      full = x < full ? x : full;
+    }
+    float acc[OT][NB][4];
+#pragma unroll
+    for (int t = 0; t < OT; ++t)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
+    float vref = 0.0f;  // O is held in units of this value scale
+    bool odd = false;   // an infinity or a NaN in a value that not every row sees
+
+    int stage = 0, next = C::kStages - 1;
+    for (int j0 = first; j0 < hi; j0 += step) {
+      kv_cp_wait<C::kStages - 2>();
+      if (FP8 || dbase) __syncwarp();  // documents and scales were copied by other lanes
+      const uint32_t at = ring + stage * C::kStage;
+      const uint32_t meta = at + C::kK + C::kV;
+      float s[NB][4];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < C::KQ; ++q) {
+        const uint4 x = kv_lds16(at + q * 512 + lane * 16), y = kv_lds16(at + (C::KQ + q) * 512 + lane * 16);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            kv_mma<BF>(s[n], x.x, y.x, x.y, y.y, qf[n][2 * q][0], qf[n][2 * q][1]);
+            kv_mma<BF>(s[n], x.z, y.z, x.w, y.w, qf[n][2 * q + 1][0], qf[n][2 * q + 1][1]);
+          }
+        } else {
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = kv_codes2(xs[i]), a2 = kv_codes2_high(xs[i]);
+            const uint32_t a1 = kv_codes2(ys[i]), a3 = kv_codes2_high(ys[i]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) kv_mma<false>(s[n], a0, a1, a2, a3, qf[n][4 * q + i][0], qf[n][4 * q + i][1]);
+          }
+        }
+      }
+      float ks = 1.0f, vs = 1.0f;
+      if constexpr (FP8) {
+        ks = __uint_as_float(kv_lds4(meta + 64));
+        vs = __uint_as_float(kv_lds4(meta + 68));
+      }
+      const bool whole = !dbase && j0 + 16 <= full;  // uniform over the warp
+      uint32_t any0 = 0xffffffffu, any1 = 0xffffffffu;
+      int d0 = 0, d1 = 0;
+      if (dbase) d0 = (int)kv_lds4(meta + g * 4), d1 = (int)kv_lds4(meta + (g + 8) * 4);
+      bool seen0 = false, seen1 = false;
+      bool moved = false;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = s[n][e] * (mult[n][e] * ks), y = s[n][2 + e] * (mult[n][e] * ks);
+          if (p.cap > 0.0f) {
+            x = kv_tanh_of(x) * c2;
+            y = kv_tanh_of(y) * c2;
+          }
+          if (p.slopes) {
+            const float dist = (float)(pos[n][e] - j0 - g);
+            x = fmaf(-slope[n][e], fabsf(dist), x);
+            y = fmaf(-slope[n][e], fabsf(dist - 8.0f), y);
+          }
+          if (!whole) {
+            const bool a = j0 + g < lim[n][e] && (!dbase || d0 == doc[n][e]);
+            const bool d = j0 + g + 8 < lim[n][e] && (!dbase || d1 == doc[n][e]);
+            x = a ? x : -CUDART_INF_F;
+            y = d ? y : -CUDART_INF_F;
+            seen0 |= a;
+            seen1 |= d;
+          }
+          s[n][e] = x;
+          s[n][2 + e] = y;
+          moved |= fmaxf(x, y) > m[n][e] + 8.0f;
+        }
+      if (!whole) {
+        any0 = __ballot_sync(0xffffffffu, seen0);
+        any1 = __ballot_sync(0xffffffffu, seen1);
+      }
+      if (any0 | any1) {  // a unit that no row sees is left out
+        const bool grown = FP8 && vs > vref;
+        if (__any_sync(0xffffffffu, moved) || grown) {
+          float fv = 1.0f;
+          if (grown) {
+            fv = vref * __uint_as_float((254u << 23) - __float_as_uint(vs));  // old / new, powers of two
+            vref = vs;
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+              for (int o = 4; o <= 16; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              x = fmaxf(m[n][e], x);
+              const float a = x == -CUDART_INF_F ? 1.0f : kv_exp2(m[n][e] - x);
+              m[n][e] = x;
+              l[n][e] *= a;
+#pragma unroll
+              for (int t = 0; t < OT; ++t) {
+                acc[t][n][e] *= a * fv;
+                acc[t][n][2 + e] *= a * fv;
+              }
+            }
+        }
+        const float fp = FP8 ? vs * __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float base = m[n][e] == -CUDART_INF_F ? 0.0f : m[n][e];
+            w[e] = kv_exp2(s[n][e] - base);
+            w[2 + e] = kv_exp2(s[n][2 + e] - base);
+            l[n][e] += w[e] + w[2 + e];
+          }
+          if constexpr (FP8) w[0] *= fp, w[1] *= fp, w[2] *= fp, w[3] *= fp;
+          pf[n][0] = kv_transpose8(kv_pack2<BF>(w[0], w[1]));
+          pf[n][1] = kv_transpose8(kv_pack2<BF>(w[2], w[3]));
+        }
+        // tokens 2c, 2c + 1, 2c + 8, 2c + 9: whether some row sees them
+        const bool on[4] = {((any0 >> (8 * c)) & 15u) != 0, ((any0 >> (8 * c + 4)) & 15u) != 0,
+                            ((any1 >> (8 * c)) & 15u) != 0, ((any1 >> (8 * c + 4)) & 15u) != 0};
+#pragma unroll
+        for (int v = 0; v < C::VQ; ++v) {
+          uint32_t x[4][C::VB / 4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t a = at + C::kK + ((t * C::VQ + v) * 32 + lane) * C::VB;
+            if constexpr (C::VB == 16) {
+              const uint4 y = kv_lds16(a);
+              x[t][0] = y.x, x[t][1] = y.y, x[t][2] = y.z, x[t][3] = y.w;
+            } else {
+              const uint2 y = kv_lds8(a);
+              x[t][0] = y.x, x[t][1] = y.y;
+            }
+            if (!whole && !on[t]) {
+#pragma unroll
+              for (int w = 0; w < C::VB / 4; ++w) x[t][w] = 0u;
+            }
+            if (!whole && p.S > 1) {
+#pragma unroll
+              for (int w = 0; w < C::VB / 4; ++w) odd |= FP8 ? kv_nan4(x[t][w]) : kv_odd2<BF>(x[t][w]);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < C::VB / 4; ++w) {
+            if constexpr (!FP8) {  // word w: dims 2w, 2w + 1 of the piece
+              const uint32_t a[4] = {__byte_perm(x[0][w], x[1][w], 0x5410), __byte_perm(x[0][w], x[1][w], 0x7632),
+                                     __byte_perm(x[2][w], x[3][w], 0x5410), __byte_perm(x[2][w], x[3][w], 0x7632)};
+              #pragma unroll
+              for (int n = 0; n < NB; ++n) kv_mma<BF>(acc[v * 4 + w][n], a[0], a[1], a[2], a[3], pf[n][0], pf[n][1]);
+            } else {  // word w: dims 4w .. 4w + 3
+              const uint32_t p01 = __byte_perm(x[0][w], x[1][w], 0x5140), p23 = __byte_perm(x[0][w], x[1][w], 0x7362);
+              const uint32_t r01 = __byte_perm(x[2][w], x[3][w], 0x5140), r23 = __byte_perm(x[2][w], x[3][w], 0x7362);
+              const uint32_t a[4] = {kv_codes2(p01), kv_codes2_high(p01), kv_codes2(r01), kv_codes2_high(r01)};
+              const uint32_t d[4] = {kv_codes2(p23), kv_codes2_high(p23), kv_codes2(r23), kv_codes2_high(r23)};
+              const int t = v * (C::VD / 2) + 2 * w;
+#pragma unroll
+              for (int n = 0; n < NB; ++n) {
+                kv_mma<BF>(acc[t][n], a[0], a[1], a[2], a[3], pf[n][0], pf[n][1]);
+                kv_mma<BF>(acc[t + 1][n], d[0], d[1], d[2], d[3], pf[n][0], pf[n][1]);
+              }
+            }
+          }
+        }
+      }
+      // refill the stage of the unit before this one, whose reads are done
+      const int ahead = j0 + (C::kStages - 1) * step;
+      if (FP8 || dbase) __syncwarp();
+      if (ahead < hi) copy_unit(ahead, next);
+      kv_cp_commit();
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      next = next + 1 == C::kStages ? 0 : next + 1;
+    }
+    kv_cp_wait<0>();
+
+    if (__syncthreads_or(odd)) {
+#pragma unroll 1
+      for (int r = warp; r < NB * 8; r += kTokWarps)
+        if (rows0 + r < p.R) kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + r, lo64, hi64, split, lane);
+      __syncthreads();
+      continue;
+    }
+    // join the warps: their O (in units of 1) and statistics meet in shared memory
+    float* so = reinterpret_cast<float*>(smem);
+    constexpr int LD = HD + 4;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int o = 4; o <= 16; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int r = n * 8 + 2 * c + e;
+        if (g == 0) s_m[warp][r] = m[n][e], s_l[warp][r] = sum;
+        float* o = so + (warp * NB * 8 + r) * LD;
+        const float f = FP8 ? vref : 1.0f;
+#pragma unroll
+        for (int t = 0; t < OT; ++t) {
+          // tile t: dims piece(t / (VD / 2)) + g * VD + 2 * (t % (VD / 2)) and the next
+          const int d = (t / (C::VD / 2)) * 8 * C::VD + g * C::VD + 2 * (t % (C::VD / 2));
+          o[d] = acc[t][n][e] * f;
+          o[d + 1] = acc[t][n][2 + e] * f;
+        }
+      }
+    __syncthreads();
+    for (int i = tid; i < NB * 8 * (HD / 4); i += kKvTokenThreads) {
+      const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
+      const int64_t row = rows0 + r;
+      if (row >= p.R || d >= p.H) continue;
+      float M = s_m[0][r];
+#pragma unroll
+      for (int w = 1; w < kTokWarps; ++w) M = fmaxf(M, s_m[w][r]);
+      float L = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        const float lw = s_l[w][r];
+        if (s_m[w][r] == -CUDART_INF_F && lw == 0.0f) continue;
+        const float f = kv_exp2(s_m[w][r] - (M == -CUDART_INF_F ? 0.0f : M));
+        const float4 x = *reinterpret_cast<const float4*>(so + (w * NB * 8 + r) * LD + d);
+        L = fmaf(lw, f, L);
+        o0 = fmaf(x.x, f, o0), o1 = fmaf(x.y, f, o1), o2 = fmaf(x.z, f, o2), o3 = fmaf(x.w, f, o3);
+      }
+      if (p.splits > 1) {
+        const int64_t at = (plane * p.splits + split) * p.R + row;
+        if (d == 0) p.ws_ml[at] = make_float2(M, L);
+        *reinterpret_cast<float4*>(p.ws_o + at * p.H + d) = make_float4(o0, o1, o2, o3);
+      } else {
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        VecT<T, 4> y;
+        y.v[0] = Elem<T>::fromf(o0 * inv), y.v[1] = Elem<T>::fromf(o1 * inv);
+        y.v[2] = Elem<T>::fromf(o2 * inv), y.v[3] = Elem<T>::fromf(o3 * inv);
+        *reinterpret_cast<VecT<T, 4>*>(static_cast<bits*>(p.out) + row_of(row) + d) = y;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace rope_gb300
