@@ -576,7 +576,8 @@ const char* rope_last_error(void);
    "rope_fused_kernel", "rope_qkv_kernel" (SIMT, one head per thread),
    "rope_qkv_heads_kernel" (SIMT Q/K, several heads of one role per thread),
    "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
-   (8-bit append), "kv_token_kernel" (attention, few rows) or "kv_simple_kernel"
+   (8-bit append), "kv_token_kernel" (attention, few rows), "kv_tile_kernel"
+   (attention, many rows) or "kv_simple_kernel"
    (attention on CUDA cores); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.
    The string is static; never free it. */

@@ -1,0 +1,11 @@
+// Attention over a key/value cache for many rows (tcgen05): instances for
+// float16 queries.
+#include "kv_tile.cuh"
+
+namespace rope_gb300 {
+
+KvTileKernel kv_tile_kernel_f16(int H) {
+  return kv_tile_pick<__half, false>(H);
+}
+
+}  // namespace rope_gb300

@@ -132,7 +132,7 @@ rope_status launch(const void* fn, dim3 grid, int threads, size_t smem, rope_str
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
-enum class Family { kSimple, kToken };
+enum class Family { kSimple, kToken, kTile };
 
 struct Plan {
   Family family = Family::kSimple;
@@ -148,7 +148,9 @@ Plan plan_attention(Family family, int64_t B, int64_t S, int64_t Nq, int64_t Nkv
   Plan pl;
   pl.family = family;
   const int64_t R = S * (Nq / Nkv);
-  const int64_t rows = family == Family::kToken ? (R > 8 ? 16 : 8) : kKvSimpleRows;
+  const int64_t rows = family == Family::kToken  ? (R > 8 ? 16 : 8)
+                       : family == Family::kTile ? kv_tile_rows(H)
+                                                 : kKvSimpleRows;
   pl.tiles = (R + rows - 1) / rows;
   const int64_t ctas = pl.tiles * Nkv * B;
   int64_t n = (2 * kSms + ctas - 1) / ctas;
@@ -156,12 +158,22 @@ Plan plan_attention(Family family, int64_t B, int64_t S, int64_t Nq, int64_t Nkv
     n = (4 * kSms + ctas - 1) / ctas;
     if (n < (max_len + 1023) / 1024 && ctas < 16 * kSms) n = (max_len + 1023) / 1024;
   }
-  const int64_t least = family == Family::kToken ? 64 : 256;
+  if (family == Family::kTile) n = kSms / ctas;
+  const int64_t least = family == Family::kToken ? 64 : family == Family::kTile ? 512 : 256;
   if (n > (max_len + least - 1) / least) n = (max_len + least - 1) / least;
   if (n > 128) n = 128;
   pl.splits = n < 1 ? 1 : (int)n;
   pl.split_bytes = B * Nkv * R * (H * 4 + 8);
   return pl;
+}
+
+// The matrix kernels take 16-bit types whose rows are 16-byte aligned; up to 16
+// rows of a (b, kvh) go to the one for few rows.
+Family choose_family(bool matrix, int64_t B, int64_t S, int64_t G, int64_t Nkv, int64_t H) {
+  if (!matrix || rope_get_variant() == ROPE_VARIANT_SIMT) return Family::kSimple;
+  const int64_t R = S * G;
+  const bool grid = B <= 65535 && (R + kv_tile_rows(H) - 1) / kv_tile_rows(H) <= 65535;
+  return R > 16 && grid ? Family::kTile : Family::kToken;
 }
 
 rope_status check_attention_sizes(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
@@ -216,8 +228,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
 
   const bool vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) &&
                    aligned(v_cache, 16) && aligned(out, 16);
-  const Family family =
-      vec && dtype != ROPE_F32 && rope_get_variant() != ROPE_VARIANT_SIMT ? Family::kToken : Family::kSimple;
+  const Family family = choose_family(vec && dtype != ROPE_F32, batch, seq, num_heads / kv_num_heads, kv_num_heads,
+                                      head_size);
   Plan pl = plan_attention(family, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
   const int64_t fits =
       workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
@@ -259,7 +271,14 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   const int64_t gx = pl.tiles * pl.splits;
   if (gx > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
   const dim3 grid((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
-  if (family == Family::kToken) {
+  if (family == Family::kTile) {
+    const int h = (int)head_size;
+    const KvTileKernel k = dtype == ROPE_F16 ? (fp8 ? kv_tile_kernel_f16_fp8(h) : kv_tile_kernel_f16(h))
+                                             : (fp8 ? kv_tile_kernel_bf16_fp8(h) : kv_tile_kernel_bf16(h));
+    const dim3 tg((unsigned)(kv_num_heads * pl.splits), (unsigned)batch, (unsigned)pl.tiles);
+    KV_TRY(launch(k.fn, tg, kKvTileThreads, k.smem, stream, args, "kv_attention launch (many rows)"));
+    set_last_kernel("kv_tile_kernel");
+  } else if (family == Family::kToken) {
     const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.R > 8);
     KV_TRY(launch(k.fn, grid, kKvTokenThreads, k.smem, stream, args, "kv_attention launch (few rows)"));
     set_last_kernel("kv_token_kernel");
@@ -288,7 +307,7 @@ int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, in
   if (check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len) != ROPE_OK) return -1;
   if (batch == 0 || seq == 0) return 0;
   int64_t most = 0;
-  for (Family f : {Family::kSimple, Family::kToken}) {  // whichever kernel the call turns out to take
+  for (Family f : {Family::kSimple, Family::kToken, Family::kTile}) {  // whichever kernel the call turns out to take
     const Plan pl = plan_attention(f, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
     if (pl.splits > 1 && pl.splits * pl.split_bytes + kWorkspaceSlack > most)
       most = pl.splits * pl.split_bytes + kWorkspaceSlack;

@@ -52,6 +52,19 @@ struct KvTokenKernel {
 constexpr int kKvTokenThreads = 128;
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
+// Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above
+// H = 128), grid (Nkv * splits, B, row tiles).
+struct KvTileKernel {
+  const void* fn;
+  size_t smem;
+};
+constexpr int kKvTileThreads = 384;
+constexpr int kv_tile_rows(int64_t H) { return H <= 128 ? 256 : 128; }
+KvTileKernel kv_tile_kernel_f16(int H);
+KvTileKernel kv_tile_kernel_f16_fp8(int H);
+KvTileKernel kv_tile_kernel_bf16(int H);
+KvTileKernel kv_tile_kernel_bf16_fp8(int H);
+
 constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;  // one warp a row
 

@@ -1,0 +1,736 @@
+// Attention over a key/value cache for many rows (prompts, chunks): tcgen05.
+//
+// R = S * G rows of a (b, kvh) (token-major, so the G query heads that share K
+// and V sit in one tile), 16-bit T. A CTA takes NT tiles of 128 rows and walks
+// the keys in tiles of N; per row tile and key tile
+//   S = Q K^T   (128 x N, accumulated in TMEM),
+//   P = 2^(x - m) of the scores x (registers), back to TMEM as 16-bit values,
+//   O += P V    (A from TMEM, accumulated in TMEM).
+// Bound by the tensor cores: 4 H flops a pair of row and key, 1024 clocks a
+// row tile and key tile at H = 128, against which the 128 x 128 exponentials and
+// what surrounds them have to be hidden. So with NT = 2 the two row tiles take
+// turns: while one tile's scores are in registers, the tensor cores work for
+// the other. H = 256 fills TMEM with one tile: NT = 1, N = 64, S double-buffered.
+//
+// Warps (12): 0-3 and 4-7 softmax of row tile 0 and 1, a thread a row; 8 (one
+// lane) issues every MMA; 9-11 bring K and V to shared memory.
+//   8-bit caches: the bringing warps load codes and write float16 (exact); the
+//   key scale of each 16 keys multiplies scores, the value scale weights,
+//   relative to the largest value scale so far (powers of two); bfloat16 Q rows
+//   become float16 after scaling by a power of two that the scores undo.
+// Shared memory: Q, two stages of K and two of V, each as slabs of 64 elements
+// (128-byte rows, 128-byte swizzle): the K-major form for Q and K, and the same
+// bytes read MN-major for V.
+// TMEM (512 columns): S (P over its first half), O at 256.
+//
+// Barriers: k_full, v_full (the bringing threads) and k_free, v_free (commits)
+// for each stage; s_full (commit) and p_full (128 threads) for each S buffer;
+// o_full at the end; info (documents and scales of a key tile, four slots). A
+// commit covers every MMA issued before it, so s_full of step j also says that
+// P V of step j - 1 of that row tile is complete: O may be rescaled then. MMAs
+// of a CTA run in the order of issue, so S of the next step may overwrite the P
+// that P V has yet to read.
+// Every wait is bounded (2 s); one that runs out sets status bit 1, and the warp
+// goes to the common end, where TMEM is freed.
+//
+// The running maximum moves only where a score passes it by 8 (in log2): O is
+// rescaled by its softmax threads then, seldom after the first tiles, so there
+// is no separate correction warp. The last key tile's rows behind the keys are
+// zeros. Key tiles whose documents no row of the CTA can have are left out.
+#pragma once
+
+#include "kv_careful.cuh"
+#include "kv_token.cuh"
+#include "rope_tma.cuh"
+
+namespace rope_gb300 {
+
+constexpr int kTileThreads = kKvTileThreads;
+constexpr int kTileRows = 128;
+constexpr int kTileBring = 96;         // bringing threads
+constexpr int kTileListed = 4096;      // key tiles of a CTA whose documents are looked at
+
+template <bool FP8, int HD>
+struct TileCfg {
+  static constexpr int NT = HD <= 128 ? 2 : 1;
+  static constexpr int N = HD <= 128 ? 128 : 64;
+  static constexpr int SLABS = HD / 64;
+  static constexpr int kQ = NT * kTileRows * HD * 2;
+  static constexpr int kStage = N * HD * 2;  // of K, and of V
+  static constexpr int kInfo = N * 4 + 128;  // documents, N/16 key scales, N/16 value scales
+  static constexpr int kTail = 4 * kInfo + 2 * kTileListed / 8 + NT * kTileRows * 4 + 256;
+  static constexpr int kSmem = 1024 + kQ + 4 * kStage + kTail;
+};
+
+struct TileBars {
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], info[4], drain;
+};
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// D (TMEM) (+)= A (shared memory) B (shared memory)
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// D (TMEM) (+)= A (TMEM) B (shared memory)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// Matrix descriptor of a 128-byte-swizzled operand at shared address `a`:
+// groups of 8 rows 1024 bytes apart; `lead` between 64-element slabs (read
+// MN-major; ignored K-major).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t a, uint32_t lead) {
+  return (uint64_t)((a & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
+         2ull << 61;
+}
+// Instruction descriptor: float32 accumulator, 16-bit operands, M = 128.
+__device__ __forceinline__ uint32_t tc_idesc(bool bf16, int n, bool b_mn_major) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(128 >> 4) << 24;
+}
+
+#define KV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define KV_W8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+
+// 32 columns of this thread's TMEM lane (not complete before tc_wait_ld).
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KV_R8(r, 0), KV_R8(r, 8), KV_R8(r, 16), KV_R8(r, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KV_W8(r, 0),
+      KV_W8(r, 8), KV_W8(r, 16), KV_W8(r, 24), "r"(addr)
+      : "memory");
+}
+// Waits for this thread's loads; the registers pass through, so that no use of
+// them moves ahead of the wait.
+#define KV_RW8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+__device__ __forceinline__ void tc_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KV_RW8(r, 0), KV_RW8(r, 8), KV_RW8(r, 16), KV_RW8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 columns, waited for; and back.
+__device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : KV_R8(r, 0), KV_R8(r, 8)
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KV_RW8(r, 0), KV_RW8(r, 8)::"memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KV_W8(r, 0),
+      KV_W8(r, 8), "r"(addr)
+      : "memory");
+}
+
+// Byte offset of 16-byte piece `piece` (8 elements) of row `row` in an operand
+// of `rows` rows: slabs of 8 pieces, swizzled by the row.
+__device__ __forceinline__ uint32_t tile_at(int rows, int row, int piece) {
+  return (uint32_t)((piece >> 3) * rows * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+// The key tiles of a CTA: all of [0, count), or those that `need` names.
+struct TileList {
+  const uint32_t* need;
+  int count;
+  bool listed;
+  __device__ __forceinline__ int next(int t) const {  // the first one from t on, or count
+    if (!listed) return t < count ? t : count;
+    while (t < count && t < kTileListed) {
+      const uint32_t w = need[t >> 5] >> (t & 31);
+      if (w) {
+        t += __ffs(w) - 1;
+        return t < count ? t : count;
+      }
+      t = (t | 31) + 1;
+    }
+    return t < count ? t : count;
+  }
+};
+
+template <class T, bool FP8, int HD>
+__global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvParams p) {
+  using C = TileCfg<FP8, HD>;
+  using bits = typename Elem<T>::bits;
+  constexpr bool BF = !FP8 && kIsBf16<T>;
+  constexpr int NT = C::NT, N = C::N, NB = N / 16;
+  extern __shared__ uint8_t kv_tiles[];
+  __shared__ TileBars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_qdoc[2];
+  uint8_t* base = kv_tiles + ((1024 - (kv_smem(kv_tiles) & 1023)) & 1023);
+  const uint32_t sq = kv_smem(base), sk = sq + C::kQ, sv = sk + 2 * C::kStage;
+  uint8_t* info = base + C::kQ + 4 * C::kStage;
+  uint32_t* need = reinterpret_cast<uint32_t*>(info + 4 * C::kInfo);
+  uint32_t* mixed = need + kTileListed / 32;
+  float* undo = reinterpret_cast<float*>(mixed + kTileListed / 32);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](uint64_t* b) { return kv_smem(b); };
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(&bars.k_full[i]), kTileBring);
+      mbar_init(bar(&bars.v_full[i]), kTileBring);
+      mbar_init(bar(&bars.k_free[i]), 1);
+      mbar_init(bar(&bars.v_free[i]), 1);
+      mbar_init(bar(&bars.s_full[i]), 1);
+      mbar_init(bar(&bars.p_full[i]), kTileRows);
+      mbar_init(bar(&bars.o_full[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(&bars.info[i]), kTileBring);
+    mbar_init(bar(&bars.drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_qdoc[0] = 0x7fffffff;
+    s_qdoc[1] = (int)0x80000000;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem(&s_tmem)), "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int kvh = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  const int b = blockIdx.y;
+  const int64_t rows0 = (int64_t)(gridDim.z - 1 - blockIdx.z) * (NT * kTileRows);  // the longest rows first
+  const KvSeq seq = kv_seq(p, b);
+  if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) kv_flag_rows(p, seq);
+  const int64_t rlast = (rows0 + NT * kTileRows < p.R ? rows0 + NT * kTileRows : p.R) - 1;
+  const int live_tiles = rlast - rows0 >= kTileRows ? NT : 1;
+  int64_t end = kv_limit(seq, seq.past + rlast / p.G);
+  if (end < 0) end = 0;
+  int64_t lo64, hi64;
+  kv_split(end, p.splits, split, N, &lo64, &hi64);
+  const int lo = (int)lo64, hi = (int)hi64;
+  const int64_t plane = (int64_t)b * p.Nkv + kvh;
+  const int32_t* docs = p.docs ? p.docs + (int64_t)b * p.max_len : nullptr;
+  auto row_at = [&](int64_t r) {
+    return (((int64_t)b * p.S + r / p.G) * p.Nq + (int64_t)kvh * p.G + r % p.G) * p.H;
+  };
+
+  // Q to shared memory: half a warp (a warp for H > 128) a row
+  {
+    constexpr int LANES = HD <= 128 ? 16 : 32;
+    const int per = 32 / LANES, sub = lane / LANES, piece = lane % LANES;
+    for (int r = warp * per + sub; r < NT * kTileRows; r += kTileThreads / 32 * per) {
+      const int64_t row = rows0 + r;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (row < p.R && piece * 8 < p.H)
+        w = __ldg(reinterpret_cast<const uint4*>(static_cast<const bits*>(p.q) + row_at(row) + piece * 8));
+      if constexpr (FP8 && kIsBf16<T>) {
+        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(Elem<T>::tof((bits)x[i])), fabsf(Elem<T>::tof((bits)(x[i] >> 16)))));
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float f;
+        const float u = kv_row_shift(amax, &f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = kv_pack2<false>(Elem<T>::tof((bits)x[i]) * f, Elem<T>::tof((bits)(x[i] >> 16)) * f);
+        w = make_uint4(x[0], x[1], x[2], x[3]);
+        if (piece == 0) undo[r] = u;
+      }
+      if (piece * 8 < HD)
+        *reinterpret_cast<uint4*>(base + (r / kTileRows) * (kTileRows * HD * 2) +
+                                  tile_at(kTileRows, r % kTileRows, piece)) = w;
+    }
+  }
+  TileList list{need, (hi - lo + N - 1) / N, docs != nullptr};
+  if (docs) {
+    // which key tiles hold a document of some row, and which need a look at each key
+    for (int i = tid; i < 2 * kTileListed / 32; i += kTileThreads) need[i] = 0;
+    __syncthreads();
+    int dmin = 0x7fffffff, dmax = (int)0x80000000;
+    for (int64_t s = rows0 / p.G + tid; s <= rlast / p.G; s += kTileThreads) {
+      int32_t d;
+      if (kv_document(p, b, seq.past + s, &d)) dmin = d < dmin ? d : dmin, dmax = d > dmax ? d : dmax;
+    }
+    dmin = __reduce_min_sync(0xffffffffu, dmin);
+    dmax = __reduce_max_sync(0xffffffffu, dmax);
+    if (lane == 0) {
+      atomicMin(&s_qdoc[0], dmin);
+      atomicMax(&s_qdoc[1], dmax);
+    }
+    __syncthreads();
+    dmin = s_qdoc[0];
+    dmax = s_qdoc[1];
+    const int look = list.count < kTileListed ? list.count : kTileListed;
+    for (int t0 = warp * 4; t0 < look; t0 += kTileThreads / 32 * 4) {
+      int kmin[4], kmax[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        kmin[u] = 0x7fffffff, kmax[u] = (int)0x80000000;
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) {
+          const int j = lo + (t0 + u) * N + i * 32 + lane;
+          if (j < hi) {
+            const int d = __ldg(docs + j);
+            kmin[u] = d < kmin[u] ? d : kmin[u], kmax[u] = d > kmax[u] ? d : kmax[u];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int a = __reduce_min_sync(0xffffffffu, kmin[u]), z = __reduce_max_sync(0xffffffffu, kmax[u]);
+        const int t = t0 + u;
+        if (lane == 0 && t < look && a <= dmax && z >= dmin) {
+          atomicOr(&need[t >> 5], 1u << (t & 31));
+          if (a != z || dmin != dmax || a != dmin) atomicOr(&mixed[t >> 5], 1u << (t & 31));
+        }
+      }
+    }
+  }
+  tc_fence_smem();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s_tmem;
+  const int first = list.next(0);
+  bool ok = true;
+
+  if (warp < 4 * NT) {
+    // ------------------------------------------------------------------ softmax
+    const int t = warp >> 2;
+    const int64_t row = rows0 + tid;  // 128 t + lane of TMEM
+    const bool live = row < p.R;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes of TMEM a warp
+    const int64_t pos = seq.past + (live ? row : p.R - 1) / p.G;
+    int lim = 0, doc = 0;
+    {
+      int64_t k = live ? kv_limit(seq, pos) : 0;
+      if (docs && live && !kv_document(p, b, pos, &doc)) k = 0;
+      lim = k > 0 ? (int)k : 0;
+    }
+    const int full = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+    const float slope = p.slopes && live ? __ldg(p.slopes + kvh * p.G + row % p.G) * kLog2e : 0.0f;
+    float mult = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid];
+    const float c2 = p.cap * kLog2e;
+    float m = -CUDART_INF_F, l = 0.0f, vref = 0.0f;
+    if (t < live_tiles) {
+      int step = 0;
+      for (int tile = first; tile < list.count; ++step) {
+        const int j0 = lo + tile * N;
+        const int buf = NT == 2 ? t : step & 1;
+        const uint32_t par = (NT == 2 ? step : step >> 1) & 1;
+        const uint32_t ts = tmem + lanes + (NT == 2 ? t * 128 : buf * N);
+        const uint32_t to = tmem + lanes + 256 + (NT == 2 ? t * 128 : 0);
+        const uint8_t* in = info + (step & 3) * C::kInfo;
+        ok = mbar_wait(bar(&bars.s_full[buf]), par);
+        if (FP8 || docs) ok = ok && mbar_wait(bar(&bars.info[step & 3]), (step >> 2) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_after();
+        uint32_t xr[N];
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tc_ld32(xr + i, ts + i);
+        const float* ks = reinterpret_cast<const float*>(in + N * 4);
+        const float* vs = ks + NB;
+        bool grown = false;
+        float vmax = 0.0f;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) vmax = fmaxf(vmax, vs[i]);
+          grown = vmax > vref;
+        }
+        const bool look = docs && (tile >= kTileListed || (mixed[tile >> 5] >> (tile & 31)) & 1u);
+        const bool part = j0 + N > full;
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tc_wait_ld32(xr + i);
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = __uint_as_float(xr[i]);
+        // scores in log2; `mul` and `x` of the plain case stay apart for one FMA in the exponent
+        float mul = mult;
+        const bool plain = !FP8 && p.cap == 0.0f && !p.slopes && mult > 0.0f;
+        if (!plain) {
+          mul = 1.0f;
+          if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              const float f = mult * ks[i];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[16 * i + k] *= f;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] *= mult;
+          }
+          if (p.cap > 0.0f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = kv_tanh_of(x[i]) * c2;
+          }
+          if (p.slopes) {
+            const float d0 = (float)(pos - j0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
+          }
+        }
+        if (part) {
+          const int n = lim - j0;
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] = i < n ? x[i] : -CUDART_INF_F;
+        }
+        if (look) {
+          const int4* dk = reinterpret_cast<const int4*>(in);
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const int4 d = dk[i / 4];
+            x[i] = d.x == doc ? x[i] : -CUDART_INF_F;
+            x[i + 1] = d.y == doc ? x[i + 1] : -CUDART_INF_F;
+            x[i + 2] = d.z == doc ? x[i + 2] : -CUDART_INF_F;
+            x[i + 3] = d.w == doc ? x[i + 3] : -CUDART_INF_F;
+          }
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) mx = fmaxf(mx, x[i]);
+        mx *= mul;
+        if (__any_sync(0xffffffffu, mx > m + 8.0f) || grown) {
+          const float mn = fmaxf(m, mx);
+          float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
+          m = mn;
+          l *= a;
+          if constexpr (FP8) {
+            if (grown) {
+              a *= vref * __uint_as_float((254u << 23) - __float_as_uint(vmax));  // old / new, powers of two
+              vref = vmax;
+            }
+          }
+          if (step > 0) {
+            if constexpr (NT == 1) {  // here S runs ahead of P V
+              ok = mbar_wait(bar(&bars.o_full[1]), (step - 1) & 1);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_after();
+            }
+#pragma unroll 1
+            for (int i = 0; i < HD; i += 16) {
+              uint32_t o[16];
+              tc_ld16(o, to + i);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tc_st16(to + i, o);
+            }
+          }
+        }
+        const float nm = m == -CUDART_INF_F ? 0.0f : -m;
+#pragma unroll
+        for (int h = 0; h < N; h += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 16) {
+            float sum0 = 0.0f, sum1 = 0.0f, fv = 1.0f;
+            if constexpr (FP8) {
+              const float v = vs[(h + i) / 16];
+              fv = v > 0.0f ? v * __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float e0 = kv_exp2(fmaf(x[h + i + k], mul, nm)), e1 = kv_exp2(fmaf(x[h + i + k + 1], mul, nm));
+              sum0 += e0;
+              sum1 += e1;
+              if constexpr (FP8) e0 *= fv, e1 *= fv;
+              w[(i + k) / 2] = kv_pack2<BF>(e0, e1);
+            }
+            l += sum0 + sum1;
+          }
+          tc_st32(ts + h / 2, w);
+        }
+        tc_wait_st();
+        tc_before();
+        mbar_arrive(bar(&bars.p_full[buf]));
+        tile = list.next(tile + 1);
+      }
+      // ---------------------------------------------------------------- output
+      if (ok && first < list.count) {
+        ok = mbar_wait(bar(&bars.o_full[NT == 2 ? t : 0]), 0);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_after();
+      }
+      if (ok) {
+        const uint32_t to = tmem + lanes + 256 + (NT == 2 ? t * 128 : 0);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float f = (p.splits > 1 ? 1.0f : inv) * (FP8 ? vref : 1.0f);
+        const bool empty = m == -CUDART_INF_F && l == 0.0f;  // nothing seen (TMEM may never have been written)
+        const int64_t at = (plane * p.splits + split) * p.R + row;
+        bits* dst = static_cast<bits*>(p.out) + row_at(live ? row : 0);
+        bool odd = false;
+        if (live && p.splits > 1) p.ws_ml[at] = make_float2(m, l);
+#pragma unroll 1
+        for (int i = 0; i < HD && i < p.H; i += 32) {
+          uint32_t o[32];
+          tc_ld32(o, to + i);
+          tc_wait_ld32(o);
+          float y[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
+            odd |= !(fabsf(y[k]) < CUDART_INF_F) && i + k < p.H;
+          }
+          if (!live) continue;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            if (i + k >= p.H) continue;
+            if (p.splits > 1) {
+              float* part = p.ws_o + at * p.H + i + k;
+              *reinterpret_cast<float4*>(part) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+              *reinterpret_cast<float4*>(part + 4) = make_float4(y[k + 4], y[k + 5], y[k + 6], y[k + 7]);
+            } else {
+              VecT<T, 8> v;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v.v[q] = Elem<T>::fromf(y[k + q]);
+              *reinterpret_cast<VecT<T, 8>*>(dst + i + k) = v;
+            }
+          }
+        }
+        // An infinity or a NaN may have come from a value that the row does not see
+        uint32_t again = __ballot_sync(0xffffffffu, odd && live);
+        if (again && !docs) {
+          bool found = false;  // in a value that some row of the warp does not see and its key tile holds
+          const int upto = hi < lo + list.count * N ? hi : lo + list.count * N;
+          const int from = full > lo ? full : lo;
+          for (int64_t e = (plane * p.max_len + from) * p.H + lane; e < (plane * p.max_len + upto) * p.H; e += 32) {
+            if constexpr (FP8)
+              found |= (static_cast<const uint8_t*>(p.v)[e] & 127) == 127;
+            else
+              found |= !(fabsf(Elem<T>::tof(static_cast<const bits*>(p.v)[e])) < CUDART_INF_F);
+          }
+          if (!__any_sync(0xffffffffu, found)) again = 0;
+        }
+        __syncwarp();
+        while (again) {
+          const int r = __ffs(again) - 1;
+          again &= again - 1;
+          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + (warp * 32 + r), lo64, hi64, split, lane);
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0 && first < list.count) {
+      const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
+      const int steps = (p.H + 15) / 16;
+      auto qk = [&](int t, int stage, uint32_t d) {
+        for (int k = 0; k < steps; ++k) {
+          const uint32_t a = sq + t * (kTileRows * HD * 2) + (k >> 2) * (kTileRows * 128) + (k & 3) * 32;
+          const uint32_t c = sk + stage * C::kStage + (k >> 2) * (N * 128) + (k & 3) * 32;
+          tc_mma_ss(d, tc_desc(a, 16), tc_desc(c, 16), iqk, k > 0);
+        }
+      };
+      auto pv = [&](uint32_t d, uint32_t a, int stage, bool add) {
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k)
+          tc_mma_ts(d, a + k * 8, tc_desc(sv + stage * C::kStage + k * 2048, N * 128), ipv, add || k > 0);
+      };
+      int step = 0;
+      int tile = first;
+      ok = mbar_wait(bar(&bars.k_full[0]), 0);
+      tc_after();
+      if (ok) {
+        for (int t = 0; t < live_tiles; ++t) {
+          qk(t, 0, tmem + t * 128);
+          tc_commit(bar(&bars.s_full[t]));
+        }
+        tc_commit(bar(&bars.k_free[0]));
+      }
+      while (ok && tile < list.count) {
+        const int after = list.next(tile + 1);
+        const bool more = after < list.count;
+        const int st = step & 1, sn = (step + 1) & 1;
+        if constexpr (NT == 2) {
+          for (int t = 0; t < live_tiles && ok; ++t) {
+            ok = mbar_wait(bar(&bars.p_full[t]), step & 1);
+            if (t == 0) ok = ok && mbar_wait(bar(&bars.v_full[st]), (step >> 1) & 1);
+            if (!ok) break;
+            tc_after();
+            pv(tmem + 256 + t * 128, tmem + t * 128, st, step > 0);
+            if (t == live_tiles - 1) tc_commit(bar(&bars.v_free[st]));
+            if (more) {
+              if (t == 0) ok = mbar_wait(bar(&bars.k_full[sn]), ((step + 1) >> 1) & 1);
+              if (!ok) break;
+              tc_after();
+              qk(t, sn, tmem + t * 128);
+              tc_commit(bar(&bars.s_full[t]));
+              if (t == live_tiles - 1) tc_commit(bar(&bars.k_free[sn]));
+            } else {
+              tc_commit(bar(&bars.o_full[t]));
+            }
+          }
+        } else {
+          if (more) {
+            ok = mbar_wait(bar(&bars.k_full[sn]), ((step + 1) >> 1) & 1);
+            if (!ok) break;
+            tc_after();
+            qk(0, sn, tmem + sn * N);
+            tc_commit(bar(&bars.s_full[sn]));
+            tc_commit(bar(&bars.k_free[sn]));
+          }
+          ok = mbar_wait(bar(&bars.p_full[st]), (step >> 1) & 1);
+          ok = ok && mbar_wait(bar(&bars.v_full[st]), (step >> 1) & 1);
+          if (!ok) break;
+          tc_after();
+          pv(tmem + 256, tmem + st * N, st, step > 0);
+          tc_commit(bar(&bars.v_free[st]));
+          tc_commit(bar(&bars.o_full[1]));
+          if (!more) tc_commit(bar(&bars.o_full[0]));
+        }
+        tile = after;
+        ++step;
+      }
+      if (!ok) {  // let what was issued end before TMEM and shared memory go
+        tc_commit(bar(&bars.drain));
+        mbar_wait(bar(&bars.drain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp > 8) {
+    // ------------------------------------------------------------------ K and V
+    const int me = tid - 288;
+    constexpr int PPR = HD / 8;              // 16-byte pieces of a row in shared memory
+    const int HB = p.H * (FP8 ? 1 : 2);      // bytes of a cache row
+    const uint8_t* kb = static_cast<const uint8_t*>(p.k) + plane * p.max_len * HB;
+    const uint8_t* vb = static_cast<const uint8_t*>(p.v) + plane * p.max_len * HB;
+    auto put_info = [&](int j0, int step) {
+      if (!FP8 && !docs) return;
+      uint8_t* in = info + (step & 3) * C::kInfo;
+      if (docs)
+        for (int i = me; i < N; i += kTileBring)
+          reinterpret_cast<int32_t*>(in)[i] = j0 + i < hi ? __ldg(docs + j0 + i) : 0;
+      if (FP8 && me < 2 * NB) {
+        const int blk = me % NB;
+        const float* s = me < NB ? p.ks : p.vs;
+        float f = j0 + blk * 16 < hi ? __ldg(s + plane * p.nblk + j0 / kKvBlock + blk) : 0.0f;
+        if (!(f < CUDART_INF_F)) f = 0.0f;
+        reinterpret_cast<float*>(in + N * 4)[me] = f;
+      }
+      mbar_arrive(bar(&bars.info[step & 3]));
+    };
+    if constexpr (!FP8) {
+      auto fill = [&](uint32_t dst, const uint8_t* src, int j0) {
+        for (int i = me; i < N * PPR; i += kTileBring) {
+          const int r = i / PPR, piece = i % PPR;
+          const bool on = j0 + r < hi && piece * 16 < HB;
+          kv_cp<16>(dst + tile_at(N, r, piece), src + (on ? (int64_t)(j0 + r) * HB + piece * 16 : 0), on);
+        }
+        kv_cp_commit();
+      };
+      // items K0 V0 K1 V1 ..: two are in flight behind the one that is signalled
+      int item = 0;
+      auto signal = [&](int i) {
+        tc_fence_smem();
+        mbar_arrive(bar(i & 1 ? &bars.v_full[(i >> 1) & 1] : &bars.k_full[(i >> 1) & 1]));
+      };
+      for (int tile = first; tile < list.count && ok; tile = list.next(tile + 1)) {
+        const int step = item >> 1, st = step & 1, j0 = lo + tile * N;
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v, ++item) {
+          if (step >= 2) ok = mbar_wait(bar(v ? &bars.v_free[st] : &bars.k_free[st]), ((step >> 1) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (!v) put_info(j0, step);
+          fill((v ? sv : sk) + st * C::kStage, v ? vb : kb, j0);
+          if (item >= 2) {
+            kv_cp_wait<2>();
+            signal(item - 2);
+          }
+        }
+      }
+      if (ok && item) {
+        kv_cp_wait<1>();
+        signal(item - 2);
+        kv_cp_wait<0>();
+        signal(item - 1);
+      }
+      kv_cp_wait<0>();
+    } else {
+      // a 16-byte piece of codes becomes two 16-byte pieces of float16
+      constexpr int CPR = HD / 16, PER = (N * CPR + kTileBring - 1) / kTileBring;
+      uint4 a[PER], c[PER];
+      auto load = [&](uint4 (&x)[PER], const uint8_t* src, int j0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int e = me + i * kTileBring, r = e / CPR, piece = e % CPR;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (e < N * CPR && j0 + r < hi && piece * 16 < HB)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(j0 + r) * HB + piece * 16));
+        }
+      };
+      auto store = [&](const uint4 (&x)[PER], uint8_t* dst) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int e = me + i * kTileBring, r = e / CPR, piece = e % CPR;
+          if (e >= N * CPR) continue;
+          *reinterpret_cast<uint4*>(dst + tile_at(N, r, 2 * piece)) =
+              make_uint4(kv_codes2(x[i].x), kv_codes2_high(x[i].x), kv_codes2(x[i].y), kv_codes2_high(x[i].y));
+          *reinterpret_cast<uint4*>(dst + tile_at(N, r, 2 * piece + 1)) =
+              make_uint4(kv_codes2(x[i].z), kv_codes2_high(x[i].z), kv_codes2(x[i].w), kv_codes2_high(x[i].w));
+        }
+      };
+      uint8_t* pk = base + C::kQ;
+      uint8_t* pv8 = pk + 2 * C::kStage;
+      int step = 0, tile = first;
+      if (tile < list.count) load(a, kb, lo + tile * N);
+      while (tile < list.count) {
+        const int st = step & 1, j0 = lo + tile * N;
+        const int after = list.next(tile + 1);
+        load(c, vb, j0);
+        if (step >= 2) ok = mbar_wait(bar(&bars.k_free[st]), ((step >> 1) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        put_info(j0, step);
+        store(a, pk + st * C::kStage);
+        tc_fence_smem();
+        mbar_arrive(bar(&bars.k_full[st]));
+        if (after < list.count) load(a, kb, lo + after * N);
+        if (step >= 2) ok = mbar_wait(bar(&bars.v_free[st]), ((step >> 1) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        store(c, pv8 + st * C::kStage);
+        tc_fence_smem();
+        mbar_arrive(bar(&bars.v_full[st]));
+        tile = after;
+        ++step;
+      }
+    }
+  }
+  if (!ok && p.status) atomicOr(p.status, 2);
+  tc_before();
+  __syncthreads();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+template <class T, bool FP8>
+KvTileKernel kv_tile_pick(int H) {
+  if (H <= 64) return {(const void*)kv_tile_kernel_t<T, FP8, 64>, TileCfg<FP8, 64>::kSmem};
+  if (H <= 128) return {(const void*)kv_tile_kernel_t<T, FP8, 128>, TileCfg<FP8, 128>::kSmem};
+  return {(const void*)kv_tile_kernel_t<T, FP8, 256>, TileCfg<FP8, 256>::kSmem};
+}
+
+}  // namespace rope_gb300

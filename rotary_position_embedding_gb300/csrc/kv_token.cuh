@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
   using bits = typename Elem<T>::bits;
   constexpr bool BF = !FP8 && kIsBf16<T>;  // type of the matrix operands
   constexpr int OT = HD / 16;                                   // 16-dim tiles of O^T
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t kv_ring[];
   __shared__ float s_m[kTokWarps][NB * 8], s_l[kTokWarps][NB * 8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
   const int64_t rows0 = (int64_t)(blockIdx.x / p.splits) * (NB * 8);
   const int split = blockIdx.x % p.splits;
   const int kvh = blockIdx.y;
-  const uint32_t ring = kv_smem(smem) + warp * (C::kStage * C::kStages);
+  const uint32_t ring = kv_smem(kv_ring) + warp * (C::kStage * C::kStages);
   for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
     const KvSeq seq = kv_seq(p, b);
     if (blockIdx.x == 0 && kvh == 0 && tid == 0) kv_flag_rows(p, seq);
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
       continue;
     }
     // join the warps: their O (in units of 1) and statistics meet in shared memory
-    float* so = reinterpret_cast<float*>(smem);
+    float* so = reinterpret_cast<float*>(kv_ring);
     constexpr int LD = HD + 4;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
