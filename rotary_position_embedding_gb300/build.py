@@ -22,7 +22,7 @@ SOURCES = ["rope_api.cu", "k_rope.cu", "k_mrope.cu", "k_fused.cu", "k_tma.cu", "
            "k_mrope_heads.cu", "k_qkv_heads.cu", "no_alloc.cu", "kv_api.cu", "k_kv_append.cu", "k_kv_simple.cu", "k_kv_token.cu", "k_kv_tile_f16.cu",
            "k_kv_tile_f16_fp8.cu", "k_kv_tile_bf16.cu", "k_kv_tile_bf16_fp8.cu"]
 HEADERS = ["rope_kernels.cuh", "rope_internal.h", "rope_tma.cuh", "rope_qkv.cuh", "rope_qkv_tma.cuh", "rope_packed.cuh", "rope_fused.cuh",
-           "rope_mrope_heads.cuh", "rope_qkv_heads.cuh", "kv_internal.h", "kv_common.cuh", "kv_append.cuh", "kv_simple.cuh", "kv_careful.cuh", "kv_token.cuh", "kv_tile.cuh"]
+           "rope_mrope_heads.cuh", "rope_qkv_heads.cuh", "kv_internal.h", "kv_common.cuh", "kv_append.cuh", "kv_simple.cuh", "kv_careful.cuh", "kv_token.cuh", "kv_tile.cuh", "kv_maps.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -14,6 +14,7 @@
 #include <utility>
 
 #include "kv_internal.h"
+#include "kv_maps.h"
 #include "rope.h"
 #include "rope_internal.h"
 
@@ -275,8 +276,15 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     const int h = (int)head_size;
     const KvTileKernel k = dtype == ROPE_F16 ? (fp8 ? kv_tile_kernel_f16_fp8(h) : kv_tile_kernel_f16(h))
                                              : (fp8 ? kv_tile_kernel_bf16_fp8(h) : kv_tile_kernel_bf16(h));
+    KvTileMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int64_t planes = batch * kv_num_heads;
+    p.tma = !fp8 &&
+            encode_kv_map(&maps.k, dtype == ROPE_BF16, k_cache, head_size, max_cache_len, planes, kv_tile_keys(h)) &&
+            encode_kv_map(&maps.v, dtype == ROPE_BF16, v_cache, head_size, max_cache_len, planes, kv_tile_keys(h));
+    void* targs[] = {&p, &maps};
     const dim3 tg((unsigned)(kv_num_heads * pl.splits), (unsigned)batch, (unsigned)pl.tiles);
-    KV_TRY(launch(k.fn, tg, kKvTileThreads, k.smem, stream, args, "kv_attention launch (many rows)"));
+    KV_TRY(launch(k.fn, tg, kKvTileThreads, k.smem, stream, targs, "kv_attention launch (many rows)"));
     set_last_kernel("kv_tile_kernel");
   } else if (family == Family::kToken) {
     const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.R > 8);
@@ -289,7 +297,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   }
   if (pl.splits > 1) {
     const int64_t rows = batch * kv_num_heads * p.R;
-    int64_t gc = (rows + kKvCombineThreads / 32 - 1) / (kKvCombineThreads / 32);
+    const int per = pl.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
+    int64_t gc = (rows + per - 1) / per;
     if (gc > INT32_MAX) gc = INT32_MAX;
     KV_TRY(launch(kv_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
                   "kv_attention launch (joining the splits)"));

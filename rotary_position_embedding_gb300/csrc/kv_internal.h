@@ -34,6 +34,7 @@ struct KvParams {
   int32_t B, Nq, Nkv, G, H;
   int32_t splits;
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
+  int32_t tma;             // kv_tile_kernel: the tensor maps are there
   float scale;             // factor of q.k
   float cap;               // 0: no cap
 };
@@ -53,12 +54,14 @@ constexpr int kKvTokenThreads = 128;
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
 // Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above
-// H = 128), grid (Nkv * splits, B, row tiles).
+// H = 128), grid (Nkv * splits, B, row tiles); the launch takes (KvParams,
+// KvTileMaps).
 struct KvTileKernel {
   const void* fn;
   size_t smem;
 };
-constexpr int kKvTileThreads = 384;
+constexpr int kKvTileThreads = 416;
+constexpr int kv_tile_keys(int64_t H) { return H <= 128 ? 128 : 64; }
 constexpr int kv_tile_rows(int64_t H) { return H <= 128 ? 256 : 128; }
 KvTileKernel kv_tile_kernel_f16(int H);
 KvTileKernel kv_tile_kernel_f16_fp8(int H);
@@ -66,7 +69,8 @@ KvTileKernel kv_tile_kernel_bf16(int H);
 KvTileKernel kv_tile_kernel_bf16_fp8(int H);
 
 constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
-constexpr int kKvCombineThreads = 128;  // one warp a row
+constexpr int kKvCombineThreads = 128;
+constexpr int kKvCombineWarpSplits = 8;  // up to so many splits a warp joins a row alone, above a CTA
 
 // Q and K rotation with the append to 8-bit caches.
 struct KvAppendParams {

@@ -12,12 +12,20 @@
 // turns: while one tile's scores are in registers, the tensor cores work for
 // the other. H = 256 fills TMEM with one tile: NT = 1, N = 64, S double-buffered.
 //
-// Warps (12): 0-3 and 4-7 softmax of row tile 0 and 1, a thread a row; 8 (one
-// lane) issues every MMA; 9-11 bring K and V to shared memory.
+// Warps (13): 0-3 and 4-7 softmax of row tile 0 and 1, a thread a row (they
+// bring Q to shared memory first); 8-11 bring K and V; 12 (one lane) issues
+// every MMA.
+//   K and V tiles come by TMA; the last one, whose rows behind the keys have to
+//   be zeros, by cp.async.
 //   8-bit caches: the bringing warps load codes and write float16 (exact); the
 //   key scale of each 16 keys multiplies scores, the value scale weights,
 //   relative to the largest value scale so far (powers of two); bfloat16 Q rows
 //   become float16 after scaling by a power of two that the scores undo.
+// A softmax thread reads its scores from TMEM twice, 32 columns at a time, once
+// for the maximum and once for the weights: held in registers in between they
+// spilled. Where the scores only grow with q.k (no bias), the maximum is taken
+// before the cap, and where all of a warp's capped scores have |y| <= 1/2,
+// tanh(y) is a polynomial: 3 exponential-unit operations a score become one.
 // Shared memory: Q, two stages of K and two of V, each as slabs of 64 elements
 // (128-byte rows, 128-byte swizzle): the K-major form for Q and K, and the same
 // bytes read MN-major for V.
@@ -40,6 +48,7 @@
 #pragma once
 
 #include "kv_careful.cuh"
+#include "kv_maps.h"
 #include "kv_token.cuh"
 #include "rope_tma.cuh"
 
@@ -47,7 +56,7 @@ namespace rope_gb300 {
 
 constexpr int kTileThreads = kKvTileThreads;
 constexpr int kTileRows = 128;
-constexpr int kTileBring = 96;         // bringing threads
+constexpr int kTileBring = 128;        // bringing threads
 constexpr int kTileListed = 4096;      // key tiles of a CTA whose documents are looked at
 
 template <bool FP8, int HD>
@@ -62,8 +71,11 @@ struct TileCfg {
   static constexpr int kSmem = 1024 + kQ + 4 * kStage + kTail;
 };
 
+// coefficients of y, y^3, y^5, y^7: see tile_tanh_small
+constexpr float kTanh0 = 0.999997675f, kTanh1 = -0.333206564f, kTanh2 = 0.131451532f, kTanh3 = -0.0433726683f;
+
 struct TileBars {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], info[4], drain;
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], info[4], q_full, drain;
 };
 
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -169,8 +181,177 @@ struct TileList {
   }
 };
 
+// tanh(y) for |y| <= 1/2, off by at most 1.3e-7: an odd polynomial of degree 7,
+// fitted to the smallest largest error over [0, 1/2]. Two at a time.
+__device__ __forceinline__ float2 tile_tanh_small(float2 y) {
+  const float2 z = __fmul2_rn(y, y);
+  float2 q = make_float2(kTanh3, kTanh3);
+  q = __ffma2_rn(q, z, make_float2(kTanh2, kTanh2));
+  q = __ffma2_rn(q, z, make_float2(kTanh1, kTanh1));
+  q = __ffma2_rn(q, z, make_float2(kTanh0, kTanh0));
+  return __fmul2_rn(q, y);
+}
+
+__device__ __forceinline__ void tile_tma(uint32_t dst, const CUtensorMap* map, int x, int row, int plane, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(plane), "r"(bar)
+      : "memory");
+}
+
+// What a softmax thread knows of its row, and the tile it is at.
+struct TileRow {
+  float mult, slope, cap2;      // score factor; bias and cap in log2
+  float dist;                   // the row's position less the tile's first key
+  int limit;                    // columns of the tile below this are not ahead of it
+  int doc;
+  bool part, look;              // some column is hidden: by position, by document
+  const int4* docs;             // of the tile
+  const float* ks;              // of each 16 columns
+};
+
+// 32 raw scores -> scores in log2 (GENERAL), or raw scores times what depends on
+// the column.
+template <bool FP8, bool GENERAL>
+__device__ __forceinline__ void tile_scores(float (&x)[32], int c0, const TileRow& r, bool capped) {
+  if constexpr (FP8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = r.ks[c0 / 16 + h] * (GENERAL ? r.mult : 1.0f);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[16 * h + k], x[16 * h + k + 1]), make_float2(f, f));
+        x[16 * h + k] = y.x, x[16 * h + k + 1] = y.y;
+      }
+    }
+  } else if constexpr (GENERAL) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] *= r.mult;
+  }
+  if constexpr (GENERAL) {
+    if (capped) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = kv_tanh_of(x[i]) * r.cap2;
+    }
+    const float d = r.dist - (float)c0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = fmaf(-r.slope, fabsf(d - (float)i), x[i]);
+  }
+}
+
+// Hidden ones: -inf.
+__device__ __forceinline__ void tile_mask(float (&x)[32], int c0, const TileRow& r) {
+  if (r.part) {
+    const int n = r.limit - c0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -CUDART_INF_F;
+  }
+  if (r.look) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const int4 d = r.docs[(c0 + i) / 4];
+      x[i] = d.x == r.doc ? x[i] : -CUDART_INF_F;
+      x[i + 1] = d.y == r.doc ? x[i + 1] : -CUDART_INF_F;
+      x[i + 2] = d.z == r.doc ? x[i + 2] : -CUDART_INF_F;
+      x[i + 3] = d.w == r.doc ? x[i + 3] : -CUDART_INF_F;
+    }
+  }
+}
+
+// The largest score of the row in N columns at `ts`; *mag the largest
+// magnitude of a visible raw score (for the cap's polynomial).
+template <bool FP8, bool GENERAL, int N>
+__device__ __forceinline__ float tile_max(uint32_t ts, const TileRow& r, bool capped, float* mag) {
+  uint32_t c[2][32];
+  float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, lo = CUDART_INF_F;
+  tc_ld32(c[0], ts);
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    tc_wait_ld32(c[k & 1]);
+    if (k + 1 < N / 32) tc_ld32(c[(k + 1) & 1], ts + 32 * (k + 1));
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(c[k & 1][i]);
+    tile_scores<FP8, GENERAL>(x, 32 * k, r, capped);
+    if (!GENERAL && capped) {  // hidden ones may count here
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) lo = fminf(lo, fminf(x[i], x[i + 1]));
+    }
+    tile_mask(x, 32 * k, r);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      m0 = fmaxf(m0, fmaxf(x[i], x[i + 1]));
+      m1 = fmaxf(m1, fmaxf(x[i + 2], x[i + 3]));
+    }
+  }
+  const float mx = fmaxf(m0, m1);
+  *mag = fmaxf(-lo, mx);
+  return mx;
+}
+
+// Weights 2^(score - base) of N columns at `ts`, written over the scores as
+// 16-bit values (times fv[16-column block] over 8-bit caches); their sum.
+// MODE 0: score = raw * mult; 1: capped by the polynomial; 2: capped; 3: general.
+template <bool FP8, bool BF, int MODE, int N>
+__device__ __forceinline__ float tile_weights(uint32_t ts, const TileRow& r, bool capped, float nbase, const float* vs,
+                                              float vinv) {
+  uint32_t c[2][32];
+  float2 sum = make_float2(0.0f, 0.0f);
+  tc_ld32(c[0], ts);
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    tc_wait_ld32(c[k & 1]);
+    if (k + 1 < N / 32) tc_ld32(c[(k + 1) & 1], ts + 32 * (k + 1));
+    float x[32];
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(c[k & 1][i]);
+    tile_scores<FP8, MODE == 3>(x, 32 * k, r, capped);
+    tile_mask(x, 32 * k, r);
+    const float2 mul = make_float2(r.mult, r.mult), nb = make_float2(nbase, nbase);
+    const float2 c2 = make_float2(r.cap2, r.cap2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float2 fv = make_float2(1.0f, 1.0f);
+      if constexpr (FP8) fv.x = fv.y = vs[2 * k + h] * vinv;
+#pragma unroll
+      for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+        float2 y = make_float2(x[i], x[i + 1]);
+        if constexpr (MODE == 0) {
+          y = __ffma2_rn(y, mul, nb);
+        } else if constexpr (MODE == 1) {  // r.mult is scale / cap here
+          const float2 t = tile_tanh_small(__fmul2_rn(y, mul));
+          y = __ffma2_rn(t, c2, nb);
+          // a hidden score is -inf before the polynomial, which makes NaN of it
+          if (r.part || r.look) {
+            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
+            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
+          }
+        } else if constexpr (MODE == 2) {
+          const float2 e = __fmul2_rn(y, mul);
+          y = __ffma2_rn(make_float2(kv_tanh_of(e.x), kv_tanh_of(e.y)), c2, nb);
+          if (r.part || r.look) {
+            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
+            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
+          }
+        } else {
+          y = __fadd2_rn(y, nb);
+        }
+        float2 e = make_float2(kv_exp2(y.x), kv_exp2(y.y));
+        sum = __fadd2_rn(sum, e);
+        if constexpr (FP8) e = __fmul2_rn(e, fv);
+        w[i / 2] = kv_pack2<BF>(e.x, e.y);
+      }
+    }
+    tc_st16(ts + 16 * k, w);
+  }
+  return sum.x + sum.y;
+}
+
 template <class T, bool FP8, int HD>
-__global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvParams p) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    kv_tile_kernel_t(const KvParams p, const __grid_constant__ KvTileMaps maps) {
   using C = TileCfg<FP8, HD>;
   using bits = typename Elem<T>::bits;
   constexpr bool BF = !FP8 && kIsBf16<T>;
@@ -199,12 +380,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
       mbar_init(bar(&bars.o_full[i]), 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(&bars.info[i]), kTileBring);
+    mbar_init(bar(&bars.q_full), NT * kTileRows);
     mbar_init(bar(&bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_qdoc[0] = 0x7fffffff;
     s_qdoc[1] = (int)0x80000000;
   }
-  if (warp == 8) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem(&s_tmem)), "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -217,62 +399,35 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
   const int64_t rows0 = (int64_t)(gridDim.z - 1 - blockIdx.z) * (NT * kTileRows);  // the longest rows first
   const KvSeq seq = kv_seq(p, b);
   if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) kv_flag_rows(p, seq);
-  const int64_t rlast = (rows0 + NT * kTileRows < p.R ? rows0 + NT * kTileRows : p.R) - 1;
-  const int live_tiles = rlast - rows0 >= kTileRows ? NT : 1;
-  int64_t end = kv_limit(seq, seq.past + rlast / p.G);
+  const int nrows = p.R - rows0 < NT * kTileRows ? (int)(p.R - rows0) : NT * kTileRows;  // at least 1
+  const int live_tiles = nrows > kTileRows ? NT : 1;
+  const int64_t tok0 = rows0 / p.G;  // token and head of row r: see tok_of, row_at
+  const uint32_t rem0 = (uint32_t)(rows0 - tok0 * p.G), G = (uint32_t)p.G;
+  auto tok_of = [&](int r) { return tok0 + (rem0 + (uint32_t)r) / G; };
+  auto row_at = [&](int r) {
+    const uint32_t d = (rem0 + (uint32_t)r) / G, h = rem0 + (uint32_t)r - d * G;
+    return (((int64_t)b * p.S + tok0 + d) * p.Nq + (int64_t)kvh * p.G + h) * p.H;
+  };
+  int64_t end = kv_limit(seq, seq.past + tok_of(nrows - 1));
   if (end < 0) end = 0;
   int64_t lo64, hi64;
   kv_split(end, p.splits, split, N, &lo64, &hi64);
   const int lo = (int)lo64, hi = (int)hi64;
   const int64_t plane = (int64_t)b * p.Nkv + kvh;
   const int32_t* docs = p.docs ? p.docs + (int64_t)b * p.max_len : nullptr;
-  auto row_at = [&](int64_t r) {
-    return (((int64_t)b * p.S + r / p.G) * p.Nq + (int64_t)kvh * p.G + r % p.G) * p.H;
-  };
-
-  // Q to shared memory: half a warp (a warp for H > 128) a row
-  {
-    constexpr int LANES = HD <= 128 ? 16 : 32;
-    const int per = 32 / LANES, sub = lane / LANES, piece = lane % LANES;
-    for (int r = warp * per + sub; r < NT * kTileRows; r += kTileThreads / 32 * per) {
-      const int64_t row = rows0 + r;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (row < p.R && piece * 8 < p.H)
-        w = __ldg(reinterpret_cast<const uint4*>(static_cast<const bits*>(p.q) + row_at(row) + piece * 8));
-      if constexpr (FP8 && kIsBf16<T>) {
-        uint32_t x[4] = {w.x, w.y, w.z, w.w};
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          amax = fmaxf(amax, fmaxf(fabsf(Elem<T>::tof((bits)x[i])), fabsf(Elem<T>::tof((bits)(x[i] >> 16)))));
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float f;
-        const float u = kv_row_shift(amax, &f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = kv_pack2<false>(Elem<T>::tof((bits)x[i]) * f, Elem<T>::tof((bits)(x[i] >> 16)) * f);
-        w = make_uint4(x[0], x[1], x[2], x[3]);
-        if (piece == 0) undo[r] = u;
-      }
-      if (piece * 8 < HD)
-        *reinterpret_cast<uint4*>(base + (r / kTileRows) * (kTileRows * HD * 2) +
-                                  tile_at(kTileRows, r % kTileRows, piece)) = w;
-    }
-  }
   TileList list{need, (hi - lo + N - 1) / N, docs != nullptr};
   if (docs) {
     // which key tiles hold a document of some row, and which need a look at each key
     for (int i = tid; i < 2 * kTileListed / 32; i += kTileThreads) need[i] = 0;
     __syncthreads();
     int dmin = 0x7fffffff, dmax = (int)0x80000000;
-    for (int64_t s = rows0 / p.G + tid; s <= rlast / p.G; s += kTileThreads) {
+    for (int64_t t = tok0 + tid; t <= tok_of(nrows - 1); t += kTileThreads) {
       int32_t d;
-      if (kv_document(p, b, seq.past + s, &d)) dmin = d < dmin ? d : dmin, dmax = d > dmax ? d : dmax;
+      if (kv_document(p, b, seq.past + t, &d)) dmin = d < dmin ? d : dmin, dmax = d > dmax ? d : dmax;
     }
     dmin = __reduce_min_sync(0xffffffffu, dmin);
     dmax = __reduce_max_sync(0xffffffffu, dmax);
-    if (lane == 0) {
+    if (lane == 0 && dmin <= dmax) {
       atomicMin(&s_qdoc[0], dmin);
       atomicMax(&s_qdoc[1], dmax);
     }
@@ -305,7 +460,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
       }
     }
   }
-  tc_fence_smem();
   tc_before();
   __syncthreads();
   tc_after();
@@ -316,21 +470,77 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
   if (warp < 4 * NT) {
     // ------------------------------------------------------------------ softmax
     const int t = warp >> 2;
-    const int64_t row = rows0 + tid;  // 128 t + lane of TMEM
-    const bool live = row < p.R;
+    const bool live = tid < nrows;  // row rows0 + tid: TMEM lane tid % 128 of row tile t
+    const int64_t row = rows0 + tid;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes of TMEM a warp
-    const int64_t pos = seq.past + (live ? row : p.R - 1) / p.G;
-    int lim = 0, doc = 0;
+    // Q to shared memory, 16 bytes at a time
+    if constexpr (FP8 && kIsBf16<T>) {
+      constexpr int LANES = HD <= 128 ? 16 : 32, PER = 32 / LANES, ROUNDS = 32 / PER;
+      const int sub = lane / LANES, piece = lane % LANES;
+#pragma unroll 1
+      for (int i0 = 0; i0 < ROUNDS; i0 += 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = warp * 32 + (i0 + i) * PER + sub;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r < nrows && piece * 8 < p.H)
+            w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bits*>(p.q) + row_at(r) + piece * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = warp * 32 + (i0 + i) * PER + sub;
+          uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(Elem<T>::tof((bits)x[k])), fabsf(Elem<T>::tof((bits)(x[k] >> 16)))));
+#pragma unroll
+          for (int o = LANES / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float f;
+          const float u = kv_row_shift(amax, &f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = kv_pack2<false>(Elem<T>::tof((bits)x[k]) * f, Elem<T>::tof((bits)(x[k] >> 16)) * f);
+          if (piece == 0) undo[r] = u;
+          if (piece * 8 < HD)
+            *reinterpret_cast<uint4*>(base + t * (kTileRows * HD * 2) + tile_at(kTileRows, r % kTileRows, piece)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+      __syncwarp();  // a warp brings its own 32 rows: undo[] stays within it
+    } else {
+      constexpr int PPR = HD / 8;
+#pragma unroll 4
+      for (int i = lane; i < 32 * PPR; i += 32) {
+        const int r = warp * 32 + i / PPR, piece = i % PPR;
+        const bool on = r < nrows && piece * 8 < p.H;
+        kv_cp<16>(sq + t * (kTileRows * HD * 2) + tile_at(kTileRows, r % kTileRows, piece),
+                  static_cast<const bits*>(p.q) + (on ? row_at(r) + piece * 8 : 0), on);
+      }
+      kv_cp_commit();
+      kv_cp_wait<0>();
+    }
+    tc_fence_smem();
+    mbar_arrive(bar(&bars.q_full));
+
+    const int64_t pos = seq.past + tok_of(live ? tid : nrows - 1);
+    int lim = 0;
+    TileRow tr;
+    tr.doc = 0;
     {
       int64_t k = live ? kv_limit(seq, pos) : 0;
-      if (docs && live && !kv_document(p, b, pos, &doc)) k = 0;
+      if (docs && live && !kv_document(p, b, pos, &tr.doc)) k = 0;
       lim = k > 0 ? (int)k : 0;
     }
     const int full = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
-    const float slope = p.slopes && live ? __ldg(p.slopes + kvh * p.G + row % p.G) * kLog2e : 0.0f;
-    float mult = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    tr.slope = 0.0f;
+    if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + (rem0 + tid) % G) * kLog2e;
+    const bool capped = p.cap > 0.0f;
+    float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
     if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid];
-    const float c2 = p.cap * kLog2e;
+    tr.cap2 = p.cap * kLog2e;
+    const bool general = p.slopes || !(p.scale > 0.0f);
     float m = -CUDART_INF_F, l = 0.0f, vref = 0.0f;
     if (t < live_tiles) {
       int step = 0;
@@ -341,6 +551,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
         const uint32_t ts = tmem + lanes + (NT == 2 ? t * 128 : buf * N);
         const uint32_t to = tmem + lanes + 256 + (NT == 2 ? t * 128 : 0);
         const uint8_t* in = info + (step & 3) * C::kInfo;
+        tr.mult = mult;
+        tr.dist = (float)(pos - j0);
+        tr.limit = lim - j0;
+        tr.part = j0 + N > full;
+        tr.look = docs && (tile >= kTileListed || (mixed[tile >> 5] >> (tile & 31)) & 1u);
+        tr.docs = reinterpret_cast<const int4*>(in);
+        tr.ks = reinterpret_cast<const float*>(in + N * 4);
+        const float* vs = tr.ks + NB;
         ok = mbar_wait(bar(&bars.s_full[buf]), par);
         if (FP8 || docs) ok = ok && mbar_wait(bar(&bars.info[step & 3]), (step >> 2) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -348,11 +566,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
           break;
         }
         tc_after();
-        uint32_t xr[N];
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tc_ld32(xr + i, ts + i);
-        const float* ks = reinterpret_cast<const float*>(in + N * 4);
-        const float* vs = ks + NB;
         bool grown = false;
         float vmax = 0.0f;
         if constexpr (FP8) {
@@ -360,59 +573,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
           for (int i = 0; i < NB; ++i) vmax = fmaxf(vmax, vs[i]);
           grown = vmax > vref;
         }
-        const bool look = docs && (tile >= kTileListed || (mixed[tile >> 5] >> (tile & 31)) & 1u);
-        const bool part = j0 + N > full;
-#pragma unroll
-        for (int i = 0; i < N; i += 32) tc_wait_ld32(xr + i);
-        float x[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __uint_as_float(xr[i]);
-        // scores in log2; `mul` and `x` of the plain case stay apart for one FMA in the exponent
-        float mul = mult;
-        const bool plain = !FP8 && p.cap == 0.0f && !p.slopes && mult > 0.0f;
-        if (!plain) {
-          mul = 1.0f;
-          if constexpr (FP8) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              const float f = mult * ks[i];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[16 * i + k] *= f;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] *= mult;
-          }
-          if (p.cap > 0.0f) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = kv_tanh_of(x[i]) * c2;
-          }
-          if (p.slopes) {
-            const float d0 = (float)(pos - j0);
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
-          }
+        float mx, mag = 0.0f;
+        if (general) {
+          mx = tile_max<FP8, true, N>(ts, tr, capped, &mag);
+        } else {
+          mx = tile_max<FP8, false, N>(ts, tr, capped, &mag) * mult;
+          if (capped) mx = mx == -CUDART_INF_F ? mx : kv_tanh_of(mx) * tr.cap2;
         }
-        if (part) {
-          const int n = lim - j0;
-#pragma unroll
-          for (int i = 0; i < N; ++i) x[i] = i < n ? x[i] : -CUDART_INF_F;
-        }
-        if (look) {
-          const int4* dk = reinterpret_cast<const int4*>(in);
-#pragma unroll
-          for (int i = 0; i < N; i += 4) {
-            const int4 d = dk[i / 4];
-            x[i] = d.x == doc ? x[i] : -CUDART_INF_F;
-            x[i + 1] = d.y == doc ? x[i + 1] : -CUDART_INF_F;
-            x[i + 2] = d.z == doc ? x[i + 2] : -CUDART_INF_F;
-            x[i + 3] = d.w == doc ? x[i + 3] : -CUDART_INF_F;
-          }
-        }
-        float mx = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) mx = fmaxf(mx, x[i]);
-        mx *= mul;
         if (__any_sync(0xffffffffu, mx > m + 8.0f) || grown) {
           const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
@@ -441,30 +608,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
             }
           }
         }
-        const float nm = m == -CUDART_INF_F ? 0.0f : -m;
-#pragma unroll
-        for (int h = 0; h < N; h += 64) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 64; i += 16) {
-            float sum0 = 0.0f, sum1 = 0.0f, fv = 1.0f;
-            if constexpr (FP8) {
-              const float v = vs[(h + i) / 16];
-              fv = v > 0.0f ? v * __uint_as_float((254u << 23) - __float_as_uint(vref)) : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float e0 = kv_exp2(fmaf(x[h + i + k], mul, nm)), e1 = kv_exp2(fmaf(x[h + i + k + 1], mul, nm));
-              sum0 += e0;
-              sum1 += e1;
-              if constexpr (FP8) e0 *= fv, e1 *= fv;
-              w[(i + k) / 2] = kv_pack2<BF>(e0, e1);
-            }
-            l += sum0 + sum1;
-          }
-          tc_st32(ts + h / 2, w);
+        const float nb = m == -CUDART_INF_F ? 0.0f : -m;
+        const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
+        if (general) {
+          l += tile_weights<FP8, BF, 3, N>(ts, tr, capped, nb, vs, vinv);
+        } else if (!capped) {
+          l += tile_weights<FP8, BF, 0, N>(ts, tr, false, nb, vs, vinv);
+        } else if (!__all_sync(0xffffffffu, mag * mult <= kLog2e)) {  // 2 log2(e) |y|, |y| <= 1/2
+          l += tile_weights<FP8, BF, 2, N>(ts, tr, true, nb, vs, vinv);
+        } else {
+          tr.mult = mult * (0.5f / kLog2e);
+          l += tile_weights<FP8, BF, 1, N>(ts, tr, true, nb, vs, vinv);
         }
-        tc_wait_st();
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_before();
         mbar_arrive(bar(&bars.p_full[buf]));
         tile = list.next(tile + 1);
@@ -481,7 +637,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
         const float f = (p.splits > 1 ? 1.0f : inv) * (FP8 ? vref : 1.0f);
         const bool empty = m == -CUDART_INF_F && l == 0.0f;  // nothing seen (TMEM may never have been written)
         const int64_t at = (plane * p.splits + split) * p.R + row;
-        bits* dst = static_cast<bits*>(p.out) + row_at(live ? row : 0);
+        bits* dst = static_cast<bits*>(p.out) + row_at(live ? tid : 0);
         bool odd = false;
         if (live && p.splits > 1) p.ws_ml[at] = make_float2(m, l);
 #pragma unroll 1
@@ -533,7 +689,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------------ MMA
     if (lane == 0 && first < list.count) {
       const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
@@ -552,7 +708,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
       };
       int step = 0;
       int tile = first;
-      ok = mbar_wait(bar(&bars.k_full[0]), 0);
+      ok = mbar_wait(bar(&bars.q_full), 0);
+      ok = ok && mbar_wait(bar(&bars.k_full[0]), 0);
       tc_after();
       if (ok) {
         for (int t = 0; t < live_tiles; ++t) {
@@ -611,9 +768,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
       }
     }
     __syncwarp();
-  } else if (warp > 8) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------------ K and V
-    const int me = tid - 288;
+    const int me = tid - 256;
     constexpr int PPR = HD / 8;              // 16-byte pieces of a row in shared memory
     const int HB = p.H * (FP8 ? 1 : 2);      // bytes of a cache row
     const uint8_t* kb = static_cast<const uint8_t*>(p.k) + plane * p.max_len * HB;
@@ -634,63 +791,69 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
       mbar_arrive(bar(&bars.info[step & 3]));
     };
     if constexpr (!FP8) {
-      auto fill = [&](uint32_t dst, const uint8_t* src, int j0) {
+      auto bring = [&](uint32_t dst, const uint8_t* src, const CUtensorMap* map, int j0, uint32_t full) {
+        if (p.tma && j0 + N <= hi) {
+          if (me == 0) {
+            mbar_arrive_expect_tx(full, C::kStage);
+#pragma unroll
+            for (int q = 0; q < C::SLABS; ++q) tile_tma(dst + q * (N * 128), map, q * 64, j0, (int)plane, full);
+          } else {
+            mbar_arrive(full);
+          }
+          return;
+        }
         for (int i = me; i < N * PPR; i += kTileBring) {
           const int r = i / PPR, piece = i % PPR;
           const bool on = j0 + r < hi && piece * 16 < HB;
           kv_cp<16>(dst + tile_at(N, r, piece), src + (on ? (int64_t)(j0 + r) * HB + piece * 16 : 0), on);
         }
         kv_cp_commit();
-      };
-      // items K0 V0 K1 V1 ..: two are in flight behind the one that is signalled
-      int item = 0;
-      auto signal = [&](int i) {
-        tc_fence_smem();
-        mbar_arrive(bar(i & 1 ? &bars.v_full[(i >> 1) & 1] : &bars.k_full[(i >> 1) & 1]));
-      };
-      for (int tile = first; tile < list.count && ok; tile = list.next(tile + 1)) {
-        const int step = item >> 1, st = step & 1, j0 = lo + tile * N;
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v, ++item) {
-          if (step >= 2) ok = mbar_wait(bar(v ? &bars.v_free[st] : &bars.k_free[st]), ((step >> 1) - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (!v) put_info(j0, step);
-          fill((v ? sv : sk) + st * C::kStage, v ? vb : kb, j0);
-          if (item >= 2) {
-            kv_cp_wait<2>();
-            signal(item - 2);
-          }
-        }
-      }
-      if (ok && item) {
-        kv_cp_wait<1>();
-        signal(item - 2);
         kv_cp_wait<0>();
-        signal(item - 1);
+        tc_fence_smem();
+        mbar_arrive(full);
+      };
+      int step = 0, nk = 0, nv = 0;  // tiles of K and of V whose loads have begun
+      for (int tile = first; tile < list.count; tile = list.next(tile + 1), ++step) {
+        const int st = step & 1, j0 = lo + tile * N;
+        if (step >= 2) ok = mbar_wait(bar(&bars.k_free[st]), ((step >> 1) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        put_info(j0, step);
+        bring(sk + st * C::kStage, kb, &maps.k, j0, bar(&bars.k_full[st]));
+        ++nk;
+        if (step >= 2) ok = mbar_wait(bar(&bars.v_free[st]), ((step >> 1) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        bring(sv + st * C::kStage, vb, &maps.v, j0, bar(&bars.v_full[st]));
+        ++nv;
       }
-      kv_cp_wait<0>();
+      if (!__all_sync(0xffffffffu, ok)) {  // what TMA still brings has to land before shared memory goes
+        ok = false;
+        for (int i = nk - 2; i < nk; ++i)
+          if (i >= 0) mbar_wait(bar(&bars.k_full[i & 1]), (i >> 1) & 1);
+        for (int i = nv - 2; i < nv; ++i)
+          if (i >= 0) mbar_wait(bar(&bars.v_full[i & 1]), (i >> 1) & 1);
+      }
     } else {
       // a 16-byte piece of codes becomes two 16-byte pieces of float16
-      constexpr int CPR = HD / 16, PER = (N * CPR + kTileBring - 1) / kTileBring;
+      // (the rows of a thread are a multiple of 8 apart, so their swizzle is the same)
+      constexpr int CPR = HD / 16, RS = kTileBring / CPR, PER = N / RS;
+      const int r0 = me / CPR, piece = me % CPR;
+      const bool in_row = piece * 16 < HB;
+      const uint32_t at0 = tile_at(N, r0, 2 * piece), at1 = tile_at(N, r0, 2 * piece + 1);
       uint4 a[PER], c[PER];
       auto load = [&](uint4 (&x)[PER], const uint8_t* src, int j0) {
+        const uint8_t* from = src + (int64_t)(j0 + r0) * HB + piece * 16;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int e = me + i * kTileBring, r = e / CPR, piece = e % CPR;
           x[i] = make_uint4(0, 0, 0, 0);
-          if (e < N * CPR && j0 + r < hi && piece * 16 < HB)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(j0 + r) * HB + piece * 16));
+          if (in_row && j0 + r0 + i * RS < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(from + (int64_t)i * RS * HB));
         }
       };
       auto store = [&](const uint4 (&x)[PER], uint8_t* dst) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int e = me + i * kTileBring, r = e / CPR, piece = e % CPR;
-          if (e >= N * CPR) continue;
-          *reinterpret_cast<uint4*>(dst + tile_at(N, r, 2 * piece)) =
+          *reinterpret_cast<uint4*>(dst + at0 + i * RS * 128) =
               make_uint4(kv_codes2(x[i].x), kv_codes2_high(x[i].x), kv_codes2(x[i].y), kv_codes2_high(x[i].y));
-          *reinterpret_cast<uint4*>(dst + tile_at(N, r, 2 * piece + 1)) =
+          *reinterpret_cast<uint4*>(dst + at1 + i * RS * 128) =
               make_uint4(kv_codes2(x[i].z), kv_codes2_high(x[i].z), kv_codes2(x[i].w), kv_codes2_high(x[i].w));
         }
       };
@@ -722,7 +885,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_tile_kernel_t(const KvPara
   if (!ok && p.status) atomicOr(p.status, 2);
   tc_before();
   __syncthreads();
-  if (warp == 8)
+  if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 

@@ -27,6 +27,7 @@
 #include <tuple>
 
 #include "rope.h"
+#include "kv_maps.h"
 #include "rope_internal.h"
 #include "rope_qkv_tma.cuh"
 #include "rope_tma.cuh"
@@ -950,6 +951,18 @@ rope_status mrope_common(rope_dtype dtype, int32_t x_rank, const int64_t* x_shap
 
 void rope_gb300::set_last_error(const char* msg) { g_last_error = msg; }
 void rope_gb300::set_last_kernel(const char* name) { g_last_kernel = name; }
+
+bool rope_gb300::encode_kv_map(CUtensorMap* m, bool bf16, const void* base, int64_t H, int64_t len, int64_t planes,
+                               int rows) {
+  if (!encode_tiled() || len >= (1ll << 32) || planes >= (1ll << 32) || H * len * 2 >= (1ll << 40)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)H, (cuuint64_t)len, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)H * 2, (cuuint64_t)(H * len * 2)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
+  return encode_tiled()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 extern "C" {
 
