@@ -89,7 +89,9 @@ int pow2_at_least(int64_t n) {
 std::mutex g_mu;
 std::set<std::pair<int, const void*>> g_raised;
 
-rope_status allow_smem(const void* fn, size_t smem) {
+// `registers`: what a kernel that deals its registers out again has to be
+// launched with (0: any).
+rope_status allow_smem(const void* fn, size_t smem, int registers) {
   if (smem <= 48 * 1024) return ROPE_OK;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -102,6 +104,8 @@ rope_status allow_smem(const void* fn, size_t smem) {
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, fn);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+  if (registers && fa.numRegs != registers)
+    return fail(ROPE_ERR_UNSUPPORTED, "the kernel was built with %d registers a thread, not %d", fa.numRegs, registers);
   most -= (int)fa.sharedSizeBytes;  // what the kernel holds statically
   if (most < (int)smem) return fail(ROPE_ERR_UNSUPPORTED, "needs %zu bytes of shared memory", smem);
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -112,8 +116,8 @@ rope_status allow_smem(const void* fn, size_t smem) {
 
 // Launched as a programmatic dependent, as every kernel of the library.
 rope_status launch(const void* fn, dim3 grid, int threads, size_t smem, rope_stream_t stream, void** args,
-                   const char* what) {
-  KV_TRY(allow_smem(fn, smem));
+                   const char* what, int registers = 0) {
+  KV_TRY(allow_smem(fn, smem, registers));
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
@@ -284,7 +288,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
             encode_kv_map(&maps.v, dtype == ROPE_BF16, v_cache, head_size, max_cache_len, planes, kv_tile_keys(h));
     void* targs[] = {&p, &maps};
     const dim3 tg((unsigned)(kv_num_heads * pl.splits), (unsigned)batch, (unsigned)pl.tiles);
-    KV_TRY(launch(k.fn, tg, kKvTileThreads, k.smem, stream, targs, "kv_attention launch (many rows)"));
+    KV_TRY(launch(k.fn, tg, kKvTileThreads, k.smem, stream, targs, "kv_attention launch (many rows)",
+                  kKvTileRegisters));
     set_last_kernel("kv_tile_kernel");
   } else if (family == Family::kToken) {
     const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.R > 8);

@@ -60,7 +60,11 @@ struct KvTileKernel {
   const void* fn;
   size_t smem;
 };
-constexpr int kKvTileThreads = 416;
+constexpr int kKvTileThreads = 512;
+// The kernel deals its registers out again (setmaxnreg): 256 x 192 + 128 x 88 +
+// 128 x 40 = 512 x 128, so it must have been launched with 128 a thread.
+constexpr int kKvTileRegisters = 128;
+static_assert(256 * 192 + 128 * 88 + 128 * 40 <= kKvTileThreads * kKvTileRegisters, "registers of kv_tile_kernel");
 constexpr int kv_tile_keys(int64_t H) { return H <= 128 ? 128 : 64; }
 constexpr int kv_tile_rows(int64_t H) { return H <= 128 ? 256 : 128; }
 KvTileKernel kv_tile_kernel_f16(int H);

@@ -12,20 +12,22 @@
 // turns: while one tile's scores are in registers, the tensor cores work for
 // the other. H = 256 fills TMEM with one tile: NT = 1, N = 64, S double-buffered.
 //
-// Warps (13): 0-3 and 4-7 softmax of row tile 0 and 1, a thread a row (they
+// Warps (16): 0-3 and 4-7 softmax of row tile 0 and 1, a thread a row (they
 // bring Q to shared memory first); 8-11 bring K and V; 12 (one lane) issues
-// every MMA.
+// every MMA; 13-15 only give up their registers.
 //   K and V tiles come by TMA; the last one, whose rows behind the keys have to
 //   be zeros, by cp.async.
 //   8-bit caches: the bringing warps load codes and write float16 (exact); the
 //   key scale of each 16 keys multiplies scores, the value scale weights,
 //   relative to the largest value scale so far (powers of two); bfloat16 Q rows
 //   become float16 after scaling by a power of two that the scores undo.
-// A softmax thread reads its scores from TMEM twice, 32 columns at a time, once
-// for the maximum and once for the weights: held in registers in between they
-// spilled. Where the scores only grow with q.k (no bias), the maximum is taken
-// before the cap, and where all of a warp's capped scores have |y| <= 1/2,
-// tanh(y) is a polynomial: 3 exponential-unit operations a score become one.
+// A softmax thread holds its 128 scores in registers from one TMEM load on
+// (32 at a time, read twice, the loads' latency was two thirds of a step: 3.3 us
+// a step of both row tiles): hence 192 registers a softmax thread, 88 a bringing
+// one, 40 a thread of the MMA warps. Where the scores only grow with q.k (no
+// bias), the maximum is taken before the cap, and where all of a warp's capped
+// scores have |y| <= 1/2, tanh(y) is a polynomial: 3 exponential-unit operations
+// a score become one.
 // Shared memory: Q, two stages of K and two of V, each as slabs of 64 elements
 // (128-byte rows, 128-byte swizzle): the K-major form for Q and K, and the same
 // bytes read MN-major for V.
@@ -203,6 +205,7 @@ __device__ __forceinline__ void tile_tma(uint32_t dst, const CUtensorMap* map, i
 // What a softmax thread knows of its row, and the tile it is at.
 struct TileRow {
   float mult, slope, cap2;      // score factor; bias and cap in log2
+  bool ahead;                   // some key of the tile is ahead of some row of the warp
   float dist;                   // the row's position less the tile's first key
   int limit;                    // columns of the tile below this are not ahead of it
   int doc;
@@ -211,142 +214,118 @@ struct TileRow {
   const float* ks;              // of each 16 columns
 };
 
-// 32 raw scores -> scores in log2 (GENERAL), or raw scores times what depends on
-// the column.
-template <bool FP8, bool GENERAL>
-__device__ __forceinline__ void tile_scores(float (&x)[32], int c0, const TileRow& r, bool capped) {
+// N raw scores of a row -> scores in log2 (GENERAL), or raw scores times what
+// depends on the column, hidden ones -inf; returns the largest. *mag: for a cap,
+// the largest magnitude before masking.
+template <bool FP8, bool GENERAL, int N>
+__device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bool capped, float* mag) {
   if constexpr (FP8) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = r.ks[c0 / 16 + h] * (GENERAL ? r.mult : 1.0f);
+    for (int h = 0; h < N / 16; ++h) {
+      const float f = r.ks[h] * (GENERAL ? r.mult : 1.0f);
 #pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const float2 y = __fmul2_rn(make_float2(x[16 * h + k], x[16 * h + k + 1]), make_float2(f, f));
-        x[16 * h + k] = y.x, x[16 * h + k + 1] = y.y;
+      for (int k = 16 * h; k < 16 * h + 16; k += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[k], x[k + 1]), make_float2(f, f));
+        x[k] = y.x, x[k + 1] = y.y;
       }
     }
   } else if constexpr (GENERAL) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] *= r.mult;
+    for (int i = 0; i < N; ++i) x[i] *= r.mult;
   }
   if constexpr (GENERAL) {
     if (capped) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = kv_tanh_of(x[i]) * r.cap2;
+      for (int i = 0; i < N; ++i) x[i] = kv_tanh_of(x[i]) * r.cap2;
     }
-    const float d = r.dist - (float)c0;
+    if (r.ahead) {  // some key is ahead of its query (a prefix)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = fmaf(-r.slope, fabsf(d - (float)i), x[i]);
+      for (int i = 0; i < N; ++i) x[i] = fmaf(-r.slope, fabsf(r.dist - (float)i), x[i]);
+    } else {  // -slope * (dist - i)
+      const float2 at = make_float2(-r.slope * r.dist, -r.slope * r.dist);
+      const float2 sl = make_float2(r.slope, r.slope);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 y = __fadd2_rn(make_float2(x[i], x[i + 1]), __ffma2_rn(sl, make_float2((float)i, (float)(i + 1)), at));
+        x[i] = y.x, x[i + 1] = y.y;
+      }
+    }
   }
-}
-
-// Hidden ones: -inf.
-__device__ __forceinline__ void tile_mask(float (&x)[32], int c0, const TileRow& r) {
-  if (r.part) {
-    const int n = r.limit - c0;
+  if (!GENERAL && capped) {
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -CUDART_INF_F;
+    for (int i = 0; i < N; i += 2) lo = fminf(lo, fminf(x[i], x[i + 1])), hi = fmaxf(hi, fmaxf(x[i], x[i + 1]));
+    *mag = fmaxf(-lo, hi);
+  }
+  if (r.part) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < r.limit ? x[i] : -CUDART_INF_F;
   }
   if (r.look) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const int4 d = r.docs[(c0 + i) / 4];
+    for (int i = 0; i < N; i += 4) {
+      const int4 d = r.docs[i / 4];
       x[i] = d.x == r.doc ? x[i] : -CUDART_INF_F;
       x[i + 1] = d.y == r.doc ? x[i + 1] : -CUDART_INF_F;
       x[i + 2] = d.z == r.doc ? x[i + 2] : -CUDART_INF_F;
       x[i + 3] = d.w == r.doc ? x[i + 3] : -CUDART_INF_F;
     }
   }
-}
-
-// The largest score of the row in N columns at `ts`; *mag the largest
-// magnitude of a visible raw score (for the cap's polynomial).
-template <bool FP8, bool GENERAL, int N>
-__device__ __forceinline__ float tile_max(uint32_t ts, const TileRow& r, bool capped, float* mag) {
-  uint32_t c[2][32];
-  float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, lo = CUDART_INF_F;
-  tc_ld32(c[0], ts);
+  float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-  for (int k = 0; k < N / 32; ++k) {
-    tc_wait_ld32(c[k & 1]);
-    if (k + 1 < N / 32) tc_ld32(c[(k + 1) & 1], ts + 32 * (k + 1));
-    float x[32];
+  for (int i = 4; i + 8 <= N; i += 8) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(c[k & 1][i]);
-    tile_scores<FP8, GENERAL>(x, 32 * k, r, capped);
-    if (!GENERAL && capped) {  // hidden ones may count here
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) lo = fminf(lo, fminf(x[i], x[i + 1]));
-    }
-    tile_mask(x, 32 * k, r);
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      m0 = fmaxf(m0, fmaxf(x[i], x[i + 1]));
-      m1 = fmaxf(m1, fmaxf(x[i + 2], x[i + 3]));
-    }
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], fmaxf(x[i + k], x[i + 4 + k]));
   }
-  const float mx = fmaxf(m0, m1);
-  *mag = fmaxf(-lo, mx);
-  return mx;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[N - 4 + k]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Weights 2^(score - base) of N columns at `ts`, written over the scores as
-// 16-bit values (times fv[16-column block] over 8-bit caches); their sum.
-// MODE 0: score = raw * mult; 1: capped by the polynomial; 2: capped; 3: general.
+// Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
+// vs[16-column block] * vinv over 8-bit caches); their sum.
+// MODE 0: score = x * mult; 1: capped by the polynomial; 2: capped; 3: x itself.
 template <bool FP8, bool BF, int MODE, int N>
-__device__ __forceinline__ float tile_weights(uint32_t ts, const TileRow& r, bool capped, float nbase, const float* vs,
-                                              float vinv) {
-  uint32_t c[2][32];
-  float2 sum = make_float2(0.0f, 0.0f);
-  tc_ld32(c[0], ts);
+__device__ __forceinline__ float tile_weights(float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
+                                              const float* vs, float vinv) {
+  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  const float2 mul = make_float2(mult, mult), nb = make_float2(nbase, nbase), c2 = make_float2(r.cap2, r.cap2);
 #pragma unroll
-  for (int k = 0; k < N / 32; ++k) {
-    tc_wait_ld32(c[k & 1]);
-    if (k + 1 < N / 32) tc_ld32(c[(k + 1) & 1], ts + 32 * (k + 1));
-    float x[32];
+  for (int q = 0; q < N / 32; ++q) {
     uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(c[k & 1][i]);
-    tile_scores<FP8, MODE == 3>(x, 32 * k, r, capped);
-    tile_mask(x, 32 * k, r);
-    const float2 mul = make_float2(r.mult, r.mult), nb = make_float2(nbase, nbase);
-    const float2 c2 = make_float2(r.cap2, r.cap2);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float2 fv = make_float2(1.0f, 1.0f);
-      if constexpr (FP8) fv.x = fv.y = vs[2 * k + h] * vinv;
+      if constexpr (FP8) fv.x = fv.y = vs[2 * q + h] * vinv;
 #pragma unroll
-      for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+      for (int k = 0; k < 16; k += 2) {
+        const int i = 32 * q + 16 * h + k;
         float2 y = make_float2(x[i], x[i + 1]);
         if constexpr (MODE == 0) {
           y = __ffma2_rn(y, mul, nb);
-        } else if constexpr (MODE == 1) {  // r.mult is scale / cap here
-          const float2 t = tile_tanh_small(__fmul2_rn(y, mul));
-          y = __ffma2_rn(t, c2, nb);
-          // a hidden score is -inf before the polynomial, which makes NaN of it
-          if (r.part || r.look) {
-            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
-            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
-          }
-        } else if constexpr (MODE == 2) {
-          const float2 e = __fmul2_rn(y, mul);
-          y = __ffma2_rn(make_float2(kv_tanh_of(e.x), kv_tanh_of(e.y)), c2, nb);
-          if (r.part || r.look) {
-            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
-            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
-          }
-        } else {
+        } else if constexpr (MODE == 3) {
           y = __fadd2_rn(y, nb);
+        } else {
+          float2 t = __fmul2_rn(y, mul);
+          if constexpr (MODE == 1)
+            t = tile_tanh_small(t);
+          else
+            t = make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y));
+          y = __ffma2_rn(t, c2, nb);
+          if (r.part || r.look) {  // a hidden score is -inf, not the cap's end
+            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
+            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
+          }
         }
         float2 e = make_float2(kv_exp2(y.x), kv_exp2(y.y));
-        sum = __fadd2_rn(sum, e);
+        sum[h] = __fadd2_rn(sum[h], e);
         if constexpr (FP8) e = __fmul2_rn(e, fv);
-        w[i / 2] = kv_pack2<BF>(e.x, e.y);
+        w[8 * h + k / 2] = kv_pack2<BF>(e.x, e.y);
       }
     }
-    tc_st16(ts + 16 * k, w);
+    tc_st16(ts + 16 * q, w);
   }
-  return sum.x + sum.y;
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 template <class T, bool FP8, int HD>
@@ -465,16 +444,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_after();
   const uint32_t tmem = s_tmem;
   const int first = list.next(0);
+  // 512 threads x 128 registers, dealt out again: see kKvTileRegisters
   bool ok = true;
 
-  if (warp < 4 * NT) {
+  if (warp < 8) {
     // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = warp >> 2;
     const bool live = tid < nrows;  // row rows0 + tid: TMEM lane tid % 128 of row tile t
     const int64_t row = rows0 + tid;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes of TMEM a warp
     // Q to shared memory, 16 bytes at a time
-    if constexpr (FP8 && kIsBf16<T>) {
+    if (t >= NT) {  // no second row tile
+    } else if constexpr (FP8 && kIsBf16<T>) {
       constexpr int LANES = HD <= 128 ? 16 : 32, PER = 32 / LANES, ROUNDS = 32 / PER;
       const int sub = lane / LANES, piece = lane % LANES;
 #pragma unroll 1
@@ -521,8 +503,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       kv_cp_commit();
       kv_cp_wait<0>();
     }
-    tc_fence_smem();
-    mbar_arrive(bar(&bars.q_full));
+    if (t < NT) {
+      tc_fence_smem();
+      mbar_arrive(bar(&bars.q_full));
+    }
 
     const int64_t pos = seq.past + tok_of(live ? tid : nrows - 1);
     int lim = 0;
@@ -534,11 +518,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       lim = k > 0 ? (int)k : 0;
     }
     const int full = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+    const int first_pos = __reduce_min_sync(0xffffffffu, pos > 0x7fffffff ? 0x7fffffff : (int)pos);
     tr.slope = 0.0f;
     if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + (rem0 + tid) % G) * kLog2e;
     const bool capped = p.cap > 0.0f;
     float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
-    if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid];
+    if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid % (NT * kTileRows)];
+    tr.mult = mult;
     tr.cap2 = p.cap * kLog2e;
     const bool general = p.slopes || !(p.scale > 0.0f);
     float m = -CUDART_INF_F, l = 0.0f, vref = 0.0f;
@@ -551,10 +537,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t ts = tmem + lanes + (NT == 2 ? t * 128 : buf * N);
         const uint32_t to = tmem + lanes + 256 + (NT == 2 ? t * 128 : 0);
         const uint8_t* in = info + (step & 3) * C::kInfo;
-        tr.mult = mult;
         tr.dist = (float)(pos - j0);
         tr.limit = lim - j0;
         tr.part = j0 + N > full;
+        tr.ahead = j0 + N > first_pos;
         tr.look = docs && (tile >= kTileListed || (mixed[tile >> 5] >> (tile & 31)) & 1u);
         tr.docs = reinterpret_cast<const int4*>(in);
         tr.ks = reinterpret_cast<const float*>(in + N * 4);
@@ -566,6 +552,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         tc_after();
+        float x[N];
+        {
+          uint32_t c[N];
+#pragma unroll
+          for (int i = 0; i < N; i += 32) tc_ld32(c + i, ts + i);
+#pragma unroll
+          for (int i = 0; i < N; i += 32) tc_wait_ld32(c + i);
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] = __uint_as_float(c[i]);
+        }
         bool grown = false;
         float vmax = 0.0f;
         if constexpr (FP8) {
@@ -575,9 +571,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         float mx, mag = 0.0f;
         if (general) {
-          mx = tile_max<FP8, true, N>(ts, tr, capped, &mag);
+          mx = tile_scores<FP8, true, N>(x, tr, capped, &mag);
         } else {
-          mx = tile_max<FP8, false, N>(ts, tr, capped, &mag) * mult;
+          mx = tile_scores<FP8, false, N>(x, tr, capped, &mag) * mult;
           if (capped) mx = mx == -CUDART_INF_F ? mx : kv_tanh_of(mx) * tr.cap2;
         }
         if (__any_sync(0xffffffffu, mx > m + 8.0f) || grown) {
@@ -611,14 +607,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float nb = m == -CUDART_INF_F ? 0.0f : -m;
         const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
         if (general) {
-          l += tile_weights<FP8, BF, 3, N>(ts, tr, capped, nb, vs, vinv);
+          l += tile_weights<FP8, BF, 3, N>(x, ts, tr, 1.0f, nb, vs, vinv);
         } else if (!capped) {
-          l += tile_weights<FP8, BF, 0, N>(ts, tr, false, nb, vs, vinv);
+          l += tile_weights<FP8, BF, 0, N>(x, ts, tr, mult, nb, vs, vinv);
         } else if (!__all_sync(0xffffffffu, mag * mult <= kLog2e)) {  // 2 log2(e) |y|, |y| <= 1/2
-          l += tile_weights<FP8, BF, 2, N>(ts, tr, true, nb, vs, vinv);
+          l += tile_weights<FP8, BF, 2, N>(x, ts, tr, mult, nb, vs, vinv);
         } else {
-          tr.mult = mult * (0.5f / kLog2e);
-          l += tile_weights<FP8, BF, 1, N>(ts, tr, true, nb, vs, vinv);
+          l += tile_weights<FP8, BF, 1, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vinv);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_before();
@@ -689,9 +684,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
     }
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0 && first < list.count) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 12 && lane == 0 && first < list.count) {
       const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
       const int steps = (p.H + 15) / 16;
       auto qk = [&](int t, int stage, uint32_t d) {
@@ -770,6 +766,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ K and V
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const int me = tid - 256;
     constexpr int PPR = HD / 8;              // 16-byte pieces of a row in shared memory
     const int HB = p.H * (FP8 ? 1 : 2);      // bytes of a cache row
