@@ -73,7 +73,8 @@ struct TileCfg {
   static constexpr int kSmem = 1024 + kQ + 4 * kStage + kTail;
 };
 
-// coefficients of y, y^3, y^5, y^7: see tile_tanh_small
+// tanh(y) for |y| <= 1/2, off by at most 1.3e-7: the odd polynomial of degree 7
+// with the smallest largest error over [0, 1/2]. Coefficients of y, y^3, y^5, y^7.
 constexpr float kTanh0 = 0.999997675f, kTanh1 = -0.333206564f, kTanh2 = 0.131451532f, kTanh3 = -0.0433726683f;
 
 struct TileBars {
@@ -87,30 +88,39 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void tc_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// D (TMEM) (+)= A (shared memory) B (shared memory)
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
+
+// Matrix descriptor of a 128-byte-swizzled operand: the low word holds the
+// shared address and the distance `lead` between 64-element slabs (read
+// MN-major; ignored K-major), both / 16, the high word that groups of 8 rows are
+// 1024 bytes apart, the version and the swizzle. Only the low word changes.
+__device__ __forceinline__ uint32_t tc_desc(uint32_t a, uint32_t lead) { return ((a & 0x3ffffu) >> 4) | (lead >> 4) << 16; }
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+// D (TMEM) (+)= A (shared memory) B (shared memory); low words of descriptors
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kDescHigh)
       : "memory");
 }
 // D (TMEM) (+)= A (TMEM) B (shared memory)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kDescHigh)
       : "memory");
 }
 
-// Matrix descriptor of a 128-byte-swizzled operand at shared address `a`:
-// groups of 8 rows 1024 bytes apart; `lead` between 64-element slabs (read
-// MN-major; ignored K-major).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t a, uint32_t lead) {
-  return (uint64_t)((a & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
-         2ull << 61;
-}
 // Instruction descriptor: float32 accumulator, 16-bit operands, M = 128.
 __device__ __forceinline__ uint32_t tc_idesc(bool bf16, int n, bool b_mn_major) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
@@ -183,17 +193,6 @@ struct TileList {
   }
 };
 
-// tanh(y) for |y| <= 1/2, off by at most 1.3e-7: an odd polynomial of degree 7,
-// fitted to the smallest largest error over [0, 1/2]. Two at a time.
-__device__ __forceinline__ float2 tile_tanh_small(float2 y) {
-  const float2 z = __fmul2_rn(y, y);
-  float2 q = make_float2(kTanh3, kTanh3);
-  q = __ffma2_rn(q, z, make_float2(kTanh2, kTanh2));
-  q = __ffma2_rn(q, z, make_float2(kTanh1, kTanh1));
-  q = __ffma2_rn(q, z, make_float2(kTanh0, kTanh0));
-  return __fmul2_rn(q, y);
-}
-
 __device__ __forceinline__ void tile_tma(uint32_t dst, const CUtensorMap* map, int x, int row, int plane, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
@@ -252,10 +251,13 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
     }
   }
   if (!GENERAL && capped) {
-    float lo = x[0], hi = x[0];
+    float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) lo = fminf(lo, fminf(x[i], x[i + 1])), hi = fmaxf(hi, fmaxf(x[i], x[i + 1]));
-    *mag = fmaxf(-lo, hi);
+    for (int i = 0; i < N; i += 4) {
+      a0 = fmaxf(a0, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+      a1 = fmaxf(a1, fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
+    }
+    *mag = fmaxf(a0, a1);
   }
   if (r.part) {
 #pragma unroll
@@ -284,11 +286,20 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
 
 // Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
 // vs[16-column block] * vinv over 8-bit caches); their sum.
-// MODE 0: score = x * mult; 1: capped by the polynomial; 2: capped; 3: x itself.
+// MODE 0: score = x * mult; 1: capped by the polynomial, mult = scale / cap; 2:
+// capped; 3: x itself.
 template <bool FP8, bool BF, int MODE, int N>
 __device__ __forceinline__ float tile_weights(float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
                                               const float* vs, float vinv) {
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  float2 k0, k1, k2, k3;  // cap * tanh(mult * x) = x (k0 + x^2 (k1 + x^2 (k2 + x^2 k3)))
+  if constexpr (MODE == 1) {
+    const float u = mult * mult, v = r.cap2 * mult;
+    k0 = make_float2(v * kTanh0, v * kTanh0);
+    k1 = make_float2(v * u * kTanh1, v * u * kTanh1);
+    k2 = make_float2(v * u * u * kTanh2, v * u * u * kTanh2);
+    k3 = make_float2(v * u * u * u * kTanh3, v * u * u * u * kTanh3);
+  }
   const float2 mul = make_float2(mult, mult), nb = make_float2(nbase, nbase), c2 = make_float2(r.cap2, r.cap2);
 #pragma unroll
   for (int q = 0; q < N / 32; ++q) {
@@ -306,12 +317,13 @@ __device__ __forceinline__ float tile_weights(float (&x)[N], uint32_t ts, const 
         } else if constexpr (MODE == 3) {
           y = __fadd2_rn(y, nb);
         } else {
-          float2 t = __fmul2_rn(y, mul);
-          if constexpr (MODE == 1)
-            t = tile_tanh_small(t);
-          else
-            t = make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y));
-          y = __ffma2_rn(t, c2, nb);
+          if constexpr (MODE == 1) {
+            const float2 z = __fmul2_rn(y, y);
+            y = __ffma2_rn(y, __ffma2_rn(z, __ffma2_rn(z, __ffma2_rn(z, k3, k2), k1), k0), nb);
+          } else {
+            const float2 t = __fmul2_rn(y, mul);
+            y = __ffma2_rn(make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y)), c2, nb);
+          }
           if (r.part || r.look) {  // a hidden score is -inf, not the cap's end
             y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
             y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
@@ -364,6 +376,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_qdoc[0] = 0x7fffffff;
     s_qdoc[1] = (int)0x80000000;
+  }
+  if (!FP8 && tid == 256) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem(&s_tmem)), "n"(512)
@@ -492,13 +508,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();  // a warp brings its own 32 rows: undo[] stays within it
     } else {
-      constexpr int PPR = HD / 8;
+      // a lane keeps its piece of the row and goes from row to row of the (S, Nq) plane
+      constexpr int PPR = HD / 8, RS = PPR < 32 ? 32 / PPR : 1;
+      const int piece = lane % PPR;
+      int r = warp * 32 + lane / PPR;
+      uint32_t h = (rem0 + (uint32_t)r) % G;
+      const bits* src = static_cast<const bits*>(p.q) + row_at(r) + piece * 8;
+      const uint32_t dst = sq + t * (kTileRows * HD * 2);
 #pragma unroll 4
-      for (int i = lane; i < 32 * PPR; i += 32) {
-        const int r = warp * 32 + i / PPR, piece = i % PPR;
+      for (int i = 0; i < 32 / RS; ++i, r += RS) {
         const bool on = r < nrows && piece * 8 < p.H;
-        kv_cp<16>(sq + t * (kTileRows * HD * 2) + tile_at(kTileRows, r % kTileRows, piece),
-                  static_cast<const bits*>(p.q) + (on ? row_at(r) + piece * 8 : 0), on);
+        kv_cp<16>(dst + tile_at(kTileRows, r % kTileRows, piece), on ? src : static_cast<const bits*>(p.q), on);
+        src += (int64_t)RS * p.H;
+        for (h += RS; h >= G; h -= G) src += (int64_t)(p.Nq - p.G) * p.H;
       }
       kv_cp_commit();
       kv_cp_wait<0>();
@@ -610,7 +632,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           l += tile_weights<FP8, BF, 3, N>(x, ts, tr, 1.0f, nb, vs, vinv);
         } else if (!capped) {
           l += tile_weights<FP8, BF, 0, N>(x, ts, tr, mult, nb, vs, vinv);
-        } else if (!__all_sync(0xffffffffu, mag * mult <= kLog2e)) {  // 2 log2(e) |y|, |y| <= 1/2
+        } else if (!__all_sync(0xffffffffu, mag * mult <= kLog2e && mult < 1e4f)) {  // 2 log2(e) |y|, |y| <= 1/2
           l += tile_weights<FP8, BF, 2, N>(x, ts, tr, mult, nb, vs, vinv);
         } else {
           l += tile_weights<FP8, BF, 1, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vinv);
@@ -635,33 +657,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         bits* dst = static_cast<bits*>(p.out) + row_at(live ? tid : 0);
         bool odd = false;
         if (live && p.splits > 1) p.ws_ml[at] = make_float2(m, l);
+        constexpr int OC = HD < 128 ? HD : 128;  // columns at once
 #pragma unroll 1
-        for (int i = 0; i < HD && i < p.H; i += 32) {
-          uint32_t o[32];
-          tc_ld32(o, to + i);
-          tc_wait_ld32(o);
-          float y[32];
+        for (int i0 = 0; i0 < HD; i0 += OC) {
+          uint32_t all[OC];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
-            odd |= !(fabsf(y[k]) < CUDART_INF_F) && i + k < p.H;
-          }
-          if (!live) continue;
+          for (int i = 0; i < OC; i += 32) tc_ld32(all + i, to + i0 + i);
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            if (i + k >= p.H) continue;
-            if (p.splits > 1) {
-              float* part = p.ws_o + at * p.H + i + k;
-              *reinterpret_cast<float4*>(part) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-              *reinterpret_cast<float4*>(part + 4) = make_float4(y[k + 4], y[k + 5], y[k + 6], y[k + 7]);
-            } else {
-              VecT<T, 8> v;
+          for (int i = 0; i < OC; i += 32) tc_wait_ld32(all + i);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) v.v[q] = Elem<T>::fromf(y[k + q]);
-              *reinterpret_cast<VecT<T, 8>*>(dst + i + k) = v;
+          for (int i1 = 0; i1 < OC; i1 += 32) {
+            const int i = i0 + i1;
+            const uint32_t* o = all + i1;
+            float y[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
+              odd |= !(fabsf(y[k]) < CUDART_INF_F) && i + k < p.H;
             }
-          }
+            if (!live) continue;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              if (i + k >= p.H) continue;
+              if (p.splits > 1) {
+                float* part = p.ws_o + at * p.H + i + k;
+                *reinterpret_cast<float4*>(part) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                *reinterpret_cast<float4*>(part + 4) = make_float4(y[k + 4], y[k + 5], y[k + 6], y[k + 7]);
+              } else {
+                VecT<T, 8> v;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v.v[q] = Elem<T>::fromf(y[k + q]);
+                *reinterpret_cast<VecT<T, 8>*>(dst + i + k) = v;
+              }
+            }
         }
+          }
         // An infinity or a NaN may have come from a value that the row does not see
         uint32_t again = __ballot_sync(0xffffffffu, odd && live);
         if (again && !docs) {
@@ -687,83 +717,100 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12 && lane == 0 && first < list.count) {
+    if (warp == 12 && first < list.count) {
+      // The whole warp walks the steps, so that what an MMA takes stays in uniform
+      // registers; one lane issues.
       const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
       const int steps = (p.H + 15) / 16;
+      const uint32_t dq = tc_desc(sq, 16), dk = tc_desc(sk, 16), dv = tc_desc(sv, N * 128);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto wait = [&](uint64_t* w, int parity) {
+        ok = ok && mbar_wait(bar(w), parity);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      auto commit = [&](uint64_t* w) {
+        if (tc_elect()) tc_commit(bar(w));
+      };
       auto qk = [&](int t, int stage, uint32_t d) {
-        for (int k = 0; k < steps; ++k) {
-          const uint32_t a = sq + t * (kTileRows * HD * 2) + (k >> 2) * (kTileRows * 128) + (k & 3) * 32;
-          const uint32_t c = sk + stage * C::kStage + (k >> 2) * (N * 128) + (k & 3) * 32;
-          tc_mma_ss(d, tc_desc(a, 16), tc_desc(c, 16), iqk, k > 0);
+        const uint32_t a = dq + t * (kTileRows * HD * 2 / 16), c = dk + stage * (C::kStage / 16);
+        if (tc_elect()) {
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            if (k < steps)
+              tc_mma_ss(d, a + ((k >> 2) * (kTileRows * 128) + (k & 3) * 32) / 16,
+                        c + ((k >> 2) * (N * 128) + (k & 3) * 32) / 16, iqk, k > 0);
         }
       };
       auto pv = [&](uint32_t d, uint32_t a, int stage, bool add) {
+        const uint32_t c = dv + stage * (C::kStage / 16);
+        if (tc_elect()) {
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k)
-          tc_mma_ts(d, a + k * 8, tc_desc(sv + stage * C::kStage + k * 2048, N * 128), ipv, add || k > 0);
+          for (int k = 0; k < N / 16; ++k)
+            tc_mma_ts(d, a + k * 8, c + k * (2048 / 16), ipv, k > 0 ? 1u : (uint32_t)add);
+        }
       };
-      int step = 0;
-      int tile = first;
-      ok = mbar_wait(bar(&bars.q_full), 0);
-      ok = ok && mbar_wait(bar(&bars.k_full[0]), 0);
+      int step = 0, tile = first;
+      wait(&bars.q_full, 0);
+      wait(&bars.k_full[0], 0);
       tc_after();
       if (ok) {
         for (int t = 0; t < live_tiles; ++t) {
-          qk(t, 0, tmem + t * 128);
-          tc_commit(bar(&bars.s_full[t]));
+          qk(t, 0, tm + t * 128);
+          commit(&bars.s_full[t]);
         }
-        tc_commit(bar(&bars.k_free[0]));
+        commit(&bars.k_free[0]);
       }
       while (ok && tile < list.count) {
         const int after = list.next(tile + 1);
         const bool more = after < list.count;
-        const int st = step & 1, sn = (step + 1) & 1;
+        const int st = step & 1, sn = st ^ 1;
         if constexpr (NT == 2) {
-          for (int t = 0; t < live_tiles && ok; ++t) {
-            ok = mbar_wait(bar(&bars.p_full[t]), step & 1);
-            if (t == 0) ok = ok && mbar_wait(bar(&bars.v_full[st]), (step >> 1) & 1);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= live_tiles) break;
+            wait(&bars.p_full[t], step & 1);
+            if (t == 0) wait(&bars.v_full[st], (step >> 1) & 1);
             if (!ok) break;
             tc_after();
-            pv(tmem + 256 + t * 128, tmem + t * 128, st, step > 0);
-            if (t == live_tiles - 1) tc_commit(bar(&bars.v_free[st]));
+            pv(tm + 256 + t * 128, tm + t * 128, st, step > 0);
+            if (t == live_tiles - 1) commit(&bars.v_free[st]);
             if (more) {
-              if (t == 0) ok = mbar_wait(bar(&bars.k_full[sn]), ((step + 1) >> 1) & 1);
+              if (t == 0) wait(&bars.k_full[sn], ((step + 1) >> 1) & 1);
               if (!ok) break;
               tc_after();
-              qk(t, sn, tmem + t * 128);
-              tc_commit(bar(&bars.s_full[t]));
-              if (t == live_tiles - 1) tc_commit(bar(&bars.k_free[sn]));
+              qk(t, sn, tm + t * 128);
+              commit(&bars.s_full[t]);
+              if (t == live_tiles - 1) commit(&bars.k_free[sn]);
             } else {
-              tc_commit(bar(&bars.o_full[t]));
+              commit(&bars.o_full[t]);
             }
           }
         } else {
           if (more) {
-            ok = mbar_wait(bar(&bars.k_full[sn]), ((step + 1) >> 1) & 1);
+            wait(&bars.k_full[sn], ((step + 1) >> 1) & 1);
             if (!ok) break;
             tc_after();
-            qk(0, sn, tmem + sn * N);
-            tc_commit(bar(&bars.s_full[sn]));
-            tc_commit(bar(&bars.k_free[sn]));
+            qk(0, sn, tm + sn * N);
+            commit(&bars.s_full[sn]);
+            commit(&bars.k_free[sn]);
           }
-          ok = mbar_wait(bar(&bars.p_full[st]), (step >> 1) & 1);
-          ok = ok && mbar_wait(bar(&bars.v_full[st]), (step >> 1) & 1);
+          wait(&bars.p_full[st], (step >> 1) & 1);
+          wait(&bars.v_full[st], (step >> 1) & 1);
           if (!ok) break;
           tc_after();
-          pv(tmem + 256, tmem + st * N, st, step > 0);
-          tc_commit(bar(&bars.v_free[st]));
-          tc_commit(bar(&bars.o_full[1]));
-          if (!more) tc_commit(bar(&bars.o_full[0]));
+          pv(tm + 256, tm + st * N, st, step > 0);
+          commit(&bars.v_free[st]);
+          commit(&bars.o_full[1]);
+          if (!more) commit(&bars.o_full[0]);
         }
         tile = after;
         ++step;
       }
       if (!ok) {  // let what was issued end before TMEM and shared memory go
-        tc_commit(bar(&bars.drain));
+        commit(&bars.drain);
         mbar_wait(bar(&bars.drain), 0);
       }
     }
-    __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ K and V
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -835,7 +882,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       constexpr int CPR = HD / 16, RS = kTileBring / CPR, PER = N / RS;
       const int r0 = me / CPR, piece = me % CPR;
       const bool in_row = piece * 16 < HB;
-      const uint32_t at0 = tile_at(N, r0, 2 * piece), at1 = tile_at(N, r0, 2 * piece + 1);
+      // of 8 lanes that share a row of two slabs, half store their second piece first:
+      // their pieces then lie in different banks
+      const bool turn = HD >= 128 && (piece & 4);
+      const uint32_t at0 = tile_at(N, r0, 2 * piece + turn), at1 = tile_at(N, r0, 2 * piece + !turn);
       uint4 a[PER], c[PER];
       auto load = [&](uint4 (&x)[PER], const uint8_t* src, int j0) {
         const uint8_t* from = src + (int64_t)(j0 + r0) * HB + piece * 16;
@@ -848,10 +898,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto store = [&](const uint4 (&x)[PER], uint8_t* dst) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
+          const uint32_t u0 = turn ? x[i].z : x[i].x, u1 = turn ? x[i].w : x[i].y;
+          const uint32_t u2 = turn ? x[i].x : x[i].z, u3 = turn ? x[i].y : x[i].w;
           *reinterpret_cast<uint4*>(dst + at0 + i * RS * 128) =
-              make_uint4(kv_codes2(x[i].x), kv_codes2_high(x[i].x), kv_codes2(x[i].y), kv_codes2_high(x[i].y));
+              make_uint4(kv_codes2(u0), kv_codes2_high(u0), kv_codes2(u1), kv_codes2_high(u1));
           *reinterpret_cast<uint4*>(dst + at1 + i * RS * 128) =
-              make_uint4(kv_codes2(x[i].z), kv_codes2_high(x[i].z), kv_codes2(x[i].w), kv_codes2_high(x[i].w));
+              make_uint4(kv_codes2(u2), kv_codes2_high(u2), kv_codes2(u3), kv_codes2_high(u3));
         }
       };
       uint8_t* pk = base + C::kQ;
