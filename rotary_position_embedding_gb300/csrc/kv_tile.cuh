@@ -43,9 +43,11 @@
 // Every wait is bounded (2 s); one that runs out sets status bit 1, and the warp
 // goes to the common end, where TMEM is freed.
 //
-// The running maximum moves only where a score passes it by 8 (in log2): O is
-// rescaled by its softmax threads then, seldom after the first tiles, so there
-// is no separate correction warp. The last key tile's rows behind the keys are
+// The base of a row's weights is the maximum when it was last moved, and moves
+// only where a tile's sum of weights passes 2^15: no maximum is taken otherwise
+// (half of the arithmetic that plain scores need). O is rescaled by its softmax
+// threads then, seldom after the first tile, so there is no correction warp. Keys
+// go from the last to the first: a bias by distance then only falls. The last key tile's rows behind the keys are
 // zeros. Key tiles whose documents no row of the CTA can have are left out.
 #pragma once
 
@@ -174,22 +176,21 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int row, int piece) {
   return (uint32_t)((piece >> 3) * rows * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// The key tiles of a CTA: all of [0, count), or those that `need` names.
+// The key tiles of a CTA, from the last to the first: all of [0, count), or
+// those that `need` names and those behind what it can name.
 struct TileList {
   const uint32_t* need;
   int count;
   bool listed;
-  __device__ __forceinline__ int next(int t) const {  // the first one from t on, or count
-    if (!listed) return t < count ? t : count;
-    while (t < count && t < kTileListed) {
-      const uint32_t w = need[t >> 5] >> (t & 31);
-      if (w) {
-        t += __ffs(w) - 1;
-        return t < count ? t : count;
-      }
-      t = (t | 31) + 1;
+  __device__ __forceinline__ int next(int t) const {  // the one before t (count: the last), or -1
+    --t;
+    if (!listed) return t;
+    while (t >= 0 && t < kTileListed) {
+      const uint32_t w = need[t >> 5] << (31 - (t & 31));
+      if (w) return t - __clz(w);
+      t = (t & ~31) - 1;
     }
-    return t < count ? t : count;
+    return t;
   }
 };
 
@@ -214,10 +215,11 @@ struct TileRow {
 };
 
 // N raw scores of a row -> scores in log2 (GENERAL), or raw scores times what
-// depends on the column, hidden ones -inf; returns the largest. *mag: for a cap,
-// the largest magnitude before masking.
+// depends on the column; hidden ones -inf. Returns, for a cap, the largest
+// magnitude before masking.
 template <bool FP8, bool GENERAL, int N>
-__device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bool capped, float* mag) {
+__device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bool capped) {
+  float mag = 0.0f;
   if constexpr (FP8) {
 #pragma unroll
     for (int h = 0; h < N / 16; ++h) {
@@ -257,7 +259,7 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
       a0 = fmaxf(a0, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
       a1 = fmaxf(a1, fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
     }
-    *mag = fmaxf(a0, a1);
+    mag = fmaxf(a0, a1);
   }
   if (r.part) {
 #pragma unroll
@@ -273,6 +275,11 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
       x[i + 3] = d.w == r.doc ? x[i + 3] : -CUDART_INF_F;
     }
   }
+  return mag;
+}
+
+template <int N>
+__device__ __forceinline__ float tile_max(const float (&x)[N]) {
   float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int i = 4; i + 8 <= N; i += 8) {
@@ -287,9 +294,9 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
 // Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
 // vs[16-column block] * vinv over 8-bit caches); their sum.
 // MODE 0: score = x * mult; 1: capped by the polynomial, mult = scale / cap; 2:
-// capped; 3: x itself.
-template <bool FP8, bool BF, int MODE, int N>
-__device__ __forceinline__ float tile_weights(float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
+// capped; 3: x itself. MASKED: some x are hidden.
+template <bool FP8, bool BF, int MODE, bool MASKED, int N>
+__device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
                                               const float* vs, float vinv) {
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   float2 k0, k1, k2, k3;  // cap * tanh(mult * x) = x (k0 + x^2 (k1 + x^2 (k2 + x^2 k3)))
@@ -324,7 +331,7 @@ __device__ __forceinline__ float tile_weights(float (&x)[N], uint32_t ts, const 
             const float2 t = __fmul2_rn(y, mul);
             y = __ffma2_rn(make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y)), c2, nb);
           }
-          if (r.part || r.look) {  // a hidden score is -inf, not the cap's end
+          if constexpr (MASKED) {  // a hidden score is -inf, not the cap's end
             y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
             y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
           }
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = s_tmem;
-  const int first = list.next(0);
+  const int first = list.next(list.count);
   // 512 threads x 128 registers, dealt out again: see kKvTileRegisters
   bool ok = true;
 
@@ -549,10 +556,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tr.mult = mult;
     tr.cap2 = p.cap * kLog2e;
     const bool general = p.slopes || !(p.scale > 0.0f);
-    float m = -CUDART_INF_F, l = 0.0f, vref = 0.0f;
+    float m = live ? -CUDART_INF_F : 0.0f, l = 0.0f, vref = 0.0f;  // rows behind the last never move the base
     if (t < live_tiles) {
       int step = 0;
-      for (int tile = first; tile < list.count; ++step) {
+      for (int tile = first; tile >= 0; ++step) {
         const int j0 = lo + tile * N;
         const int buf = NT == 2 ? t : step & 1;
         const uint32_t par = (NT == 2 ? step : step >> 1) & 1;
@@ -591,14 +598,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < NB; ++i) vmax = fmaxf(vmax, vs[i]);
           grown = vmax > vref;
         }
-        float mx, mag = 0.0f;
-        if (general) {
-          mx = tile_scores<FP8, true, N>(x, tr, capped, &mag);
-        } else {
-          mx = tile_scores<FP8, false, N>(x, tr, capped, &mag) * mult;
-          if (capped) mx = mx == -CUDART_INF_F ? mx : kv_tanh_of(mx) * tr.cap2;
+        const float mag = general ? tile_scores<FP8, true, N>(x, tr, capped) : tile_scores<FP8, false, N>(x, tr, capped);
+        const bool masked = tr.part || tr.look;
+        // 2 log2(e) |y| with |y| <= 1/2; the last keeps the polynomial's powers finite
+        const bool small = capped && !general && __all_sync(0xffffffffu, mag * mult <= kLog2e && mult < 1e4f);
+        auto weights = [&]() {
+          const float nb = m == -CUDART_INF_F ? 0.0f : -m;
+          const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
+          if (general) return tile_weights<FP8, BF, 3, false, N>(x, ts, tr, 1.0f, nb, vs, vinv);
+          if (!capped) return tile_weights<FP8, BF, 0, false, N>(x, ts, tr, mult, nb, vs, vinv);
+          if (masked) return tile_weights<FP8, BF, 2, true, N>(x, ts, tr, mult, nb, vs, vinv);
+          if (!small) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, mult, nb, vs, vinv);
+          return tile_weights<FP8, BF, 1, false, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vinv);
+        };
+        // Weights by the base so far, where every row has one; only where a row's sum
+        // says that one may be too large (2^15 fits float16) is the maximum taken, the
+        // base moved and the tile's weights formed again.
+        bool move = __any_sync(0xffffffffu, m == -CUDART_INF_F) || grown;
+        float sum = 0.0f;
+        if (!move) {
+          sum = weights();
+          move = __any_sync(0xffffffffu, !(sum <= 32768.0f));
         }
-        if (__any_sync(0xffffffffu, mx > m + 8.0f) || grown) {
+        if (move) {
+          float mx = tile_max(x) * (general ? 1.0f : mult);
+          if (capped && !general) mx = mx == -CUDART_INF_F ? mx : kv_tanh_of(mx) * tr.cap2;
           const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
           m = mn;
@@ -609,7 +633,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               vref = vmax;
             }
           }
-          if (step > 0) {
+          if (step > 0 && __any_sync(0xffffffffu, a != 1.0f)) {
             if constexpr (NT == 1) {  // here S runs ahead of P V
               ok = mbar_wait(bar(&bars.o_full[1]), (step - 1) & 1);
               ok = __all_sync(0xffffffffu, ok);
@@ -625,25 +649,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               tc_st16(to + i, o);
             }
           }
+          sum = weights();
         }
-        const float nb = m == -CUDART_INF_F ? 0.0f : -m;
-        const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
-        if (general) {
-          l += tile_weights<FP8, BF, 3, N>(x, ts, tr, 1.0f, nb, vs, vinv);
-        } else if (!capped) {
-          l += tile_weights<FP8, BF, 0, N>(x, ts, tr, mult, nb, vs, vinv);
-        } else if (!__all_sync(0xffffffffu, mag * mult <= kLog2e && mult < 1e4f)) {  // 2 log2(e) |y|, |y| <= 1/2
-          l += tile_weights<FP8, BF, 2, N>(x, ts, tr, mult, nb, vs, vinv);
-        } else {
-          l += tile_weights<FP8, BF, 1, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vinv);
-        }
+        l += sum;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_before();
         mbar_arrive(bar(&bars.p_full[buf]));
-        tile = list.next(tile + 1);
+        tile = list.next(tile);
       }
       // ---------------------------------------------------------------- output
-      if (ok && first < list.count) {
+      if (ok && first >= 0) {
         ok = mbar_wait(bar(&bars.o_full[NT == 2 ? t : 0]), 0);
         ok = __all_sync(0xffffffffu, ok);
         tc_after();
@@ -717,7 +732,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ MMA
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12 && first < list.count) {
+    if (warp == 12 && first >= 0) {
       // The whole warp walks the steps, so that what an MMA takes stays in uniform
       // registers; one lane issues.
       const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
@@ -760,9 +775,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         commit(&bars.k_free[0]);
       }
-      while (ok && tile < list.count) {
-        const int after = list.next(tile + 1);
-        const bool more = after < list.count;
+      while (ok && tile >= 0) {
+        const int after = list.next(tile);
+        const bool more = after >= 0;
         const int st = step & 1, sn = st ^ 1;
         if constexpr (NT == 2) {
 #pragma unroll
@@ -857,7 +872,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         mbar_arrive(full);
       };
       int step = 0, nk = 0, nv = 0;  // tiles of K and of V whose loads have begun
-      for (int tile = first; tile < list.count; tile = list.next(tile + 1), ++step) {
+      for (int tile = first; tile >= 0; tile = list.next(tile), ++step) {
         const int st = step & 1, j0 = lo + tile * N;
         if (step >= 2) ok = mbar_wait(bar(&bars.k_free[st]), ((step >> 1) - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -909,10 +924,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint8_t* pk = base + C::kQ;
       uint8_t* pv8 = pk + 2 * C::kStage;
       int step = 0, tile = first;
-      if (tile < list.count) load(a, kb, lo + tile * N);
-      while (tile < list.count) {
+      if (tile >= 0) load(a, kb, lo + tile * N);
+      while (tile >= 0) {
         const int st = step & 1, j0 = lo + tile * N;
-        const int after = list.next(tile + 1);
+        const int after = list.next(tile);
         load(c, vb, j0);
         if (step >= 2) ok = mbar_wait(bar(&bars.k_free[st]), ((step >> 1) - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -920,7 +935,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         store(a, pk + st * C::kStage);
         tc_fence_smem();
         mbar_arrive(bar(&bars.k_full[st]));
-        if (after < list.count) load(a, kb, lo + after * N);
+        if (after >= 0) load(a, kb, lo + after * N);
         if (step >= 2) ok = mbar_wait(bar(&bars.v_free[st]), ((step >> 1) - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         store(c, pv8 + st * C::kStage);
