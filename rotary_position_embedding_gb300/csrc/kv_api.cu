@@ -84,6 +84,16 @@ int pow2_at_least(int64_t n) {
   return p;
 }
 
+// (n * m) >> shift == n / d for 0 <= n < 2^31: m = ceil(2^(31 + l) / d), l = ceil(log2 d).
+KvDiv div_of(int64_t d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  KvDiv r;
+  r.m = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)d - 1) / (uint64_t)d);
+  r.shift = 31 + l;
+  return r;
+}
+
 // A kernel with more than 48 KB of dynamic shared memory is allowed the
 // device's most, once for each device.
 std::mutex g_mu;
@@ -454,18 +464,28 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
     return fail(ROPE_ERR_UNSUPPORTED, "RMSNorm: a head has %d units, at most 32 are implemented", p.U);
   p.lanes = p.U >= 32 ? 32 : pow2_at_least(p.U);
   p.rows = pow2_at_least(seq < kKvBlock ? seq : kKvBlock);
+  const int rows_wanted = p.rows;
   while (p.lanes * p.rows > kKvAppendThreads) p.rows /= 2;
+  const bool fast = p.rows == rows_wanted && p.U <= p.lanes;
   p.wide = head_size % 16 == 0 && aligned(k_cache, 16) && aligned(v_cache, 16);
   p.blocks = (seq + kKvBlock - 2) / kKvBlock + 1;
-  if (!sizes_fit({4, batch, kv_num_heads, p.blocks}))
-    return fail(ROPE_ERR_INVALID_ARG, "more than 2^60 cache blocks");
-  p.kv_tasks = 2 * batch * kv_num_heads * p.blocks;
-  p.q_tasks = (batch * seq * num_heads + p.rows - 1) / p.rows;
+  const int64_t q_rows = batch * seq * num_heads;
+  if (!sizes_fit({batch, kv_num_heads, p.blocks, (int64_t)1 << 31}) || batch * kv_num_heads * p.blocks >= (int64_t)1 << 31 ||
+      q_rows >= (int64_t)1 << 31)
+    return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 rows of Q or blocks of the caches");
+  p.kv_tasks = (int32_t)(batch * kv_num_heads * p.blocks);
   const int per_cta = kKvAppendThreads / (p.lanes * p.rows);
-  int64_t grid = (p.kv_tasks + p.q_tasks + per_cta - 1) / per_cta;
-  if (grid > INT32_MAX) grid = INT32_MAX;
+  p.kv_ctas = (p.kv_tasks + per_cta - 1) / per_cta;
+  p.q_groups = (num_heads + kKvAppendHeads - 1) / kKvAppendHeads;
+  p.q_items = (int32_t)(batch * seq * p.q_groups);
+  const int q_per_cta = kKvAppendThreads / p.lanes;
+  const int64_t grid = p.kv_ctas + ((int64_t)p.q_items + q_per_cta - 1) / q_per_cta;
+  p.by_q = div_of(p.q_groups);
+  p.by_s = div_of(seq);
+  p.by_blocks = div_of(p.blocks);
+  p.by_kv = div_of(kv_num_heads);
   void* args[] = {&p};
-  KV_TRY(launch(kv_append_kernel(dtype, vec, interleaved != 0, norm), dim3((unsigned)grid), kKvAppendThreads, 0, stream,
+  KV_TRY(launch(kv_append_kernel(dtype, vec, interleaved != 0, norm, fast), dim3((unsigned)grid), kKvAppendThreads, 0, stream,
                 args, "rope_apply_qkv_fp8 launch"));
   set_last_kernel("kv_append_kernel");
   return ROPE_OK;

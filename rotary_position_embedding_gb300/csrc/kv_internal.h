@@ -76,7 +76,14 @@ constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;
 constexpr int kKvCombineWarpSplits = 8;  // up to so many splits a warp joins a row alone, above a CTA
 
-// Q and K rotation with the append to 8-bit caches.
+// Division of 0 <= n < 2^31 by a constant: (n * m) >> shift.
+struct KvDiv {
+  uint32_t m;
+  int32_t shift;
+};
+
+// Q and K rotation with the append to 8-bit caches. Rows, blocks and tokens are
+// below 2^31.
 struct KvAppendParams {
   const void* q;           // (B, S, Nq*H), or packed (B, S, (Nq + 2 Nkv)*H)
   const void* k;           // (B, S, Nkv*H), or null when packed
@@ -102,10 +109,14 @@ struct KvAppendParams {
   int32_t rows;            // rows of a group (a power of two <= 16)
   int32_t wide;            // the caches take 16-byte accesses
   int64_t blocks;          // most blocks that the S rows of a sequence touch
-  int64_t kv_tasks, q_tasks;
+  int32_t kv_tasks;        // blocks of rows, K and V together
+  int32_t kv_ctas;
+  int32_t q_groups, q_items;  // groups of heads of a token, and of all tokens
+  KvDiv by_q, by_s, by_blocks, by_kv;  // by q_groups, S, blocks, Nkv
   float eps;
 };
 constexpr int kKvAppendThreads = 256;
-const void* kv_append_kernel(int dtype, bool vec, bool interleaved, bool rms_norm);
+constexpr int kKvAppendHeads = 2;  // Q heads of a token that `lanes` threads take
+const void* kv_append_kernel(int dtype, bool vec, bool interleaved, bool rms_norm, bool fast);
 
 }  // namespace rope_gb300
