@@ -6,8 +6,11 @@ namespace rope_gb300 {
 namespace {
 template <class T, bool FP8, int HD>
 KvTokenKernel pick(bool two) {
-  if (two) return {(const void*)kv_token_kernel_t<T, FP8, HD, 2>, TokenCfg<T, FP8, HD, 2>::kSmem, 16};
-  return {(const void*)kv_token_kernel_t<T, FP8, HD, 1>, TokenCfg<T, FP8, HD, 1>::kSmem, 8};
+  if (two)
+    return {(const void*)kv_token_kernel_t<T, FP8, HD, 2>, (const void*)kv_join_kernel_t<T>,
+            TokenCfg<T, FP8, HD, 2>::kSmem};
+  return {(const void*)kv_token_kernel_t<T, FP8, HD, 1>, (const void*)kv_join_kernel_t<T>,
+          TokenCfg<T, FP8, HD, 1>::kSmem};
 }
 template <class T, bool FP8>
 KvTokenKernel pick_head(int H, bool two) {

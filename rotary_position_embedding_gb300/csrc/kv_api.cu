@@ -150,35 +150,44 @@ rope_status launch(const void* fn, dim3 grid, int threads, size_t smem, rope_str
 enum class Family { kSimple, kToken, kTile };
 
 struct Plan {
-  Family family = Family::kSimple;
-  int64_t tiles = 0;  // row tiles of a (b, kvh)
-  int splits = 1;
-  int64_t split_bytes = 0;  // workspace of one split of every row
+  int64_t tiles = 0;        // row tiles of a (b, kvh)
+  int splits = 1;           // kSimple, kTile: splits of the keys
+  int deal = 0;             // kToken: CTAs that the work is dealt to (0: one problem a CTA)
+  int64_t bytes = 0;        // workspace for `splits` or `deal`
+  int64_t split_bytes = 0;  // of one split, or of one CTA
 };
 
-// Kernel family and splits from the sizes alone: the lengths are on the device.
-// The keys are split where the row tiles leave SMs without a CTA, and a long
-// cache also so that sequences of other lengths even out.
-Plan plan_attention(Family family, int64_t B, int64_t S, int64_t Nq, int64_t Nkv, int64_t H, int64_t max_len) {
+// Row tiles and splits from the sizes alone: the lengths are on the device.
+// kSimple and kTile split the keys where the row tiles leave SMs without a CTA;
+// kToken deals units of keys to as many CTAs as are resident.
+Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, int64_t Nkv, int64_t H, int64_t max_len) {
   Plan pl;
-  pl.family = family;
   const int64_t R = S * (Nq / Nkv);
-  const int64_t rows = family == Family::kToken  ? (R > 8 ? 16 : 8)
-                       : family == Family::kTile ? kv_tile_rows(H)
-                                                 : kKvSimpleRows;
+  if (family == Family::kToken) {
+    const int rt = R > 8 ? 16 : 8;
+    pl.tiles = (R + rt - 1) / rt;
+    pl.split_bytes = 2 * rt * (H * 4 + 8);
+    // a (b, kvh) has one tile of up to 16 rows here, or so many tiles that a CTA
+    // each is enough
+    const int64_t problems = B * Nkv * pl.tiles;
+    const int64_t units = (max_len + 63) / 64;
+    if (B <= kKvDealMost && problems <= (1 << 20) && max_len > 64 && problems * units < (1ll << 31)) {
+      pl.deal = kv_token_ctas(fp8, H, rt == 16);
+      if (pl.deal > problems * units) pl.deal = (int)(problems * units);
+      pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
+    }
+    return pl;
+  }
+  const int64_t rows = family == Family::kTile ? kv_tile_rows(H) : kKvSimpleRows;
   pl.tiles = (R + rows - 1) / rows;
   const int64_t ctas = pl.tiles * Nkv * B;
-  int64_t n = (2 * kSms + ctas - 1) / ctas;
-  if (family == Family::kToken) {
-    n = (4 * kSms + ctas - 1) / ctas;
-    if (n < (max_len + 1023) / 1024 && ctas < 16 * kSms) n = (max_len + 1023) / 1024;
-  }
-  if (family == Family::kTile) n = kSms / ctas;
-  const int64_t least = family == Family::kToken ? 64 : family == Family::kTile ? 512 : 256;
+  int64_t n = family == Family::kTile ? kSms / ctas : (2 * kSms + ctas - 1) / ctas;
+  const int64_t least = family == Family::kTile ? 512 : 256;
   if (n > (max_len + least - 1) / least) n = (max_len + least - 1) / least;
   if (n > 128) n = 128;
   pl.splits = n < 1 ? 1 : (int)n;
   pl.split_bytes = B * Nkv * R * (H * 4 + 8);
+  if (pl.splits > 1) pl.bytes = pl.splits * pl.split_bytes + kWorkspaceSlack;
   return pl;
 }
 
@@ -188,7 +197,8 @@ Family choose_family(bool matrix, int64_t B, int64_t S, int64_t G, int64_t Nkv, 
   if (!matrix || rope_get_variant() == ROPE_VARIANT_SIMT) return Family::kSimple;
   const int64_t R = S * G;
   const bool grid = B <= 65535 && (R + kv_tile_rows(H) - 1) / kv_tile_rows(H) <= 65535;
-  return R > 16 && grid ? Family::kTile : Family::kToken;
+  if (R > 16 && grid) return Family::kTile;
+  return R < ((int64_t)1 << 30) && Nkv * ((R + 7) / 8) <= INT32_MAX ? Family::kToken : Family::kSimple;
 }
 
 rope_status check_attention_sizes(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
@@ -245,10 +255,12 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
                    aligned(v_cache, 16) && aligned(out, 16);
   const Family family = choose_family(vec && dtype != ROPE_F32, batch, seq, num_heads / kv_num_heads, kv_num_heads,
                                       head_size);
-  Plan pl = plan_attention(family, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+  Plan pl = plan_attention(family, fp8, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
   const int64_t fits =
       workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
   if (pl.splits > fits) pl.splits = fits > 1 ? (int)fits : 1;
+  // half of the planned CTAs at least, or each its own problem
+  if (pl.deal > fits) pl.deal = fits * 2 >= pl.deal ? (int)fits : 0;
 
   KvParams p;
   memset(&p, 0, sizeof(p));
@@ -273,8 +285,16 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   p.Nkv = kv_num_heads;
   p.H = (int32_t)head_size;
   p.splits = pl.splits;
-  if (pl.splits > 1) {
-    const int64_t rows = batch * kv_num_heads * pl.splits * p.R;
+  p.tiles = (int32_t)pl.tiles;
+  p.rt = p.R > 8 ? 16 : 8;
+  p.deal = pl.deal;
+  if (family == Family::kToken) {
+    p.by_g = div_of(p.G);
+    p.by_tiles = div_of(p.tiles);
+    p.by_problems = div_of((int64_t)p.tiles * kv_num_heads);
+  }
+  if (pl.splits > 1 || pl.deal > 0) {
+    const int64_t rows = pl.deal > 0 ? 2 * (int64_t)pl.deal * p.rt : batch * kv_num_heads * pl.splits * p.R;
     p.ws_o = static_cast<float*>(workspace);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
   }
@@ -283,7 +303,7 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   p.cap = softcap;
 
   void* args[] = {&p};
-  const int64_t gx = pl.tiles * pl.splits;
+  const int64_t gx = family == Family::kToken ? pl.tiles * kv_num_heads : pl.tiles * pl.splits;
   if (gx > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
   const dim3 grid((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
   if (family == Family::kTile) {
@@ -302,8 +322,15 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
                   kKvTileRegisters));
     set_last_kernel("kv_tile_kernel");
   } else if (family == Family::kToken) {
-    const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.R > 8);
-    KV_TRY(launch(k.fn, grid, kKvTokenThreads, k.smem, stream, args, "kv_attention launch (few rows)"));
+    const KvTokenKernel k = kv_token_kernel(dtype, fp8, (int)head_size, p.rt == 16);
+    const dim3 tg = p.deal ? dim3((unsigned)p.deal) : dim3((unsigned)gx, 1, grid.z);
+    KV_TRY(launch(k.fn, tg, kKvTokenThreads, k.smem, stream, args, "kv_attention launch (few rows)"));
+    if (p.deal) {
+      const int64_t problems = batch * kv_num_heads * pl.tiles;
+      const unsigned rows = problems * p.rt <= 8 * kSms ? (unsigned)p.rt : 1;
+      KV_TRY(launch(k.join, dim3((unsigned)problems, rows), kKvTokenThreads, 0, stream, args,
+                    "kv_attention launch (joining the parts)"));
+    }
     set_last_kernel("kv_token_kernel");
   } else {
     KV_TRY(launch(kv_simple_kernel(dtype, fp8), grid, kKvSimpleThreads, kv_simple_smem((int)head_size), stream, args,
@@ -331,11 +358,12 @@ int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, in
   if (check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len) != ROPE_OK) return -1;
   if (batch == 0 || seq == 0) return 0;
   int64_t most = 0;
-  for (Family f : {Family::kSimple, Family::kToken, Family::kTile}) {  // whichever kernel the call turns out to take
-    const Plan pl = plan_attention(f, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
-    if (pl.splits > 1 && pl.splits * pl.split_bytes + kWorkspaceSlack > most)
-      most = pl.splits * pl.split_bytes + kWorkspaceSlack;
-  }
+  // whichever kernel the types and alignments make the call take
+  for (Family f : {Family::kSimple, choose_family(true, batch, seq, num_heads / kv_num_heads, kv_num_heads, head_size)})
+    for (bool fp8 : {false, true}) {
+      const Plan pl = plan_attention(f, fp8, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
+      if (pl.bytes > most) most = pl.bytes;
+    }
   return most;
 }
 

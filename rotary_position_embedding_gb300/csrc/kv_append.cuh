@@ -21,7 +21,7 @@
 
 #include <type_traits>
 
-#include "kv_internal.h"
+#include "kv_common.cuh"
 #include "rope_packed.cuh"
 #include "rope_qkv.cuh"
 
@@ -195,9 +195,6 @@ __device__ __forceinline__ void kv_row_unit(const KvAppendParams& p, const typen
   }
   if (has) kv_finish<T, V, INTER, NORM>(xa, xb, r, wa, wb, rotates, c, sn);
 }
-
-// n / d for 0 <= n < 2^31 by the multiplier and shift of KvDiv.
-__device__ __forceinline__ int kv_div(int n, const KvDiv& d) { return (int)(((uint64_t)(uint32_t)n * d.m) >> d.shift); }
 
 // Q: `lanes` threads take one unit each of kKvAppendHeads heads of a token, which
 // share position, coefficients and weights; every load goes out before the first

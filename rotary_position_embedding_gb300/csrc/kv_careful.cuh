@@ -8,11 +8,11 @@
 
 namespace rope_gb300 {
 
-// Row `row` of (b, kvh) over the keys [lo, hi) of `split`: the output, or the
-// split's partial one.
+// Row `row` of (b, kvh) over the keys [lo, hi): the output, or with `part_o` (H
+// values) a partial one and its (maximum, sum) at `part_ml`.
 template <class T, bool FP8>
 __device__ __noinline__ void kv_careful_row(const KvParams& p, const KvSeq& seq, int b, int kvh, int64_t row,
-                                            int64_t lo, int64_t hi, int split, int lane) {
+                                            int64_t lo, int64_t hi, float* part_o, float2* part_ml, int lane) {
   using bits = typename Elem<T>::bits;
   constexpr int ND = kKvMaxHead / 32;
   const int64_t plane = (int64_t)b * p.Nkv + kvh;
@@ -65,14 +65,13 @@ __device__ __noinline__ void kv_careful_row(const KvParams& p, const KvSeq& seq,
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (plane * p.splits + split) * p.R + row;
-  if (p.splits > 1 && lane == 0) p.ws_ml[at] = make_float2(m, l);
+  if (part_o && lane == 0) *part_ml = make_float2(m, l);
 #pragma unroll
   for (int i = 0; i < ND; ++i) {
     const int d = lane + 32 * i;
     if (d >= p.H) continue;
-    if (p.splits > 1)
-      p.ws_o[at * p.H + d] = o[i];
+    if (part_o)
+      part_o[d] = o[i];
     else
       static_cast<bits*>(p.out)[at_row + d] = Elem<T>::fromf(o[i] * inv);
   }

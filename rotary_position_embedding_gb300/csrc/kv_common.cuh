@@ -20,6 +20,9 @@ namespace rope_gb300 {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// n / d for 0 <= n < 2^31 by the multiplier and shift of KvDiv.
+__device__ __forceinline__ int kv_div(int n, const KvDiv& d) { return (int)(((uint64_t)(uint32_t)n * d.m) >> d.shift); }
+
 struct KvSeq {
   int64_t past, total, prefix;  // prefix clipped to [0, total]
 };

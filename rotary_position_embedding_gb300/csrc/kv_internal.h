@@ -12,6 +12,12 @@ constexpr int kKvBlock = 16;
 // Largest head size of the attention kernels.
 constexpr int kKvMaxHead = 256;
 
+// Division of 0 <= n < 2^31 by a constant: (n * m) >> shift.
+struct KvDiv {
+  uint32_t m;
+  int32_t shift;
+};
+
 // Attention over a key/value cache. The Nq / Nkv = G query heads of a key/value
 // head and the S new tokens of a sequence are the R = S * G rows of one problem
 // (b, kvh): row r is token r / G, query head kvh * G + r % G, so its Q and its
@@ -28,11 +34,14 @@ struct KvParams {
   const int32_t* docs;     // (B, max_len), or null
   const int32_t* prefix;   // (B), or null
   int32_t* status;
-  float* ws_o;             // splits > 1: partial outputs (B*Nkv, splits, R, H)
-  float2* ws_ml;           // and their (maximum, sum) (B*Nkv, splits, R)
+  float* ws_o;             // partial outputs (B*Nkv, splits, R, H), or (2 * deal, rt, H)
+  float2* ws_ml;           // and their (maximum, sum)
   int64_t S, R, max_len, nblk;
   int32_t B, Nq, Nkv, G, H;
   int32_t splits;
+  int32_t tiles, rt;       // kv_token_kernel: tiles of a (b, kvh), rows of a tile
+  int32_t deal;            // CTAs that the work is dealt to, or 0: one problem a CTA
+  KvDiv by_g, by_tiles, by_problems;  // kv_token_kernel: by G, tiles, Nkv * tiles
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   int32_t tma;             // kv_tile_kernel: the tensor maps are there
   float scale;             // factor of q.k
@@ -44,13 +53,24 @@ const void* kv_simple_kernel(int dtype, bool fp8);
 size_t kv_simple_smem(int H);
 const void* kv_combine_kernel(int dtype);
 
-// Few rows, 16-bit T, KvParams.vec: `rows` rows of a (b, kvh) a CTA.
+// Few rows, 16-bit T, KvParams.vec: 8 rows of a (b, kvh) a CTA, or 16. Both
+// launches take (KvParams): fn with grid (deal), or (Nkv * tiles, 1, B); then, if
+// dealt, join with grid (B * Nkv * tiles, rows that take a CTA).
 struct KvTokenKernel {
   const void* fn;
+  const void* join;
   size_t smem;
-  int rows;
 };
 constexpr int kKvTokenThreads = 128;
+constexpr int kKvDealMost = 1024;  // sequences whose units a CTA adds up
+#ifndef TOK_F8
+#define TOK_F8 3
+#define TOK_F16 2
+#define TOK_C8 4
+#define TOK_C16 3
+#endif
+// CTAs that the work is dealt to: what is resident on 152 SMs (see TokenCfg).
+constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return 152 * (H > 128 || two ? 2 : fp8 ? TOK_C8 : TOK_C16); }
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
 // Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above
@@ -75,12 +95,6 @@ KvTileKernel kv_tile_kernel_bf16_fp8(int H);
 constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;
 constexpr int kKvCombineWarpSplits = 8;  // up to so many splits a warp joins a row alone, above a CTA
-
-// Division of 0 <= n < 2^31 by a constant: (n * m) >> shift.
-struct KvDiv {
-  uint32_t m;
-  int32_t shift;
-};
 
 // Q and K rotation with the append to 8-bit caches. Rows, blocks and tokens are
 // below 2^31.

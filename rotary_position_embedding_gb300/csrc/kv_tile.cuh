@@ -725,7 +725,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         while (again) {
           const int r = __ffs(again) - 1;
           again &= again - 1;
-          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + (warp * 32 + r), lo64, hi64, split, lane);
+          const int64_t w = (plane * p.splits + split) * p.R + rows0 + (warp * 32 + r);
+          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + (warp * 32 + r), lo64, hi64,
+                                 p.splits > 1 ? p.ws_o + w * p.H : nullptr, p.ws_ml + w, lane);
         }
       }
     }

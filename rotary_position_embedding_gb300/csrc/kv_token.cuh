@@ -8,14 +8,13 @@
 //   S^T = K Q^T   (16 tokens x 8 rows),   O^T += V^T P^T   (16 dims x 8 rows).
 // A warp walks units of 16 tokens by itself: no barrier until its keys are done.
 //
-// Loads. A lane copies exactly the 16-byte pieces of K and V that it will feed
-// to its own fragments (cp.async into a ring of its own in shared memory,
-// 32 lanes x 16 bytes side by side), so a wait for its own copies is all the
-// synchronisation there is, the reads back have no bank conflicts, and the bytes
-// in flight do not depend on registers. Any order of the head's dimensions
-// serves S as long as K and Q share it, and any order serves O as long as the
-// output undoes it; the orders are chosen so that the pieces are 64 and 128
-// contiguous bytes of a cache row:
+// Loads. A warp copies a unit's K and V, 16 rows and so 16 * H elements side by
+// side, with cp.async into a ring of its own in shared memory, in the order of
+// memory (64-byte pieces of 8 rows at once reached 5.0 TB/s). __syncwarp is all the
+// synchronisation there is, and the bytes in flight do not depend on registers.
+// Any order of the head's dimensions serves S as long as K and Q share it, and
+// any order serves O as long as the output undoes it; the orders are chosen so
+// that a lane reads 16 bytes at a time without bank conflicts:
 //   K: lane (g = lane / 4, c = lane % 4) takes tokens g and g + 8, bytes
 //      q * 64 + c * 16 .. + 15 of the row for each q;
 //   V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims v * 8 * VD + g * VD .. + VD - 1;
@@ -48,6 +47,15 @@ constexpr bool kIsBf16<__nv_bfloat16> = true;
 
 __device__ __forceinline__ uint32_t kv_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// 16 (or 8) bytes global -> shared.
+template <int BYTES>
+__device__ __forceinline__ void kv_cp(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
 // 16 (or 8, 4) bytes global -> shared; zeros where `on` is false.
 template <int BYTES>
 __device__ __forceinline__ void kv_cp(uint32_t dst, const void* src, bool on) {
@@ -61,22 +69,6 @@ __device__ __forceinline__ void kv_cp_commit() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void kv_cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 kv_lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 kv_lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t kv_lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
 }
 
 __device__ __forceinline__ float kv_exp2(float x) {
@@ -160,6 +152,79 @@ __device__ __forceinline__ float kv_row_shift(float amax, float* factor) {
   return __uint_as_float((uint32_t)(127 - s) << 23);
 }
 
+// Work is dealt out in units of 64 keys (16 a warp) of one problem (b, kvh, tile
+// of rows). With p.deal CTAs, CTA i takes the units [i T / n, (i + 1) T / n) of all T
+// in the order of the problems, whatever the sequences' lengths: a problem that
+// one CTA has whole goes to the output, the others' parts to the workspace (2
+// slots a CTA: its first segment's, its last one's), where kv_join_kernel finds
+// them by the same rule. Without (no workspace, or more sequences than fit) a CTA
+// takes one problem. Equal splits of ragged sequences left some SMs with 1.25
+// times the mean's work.
+constexpr int kTokUnit = 16 * kTokWarps;
+
+struct TokenPlan {
+  const int32_t* before;  // units of one problem of the sequences before b, for each b, and of all
+  int total;              // units of all problems, below 2^31
+  __device__ __forceinline__ int first(const KvParams& p, int cta) const {
+    return (int)((uint64_t)(uint32_t)cta * (uint32_t)total / (uint32_t)p.deal);
+  }
+  __device__ __forceinline__ int owner(const KvParams& p, int unit) const {
+    return (int)((((uint64_t)(uint32_t)unit + 1) * (uint32_t)p.deal - 1) / (uint32_t)total);
+  }
+};
+
+__device__ __forceinline__ int token_end(const KvParams& p, const KvSeq& seq, int last_row) {
+  const int64_t e = kv_limit(seq, seq.past + kv_div(last_row, p.by_g));
+  return e > 0 ? (int)e : 0;
+}
+
+// Units of a problem of sequence b: at least one, so that its output is written.
+__device__ __forceinline__ int token_units(const KvParams& p, int b) {
+  const int u = (token_end(p, kv_seq(p, b), (int)p.R - 1) + kTokUnit - 1) / kTokUnit;
+  return u > 0 ? u : 1;
+}
+
+// The units before each sequence, in shared memory (kKvDealMost + 1 values); all
+// kKvTokenThreads threads come here.
+__device__ __forceinline__ TokenPlan token_plan(const KvParams& p, int32_t* before, int32_t* warp_sum) {
+  constexpr int PER = kKvDealMost / kKvTokenThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int u[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    u[i] = b < p.B ? token_units(p, b) : 0;
+    sum += u[i];
+  }
+  int pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += x;
+  }
+  if (lane == 31) warp_sum[warp] = pre;
+  __syncthreads();
+  int at = pre - sum;
+  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (tid * PER + i <= p.B) before[tid * PER + i] = at;
+    at += u[i];
+  }
+  if (tid == kKvTokenThreads - 1 && p.B == kKvDealMost) before[p.B] = at;
+  __syncthreads();
+  TokenPlan plan;
+  plan.before = before;
+  plan.total = before[p.B] * p.Nkv * p.tiles;
+  return plan;
+}
+
+#ifndef TOK_F8
+#define TOK_F8 3
+#define TOK_F16 2
+#define TOK_C8 4
+#define TOK_C16 3
+#endif
 template <class T, bool FP8, int HD, int NB>
 struct TokenCfg {
   static constexpr int ES = FP8 ? 1 : 2;
@@ -167,68 +232,130 @@ struct TokenCfg {
   static constexpr int VD = FP8 ? (HD >= 128 ? 16 : 8) : 8;  // dims of a V piece
   static constexpr int VB = VD * ES;                    // bytes of a V piece
   static constexpr int VQ = HD / (8 * VD);              // V pieces per lane and token
+  // Byte offset of 16-byte piece `piece` of token `row` in a stage's K, and of VB-byte
+  // piece in its V: 32 lanes' pieces side by side, turned so that neither the
+  // copies (pieces of one row) nor the reads (a lane's own) meet in a bank.
+  static __device__ __forceinline__ int k_at(int row, int piece) {
+    const int q = piece >> 2, lane = (row & 7) * 4 + (piece & 3);
+    return ((row >> 3) * KQ + q) * 512 + ((lane ^ ((q & 1) << 2)) << 4);
+  }
+  static __device__ __forceinline__ int v_at(int row, int piece) {
+    const int v = piece >> 3, g = piece & 7, c = (row & 7) >> 1, t = (row & 1) + 2 * (row >> 3);
+    return ((t * VQ + v) * 32 + g * 4 + (c ^ ((g >> 1) & 3))) * VB;
+  }
   static constexpr int kK = 2 * KQ * 512;
   static constexpr int kV = 4 * VQ * 32 * VB;
   static constexpr int kStage = kK + kV + 128;          // and 16 documents, 2 scales
-  static constexpr int kStages = kStage * 4 * kTokWarps <= 112 * 1024 ? (kStage * 6 * kTokWarps <= 112 * 1024 ? 6 : 4) : 3;
+  // Measured with 1, 2, 3, 4 CTAs an SM (64 sequences of 1 to 8191 bfloat16 keys, 8
+  // heads of 128: 293, 217, 214 us) and, 8 bits, with 2, 3, 4 (256 sequences of 1 to
+  // 4096 keys: 289, 232, 220 us): warps hide more than deeper rings do.
+  static constexpr int kStages = HD > 128 ? 2 : FP8 ? TOK_F8 : TOK_F16;
+  static constexpr int kCtas = HD > 128 || NB > 1 ? 1 : FP8 ? TOK_C8 : TOK_C16;  // on an SM
   static constexpr int kMerge = kTokWarps * NB * 8 * (HD + 4) * 4;
   static constexpr int kRing = kStage * kStages * kTokWarps;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
 template <class T, bool FP8, int HD, int NB>
-__global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvParams p) {
+__global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCtas) kv_token_kernel_t(const KvParams p) {
   using C = TokenCfg<T, FP8, HD, NB>;
   using bits = typename Elem<T>::bits;
   constexpr bool BF = !FP8 && kIsBf16<T>;  // type of the matrix operands
   constexpr int OT = HD / 16;                                   // 16-dim tiles of O^T
   extern __shared__ __align__(128) uint8_t kv_ring[];
   __shared__ float s_m[kTokWarps][NB * 8], s_l[kTokWarps][NB * 8];
+  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kTokWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t rows0 = (int64_t)(blockIdx.x / p.splits) * (NB * 8);
-  const int split = blockIdx.x % p.splits;
-  const int kvh = blockIdx.y;
-  const uint32_t ring = kv_smem(kv_ring) + warp * (C::kStage * C::kStages);
-  for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
+  uint8_t* const ring = kv_ring + warp * (C::kStage * C::kStages);
+  TokenPlan plan;
+  int at_unit = 0, last_unit = 0;
+  const bool dealt = p.deal > 0;
+  if (dealt) {
+    plan = token_plan(p, s_before, s_sum);
+    at_unit = plan.first(p, blockIdx.x);
+    last_unit = plan.first(p, blockIdx.x + 1);
+    if (at_unit >= last_unit) return;
+  }
+  const int rows_all = (int)p.R;
+  bool again = true;
+  for (int segment = 0; again; ++segment) {
+    // the next problem of this CTA, and its units
+    int b, kvh, rows0, u0 = 0, u1 = -1;
+    bool whole_problem = true;
+    if (dealt) {
+      const int problems = p.Nkv * p.tiles;  // of a sequence
+      int x = 0, y = p.B;                    // the sequence of at_unit: before[x] <= . < before[x + 1]
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (plan.before[mid] * problems <= at_unit)
+          x = mid;
+        else
+          y = mid;
+      }
+      b = x;
+      const int units = plan.before[b + 1] - plan.before[b];
+      const int in = at_unit - plan.before[b] * problems;
+      const int problem = (int)((uint32_t)in / (uint32_t)units);
+      u0 = in - problem * units;
+      u1 = u0 + (last_unit - at_unit) < units ? u0 + (last_unit - at_unit) : units;
+      whole_problem = u0 == 0 && u1 == units;
+      kvh = kv_div(problem, p.by_tiles);
+      rows0 = (problem - kvh * p.tiles) * (NB * 8);
+      at_unit += u1 - u0;
+      again = at_unit < last_unit;
+    } else {
+      const int problem = blockIdx.x;
+      kvh = kv_div(problem, p.by_tiles);
+      rows0 = (problem - kvh * p.tiles) * (NB * 8);
+      b = (int)blockIdx.z + segment * (int)gridDim.z;
+      again = b + (int)gridDim.z < p.B;
+    }
     const KvSeq seq = kv_seq(p, b);
-    if (blockIdx.x == 0 && kvh == 0 && tid == 0) kv_flag_rows(p, seq);
-    const int64_t rlast = (rows0 + NB * 8 < p.R ? rows0 + NB * 8 : p.R) - 1;
-    int64_t end = kv_limit(seq, seq.past + rlast / p.G);
-    if (end < 0) end = 0;
-    int64_t lo64, hi64;
-    kv_split(end, p.splits, split, 16 * kTokWarps, &lo64, &hi64);
-    const int lo = (int)lo64, hi = (int)hi64;
+    if (kvh == 0 && rows0 == 0 && u0 == 0 && tid == 0) kv_flag_rows(p, seq);
+    const int end = token_end(p, seq, (rows0 + NB * 8 < rows_all ? rows0 + NB * 8 : rows_all) - 1);
+    int lo = u0 * kTokUnit < end ? u0 * kTokUnit : end;
+    int hi = u1 < 0 || u1 * kTokUnit > end ? end : u1 * kTokUnit;
     const int64_t plane = (int64_t)b * p.Nkv + kvh;
+    // where a part of a problem goes
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
+    float* const part_o = whole_problem ? nullptr : p.ws_o + slot * (NB * 8) * p.H;
+    float2* const part_ml = whole_problem ? nullptr : p.ws_ml + slot * (NB * 8);
     const int HB = p.H * C::ES;  // bytes of a cache row
     const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + plane * p.max_len * HB;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + plane * p.max_len * HB;
     const int32_t* dbase = p.docs ? p.docs + (int64_t)b * p.max_len : nullptr;
 
+    // A unit's K and V are 16 whole rows each, copied in the order of memory; the
+    // pieces land where kk() and vv() look for them.
     auto copy_unit = [&](int j0, int stage) {
-      const uint32_t at = ring + stage * C::kStage;
+      const uint32_t at = kv_smem(ring + stage * C::kStage);
+      constexpr int FB = HD * C::ES, KP = FB / 16, VP = FB / C::VB;  // bytes and pieces of a row
+      const bool whole_unit = HB == FB && j0 + 16 <= hi;              // constant offsets, no zeros
+      const uint8_t* ks = kbase + (int64_t)j0 * FB + lane * 16;
+      const uint8_t* vs = vbase + (int64_t)j0 * FB + lane * C::VB;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = j0 + g + 8 * h;
-        const uint8_t* src = kbase + (int64_t)(j < hi ? j : lo) * HB;
-#pragma unroll
-        for (int q = 0; q < C::KQ; ++q) {
-          const int off = q * 64 + c * 16;
-          const bool on = j < hi && off < HB;
-          kv_cp<16>(at + (h * C::KQ + q) * 512 + lane * 16, src + (on ? off : 0), on);
+      for (int i = 0; i < KP / 2; ++i) {
+        const int row = (i * 32 + lane) / KP, piece = (i * 32 + lane) % KP;
+        const uint32_t dst = at + C::k_at(row, piece);
+        if (whole_unit) {
+          kv_cp<16>(dst, ks + i * 512);
+        } else {
+          const bool on = j0 + row < hi && piece * 16 < HB;
+          kv_cp<16>(dst, on ? kbase + (int64_t)(j0 + row) * HB + piece * 16 : kbase + (int64_t)lo * HB, on);
         }
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int j = j0 + 2 * c + (t & 1) + 8 * (t >> 1);
-        const uint8_t* src = vbase + (int64_t)(j < hi ? j : lo) * HB;
-#pragma unroll
-        for (int v = 0; v < C::VQ; ++v) {
-          const int off = (v * 8 + g) * C::VB;
-          const bool on = j < hi && off < HB;
-          kv_cp<C::VB>(at + C::kK + ((t * C::VQ + v) * 32 + lane) * C::VB, src + (on ? off : 0), on);
+      for (int i = 0; i < VP / 2; ++i) {
+        const int row = (i * 32 + lane) / VP, piece = (i * 32 + lane) % VP;
+        const uint32_t dst = at + C::kK + C::v_at(row, piece);
+        if (whole_unit) {
+          kv_cp<C::VB>(dst, vs + i * 32 * C::VB);
+        } else {
+          const bool on = j0 + row < hi && piece * C::VB < HB;
+          kv_cp<C::VB>(dst, on ? vbase + (int64_t)(j0 + row) * HB + piece * C::VB : vbase + (int64_t)lo * HB, on);
         }
       }
       const uint32_t meta = at + C::kK + C::kV;
@@ -236,10 +363,10 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
       if (FP8 && lane >= 16 && lane < 18)
         kv_cp<4>(meta + lane * 4, (lane == 16 ? p.ks : p.vs) + plane * p.nblk + j0 / kKvBlock, j0 < hi);
     };
-    auto row_of = [&](int64_t r) {  // element offset of a row of Q or of the output
-      return (((int64_t)b * p.S + r / p.G) * p.Nq + (int64_t)kvh * p.G + r % p.G) * p.H;
+    auto row_of = [&](int r) {  // element offset of a row of Q or of the output
+      const int tok = kv_div(r, p.by_g);
+      return (((int64_t)b * p.S + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
     };
-
     const int first = lo + warp * 16, step = 16 * kTokWarps;
 #pragma unroll
     for (int s = 0; s < C::kStages - 1; ++s) {
@@ -252,8 +379,8 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
     float undo[NB] = {};
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const int64_t r = rows0 + n * 8 + g;
-      const bool live = r < p.R;
+      const int r = rows0 + n * 8 + g;
+      const bool live = r < rows_all;
       const bits* src = static_cast<const bits*>(p.q) + (live ? row_of(r) : 0);
       undo[n] = 1.0f;
       if constexpr (!FP8) {
@@ -313,15 +440,16 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int64_t r = rows0 + n * 8 + 2 * c + e;
-        const bool live = r < p.R;
+        const int r = rows0 + n * 8 + 2 * c + e;
+        const bool live = r < rows_all;
+        const int tok = live ? kv_div(r, p.by_g) : 0;
         mult[n][e] = c1 * __shfl_sync(0xffffffffu, undo[n], 4 * (2 * c + e));
-        pos[n][e] = seq.past + (live ? r : 0) / p.G;
+        pos[n][e] = seq.past + tok;
         int64_t k = live ? kv_limit(seq, pos[n][e]) : 0;
         doc[n][e] = 0;
         if (p.docs && live && !kv_document(p, b, pos[n][e], &doc[n][e])) k = 0;
         lim[n][e] = k > 0 ? (int)k : 0;
-        slope[n][e] = p.slopes && live ? __ldg(p.slopes + kvh * p.G + r % p.G) * kLog2e : 0.0f;
+        slope[n][e] = p.slopes && live ? __ldg(p.slopes + kvh * p.G + (r - tok * p.G)) * kLog2e : 0.0f;
         if (live && lim[n][e] < full) full = lim[n][e];
         m[n][e] = -CUDART_INF_F;
         l[n][e] = 0.0f;
@@ -344,20 +472,26 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
     int stage = 0, next = C::kStages - 1;
     for (int j0 = first; j0 < hi; j0 += step) {
       kv_cp_wait<C::kStages - 2>();
-      if (FP8 || dbase) __syncwarp();  // documents and scales were copied by other lanes
-      const uint32_t at = ring + stage * C::kStage;
-      const uint32_t meta = at + C::kK + C::kV;
-      float s[NB][4];
+      __syncwarp();  // a lane's pieces were copied by others
+      // the unit before this one is done with: its stage is filled while this one is worked on
+      if (j0 + (C::kStages - 1) * step < hi) copy_unit(j0 + (C::kStages - 1) * step, next);
+      kv_cp_commit();
+      const uint8_t* const at = ring + stage * C::kStage;
+      const uint8_t* const meta = at + C::kK + C::kV;
+      float s[NB][4], s2[NB][4];  // two sums: half as long a chain of dependent products
 #pragma unroll
-      for (int n = 0; n < NB; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
 #pragma unroll
       for (int q = 0; q < C::KQ; ++q) {
-        const uint4 x = kv_lds16(at + q * 512 + lane * 16), y = kv_lds16(at + (C::KQ + q) * 512 + lane * 16);
+        const uint4 x = *reinterpret_cast<const uint4*>(at + C::k_at(g, 4 * q + c));
+        const uint4 y = *reinterpret_cast<const uint4*>(at + C::k_at(g + 8, 4 * q + c));
         if constexpr (!FP8) {
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             kv_mma<BF>(s[n], x.x, y.x, x.y, y.y, qf[n][2 * q][0], qf[n][2 * q][1]);
-            kv_mma<BF>(s[n], x.z, y.z, x.w, y.w, qf[n][2 * q + 1][0], qf[n][2 * q + 1][1]);
+            kv_mma<BF>(s2[n], x.z, y.z, x.w, y.w, qf[n][2 * q + 1][0], qf[n][2 * q + 1][1]);
           }
         } else {
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -366,19 +500,24 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
             const uint32_t a0 = kv_codes2(xs[i]), a2 = kv_codes2_high(xs[i]);
             const uint32_t a1 = kv_codes2(ys[i]), a3 = kv_codes2_high(ys[i]);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) kv_mma<false>(s[n], a0, a1, a2, a3, qf[n][4 * q + i][0], qf[n][4 * q + i][1]);
+            for (int n = 0; n < NB; ++n)
+              kv_mma<false>(i & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][4 * q + i][0], qf[n][4 * q + i][1]);
           }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[n][i] += s2[n][i];
       float ks = 1.0f, vs = 1.0f;
       if constexpr (FP8) {
-        ks = __uint_as_float(kv_lds4(meta + 64));
-        vs = __uint_as_float(kv_lds4(meta + 68));
+        ks = reinterpret_cast<const float*>(meta)[16];
+        vs = reinterpret_cast<const float*>(meta)[17];
       }
       const bool whole = !dbase && j0 + 16 <= full;  // uniform over the warp
       uint32_t any0 = 0xffffffffu, any1 = 0xffffffffu;
       int d0 = 0, d1 = 0;
-      if (dbase) d0 = (int)kv_lds4(meta + g * 4), d1 = (int)kv_lds4(meta + (g + 8) * 4);
+      if (dbase) d0 = reinterpret_cast<const int*>(meta)[g], d1 = reinterpret_cast<const int*>(meta)[g + 8];
       bool seen0 = false, seen1 = false;
       bool moved = false;
 #pragma unroll
@@ -461,12 +600,12 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
           uint32_t x[4][C::VB / 4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const uint32_t a = at + C::kK + ((t * C::VQ + v) * 32 + lane) * C::VB;
+            const uint8_t* a = at + C::kK + C::v_at(2 * c + (t & 1) + 8 * (t >> 1), 8 * v + g);
             if constexpr (C::VB == 16) {
-              const uint4 y = kv_lds16(a);
+              const uint4 y = *reinterpret_cast<const uint4*>(a);
               x[t][0] = y.x, x[t][1] = y.y, x[t][2] = y.z, x[t][3] = y.w;
             } else {
-              const uint2 y = kv_lds8(a);
+              const uint2 y = *reinterpret_cast<const uint2*>(a);
               x[t][0] = y.x, x[t][1] = y.y;
             }
             if (!whole && !on[t]) {
@@ -500,11 +639,6 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
           }
         }
       }
-      // refill the stage of the unit before this one, whose reads are done
-      const int ahead = j0 + (C::kStages - 1) * step;
-      if (FP8 || dbase) __syncwarp();
-      if (ahead < hi) copy_unit(ahead, next);
-      kv_cp_commit();
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
       next = next + 1 == C::kStages ? 0 : next + 1;
     }
@@ -513,7 +647,9 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
     if (__syncthreads_or(odd)) {
 #pragma unroll 1
       for (int r = warp; r < NB * 8; r += kTokWarps)
-        if (rows0 + r < p.R) kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + r, lo64, hi64, split, lane);
+        if (rows0 + r < rows_all)
+          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + r, lo, hi, part_o ? part_o + r * p.H : nullptr,
+                                 part_ml + r, lane);
       __syncthreads();
       continue;
     }
@@ -542,8 +678,8 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
     __syncthreads();
     for (int i = tid; i < NB * 8 * (HD / 4); i += kKvTokenThreads) {
       const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
-      const int64_t row = rows0 + r;
-      if (row >= p.R || d >= p.H) continue;
+      const int row = rows0 + r;
+      if (row >= rows_all || d >= p.H) continue;
       float M = s_m[0][r];
 #pragma unroll
       for (int w = 1; w < kTokWarps; ++w) M = fmaxf(M, s_m[w][r]);
@@ -557,10 +693,9 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
         L = fmaf(lw, f, L);
         o0 = fmaf(x.x, f, o0), o1 = fmaf(x.y, f, o1), o2 = fmaf(x.z, f, o2), o3 = fmaf(x.w, f, o3);
       }
-      if (p.splits > 1) {
-        const int64_t at = (plane * p.splits + split) * p.R + row;
-        if (d == 0) p.ws_ml[at] = make_float2(M, L);
-        *reinterpret_cast<float4*>(p.ws_o + at * p.H + d) = make_float4(o0, o1, o2, o3);
+      if (part_o) {
+        if (d == 0) part_ml[r] = make_float2(M, L);
+        *reinterpret_cast<float4*>(part_o + r * p.H + d) = make_float4(o0, o1, o2, o3);
       } else {
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         VecT<T, 4> y;
@@ -570,6 +705,96 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_token_kernel_t(const KvPar
       }
     }
     __syncthreads();
+  }
+}
+
+// Joins the parts of the problems that kv_token_kernel_t dealt to several CTAs.
+// CTA (x, y): problem x, its rows y, y + gridDim.y, ..; with more than 8 parts the
+// four warps share a row, else each takes rows of its own.
+template <class T>
+__global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvParams p) {
+  using bits = typename Elem<T>::bits;
+  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kTokWarps];
+  __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const TokenPlan plan = token_plan(p, s_before, s_sum);
+  const int per = p.Nkv * p.tiles;
+  const int b = kv_div(blockIdx.x, p.by_problems), in = (int)blockIdx.x - b * per;
+  const int kvh = kv_div(in, p.by_tiles), tile = in - kvh * p.tiles;
+  const int units = plan.before[b + 1] - plan.before[b];
+  const int u0 = plan.before[b] * per + in * units;
+  const int c0 = plan.owner(p, u0), c1 = plan.owner(p, u0 + units - 1);
+  if (c0 == c1) return;  // one CTA had all of it
+  // part n: of CTA c0 + n; only c0 can have begun before the problem
+  const int slot0 = 2 * c0 + (plan.first(p, c0) < u0 ? 1 : 0);
+  const int parts = c1 - c0 + 1;
+  const bool shared_row = parts > 8;
+  const int rows = (int)p.R - tile * p.rt < p.rt ? (int)p.R - tile * p.rt : p.rt;
+  const int dr = shared_row ? gridDim.y : gridDim.y * kTokWarps;
+  const int n0 = shared_row ? warp : 0, dn = shared_row ? kTokWarps : 1;
+  // with fewer units than CTAs some CTAs in between have none
+  const bool sparse = plan.total < p.deal;
+  auto slot_of = [&](int n) -> int64_t {
+    if (n == 0) return slot0;
+    return sparse && plan.first(p, c0 + n) == plan.first(p, c0 + n + 1) ? -1 : 2 * (int64_t)(c0 + n);
+  };
+  for (int r = shared_row ? (int)blockIdx.y : (int)blockIdx.y * kTokWarps + warp; r < rows; r += dr) {
+    float M = -CUDART_INF_F;
+    for (int n = lane; n < parts; n += 32) {
+      const int64_t s = slot_of(n);
+      if (s >= 0) M = fmaxf(M, p.ws_ml[s * p.rt + r].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -CUDART_INF_F ? 0.0f : M;
+    float L = 0.0f, acc[kKvMaxHead / 32];
+#pragma unroll
+    for (int j = 0; j < kKvMaxHead / 32; ++j) acc[j] = 0.0f;
+#pragma unroll 4
+    for (int n = n0; n < parts; n += dn) {
+      const int64_t s = slot_of(n);
+      if (s < 0) continue;
+      const float2 ml = p.ws_ml[s * p.rt + r];
+      const float* o = p.ws_o + (s * p.rt + r) * p.H;
+      const float f = exp2f(ml.x - base);
+      L = fmaf(ml.y, f, L);
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+        if (lane * 4 + 128 * j < p.H) {
+          const float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
+          acc[4 * j] = fmaf(x.x, f, acc[4 * j]);
+          acc[4 * j + 1] = fmaf(x.y, f, acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(x.z, f, acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(x.w, f, acc[4 * j + 3]);
+        }
+    }
+    const int row = tile * p.rt + r, tok = kv_div(row, p.by_g);
+    bits* y = static_cast<bits*>(p.out) + (((int64_t)b * p.S + tok) * p.Nq + (int64_t)kvh * p.G + (row - tok * p.G)) * p.H;
+    if (shared_row) {
+      __syncthreads();  // the previous row's sums have been read
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (lane * 4 + 128 * j < p.H) s_o[warp][lane * 4 + 128 * j + i] = acc[4 * j + i];
+      if (lane == 0) s_l[warp] = L;
+      __syncthreads();
+      L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      for (int d = threadIdx.x; d < p.H; d += kKvTokenThreads)
+        y[d] = Elem<T>::fromf(((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) * inv);
+    } else {
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+        if (lane * 4 + 128 * j < p.H) {
+          VecT<T, 4> v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v.v[i] = Elem<T>::fromf(acc[4 * j + i] * inv);
+          *reinterpret_cast<VecT<T, 4>*>(y + lane * 4 + 128 * j) = v;
+        }
+    }
   }
 }
 
