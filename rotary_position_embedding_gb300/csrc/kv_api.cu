@@ -166,7 +166,7 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
   if (family == Family::kToken) {
     const int rt = R > 8 ? 16 : 8;
     pl.tiles = (R + rt - 1) / rt;
-    pl.split_bytes = 2 * rt * (H * 4 + 8);
+    pl.split_bytes = 2 * rt * (H * 4 + 8) + 32;
     // a (b, kvh) has one tile of up to 16 rows here, or so many tiles that a CTA
     // each is enough
     const int64_t problems = B * Nkv * pl.tiles;
@@ -297,6 +297,10 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     const int64_t rows = pl.deal > 0 ? 2 * (int64_t)pl.deal * p.rt : batch * kv_num_heads * pl.splits * p.R;
     p.ws_o = static_cast<float*>(workspace);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
+    if (pl.deal > 0) {  // rows * 8 and head_size * 4 are multiples of 16 here
+      p.ws_join = reinterpret_cast<int4*>(p.ws_ml + rows);
+      p.ws_slot = reinterpret_cast<int32_t*>(p.ws_join + pl.deal);
+    }
   }
   p.vec = vec;
   p.scale = scale;
@@ -326,9 +330,9 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     const dim3 tg = p.deal ? dim3((unsigned)p.deal) : dim3((unsigned)gx, 1, grid.z);
     KV_TRY(launch(k.fn, tg, kKvTokenThreads, k.smem, stream, args, "kv_attention launch (few rows)"));
     if (p.deal) {
-      const int64_t problems = batch * kv_num_heads * pl.tiles;
-      const unsigned rows = problems * p.rt <= 8 * kSms ? (unsigned)p.rt : 1;
-      KV_TRY(launch(k.join, dim3((unsigned)problems, rows), kKvTokenThreads, 0, stream, args,
+      // few problems, each of many parts: a CTA a row
+      const unsigned rows = batch * kv_num_heads * pl.tiles * 8 <= p.deal ? (unsigned)(p.R < p.rt ? p.R : p.rt) : 1;
+      KV_TRY(launch(k.join, dim3((unsigned)p.deal, rows), kKvTokenThreads, 0, stream, args,
                     "kv_attention launch (joining the parts)"));
     }
     set_last_kernel("kv_token_kernel");

@@ -36,6 +36,8 @@ struct KvParams {
   int32_t* status;
   float* ws_o;             // partial outputs (B*Nkv, splits, R, H), or (2 * deal, rt, H)
   float2* ws_ml;           // and their (maximum, sum)
+  int4* ws_join;           // (deal): the problem that a CTA leaves unfinished
+  int32_t* ws_slot;        // (deal): which of its slots that is in, -1: no work
   int64_t S, R, max_len, nblk;
   int32_t B, Nq, Nkv, G, H;
   int32_t splits;
@@ -55,7 +57,7 @@ const void* kv_combine_kernel(int dtype);
 
 // Few rows, 16-bit T, KvParams.vec: 8 rows of a (b, kvh) a CTA, or 16. Both
 // launches take (KvParams): fn with grid (deal), or (Nkv * tiles, 1, B); then, if
-// dealt, join with grid (B * Nkv * tiles, rows that take a CTA).
+// dealt, join with grid (deal, rows that take a CTA).
 struct KvTokenKernel {
   const void* fn;
   const void* join;
@@ -69,8 +71,11 @@ constexpr int kKvDealMost = 1024;  // sequences whose units a CTA adds up
 #define TOK_C8 4
 #define TOK_C16 3
 #endif
+#ifndef TOK_M
+#define TOK_M 1
+#endif
 // CTAs that the work is dealt to: what is resident on 152 SMs (see TokenCfg).
-constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return 152 * (H > 128 || two ? 2 : fp8 ? TOK_C8 : TOK_C16); }
+constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return TOK_M * 152 * (H > 128 || two ? 2 : fp8 ? TOK_C8 : TOK_C16); }
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
 // Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above

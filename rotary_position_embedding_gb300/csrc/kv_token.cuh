@@ -156,8 +156,8 @@ __device__ __forceinline__ float kv_row_shift(float amax, float* factor) {
 // of rows). With p.deal CTAs, CTA i takes the units [i T / n, (i + 1) T / n) of all T
 // in the order of the problems, whatever the sequences' lengths: a problem that
 // one CTA has whole goes to the output, the others' parts to the workspace (2
-// slots a CTA: its first segment's, its last one's), where kv_join_kernel finds
-// them by the same rule. Without (no workspace, or more sequences than fit) a CTA
+// slots a CTA: its first segment's, its last one's), with a word on the problem that
+// the CTA begins and leaves unfinished, for kv_join_kernel. Without (no workspace, or more sequences than fit) a CTA
 // takes one problem. Equal splits of ragged sequences left some SMs with 1.25
 // times the mean's work.
 constexpr int kTokUnit = 16 * kTokWarps;
@@ -277,7 +277,13 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
     plan = token_plan(p, s_before, s_sum);
     at_unit = plan.first(p, blockIdx.x);
     last_unit = plan.first(p, blockIdx.x + 1);
-    if (at_unit >= last_unit) return;
+    if (at_unit >= last_unit) {
+      if (tid == 0) {
+        p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+        p.ws_slot[blockIdx.x] = -1;
+      }
+      return;
+    }
   }
   const int rows_all = (int)p.R;
   bool again = true;
@@ -306,6 +312,13 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       rows0 = (problem - kvh * p.tiles) * (NB * 8);
       at_unit += u1 - u0;
       again = at_unit < last_unit;
+      // the one problem that may begin in this CTA and go on in others: kv_join_kernel_t's
+      if (!again && tid == 0) {
+        const bool open = u0 == 0 && u1 < units;  // a problem that began before is another CTA's
+        p.ws_join[blockIdx.x] =
+            make_int4(b, kvh, rows0, open ? plan.owner(p, at_unit - u1 + units - 1) - (int)blockIdx.x : 0);
+        p.ws_slot[blockIdx.x] = segment > 0 ? 1 : 0;
+      }
     } else {
       const int problem = blockIdx.x;
       kvh = kv_div(problem, p.by_tiles);
@@ -336,26 +349,27 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       const bool whole_unit = HB == FB && j0 + 16 <= hi;              // constant offsets, no zeros
       const uint8_t* ks = kbase + (int64_t)j0 * FB + lane * 16;
       const uint8_t* vs = vbase + (int64_t)j0 * FB + lane * C::VB;
+      if (whole_unit) {
 #pragma unroll
-      for (int i = 0; i < KP / 2; ++i) {
-        const int row = (i * 32 + lane) / KP, piece = (i * 32 + lane) % KP;
-        const uint32_t dst = at + C::k_at(row, piece);
-        if (whole_unit) {
-          kv_cp<16>(dst, ks + i * 512);
-        } else {
+        for (int i = 0; i < KP / 2; ++i)
+          kv_cp<16>(at + C::k_at((i * 32 + lane) / KP, (i * 32 + lane) % KP), ks + i * 512);
+#pragma unroll
+        for (int i = 0; i < VP / 2; ++i)
+          kv_cp<C::VB>(at + C::kK + C::v_at((i * 32 + lane) / VP, (i * 32 + lane) % VP), vs + i * 32 * C::VB);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < KP / 2; ++i) {
+          const int row = (i * 32 + lane) / KP, piece = (i * 32 + lane) % KP;
           const bool on = j0 + row < hi && piece * 16 < HB;
-          kv_cp<16>(dst, on ? kbase + (int64_t)(j0 + row) * HB + piece * 16 : kbase + (int64_t)lo * HB, on);
+          kv_cp<16>(at + C::k_at(row, piece), on ? kbase + (int64_t)(j0 + row) * HB + piece * 16 : kbase + (int64_t)lo * HB,
+                    on);
         }
-      }
-#pragma unroll
-      for (int i = 0; i < VP / 2; ++i) {
-        const int row = (i * 32 + lane) / VP, piece = (i * 32 + lane) % VP;
-        const uint32_t dst = at + C::kK + C::v_at(row, piece);
-        if (whole_unit) {
-          kv_cp<C::VB>(dst, vs + i * 32 * C::VB);
-        } else {
+#pragma unroll 1
+        for (int i = 0; i < VP / 2; ++i) {
+          const int row = (i * 32 + lane) / VP, piece = (i * 32 + lane) % VP;
           const bool on = j0 + row < hi && piece * C::VB < HB;
-          kv_cp<C::VB>(dst, on ? vbase + (int64_t)(j0 + row) * HB + piece * C::VB : vbase + (int64_t)lo * HB, on);
+          kv_cp<C::VB>(at + C::kK + C::v_at(row, piece),
+                       on ? vbase + (int64_t)(j0 + row) * HB + piece * C::VB : vbase + (int64_t)lo * HB, on);
         }
       }
       const uint32_t meta = at + C::kK + C::kV;
@@ -367,65 +381,57 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       const int tok = kv_div(r, p.by_g);
       return (((int64_t)b * p.S + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
     };
-    const int first = lo + warp * 16, step = 16 * kTokWarps;
+    // Q fragments: row g of each column tile, in the order of K's pieces. Their
+    // loads go out first, then the copies of the first units.
+    constexpr int QP = FP8 ? 2 * C::KQ : C::KQ;  // 8-element pieces of Q a lane
+    uint4 raw[NB][QP];
 #pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int r = rows0 + n * 8 + g;
+      const bits* src = static_cast<const bits*>(p.q) + (r < rows_all ? row_of(r) : 0);
+#pragma unroll
+      for (int q = 0; q < QP; ++q) {
+        const int d = FP8 ? (q >> 1) * 64 + c * 16 + (q & 1) * 8 : q * 32 + c * 8;
+        raw[n][q] = make_uint4(0, 0, 0, 0);
+        if (r < rows_all && d < p.H) raw[n][q] = __ldg(reinterpret_cast<const uint4*>(src + d));
+      }
+    }
+    const int first = lo + warp * 16, step = 16 * kTokWarps;
+#pragma unroll 1
     for (int s = 0; s < C::kStages - 1; ++s) {
       if (first + s * step < hi) copy_unit(first + s * step, s);
       kv_cp_commit();
     }
-
-    // Q fragments: row g of each column tile, in the order of K's pieces
     uint32_t qf[NB][HD / 16][2];
-    float undo[NB] = {};
+    float undo[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const int r = rows0 + n * 8 + g;
-      const bool live = r < rows_all;
-      const bits* src = static_cast<const bits*>(p.q) + (live ? row_of(r) : 0);
       undo[n] = 1.0f;
-      if constexpr (!FP8) {
+      if constexpr (FP8 && kIsBf16<T>) {  // bfloat16 rows become float16 after scaling by a power of two
+        float amax = 0.0f, f;
 #pragma unroll
-        for (int q = 0; q < C::KQ; ++q) {
-          const int d = q * 32 + c * 8;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live && d < p.H) w = __ldg(reinterpret_cast<const uint4*>(src + d));
-          qf[n][2 * q][0] = w.x, qf[n][2 * q][1] = w.y, qf[n][2 * q + 1][0] = w.z, qf[n][2 * q + 1][1] = w.w;
+        for (int q = 0; q < QP; ++q) {
+          const uint32_t w[4] = {raw[n][q].x, raw[n][q].y, raw[n][q].z, raw[n][q].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            amax = fmaxf(amax, fmaxf(fabsf(Elem<T>::tof((bits)w[i])), fabsf(Elem<T>::tof((bits)(w[i] >> 16)))));
         }
-      } else {
-        // 16 dims a piece; bfloat16 rows become float16 after scaling by a power of two
-        uint32_t raw[C::KQ][8];
-        float amax = 0.0f;
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        undo[n] = kv_row_shift(amax, &f);
 #pragma unroll
-        for (int q = 0; q < C::KQ; ++q)
+        for (int q = 0; q < QP; ++q) {
+          uint32_t w[4] = {raw[n][q].x, raw[n][q].y, raw[n][q].z, raw[n][q].w};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int d = q * 64 + c * 16 + i * 8;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live && d < p.H) w = __ldg(reinterpret_cast<const uint4*>(src + d));
-            raw[q][4 * i] = w.x, raw[q][4 * i + 1] = w.y, raw[q][4 * i + 2] = w.z, raw[q][4 * i + 3] = w.w;
-          }
-        if constexpr (kIsBf16<T>) {
-#pragma unroll
-          for (int q = 0; q < C::KQ; ++q)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = fabsf(Elem<T>::tof((bits)raw[q][i])), d = fabsf(Elem<T>::tof((bits)(raw[q][i] >> 16)));
-              amax = fmaxf(amax, fmaxf(a, d));
-            }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          float f;
-          undo[n] = kv_row_shift(amax, &f);
-#pragma unroll
-          for (int q = 0; q < C::KQ; ++q)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              raw[q][i] = kv_pack2<false>(Elem<T>::tof((bits)raw[q][i]) * f, Elem<T>::tof((bits)(raw[q][i] >> 16)) * f);
+          for (int i = 0; i < 4; ++i)
+            w[i] = kv_pack2<false>(Elem<T>::tof((bits)w[i]) * f, Elem<T>::tof((bits)(w[i] >> 16)) * f);
+          raw[n][q] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
 #pragma unroll
-        for (int q = 0; q < C::KQ; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) qf[n][4 * q + i][0] = raw[q][2 * i], qf[n][4 * q + i][1] = raw[q][2 * i + 1];
+      for (int q = 0; q < QP; ++q) {
+        qf[n][2 * q][0] = raw[n][q].x, qf[n][2 * q][1] = raw[n][q].y;
+        qf[n][2 * q + 1][0] = raw[n][q].z, qf[n][2 * q + 1][1] = raw[n][q].w;
       }
     }
 
@@ -709,35 +715,29 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
 }
 
 // Joins the parts of the problems that kv_token_kernel_t dealt to several CTAs.
-// CTA (x, y): problem x, its rows y, y + gridDim.y, ..; with more than 8 parts the
-// four warps share a row, else each takes rows of its own.
+// CTA (x, y): the problem that begins in CTA x there and goes on in others, if
+// there is one; its rows y, y + gridDim.y, ..; with more than 8 parts the four
+// warps share a row, else each takes rows of its own.
 template <class T>
 __global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvParams p) {
   using bits = typename Elem<T>::bits;
-  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kTokWarps];
   __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
-  pdl_wait();
+  pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const TokenPlan plan = token_plan(p, s_before, s_sum);
-  const int per = p.Nkv * p.tiles;
-  const int b = kv_div(blockIdx.x, p.by_problems), in = (int)blockIdx.x - b * per;
-  const int kvh = kv_div(in, p.by_tiles), tile = in - kvh * p.tiles;
-  const int units = plan.before[b + 1] - plan.before[b];
-  const int u0 = plan.before[b] * per + in * units;
-  const int c0 = plan.owner(p, u0), c1 = plan.owner(p, u0 + units - 1);
-  if (c0 == c1) return;  // one CTA had all of it
-  // part n: of CTA c0 + n; only c0 can have begun before the problem
-  const int slot0 = 2 * c0 + (plan.first(p, c0) < u0 ? 1 : 0);
-  const int parts = c1 - c0 + 1;
+  const int4 what = p.ws_join[blockIdx.x];  // b, kvh, first row, further CTAs
+  if (what.w == 0) return;
+  const int b = what.x, kvh = what.y, rows0 = what.z, parts = what.w + 1, c0 = blockIdx.x;
+  // Part 0 is the last segment of CTA c0: its first one too if the CTA has no other
+  // (ws_slot). The others are first segments. With fewer units than CTAs some
+  // CTAs in between have none: their sum is not there.
+  const int slot0 = 2 * c0 + p.ws_slot[c0];
   const bool shared_row = parts > 8;
-  const int rows = (int)p.R - tile * p.rt < p.rt ? (int)p.R - tile * p.rt : p.rt;
+  const int rows = (int)p.R - rows0 < p.rt ? (int)p.R - rows0 : p.rt;
   const int dr = shared_row ? gridDim.y : gridDim.y * kTokWarps;
   const int n0 = shared_row ? warp : 0, dn = shared_row ? kTokWarps : 1;
-  // with fewer units than CTAs some CTAs in between have none
-  const bool sparse = plan.total < p.deal;
   auto slot_of = [&](int n) -> int64_t {
     if (n == 0) return slot0;
-    return sparse && plan.first(p, c0 + n) == plan.first(p, c0 + n + 1) ? -1 : 2 * (int64_t)(c0 + n);
+    return p.ws_slot[c0 + n] < 0 ? -1 : 2 * (int64_t)(c0 + n);
   };
   for (int r = shared_row ? (int)blockIdx.y : (int)blockIdx.y * kTokWarps + warp; r < rows; r += dr) {
     float M = -CUDART_INF_F;
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvPara
           acc[4 * j + 3] = fmaf(x.w, f, acc[4 * j + 3]);
         }
     }
-    const int row = tile * p.rt + r, tok = kv_div(row, p.by_g);
+    const int row = rows0 + r, tok = kv_div(row, p.by_g);
     bits* y = static_cast<bits*>(p.out) + (((int64_t)b * p.S + tok) * p.Nq + (int64_t)kvh * p.G + (row - tok * p.G)) * p.H;
     if (shared_row) {
       __syncthreads();  // the previous row's sums have been read
