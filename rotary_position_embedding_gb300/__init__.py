@@ -90,6 +90,8 @@ class RopeError(RuntimeError):
 def load_library(path=None):
     """Load librope_gb300.so (built in-tree by ``build_library()``)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -462,19 +464,22 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-class _on:
-    """The device of ``x`` current and, where the caller names one, ``stream`` too (so that what is
-    allocated belongs to the stream that the launch runs on). Free where nothing has to change."""
+def _fits(t, dev, shape, dtype):
+    """Whether ``t`` is what ``_shaped`` asks for (that one says what is wrong)."""
+    return t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()
 
-    def __init__(self, x, stream):
+
+class _on:
+    """The device current and, where the caller names one, ``stream`` too, so that what is allocated
+    belongs to the stream that the launch runs on."""
+
+    def __init__(self, dev, stream):
         import torch
 
-        self.handle = (stream or torch.cuda.current_stream(x.device)).cuda_stream
-        self.was = []
+        self.handle = (stream or torch.cuda.current_stream(dev)).cuda_stream
+        self.was = [torch.cuda.device(dev)]
         if stream is not None:
             self.was.append(torch.cuda.stream(stream))
-        if x.device.index != torch.cuda.current_device():
-            self.was.append(torch.cuda.device(x.device))
 
     def __enter__(self):
         for c in self.was:
@@ -484,6 +489,28 @@ class _on:
     def __exit__(self, *exc):
         for c in reversed(self.was):
             c.__exit__(*exc)
+
+
+class _here:
+    """What ``_on`` gives where nothing has to change: the present device and its current stream."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _place(dev, stream):
+    """Context of a launch on ``dev`` and ``stream`` (None: the current one); its value is the stream handle."""
+    import torch
+
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        return _here(torch._C._cuda_getCurrentRawStream(dev.index))
+    return _on(dev, stream)
 
 
 def kv_cache_fp8(batch, kv_num_heads, max_cache_len, head_size, device=None):
@@ -526,26 +553,29 @@ def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_he
     plane = (B, kv_num_heads, L, H)
     blocks = (B, kv_num_heads, -(-L // ROPE_KV_SCALE_BLOCK))
     codes = (torch.float8_e4m3fn, torch.uint8)
+    kind = torch.uint8 if k_cache.dtype == torch.uint8 else torch.float8_e4m3fn
+    f32, dev = torch.float32, query.device
     table = (cos_cache.shape[0], (rotary_embedding_dim or H) // 2)
     _shaped("query", query, query, query.shape, T)
-    _shaped("key", key, query, (B, S, kv_num_heads * H), T)
-    _shaped("value", value, query, (B, S, kv_num_heads * H), T)
-    _shaped("cos_cache", cos_cache, query, table, T)
-    _shaped("sin_cache", sin_cache, query, table, T)
+    for name, t, shape, dtype in (
+            ("past_seq_lens", past_seq_lens, (B,), torch.int32), ("k_cache", k_cache, plane, kind),
+            ("v_cache", v_cache, plane, kind), ("k_scale", k_scale, blocks, f32), ("v_scale", v_scale, blocks, f32),
+            ("cos_cache", cos_cache, table, T), ("sin_cache", sin_cache, table, T)):
+        if t is None or not _fits(t, dev, shape, dtype):
+            _shaped(name, t, query, shape, *(codes if dtype is kind else (dtype,)))
+    if not packed:
+        _shaped("key", key, query, (B, S, kv_num_heads * H), T)
+        _shaped("value", value, query, (B, S, kv_num_heads * H), T)
+    if q_norm_weight is not None or k_norm_weight is not None:
+        _shaped("q_norm_weight", q_norm_weight, query, (H,), T)
+        _shaped("k_norm_weight", k_norm_weight, query, (H,), T)
     _shaped("position_ids", position_ids, query, (B, S), torch.int64)
-    _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
-    _shaped("k_cache", k_cache, query, plane, *codes)
-    _shaped("v_cache", v_cache, query, plane, *codes)
-    _shaped("k_scale", k_scale, query, blocks, torch.float32)
-    _shaped("v_scale", v_scale, query, blocks, torch.float32)
-    _shaped("q_norm_weight", q_norm_weight, query, (H,), T)
-    _shaped("k_norm_weight", k_norm_weight, query, (H,), T)
     _shaped("q_out", q_out, query, (B, S, num_heads * H), T)
     if status is not None:
         _shaped("status", status, query, status.shape, torch.int32)
-    with _on(query, stream) as handle:
+    with _place(dev, stream) as handle:
         if q_out is None:
-            q_out = torch.empty((B, S, num_heads * H), dtype=T, device=query.device)
+            q_out = torch.empty((B, S, num_heads * H), dtype=T, device=dev)
         st = lib.rope_apply_qkv_fp8(
             _dtype_code(query), B, S, num_heads, kv_num_heads, H, _address(query), _address(key), _address(value),
             _address(q_norm_weight), _address(k_norm_weight), epsilon, _address(cos_cache), _address(sin_cache),
@@ -564,53 +594,75 @@ def kv_attention_workspace(batch, seq, num_heads, kv_num_heads, head_size, max_c
     return n
 
 
+_workspace_bytes = {}
+
+
+def _workspace(lib, key):
+    """kv_attention_workspace of a call's sizes, asked for once (it follows from them and the variant)."""
+    n = _workspace_bytes.get(key)
+    if n is None:
+        if len(_workspace_bytes) > 4096:
+            _workspace_bytes.clear()
+        n = _workspace_bytes[key] = lib.kv_attention_workspace(*key)
+    return n
+
+
 def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap, alibi_slopes,
                document_ids, prefix_lens, out, status, workspace, stream):
     import torch
 
     lib = load_library()
-    T = query.dtype
+    T, dev, f32, i32 = query.dtype, query.device, torch.float32, torch.int32
     if query.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("query must be (B, S, num_heads*H) and k_cache (B, kv_num_heads, max_len, H)")
     B, S, hidden = query.shape
-    _, N, L, H = k_cache.shape
-    plane = (B, N, L, H)
+    plane = k_cache.shape
+    _, N, L, H = plane
     _shaped("query", query, query, (B, S, num_heads * H), T)
+    if plane[0] != B:
+        _shaped("k_cache", k_cache, query, (B, N, L, H), k_cache.dtype)
     kinds = (T,) if scales is None else (torch.float8_e4m3fn, torch.uint8)
-    _shaped("k_cache", k_cache, query, plane, *kinds)
-    _shaped("v_cache", v_cache, query, plane, *kinds)
-    _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
-    _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), torch.float32)
-    _shaped("document_ids", document_ids, query, (B, L), torch.int32)
-    _shaped("prefix_lens", prefix_lens, query, (B,), torch.int32)
-    _shaped("out", out, query, (B, S, hidden), T)
+    if k_cache.dtype not in kinds or not _fits(k_cache, dev, plane, k_cache.dtype):
+        _shaped("k_cache", k_cache, query, plane, *kinds)
+    if not _fits(v_cache, dev, plane, k_cache.dtype):
+        _shaped("v_cache", v_cache, query, plane, k_cache.dtype)
+    _shaped("past_seq_lens", past_seq_lens, query, (B,), i32)
+    if alibi_slopes is not None:
+        _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), f32)
+    if document_ids is not None:
+        _shaped("document_ids", document_ids, query, (B, L), i32)
+    if prefix_lens is not None:
+        _shaped("prefix_lens", prefix_lens, query, (B,), i32)
+    if out is not None:
+        _shaped("out", out, query, (B, S, hidden), T)
     if status is not None:
-        _shaped("status", status, query, status.shape, torch.int32)
+        _shaped("status", status, query, status.shape, i32)
     if workspace is not None:
         _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
-    scale = H ** -0.5 if scale is None else scale
-    with _on(query, stream) as handle:
+    if scale is None:
+        scale = H ** -0.5
+    with _place(dev, stream) as handle:
         if out is None:
             out = torch.empty_like(query)
         if workspace is None:
-            need = lib.kv_attention_workspace(B, S, num_heads, N, H, L)
+            need = _workspace(lib, (B, S, num_heads, N, H, L))
             if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         room = 0 if workspace is None else workspace.numel()
         code = _dtype_code(query)
         if scales is None:
-            st = lib.kv_attention(code, B, S, num_heads, N, H, _address(query), _address(k_cache), _address(v_cache),
-                                  L, _address(past_seq_lens), scale, softcap, _address(alibi_slopes),
-                                  _address(document_ids), _address(prefix_lens), _address(out), _address(status),
-                                  _address(workspace), room, handle)
+            st = lib.kv_attention(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
+                                  v_cache.data_ptr(), L, _address(past_seq_lens), scale, softcap,
+                                  _address(alibi_slopes), _address(document_ids), _address(prefix_lens),
+                                  out.data_ptr(), _address(status), _address(workspace), room, handle)
         else:
             blocks = (B, N, -(-L // ROPE_KV_SCALE_BLOCK))
-            ks = _shaped("k_scale", scales[0], query, blocks, torch.float32)
-            vs = _shaped("v_scale", scales[1], query, blocks, torch.float32)
-            st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, _address(query), _address(k_cache),
-                                      _address(v_cache), _address(ks), _address(vs), L, _address(past_seq_lens),
+            ks = _shaped("k_scale", scales[0], query, blocks, f32)
+            vs = _shaped("v_scale", scales[1], query, blocks, f32)
+            st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
+                                      v_cache.data_ptr(), _address(ks), _address(vs), L, _address(past_seq_lens),
                                       scale, softcap, _address(alibi_slopes), _address(document_ids),
-                                      _address(prefix_lens), _address(out), _address(status), _address(workspace),
+                                      _address(prefix_lens), out.data_ptr(), _address(status), _address(workspace),
                                       room, handle)
     _check(name, st)
     return out
@@ -639,6 +691,7 @@ def set_variant(name):
     """Kernel variant for later calls in this process: "auto", "simt" or "tma"."""
     lib = load_library()
     _check("rope_set_variant", lib.rope_set_variant(VARIANTS[name]))
+    _workspace_bytes.clear()
 
 
 def get_variant():

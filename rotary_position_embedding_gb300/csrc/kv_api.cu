@@ -166,12 +166,14 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
   if (family == Family::kToken) {
     const int rt = R > 8 ? 16 : 8;
     pl.tiles = (R + rt - 1) / rt;
-    pl.split_bytes = 2 * rt * (H * 4 + 8) + 32;
+    pl.split_bytes = 2 * rt * (H * 4 + 8) + 16;
     // a (b, kvh) has one tile of up to 16 rows here, or so many tiles that a CTA
     // each is enough
     const int64_t problems = B * Nkv * pl.tiles;
     const int64_t units = (max_len + 63) / 64;
-    if (B <= kKvDealMost && problems <= (1 << 20) && max_len > 64 && problems * units < (1ll << 31)) {
+    // Many more problems than CTAs even out by themselves (2048 problems of 1 to 4096
+    // keys in 8 bits on 608 places: 225 us one a CTA, 233 us dealt).
+    if (problems < 3 * kv_token_ctas(fp8, H, rt == 16) && B <= kKvDealMost && problems <= (1 << 20) && max_len > 64 && problems * units < (1ll << 31)) {
       pl.deal = kv_token_ctas(fp8, H, rt == 16);
       if (pl.deal > problems * units) pl.deal = (int)(problems * units);
       pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -297,10 +299,7 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     const int64_t rows = pl.deal > 0 ? 2 * (int64_t)pl.deal * p.rt : batch * kv_num_heads * pl.splits * p.R;
     p.ws_o = static_cast<float*>(workspace);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
-    if (pl.deal > 0) {  // rows * 8 and head_size * 4 are multiples of 16 here
-      p.ws_join = reinterpret_cast<int4*>(p.ws_ml + rows);
-      p.ws_slot = reinterpret_cast<int32_t*>(p.ws_join + pl.deal);
-    }
+    if (pl.deal > 0) p.ws_join = reinterpret_cast<int4*>(p.ws_ml + rows);  // 16-byte aligned: H and rows are multiples of 8
   }
   p.vec = vec;
   p.scale = scale;

@@ -37,7 +37,6 @@ struct KvParams {
   float* ws_o;             // partial outputs (B*Nkv, splits, R, H), or (2 * deal, rt, H)
   float2* ws_ml;           // and their (maximum, sum)
   int4* ws_join;           // (deal): the problem that a CTA leaves unfinished
-  int32_t* ws_slot;        // (deal): which of its slots that is in, -1: no work
   int64_t S, R, max_len, nblk;
   int32_t B, Nq, Nkv, G, H;
   int32_t splits;
@@ -65,17 +64,8 @@ struct KvTokenKernel {
 };
 constexpr int kKvTokenThreads = 128;
 constexpr int kKvDealMost = 1024;  // sequences whose units a CTA adds up
-#ifndef TOK_F8
-#define TOK_F8 3
-#define TOK_F16 2
-#define TOK_C8 4
-#define TOK_C16 3
-#endif
-#ifndef TOK_M
-#define TOK_M 1
-#endif
 // CTAs that the work is dealt to: what is resident on 152 SMs (see TokenCfg).
-constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return TOK_M * 152 * (H > 128 || two ? 2 : fp8 ? TOK_C8 : TOK_C16); }
+constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return 152 * (H > 128 || two ? 2 : fp8 ? 4 : 3); }
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
 // Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above

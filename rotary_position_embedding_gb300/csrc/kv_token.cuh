@@ -219,12 +219,6 @@ __device__ __forceinline__ TokenPlan token_plan(const KvParams& p, int32_t* befo
   return plan;
 }
 
-#ifndef TOK_F8
-#define TOK_F8 3
-#define TOK_F16 2
-#define TOK_C8 4
-#define TOK_C16 3
-#endif
 template <class T, bool FP8, int HD, int NB>
 struct TokenCfg {
   static constexpr int ES = FP8 ? 1 : 2;
@@ -246,11 +240,12 @@ struct TokenCfg {
   static constexpr int kK = 2 * KQ * 512;
   static constexpr int kV = 4 * VQ * 32 * VB;
   static constexpr int kStage = kK + kV + 128;          // and 16 documents, 2 scales
-  // Measured with 1, 2, 3, 4 CTAs an SM (64 sequences of 1 to 8191 bfloat16 keys, 8
-  // heads of 128: 293, 217, 214 us) and, 8 bits, with 2, 3, 4 (256 sequences of 1 to
-  // 4096 keys: 289, 232, 220 us): warps hide more than deeper rings do.
-  static constexpr int kStages = HD > 128 ? 2 : FP8 ? TOK_F8 : TOK_F16;
-  static constexpr int kCtas = HD > 128 || NB > 1 ? 1 : FP8 ? TOK_C8 : TOK_C16;  // on an SM
+  // Two stages, and more warps rather than deeper rings: 64 sequences of 2 to 8191
+  // bfloat16 keys, 8 heads of 128, 212 us with 2 stages and 3 CTAs an SM, 235 with 3
+  // and 2; 256 sequences of 1 to 4096 keys in 8 bits 232 us with 2 and 4, 239 with 3
+  // and 4, 268 with 5 and 2.
+  static constexpr int kStages = 2;
+  static constexpr int kCtas = HD > 128 || NB > 1 ? 1 : FP8 ? 4 : 3;  // on an SM, at least
   static constexpr int kMerge = kTokWarps * NB * 8 * (HD + 4) * 4;
   static constexpr int kRing = kStage * kStages * kTokWarps;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
@@ -278,10 +273,10 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
     at_unit = plan.first(p, blockIdx.x);
     last_unit = plan.first(p, blockIdx.x + 1);
     if (at_unit >= last_unit) {
-      if (tid == 0) {
-        p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
-        p.ws_slot[blockIdx.x] = -1;
-      }
+      // no units: nothing begins here, and nothing of this CTA's counts where a
+      // problem's CTAs lie on both sides of it
+      if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (tid < NB * 8) p.ws_ml[2 * (int64_t)blockIdx.x * (NB * 8) + tid] = make_float2(-CUDART_INF_F, 0.0f);
       return;
     }
   }
@@ -314,10 +309,10 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       again = at_unit < last_unit;
       // the one problem that may begin in this CTA and go on in others: kv_join_kernel_t's
       if (!again && tid == 0) {
+        // (`parts` further CTAs, and which of this one's slots holds the first part)
         const bool open = u0 == 0 && u1 < units;  // a problem that began before is another CTA's
-        p.ws_join[blockIdx.x] =
-            make_int4(b, kvh, rows0, open ? plan.owner(p, at_unit - u1 + units - 1) - (int)blockIdx.x : 0);
-        p.ws_slot[blockIdx.x] = segment > 0 ? 1 : 0;
+        const int parts = open ? plan.owner(p, at_unit - u1 + units - 1) - (int)blockIdx.x : 0;
+        p.ws_join[blockIdx.x] = make_int4(b, kvh, rows0, 2 * parts + (segment > 0 ? 1 : 0));
       }
     } else {
       const int problem = blockIdx.x;
@@ -724,26 +719,19 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvPara
   __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
   pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int4 what = p.ws_join[blockIdx.x];  // b, kvh, first row, further CTAs
-  if (what.w == 0) return;
-  const int b = what.x, kvh = what.y, rows0 = what.z, parts = what.w + 1, c0 = blockIdx.x;
-  // Part 0 is the last segment of CTA c0: its first one too if the CTA has no other
-  // (ws_slot). The others are first segments. With fewer units than CTAs some
-  // CTAs in between have none: their sum is not there.
-  const int slot0 = 2 * c0 + p.ws_slot[c0];
+  const int4 what = p.ws_join[blockIdx.x];  // b, kvh, first row, 2 * further CTAs + slot
+  if (what.w < 2) return;
+  const int b = what.x, kvh = what.y, rows0 = what.z, parts = (what.w >> 1) + 1, c0 = blockIdx.x;
+  // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
   const bool shared_row = parts > 8;
   const int rows = (int)p.R - rows0 < p.rt ? (int)p.R - rows0 : p.rt;
   const int dr = shared_row ? gridDim.y : gridDim.y * kTokWarps;
   const int n0 = shared_row ? warp : 0, dn = shared_row ? kTokWarps : 1;
-  auto slot_of = [&](int n) -> int64_t {
-    if (n == 0) return slot0;
-    return p.ws_slot[c0 + n] < 0 ? -1 : 2 * (int64_t)(c0 + n);
-  };
+  auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
   for (int r = shared_row ? (int)blockIdx.y : (int)blockIdx.y * kTokWarps + warp; r < rows; r += dr) {
     float M = -CUDART_INF_F;
     for (int n = lane; n < parts; n += 32) {
-      const int64_t s = slot_of(n);
-      if (s >= 0) M = fmaxf(M, p.ws_ml[s * p.rt + r].x);
+      M = fmaxf(M, p.ws_ml[slot_of(n) * p.rt + r].x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -751,10 +739,9 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvPara
     float L = 0.0f, acc[kKvMaxHead / 32];
 #pragma unroll
     for (int j = 0; j < kKvMaxHead / 32; ++j) acc[j] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int n = n0; n < parts; n += dn) {
       const int64_t s = slot_of(n);
-      if (s < 0) continue;
       const float2 ml = p.ws_ml[s * p.rt + r];
       const float* o = p.ws_o + (s * p.rt + r) * p.H;
       const float f = exp2f(ml.x - base);
@@ -762,7 +749,8 @@ __global__ void __launch_bounds__(kKvTokenThreads) kv_join_kernel_t(const KvPara
 #pragma unroll
       for (int j = 0; j < kKvMaxHead / 128; ++j)
         if (lane * 4 + 128 * j < p.H) {
-          const float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
+          float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
+          if (f == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // never written where a CTA had no units
           acc[4 * j] = fmaf(x.x, f, acc[4 * j]);
           acc[4 * j + 1] = fmaf(x.y, f, acc[4 * j + 1]);
           acc[4 * j + 2] = fmaf(x.z, f, acc[4 * j + 2]);
