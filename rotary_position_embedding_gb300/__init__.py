@@ -492,7 +492,7 @@ class _on:
 
 
 class _here:
-    """What ``_on`` gives where nothing has to change: the present device and its current stream."""
+    """What ``_on`` gives where nothing has to change."""
 
     def __init__(self, handle):
         self.handle = handle
@@ -504,10 +504,23 @@ class _here:
         pass
 
 
-def _place(dev, stream):
-    """Context of a launch on ``dev`` and ``stream`` (None: the current one); its value is the stream handle."""
-    import torch
+_codes_of = {}
 
+
+def _torch_code(T):
+    """(torch, the C ABI's code of dtype T); torch is imported at the first call."""
+    code = _codes_of.get(T)
+    if code is None:
+        import torch
+
+        _codes_of.update({torch.float32: (torch, ROPE_F32), torch.float16: (torch, ROPE_F16),
+                          torch.bfloat16: (torch, ROPE_BF16)})
+        code = _codes_of.get(T, (torch, _UNSUPPORTED_DTYPE))
+    return code
+
+
+def _place(torch, dev, stream):
+    """Context of a launch on ``dev`` and ``stream`` (None: the current one); its value is the stream handle."""
     if stream is None and dev.index == torch._C._cuda_getDevice():
         return _here(torch._C._cuda_getCurrentRawStream(dev.index))
     return _on(dev, stream)
@@ -535,10 +548,9 @@ def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_he
     k_cache and v_cache are float8_e4m3fn (or uint8 codes) (B, kv_num_heads, max_len, H), k_scale and v_scale
     float32 (B, kv_num_heads, ceil(max_len / 16)), all updated in place (``kv_cache_fp8`` makes them). With
     q_norm_weight and k_norm_weight each Q and K head is RMS-normalised first. Returns q_out."""
-    import torch
-
     lib = load_library()
-    T = query.dtype
+    T, dev = query.dtype, query.device
+    torch, code = _torch_code(T)
     if query.dim() != 3:
         raise ValueError("query must be (B, S, hidden)")
     B, S, hidden = query.shape
@@ -552,37 +564,47 @@ def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_he
     L = k_cache.shape[2]
     plane = (B, kv_num_heads, L, H)
     blocks = (B, kv_num_heads, -(-L // ROPE_KV_SCALE_BLOCK))
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    kind = torch.uint8 if k_cache.dtype == torch.uint8 else torch.float8_e4m3fn
-    f32, dev = torch.float32, query.device
     table = (cos_cache.shape[0], (rotary_embedding_dim or H) // 2)
-    _shaped("query", query, query, query.shape, T)
-    for name, t, shape, dtype in (
-            ("past_seq_lens", past_seq_lens, (B,), torch.int32), ("k_cache", k_cache, plane, kind),
-            ("v_cache", v_cache, plane, kind), ("k_scale", k_scale, blocks, f32), ("v_scale", v_scale, blocks, f32),
-            ("cos_cache", cos_cache, table, T), ("sin_cache", sin_cache, table, T)):
-        if t is None or not _fits(t, dev, shape, dtype):
-            _shaped(name, t, query, shape, *(codes if dtype is kind else (dtype,)))
+    f32, kind = torch.float32, k_cache.dtype
+    if past_seq_lens is None or not (
+            _fits(past_seq_lens, dev, (B,), torch.int32) and _fits(k_cache, dev, plane, kind)
+            and _fits(v_cache, dev, plane, kind) and _fits(k_scale, dev, blocks, f32)
+            and _fits(v_scale, dev, blocks, f32) and _fits(cos_cache, dev, table, T) and _fits(sin_cache, dev, table, T)
+            and query.is_contiguous() and dev.type == "cuda" and kind.itemsize == 1):
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        _shaped("query", query, query, query.shape, T)
+        _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
+        _shaped("k_cache", k_cache, query, plane, *codes)
+        _shaped("v_cache", v_cache, query, plane, kind)
+        _shaped("k_scale", k_scale, query, blocks, f32)
+        _shaped("v_scale", v_scale, query, blocks, f32)
+        _shaped("cos_cache", cos_cache, query, table, T)
+        _shaped("sin_cache", sin_cache, query, table, T)
+    if kind is not torch.float8_e4m3fn and kind is not torch.uint8:
+        raise ValueError(f"k_cache must have dtype float8_e4m3fn or uint8, got {kind}")
     if not packed:
         _shaped("key", key, query, (B, S, kv_num_heads * H), T)
         _shaped("value", value, query, (B, S, kv_num_heads * H), T)
     if q_norm_weight is not None or k_norm_weight is not None:
         _shaped("q_norm_weight", q_norm_weight, query, (H,), T)
         _shaped("k_norm_weight", k_norm_weight, query, (H,), T)
-    _shaped("position_ids", position_ids, query, (B, S), torch.int64)
-    _shaped("q_out", q_out, query, (B, S, num_heads * H), T)
+    if position_ids is not None:
+        _shaped("position_ids", position_ids, query, (B, S), torch.int64)
+    if q_out is not None:
+        _shaped("q_out", q_out, query, (B, S, num_heads * H), T)
     if status is not None:
         _shaped("status", status, query, status.shape, torch.int32)
-    with _place(dev, stream) as handle:
+    with _place(torch, dev, stream) as handle:
         if q_out is None:
             q_out = torch.empty((B, S, num_heads * H), dtype=T, device=dev)
         st = lib.rope_apply_qkv_fp8(
-            _dtype_code(query), B, S, num_heads, kv_num_heads, H, _address(query), _address(key), _address(value),
-            _address(q_norm_weight), _address(k_norm_weight), epsilon, _address(cos_cache), _address(sin_cache),
+            code, B, S, num_heads, kv_num_heads, H, query.data_ptr(), _address(key), _address(value),
+            _address(q_norm_weight), _address(k_norm_weight), epsilon, cos_cache.data_ptr(), sin_cache.data_ptr(),
             table[0], _address(position_ids), _address(past_seq_lens), int(interleaved), rotary_embedding_dim,
-            _address(q_out), _address(k_cache), _address(v_cache), _address(k_scale), _address(v_scale), L,
+            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), L,
             _address(status), handle)
-    _check("rope_apply_qkv_fp8", st)
+    if st:
+        _check("rope_apply_qkv_fp8", st)
     return q_out
 
 
@@ -609,24 +631,30 @@ def _workspace(lib, key):
 
 def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap, alibi_slopes,
                document_ids, prefix_lens, out, status, workspace, stream):
-    import torch
-
     lib = load_library()
-    T, dev, f32, i32 = query.dtype, query.device, torch.float32, torch.int32
-    if query.dim() != 3 or k_cache.dim() != 4:
+    T, dev, kind, plane = query.dtype, query.device, k_cache.dtype, k_cache.shape
+    torch, code = _torch_code(T)
+    if query.dim() != 3 or len(plane) != 4:
         raise ValueError("query must be (B, S, num_heads*H) and k_cache (B, kv_num_heads, max_len, H)")
     B, S, hidden = query.shape
-    plane = k_cache.shape
     _, N, L, H = plane
-    _shaped("query", query, query, (B, S, num_heads * H), T)
-    if plane[0] != B:
-        _shaped("k_cache", k_cache, query, (B, N, L, H), k_cache.dtype)
-    kinds = (T,) if scales is None else (torch.float8_e4m3fn, torch.uint8)
-    if k_cache.dtype not in kinds or not _fits(k_cache, dev, plane, k_cache.dtype):
-        _shaped("k_cache", k_cache, query, plane, *kinds)
-    if not _fits(v_cache, dev, plane, k_cache.dtype):
-        _shaped("v_cache", v_cache, query, plane, k_cache.dtype)
-    _shaped("past_seq_lens", past_seq_lens, query, (B,), i32)
+    f32, i32 = torch.float32, torch.int32
+    ks = vs = None
+    if scales is not None:
+        ks, vs = scales
+        blocks = (B, N, -(-L // ROPE_KV_SCALE_BLOCK))
+        _shaped("k_scale", ks, query, blocks, f32)
+        _shaped("v_scale", vs, query, blocks, f32)
+    if past_seq_lens is None or not (
+            hidden == num_heads * H and plane[0] == B and query.is_contiguous() and dev.type == "cuda"
+            and _fits(past_seq_lens, dev, (B,), i32) and _fits(k_cache, dev, plane, kind)
+            and _fits(v_cache, dev, plane, kind)):
+        _shaped("query", query, query, (B, S, num_heads * H), T)
+        _shaped("k_cache", k_cache, query, (B, N, L, H), kind)
+        _shaped("v_cache", v_cache, query, (B, N, L, H), kind)
+        _shaped("past_seq_lens", past_seq_lens, query, (B,), i32)
+    if kind is not T if scales is None else kind is not torch.float8_e4m3fn and kind is not torch.uint8:
+        raise ValueError(f"k_cache must have dtype {T if scales is None else 'float8_e4m3fn or uint8'}, got {kind}")
     if alibi_slopes is not None:
         _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), f32)
     if document_ids is not None:
@@ -641,7 +669,7 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
         _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
     if scale is None:
         scale = H ** -0.5
-    with _place(dev, stream) as handle:
+    with _place(torch, dev, stream) as handle:
         if out is None:
             out = torch.empty_like(query)
         if workspace is None:
@@ -649,22 +677,19 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         room = 0 if workspace is None else workspace.numel()
-        code = _dtype_code(query)
         if scales is None:
             st = lib.kv_attention(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
                                   v_cache.data_ptr(), L, _address(past_seq_lens), scale, softcap,
                                   _address(alibi_slopes), _address(document_ids), _address(prefix_lens),
                                   out.data_ptr(), _address(status), _address(workspace), room, handle)
         else:
-            blocks = (B, N, -(-L // ROPE_KV_SCALE_BLOCK))
-            ks = _shaped("k_scale", scales[0], query, blocks, f32)
-            vs = _shaped("v_scale", scales[1], query, blocks, f32)
             st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
                                       v_cache.data_ptr(), _address(ks), _address(vs), L, _address(past_seq_lens),
                                       scale, softcap, _address(alibi_slopes), _address(document_ids),
                                       _address(prefix_lens), out.data_ptr(), _address(status), _address(workspace),
                                       room, handle)
-    _check(name, st)
+    if st:
+        _check(name, st)
     return out
 
 
