@@ -4,8 +4,8 @@
 
 namespace rope_gb300 {
 
-KvTileKernel kv_tile_kernel_bf16(int H) {
-  return kv_tile_pick<__nv_bfloat16, false>(H);
+KvTileKernel kv_tile_kernel_bf16(int H, int kind) {
+  return kv_tile_pick<__nv_bfloat16, false>(H, kind);
 }
 
 }  // namespace rope_gb300

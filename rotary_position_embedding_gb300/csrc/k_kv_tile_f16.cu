@@ -4,8 +4,8 @@
 
 namespace rope_gb300 {
 
-KvTileKernel kv_tile_kernel_f16(int H) {
-  return kv_tile_pick<__half, false>(H);
+KvTileKernel kv_tile_kernel_f16(int H, int kind) {
+  return kv_tile_pick<__half, false>(H, kind);
 }
 
 }  // namespace rope_gb300

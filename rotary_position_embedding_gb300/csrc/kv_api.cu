@@ -311,8 +311,9 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   const dim3 grid((unsigned)gx, kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
   if (family == Family::kTile) {
     const int h = (int)head_size;
-    const KvTileKernel k = dtype == ROPE_F16 ? (fp8 ? kv_tile_kernel_f16_fp8(h) : kv_tile_kernel_f16(h))
-                                             : (fp8 ? kv_tile_kernel_bf16_fp8(h) : kv_tile_kernel_bf16(h));
+    const int kind = softcap > 0.0f || !(scale > 0.0f) ? kKvAnyScore : alibi_slopes ? kKvBiased : kKvPlain;
+    const KvTileKernel k = dtype == ROPE_F16 ? (fp8 ? kv_tile_kernel_f16_fp8(h, kind) : kv_tile_kernel_f16(h, kind))
+                                             : (fp8 ? kv_tile_kernel_bf16_fp8(h, kind) : kv_tile_kernel_bf16(h, kind));
     KvTileMaps maps;
     memset(&maps, 0, sizeof(maps));
     const int64_t planes = batch * kv_num_heads;

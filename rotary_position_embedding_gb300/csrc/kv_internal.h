@@ -82,10 +82,13 @@ constexpr int kKvTileRegisters = 128;
 static_assert(256 * 192 + 128 * 88 + 128 * 40 <= kKvTileThreads * kKvTileRegisters, "registers of kv_tile_kernel");
 constexpr int kv_tile_keys(int64_t H) { return H <= 128 ? 128 : 64; }
 constexpr int kv_tile_rows(int64_t H) { return H <= 128 ? 256 : 128; }
-KvTileKernel kv_tile_kernel_f16(int H);
-KvTileKernel kv_tile_kernel_f16_fp8(int H);
-KvTileKernel kv_tile_kernel_bf16(int H);
-KvTileKernel kv_tile_kernel_bf16_fp8(int H);
+// What scores may hold besides scale * q.k with scale > 0: nothing; a bias by
+// distance; anything (a cap, or a scale <= 0 too).
+enum { kKvPlain, kKvBiased, kKvAnyScore };
+KvTileKernel kv_tile_kernel_f16(int H, int kind);
+KvTileKernel kv_tile_kernel_f16_fp8(int H, int kind);
+KvTileKernel kv_tile_kernel_bf16(int H, int kind);
+KvTileKernel kv_tile_kernel_bf16_fp8(int H, int kind);
 
 constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;

@@ -347,7 +347,12 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-template <class T, bool FP8, int HD>
+// KIND: what the scores may hold besides q.k. Each kind's instance has less code,
+// which shows in these unrolled rows: without one for plain scores, 2 x 2048
+// float16 tokens took 152 us for 140 (a row of documents 142 for 129), without
+// the biased one 3 x 1531 tokens 59.5 us for 55.7. An instance for capped scores
+// alone did not: the compiler spills there (61 -> 81 us).
+template <class T, bool FP8, int HD, int KIND>
 __global__ void __launch_bounds__(kTileThreads, 1)
     kv_tile_kernel_t(const KvParams p, const __grid_constant__ KvTileMaps maps) {
   using C = TileCfg<FP8, HD>;
@@ -550,12 +555,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int first_pos = __reduce_min_sync(0xffffffffu, pos > 0x7fffffff ? 0x7fffffff : (int)pos);
     tr.slope = 0.0f;
     if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + (rem0 + tid) % G) * kLog2e;
-    const bool capped = p.cap > 0.0f;
+    const bool capped = KIND == kKvAnyScore && p.cap > 0.0f;
     float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
     if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid % (NT * kTileRows)];
     tr.mult = mult;
     tr.cap2 = p.cap * kLog2e;
-    const bool general = p.slopes || !(p.scale > 0.0f);
+    const bool general = KIND == kKvBiased || (KIND == kKvAnyScore && (p.slopes || !(p.scale > 0.0f)));
     float m = live ? -CUDART_INF_F : 0.0f, l = 0.0f, vref = 0.0f;  // rows behind the last never move the base
     if (t < live_tiles) {
       int step = 0;
@@ -955,11 +960,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
+template <class T, bool FP8, int HD>
+KvTileKernel kv_tile_of(int kind) {
+  const void* fn = kind == kKvPlain    ? (const void*)kv_tile_kernel_t<T, FP8, HD, kKvPlain>
+                   : kind == kKvBiased ? (const void*)kv_tile_kernel_t<T, FP8, HD, kKvBiased>
+                                       : (const void*)kv_tile_kernel_t<T, FP8, HD, kKvAnyScore>;
+  return {fn, TileCfg<FP8, HD>::kSmem};
+}
+
 template <class T, bool FP8>
-KvTileKernel kv_tile_pick(int H) {
-  if (H <= 64) return {(const void*)kv_tile_kernel_t<T, FP8, 64>, TileCfg<FP8, 64>::kSmem};
-  if (H <= 128) return {(const void*)kv_tile_kernel_t<T, FP8, 128>, TileCfg<FP8, 128>::kSmem};
-  return {(const void*)kv_tile_kernel_t<T, FP8, 256>, TileCfg<FP8, 256>::kSmem};
+KvTileKernel kv_tile_pick(int H, int kind) {
+  if (H <= 64) return kv_tile_of<T, FP8, 64>(kind);
+  if (H <= 128) return kv_tile_of<T, FP8, 128>(kind);
+  return kv_tile_of<T, FP8, 256>(kind);
 }
 
 }  // namespace rope_gb300
