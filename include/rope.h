@@ -519,7 +519,8 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
  * alibi_slopes  NULL or device float32 (num_heads).
  * document_ids  NULL or device int32 (B, max_cache_len), by cache row.
  * prefix_lens   NULL or device int32 (B).
- * out       device T (B, S, num_heads*H); must not overlap an input.
+ * out       device T (B, S, num_heads*H); must not overlap an input (the
+ *           same pointer as query or a cache is refused).
  * status_flags  NULL or the status word (bits 1 and 2).
  * workspace NULL or workspace_bytes of device memory, 16-byte aligned, any
  *           contents: where there are few rows the keys are split over more
@@ -546,7 +547,12 @@ rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t n
  * kv_attention_fp8 -- kv_attention over the caches that rope_apply_qkv_fp8
  * appends to: k_cache, v_cache hold e4m3 codes, k_scale, v_scale the scales
  * (powers of two, as written there) of each block of ROPE_KV_SCALE_BLOCK rows,
- * and key or value row j is code * scale. Everything else as kv_attention.
+ * and key or value row j is code * scale. Scales that are not powers of two are
+ * outside the contract; a scale none of whose rows is visible may hold anything.
+ * What is rounded to float16 is weight * (value scale / largest value scale that
+ * the row has met so far), the row's largest weight being about 1 or more: to
+ * within 2^-11, or to within 2^-25 where that is below 2^-14.
+ * Everything else as kv_attention.
  */
 rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,
                              int32_t kv_num_heads, int64_t head_size, const void* query,

@@ -252,6 +252,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   KV_TRY(check_optional(prefix_lens, "prefix_lens", 4));
   KV_TRY(check_optional(status_flags, "status_flags", 4));
   KV_TRY(check_optional(workspace, "workspace", 16));
+  if (out == query || out == k_cache || out == v_cache)
+    return fail(ROPE_ERR_INVALID_ARG, "out cannot alias query or a cache");
 
   const bool vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) &&
                    aligned(v_cache, 16) && aligned(out, 16);

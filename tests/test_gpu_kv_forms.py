@@ -127,18 +127,6 @@ def test_kernels_and_the_simt_variant(lib, cuda, fp8, shape, kernel):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("S", [1, 40])
-def test_output_over_the_query(lib, cuda, fp8, S):
-    """out may be the query itself: a row of Q is read before its output is written."""
-    a = _make(40, "f16", 2, S, 8, 2, 64, 3000, [2900, 100], fp8)
-    want, bound = _want(a, cuda)
-    q = a["q"].to(cuda)
-    got = _call(lib, dict(a, q=q), cuda, out=q)
-    assert got is q
-    ku.close(got, want, bound)
-
-
-@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("S", [1, 33])
 def test_no_rows(lib, cuda, fp8, S):
     """No sequences or no tokens: nothing is launched, nothing is written."""

@@ -73,6 +73,16 @@ def test_scales_are_checked(lib):
     assert _attend(so, True, vs=ODD) == INVALID
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_out_is_no_input(lib, fp8):
+    so = lib.load_library()
+    for name in ("q", "kc", "vc"):
+        at = dict(q=2 * A, kc=3 * A, vc=4 * A, out=A)
+        at[name] = A
+        assert _attend(so, fp8, **at) == INVALID
+        assert b"alias" in so.rope_last_error()
+
+
 def test_empty_calls_launch_nothing(lib):
     so = lib.load_library()
     for kw in (dict(B=0), dict(S=0)):
