@@ -77,8 +77,8 @@ def test_scales_are_checked(lib):
 def test_out_is_no_input(lib, fp8):
     so = lib.load_library()
     for name in ("q", "kc", "vc"):
-        at = dict(q=2 * A, kc=3 * A, vc=4 * A, out=A)
-        at[name] = A
+        at = {n: ctypes.c_void_p(0x20000 + 0x10000 * i) for i, n in enumerate(("q", "kc", "vc"))}
+        at.update({name: A, "out": A})
         assert _attend(so, fp8, **at) == INVALID
         assert b"alias" in so.rope_last_error()
 
