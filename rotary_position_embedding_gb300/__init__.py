@@ -464,9 +464,9 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _fits(t, dev, shape, dtype):
-    """Whether ``t`` is what ``_shaped`` asks for (that one says what is wrong)."""
-    return t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()
+def _fits(t, index, shape, dtype):
+    """Whether ``t`` is what ``_shaped`` asks for, on CUDA device ``index`` (that one says what is wrong)."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
 class _on:
@@ -476,32 +476,24 @@ class _on:
     def __init__(self, dev, stream):
         import torch
 
-        self.handle = (stream or torch.cuda.current_stream(dev)).cuda_stream
         self.was = [torch.cuda.device(dev)]
         if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream must be one of {dev}, got {stream}")
             self.was.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.was:
             c.__enter__()
-        return self.handle
 
     def __exit__(self, *exc):
         for c in reversed(self.was):
             c.__exit__(*exc)
 
 
-class _here:
-    """What ``_on`` gives where nothing has to change."""
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        pass
+def _elsewhere(torch, dev, stream):
+    """Whether a call has to change the current device or stream (see ``_on``)."""
+    return stream is not None or dev.index != torch._C._cuda_getDevice()
 
 
 _codes_of = {}
@@ -517,13 +509,6 @@ def _torch_code(T):
                           torch.bfloat16: (torch, ROPE_BF16)})
         code = _codes_of.get(T, (torch, _UNSUPPORTED_DTYPE))
     return code
-
-
-def _place(torch, dev, stream):
-    """Context of a launch on ``dev`` and ``stream`` (None: the current one); its value is the stream handle."""
-    if stream is None and dev.index == torch._C._cuda_getDevice():
-        return _here(torch._C._cuda_getCurrentRawStream(dev.index))
-    return _on(dev, stream)
 
 
 def kv_cache_fp8(batch, kv_num_heads, max_cache_len, head_size, device=None):
@@ -565,12 +550,12 @@ def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_he
     plane = (B, kv_num_heads, L, H)
     blocks = (B, kv_num_heads, -(-L // ROPE_KV_SCALE_BLOCK))
     table = (cos_cache.shape[0], (rotary_embedding_dim or H) // 2)
-    f32, kind = torch.float32, k_cache.dtype
-    if past_seq_lens is None or not (
-            _fits(past_seq_lens, dev, (B,), torch.int32) and _fits(k_cache, dev, plane, kind)
-            and _fits(v_cache, dev, plane, kind) and _fits(k_scale, dev, blocks, f32)
-            and _fits(v_scale, dev, blocks, f32) and _fits(cos_cache, dev, table, T) and _fits(sin_cache, dev, table, T)
-            and query.is_contiguous() and dev.type == "cuda" and kind.itemsize == 1):
+    f32, kind, at = torch.float32, k_cache.dtype, query.get_device()
+    if past_seq_lens is None or at < 0 or not (
+            _fits(past_seq_lens, at, (B,), torch.int32) and _fits(k_cache, at, plane, kind)
+            and _fits(v_cache, at, plane, kind) and _fits(k_scale, at, blocks, f32)
+            and _fits(v_scale, at, blocks, f32) and _fits(cos_cache, at, table, T) and _fits(sin_cache, at, table, T)
+            and query.is_contiguous()):
         codes = (torch.float8_e4m3fn, torch.uint8)
         _shaped("query", query, query, query.shape, T)
         _shaped("past_seq_lens", past_seq_lens, query, (B,), torch.int32)
@@ -594,15 +579,21 @@ def rope_apply_qkv_fp8(query, cos_cache, sin_cache, position_ids=None, *, num_he
         _shaped("q_out", q_out, query, (B, S, num_heads * H), T)
     if status is not None:
         _shaped("status", status, query, status.shape, torch.int32)
-    with _place(torch, dev, stream) as handle:
-        if q_out is None:
-            q_out = torch.empty((B, S, num_heads * H), dtype=T, device=dev)
-        st = lib.rope_apply_qkv_fp8(
-            code, B, S, num_heads, kv_num_heads, H, query.data_ptr(), _address(key), _address(value),
-            _address(q_norm_weight), _address(k_norm_weight), epsilon, cos_cache.data_ptr(), sin_cache.data_ptr(),
-            table[0], _address(position_ids), _address(past_seq_lens), int(interleaved), rotary_embedding_dim,
-            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), L,
-            _address(status), handle)
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return rope_apply_qkv_fp8(
+                query, cos_cache, sin_cache, position_ids, num_heads=num_heads, kv_num_heads=kv_num_heads,
+                k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, past_seq_lens=past_seq_lens,
+                key=key, value=value, interleaved=interleaved, rotary_embedding_dim=rotary_embedding_dim, q_out=q_out,
+                status=status, q_norm_weight=q_norm_weight, k_norm_weight=k_norm_weight, epsilon=epsilon)
+    if q_out is None:
+        q_out = torch.empty((B, S, num_heads * H), dtype=T, device=dev)
+    st = lib.rope_apply_qkv_fp8(
+        code, B, S, num_heads, kv_num_heads, H, query.data_ptr(), _address(key), _address(value),
+        _address(q_norm_weight), _address(k_norm_weight), epsilon, cos_cache.data_ptr(), sin_cache.data_ptr(),
+        table[0], _address(position_ids), _address(past_seq_lens), int(interleaved), rotary_embedding_dim,
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), L,
+        _address(status), torch._C._cuda_getCurrentRawStream(at))
     if st:
         _check("rope_apply_qkv_fp8", st)
     return q_out
@@ -632,7 +623,7 @@ def _workspace(lib, key):
 def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap, alibi_slopes,
                document_ids, prefix_lens, out, status, workspace, stream):
     lib = load_library()
-    T, dev, kind, plane = query.dtype, query.device, k_cache.dtype, k_cache.shape
+    T, dev, at, kind, plane = query.dtype, query.device, query.get_device(), k_cache.dtype, k_cache.shape
     torch, code = _torch_code(T)
     if query.dim() != 3 or len(plane) != 4:
         raise ValueError("query must be (B, S, num_heads*H) and k_cache (B, kv_num_heads, max_len, H)")
@@ -643,12 +634,12 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
     if scales is not None:
         ks, vs = scales
         blocks = (B, N, -(-L // ROPE_KV_SCALE_BLOCK))
-        _shaped("k_scale", ks, query, blocks, f32)
-        _shaped("v_scale", vs, query, blocks, f32)
-    if past_seq_lens is None or not (
-            hidden == num_heads * H and plane[0] == B and query.is_contiguous() and dev.type == "cuda"
-            and _fits(past_seq_lens, dev, (B,), i32) and _fits(k_cache, dev, plane, kind)
-            and _fits(v_cache, dev, plane, kind)):
+        if ks is None or vs is None or not (_fits(ks, at, blocks, f32) and _fits(vs, at, blocks, f32)):
+            _shaped("k_scale", ks, query, blocks, f32)
+            _shaped("v_scale", vs, query, blocks, f32)
+    if past_seq_lens is None or at < 0 or not (
+            hidden == num_heads * H and plane[0] == B and query.is_contiguous() and _fits(past_seq_lens, at, (B,), i32)
+            and _fits(k_cache, at, plane, kind) and _fits(v_cache, at, plane, kind)):
         _shaped("query", query, query, (B, S, num_heads * H), T)
         _shaped("k_cache", k_cache, query, (B, N, L, H), kind)
         _shaped("v_cache", v_cache, query, (B, N, L, H), kind)
@@ -669,25 +660,28 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
         _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
     if scale is None:
         scale = H ** -0.5
-    with _place(torch, dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(query)
-        if workspace is None:
-            need = _workspace(lib, (B, S, num_heads, N, H, L))
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        room = 0 if workspace is None else workspace.numel()
-        if scales is None:
-            st = lib.kv_attention(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
-                                  v_cache.data_ptr(), L, _address(past_seq_lens), scale, softcap,
-                                  _address(alibi_slopes), _address(document_ids), _address(prefix_lens),
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap,
+                              alibi_slopes, document_ids, prefix_lens, out, status, workspace, None)
+    if out is None:
+        out = torch.empty_like(query)
+    if workspace is None:
+        need = _workspace(lib, (B, S, num_heads, N, H, L))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    room = 0 if workspace is None else workspace.numel()
+    handle = torch._C._cuda_getCurrentRawStream(at)
+    if scales is None:
+        st = lib.kv_attention(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), L,
+                              _address(past_seq_lens), scale, softcap, _address(alibi_slopes), _address(document_ids),
+                              _address(prefix_lens), out.data_ptr(), _address(status), _address(workspace), room,
+                              handle)
+    else:
+        st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
+                                  v_cache.data_ptr(), _address(ks), _address(vs), L, _address(past_seq_lens), scale,
+                                  softcap, _address(alibi_slopes), _address(document_ids), _address(prefix_lens),
                                   out.data_ptr(), _address(status), _address(workspace), room, handle)
-        else:
-            st = lib.kv_attention_fp8(code, B, S, num_heads, N, H, query.data_ptr(), k_cache.data_ptr(),
-                                      v_cache.data_ptr(), _address(ks), _address(vs), L, _address(past_seq_lens),
-                                      scale, softcap, _address(alibi_slopes), _address(document_ids),
-                                      _address(prefix_lens), out.data_ptr(), _address(status), _address(workspace),
-                                      room, handle)
     if st:
         _check(name, st)
     return out
