@@ -180,11 +180,11 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
     }
     return pl;
   }
-  const int64_t rows = family == Family::kTile ? kv_tile_rows(H) : kKvSimpleRows;
+  const int64_t rows = family == Family::kTile ? kv_tile_rows(H) : kv_simple_rows(R);
   pl.tiles = (R + rows - 1) / rows;
   const int64_t ctas = pl.tiles * Nkv * B;
-  int64_t n = family == Family::kTile ? kSms / ctas : (2 * kSms + ctas - 1) / ctas;
-  const int64_t least = family == Family::kTile ? 512 : 256;
+  int64_t n = family == Family::kTile ? kSms / ctas : kv_simple_resident(H, R) * kSms / ctas;
+  const int64_t least = family == Family::kTile ? 512 : 128;
   if (n > (max_len + least - 1) / least) n = (max_len + least - 1) / least;
   if (n > 128) n = 128;
   pl.splits = n < 1 ? 1 : (int)n;
@@ -339,8 +339,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
     }
     set_last_kernel("kv_token_kernel");
   } else {
-    KV_TRY(launch(kv_simple_kernel(dtype, fp8), grid, kKvSimpleThreads, kv_simple_smem((int)head_size), stream, args,
-                  "kv_attention launch"));
+    const KvSimpleKernel k = kv_simple_kernel(dtype, fp8, (int)head_size, p.R);
+    KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention launch"));
     set_last_kernel("kv_simple_kernel");
   }
   if (pl.splits > 1) {

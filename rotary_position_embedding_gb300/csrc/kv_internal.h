@@ -50,8 +50,16 @@ struct KvParams {
 };
 
 // Kernel entry points for cudaLaunchKernel; each launch takes (KvParams).
-const void* kv_simple_kernel(int dtype, bool fp8);
-size_t kv_simple_smem(int H);
+struct KvSimpleKernel {
+  const void* fn;
+  size_t smem;
+};
+KvSimpleKernel kv_simple_kernel(int dtype, bool fp8, int H, int64_t R);
+constexpr int kv_simple_rows(int64_t R) { return R <= 16 ? 16 : 64; }  // of a CTA
+// CTAs an SM holds (shared memory; registers)
+constexpr int kv_simple_resident(int64_t H, int64_t R) {
+  return H <= 64 || (H <= 128 && R <= 16) ? 2 : 1;
+}
 const void* kv_combine_kernel(int dtype);
 
 // Few rows, 16-bit T, KvParams.vec: 8 rows of a (b, kvh) a CTA, or 16. Both
@@ -90,7 +98,7 @@ KvTileKernel kv_tile_kernel_f16_fp8(int H, int kind);
 KvTileKernel kv_tile_kernel_bf16(int H, int kind);
 KvTileKernel kv_tile_kernel_bf16_fp8(int H, int kind);
 
-constexpr int kKvSimpleRows = 32, kKvSimpleThreads = 256;
+constexpr int kKvSimpleThreads = 256;
 constexpr int kKvCombineThreads = 128;
 constexpr int kKvCombineWarpSplits = 8;  // up to so many splits a warp joins a row alone, above a CTA
 
