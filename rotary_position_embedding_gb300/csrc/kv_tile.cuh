@@ -28,6 +28,11 @@
 // bias), the maximum is taken before the cap, and where all of a warp's capped
 // scores have |y| <= 1/2, tanh(y) is a polynomial: 3 exponential-unit operations
 // a score become one.
+// Measured, a step of 128 keys and both row tiles at H = 128: 1.58 us (its MMAs
+// alone 1.22), biased 2.12, capped 2.47, over 8-bit caches 2.24, those capped 3.23;
+// 1.40 at H = 64, 0.94 for 64 keys and one row tile at H = 256. 4 x 2048 float16
+// tokens over up to 4095 keys, 32/8 heads, capped: 408 us, 0.36 of the measured
+// bfloat16 rate.
 // Shared memory: Q, two stages of K and two of V, each as slabs of 64 elements
 // (128-byte rows, 128-byte swizzle): the K-major form for Q and K, and the same
 // bytes read MN-major for V.
@@ -47,8 +52,9 @@
 // only where a tile's sum of weights passes 2^15: no maximum is taken otherwise
 // (half of the arithmetic that plain scores need). O is rescaled by its softmax
 // threads then, seldom after the first tile, so there is no correction warp. Keys
-// go from the last to the first: a bias by distance then only falls. The last key tile's rows behind the keys are
-// zeros. Key tiles whose documents no row of the CTA can have are left out.
+// go from the last to the first: a bias by distance then only falls. The last key
+// tile's rows behind the keys are zeros. Key tiles whose documents no row of the
+// CTA can have are left out.
 #pragma once
 
 #include "kv_careful.cuh"

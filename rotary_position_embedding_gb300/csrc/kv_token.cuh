@@ -29,6 +29,10 @@
 // log2), so weights stay below 2^8 (exact in float32, far from float16's end) and
 // the common unit costs one vote. P^T fragments come from S^T by movmatrix.
 //
+// Measured: 64 sequences of 1 to 8190 bfloat16 keys (8 heads of 128, 32 query heads)
+// 214 us with the joining, 5.0 TB/s; 256 of 1 to 4096 keys in 8 bits 225 us, 4.8 TB/s;
+// one of 131001 keys in 8 bits 69.7 us. The copy rate's floors are 158, 159 and 40 us.
+//
 // A value that no row sees is zeroed before the product. Where one that only
 // some rows see is not finite, its zero weight in the others would make a NaN
 // of it: the CTA then does its rows over again one by one (kv_careful_row).
