@@ -44,6 +44,7 @@ struct KvParams {
   int32_t deal;            // CTAs that the work is dealt to, or 0: one problem a CTA
   KvDiv by_g, by_tiles, by_problems;  // kv_token_kernel: by G, tiles, Nkv * tiles
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
+  int32_t cluster;         // kv_token_kernel: CTAs of a problem that meet in shared memory (0: see deal)
   int32_t tma;             // kv_tile_kernel: the tensor maps are there
   float scale;             // factor of q.k
   float cap;               // 0: no cap
@@ -71,6 +72,7 @@ struct KvTokenKernel {
   size_t smem;
 };
 constexpr int kKvTokenThreads = 128;
+constexpr int kKvClusterMost = 8;
 constexpr int kKvDealMost = 1024;  // sequences whose units a CTA adds up
 // CTAs that the work is dealt to: what is resident on 152 SMs (see TokenCfg).
 constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return 152 * (H > 128 || two ? 2 : fp8 ? 4 : 3); }

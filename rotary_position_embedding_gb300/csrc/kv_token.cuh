@@ -138,7 +138,31 @@ __device__ __forceinline__ float kv_row_shift(float amax, float* factor) {
 // the CTA begins and leaves unfinished, for kv_join_kernel. Without (no workspace, or more sequences than fit) a CTA
 // takes one problem. Equal splits of ragged sequences left some SMs with 1.25
 // times the mean's work.
+//
+// Few problems of caches that are not long (p.cluster CTAs a problem, a cluster):
+// each CTA takes its share of the problem's units, and the parts meet in the
+// CTAs' shared memory, so there is one launch and no workspace.
 constexpr int kTokUnit = 16 * kTokWarps;
+
+__device__ __forceinline__ void kv_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster of what is at `at` in this one.
+__device__ __forceinline__ uint32_t kv_cluster_at(uint32_t at, int rank) {
+  uint32_t y;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(at), "r"(rank));
+  return y;
+}
+__device__ __forceinline__ float4 kv_cluster_ld4(uint32_t at) {
+  float4 y;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(at) : "memory");
+  return y;
+}
+__device__ __forceinline__ float2 kv_cluster_ld2(uint32_t at) {
+  float2 y;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(at) : "memory");
+  return y;
+}
 
 struct TokenPlan {
   const int32_t* before;  // units of one problem of the sequences before b, for each b, and of all
@@ -238,6 +262,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
   extern __shared__ __align__(128) uint8_t kv_ring[];
   __shared__ float s_m[kTokWarps][NB * 8], s_l[kTokWarps][NB * 8];
   __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kTokWarps];
+  __shared__ float2 s_part[NB * 8];  // statistics of this CTA's part for its cluster
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
@@ -246,6 +271,9 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
   TokenPlan plan;
   int at_unit = 0, last_unit = 0;
   const bool dealt = p.deal > 0;
+  const int ranks = p.cluster, rank = ranks > 1 ? (int)blockIdx.x % ranks : 0;
+  constexpr int LD = HD + 4;  // of a row of O in shared memory
+  float* const so = reinterpret_cast<float*>(kv_ring);
   if (dealt) {
     plan = token_plan(p, s_before, s_sum);
     at_unit = plan.first(p, blockIdx.x);
@@ -293,7 +321,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
         p.ws_join[blockIdx.x] = make_int4(b, kvh, rows0, 2 * parts + (segment > 0 ? 1 : 0));
       }
     } else {
-      const int problem = blockIdx.x;
+      const int problem = ranks > 1 ? (int)blockIdx.x / ranks : (int)blockIdx.x;
       kvh = kv_div(problem, p.by_tiles);
       rows0 = (problem - kvh * p.tiles) * (NB * 8);
       b = (int)blockIdx.z + segment * (int)gridDim.z;
@@ -302,13 +330,20 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
     const KvSeq seq = kv_seq(p, b);
     if (kvh == 0 && rows0 == 0 && u0 == 0 && tid == 0) kv_flag_rows(p, seq);
     const int end = token_end(p, seq, (rows0 + NB * 8 < rows_all ? rows0 + NB * 8 : rows_all) - 1);
+    if (ranks > 1) {
+      const int units = (end + kTokUnit - 1) / kTokUnit;
+      u0 = (int)((int64_t)units * rank / ranks);
+      u1 = (int)((int64_t)units * (rank + 1) / ranks);
+      whole_problem = false;
+    }
     int lo = u0 * kTokUnit < end ? u0 * kTokUnit : end;
     int hi = u1 < 0 || u1 * kTokUnit > end ? end : u1 * kTokUnit;
     const int64_t plane = (int64_t)b * p.Nkv + kvh;
     // where a part of a problem goes
     const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
-    float* const part_o = whole_problem ? nullptr : p.ws_o + slot * (NB * 8) * p.H;
-    float2* const part_ml = whole_problem ? nullptr : p.ws_ml + slot * (NB * 8);
+    float* const part_o = whole_problem ? nullptr : ranks > 1 ? so : p.ws_o + slot * (NB * 8) * p.H;
+    float2* const part_ml = whole_problem ? nullptr : ranks > 1 ? s_part : p.ws_ml + slot * (NB * 8);
+    const int part_ld = ranks > 1 ? LD : p.H;
     const int HB = p.H * C::ES;  // bytes of a cache row
     const uint8_t* kbase = static_cast<const uint8_t*>(p.k) + plane * p.max_len * HB;
     const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + plane * p.max_len * HB;
@@ -627,14 +662,10 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
 #pragma unroll 1
       for (int r = warp; r < NB * 8; r += kTokWarps)
         if (rows0 + r < rows_all)
-          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + r, lo, hi, part_o ? part_o + r * p.H : nullptr,
+          kv_careful_row<T, FP8>(p, seq, b, kvh, rows0 + r, lo, hi, part_o ? part_o + r * part_ld : nullptr,
                                  part_ml + r, lane);
-      __syncthreads();
-      continue;
-    }
+    } else {
     // join the warps: their O (in units of 1) and statistics meet in shared memory
-    float* so = reinterpret_cast<float*>(kv_ring);
-    constexpr int LD = HD + 4;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -674,7 +705,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       }
       if (part_o) {
         if (d == 0) part_ml[r] = make_float2(M, L);
-        *reinterpret_cast<float4*>(part_o + r * p.H + d) = make_float4(o0, o1, o2, o3);
+        *reinterpret_cast<float4*>(part_o + r * part_ld + d) = make_float4(o0, o1, o2, o3);
       } else {
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         VecT<T, 4> y;
@@ -682,6 +713,35 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
         y.v[2] = Elem<T>::fromf(o2 * inv), y.v[3] = Elem<T>::fromf(o3 * inv);
         *reinterpret_cast<VecT<T, 4>*>(static_cast<bits*>(p.out) + row_of(row) + d) = y;
       }
+    }
+    }
+    if (ranks > 1) {
+      // the cluster's parts: each thread takes four dims of a row from all of them
+      kv_cluster_sync();
+      for (int i = rank * kKvTokenThreads + tid; i < NB * 8 * (HD / 4); i += ranks * kKvTokenThreads) {
+        const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
+        const int row = rows0 + r;
+        if (row >= rows_all || d >= p.H) continue;
+        const uint32_t at_ml = kv_smem(s_part + r), at_o = kv_smem(so + r * LD + d);
+        float M = -CUDART_INF_F;
+        for (int n = 0; n < ranks; ++n) M = fmaxf(M, kv_cluster_ld2(kv_cluster_at(at_ml, n)).x);
+        const float base = M == -CUDART_INF_F ? 0.0f : M;
+        float L = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+        for (int n = 0; n < ranks; ++n) {
+          const float2 ml = kv_cluster_ld2(kv_cluster_at(at_ml, n));
+          const float4 x = kv_cluster_ld4(kv_cluster_at(at_o, n));
+          if (ml.x == -CUDART_INF_F && ml.y == 0.0f) continue;
+          const float f = kv_exp2(ml.x - base);
+          L = fmaf(ml.y, f, L);
+          o0 = fmaf(x.x, f, o0), o1 = fmaf(x.y, f, o1), o2 = fmaf(x.z, f, o2), o3 = fmaf(x.w, f, o3);
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        VecT<T, 4> y;
+        y.v[0] = Elem<T>::fromf(o0 * inv), y.v[1] = Elem<T>::fromf(o1 * inv);
+        y.v[2] = Elem<T>::fromf(o2 * inv), y.v[3] = Elem<T>::fromf(o3 * inv);
+        *reinterpret_cast<VecT<T, 4>*>(static_cast<bits*>(p.out) + row_of(row) + d) = y;
+      }
+      kv_cluster_sync();  // no CTA leaves before its part has been read
     }
     __syncthreads();
   }
