@@ -161,6 +161,17 @@ struct Plan {
   int64_t split_bytes = 0;  // of one split, or of one CTA
 };
 
+// CTAs of a cluster that takes one problem of kToken, or 0. Few problems of short
+// caches need no second launch that way. One float16 sequence, 8 key/value heads of
+// 128: 778 keys 7.0 us, dealt out 12.7; 4000 keys 14.4 against 17.4; but 8000 keys
+// 23.3 against 18.9. In 8 bits 8000 keys 17.8 against 18.0; 7 such sequences 32.6
+// against 34.2.
+int token_cluster(bool fp8, int64_t problems, int64_t H, int64_t R, int64_t max_len) {
+  if (max_len <= 64 || max_len * (fp8 ? 1 : 2) > 8192 || problems * kKvClusterMost > kv_token_ctas(fp8, H, R > 8)) return 0;
+  const int n = pow2_at_least((max_len + 63) / 64);
+  return n < kKvClusterMost ? n : kKvClusterMost;
+}
+
 // Row tiles and splits from the sizes alone: the lengths are on the device.
 // kSimple and kTile split the keys where the row tiles leave SMs without a CTA;
 // kToken deals units of keys to as many CTAs as are resident.
@@ -175,15 +186,8 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
     // each is enough
     const int64_t problems = B * Nkv * pl.tiles;
     const int64_t units = (max_len + 63) / 64;
-    // Few problems of short caches go to a cluster each: no second launch. One float16
-    // sequence, 8 key/value heads of 128: 778 keys 7.0 us, dealt out 12.7; 4000 keys
-    // 14.4 against 17.4; but 8000 keys 23.3 against 18.9. In 8 bits 8000 keys 17.8
-    // against 18.0; 7 such sequences 32.6 against 34.2.
-    if (max_len > 64 && max_len * (fp8 ? 1 : 2) <= 8192 && problems * kKvClusterMost <= kv_token_ctas(fp8, H, rt == 16)) {
-      pl.cluster = pow2_at_least(units);
-      if (pl.cluster > kKvClusterMost) pl.cluster = kKvClusterMost;
-      return pl;
-    }
+    pl.cluster = token_cluster(fp8, problems, H, R, max_len);
+    if (pl.cluster) return pl;
     // Many more problems than CTAs even out by themselves (2048 problems of 1 to 4096
     // keys in 8 bits on 608 places: 225 us one a CTA, 233 us dealt).
     if (problems < 3 * kv_token_ctas(fp8, H, rt == 16) && B <= kKvDealMost && problems <= (1 << 20) && max_len > 64 && problems * units < (1ll << 31)) {
@@ -206,13 +210,23 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
   return pl;
 }
 
-// The matrix kernels take 16-bit types whose rows are 16-byte aligned; up to 16
-// rows of a (b, kvh) go to the one for few rows.
-Family choose_family(bool matrix, int64_t B, int64_t S, int64_t G, int64_t Nkv, int64_t H) {
+// The matrix kernels take 16-bit types whose rows are 16-byte aligned. Up to 16
+// rows of a (b, kvh) go to the one for few rows, and more where it has little to
+// read or reads codes that the other one has to widen: 20 to 64 rows, one sequence
+// of 1000 keys, 8 key/value heads of 128: 11 us against 16 (8 bits: 10 against 18; of
+// 8000 keys 27 against 20);
+// 32 rows, 8 sequences of 8000 keys in 8 bits 83 us against 131, 48 rows 113 (but one
+// such sequence 26 against 20, and in float16 8 of them 118 against 60).
+Family choose_family(bool matrix, bool fp8, int64_t B, int64_t S, int64_t G, int64_t Nkv, int64_t H, int64_t max_len) {
   if (!matrix || rope_get_variant() == ROPE_VARIANT_SIMT) return Family::kSimple;
   const int64_t R = S * G;
   const bool grid = B <= 65535 && (R + kv_tile_rows(H) - 1) / kv_tile_rows(H) <= 65535;
-  if (R > 16 && grid) return Family::kTile;
+  bool few = R <= 16;
+  if (!few && R <= 64 && B <= 65535) {  // B * Nkv * max_len stays below 2^62
+    few = (max_len <= 4096 && token_cluster(fp8, B * Nkv * ((R + 15) / 16), H, R, max_len) > 0) ||
+          (fp8 && H <= 128 && R <= 48 && B * Nkv * max_len >= (R <= 32 ? 1 << 18 : 1 << 19));
+  }
+  if (!few && grid) return Family::kTile;
   return R < ((int64_t)1 << 30) && Nkv * ((R + 7) / 8) <= INT32_MAX ? Family::kToken : Family::kSimple;
 }
 
@@ -270,8 +284,8 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
 
   const bool vec = head_size % (fp8 ? 16 : 16 / es) == 0 && aligned(query, 16) && aligned(k_cache, 16) &&
                    aligned(v_cache, 16) && aligned(out, 16);
-  const Family family = choose_family(vec && dtype != ROPE_F32, batch, seq, num_heads / kv_num_heads, kv_num_heads,
-                                      head_size);
+  const Family family = choose_family(vec && dtype != ROPE_F32, fp8, batch, seq, num_heads / kv_num_heads,
+                                      kv_num_heads, head_size, max_cache_len);
   Plan pl = plan_attention(family, fp8, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
   const int64_t fits =
       workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
@@ -379,8 +393,9 @@ int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, in
   if (batch == 0 || seq == 0) return 0;
   int64_t most = 0;
   // whichever kernel the types and alignments make the call take
-  for (Family f : {Family::kSimple, choose_family(true, batch, seq, num_heads / kv_num_heads, kv_num_heads, head_size)})
-    for (bool fp8 : {false, true}) {
+  for (bool fp8 : {false, true})
+    for (Family f : {Family::kSimple, choose_family(true, fp8, batch, seq, num_heads / kv_num_heads, kv_num_heads,
+                                                    head_size, max_cache_len)}) {
       const Plan pl = plan_attention(f, fp8, batch, seq, num_heads, kv_num_heads, head_size, max_cache_len);
       if (pl.bytes > most) most = pl.bytes;
     }

@@ -57,10 +57,36 @@ def test_wide_groups(lib, cuda, fp8, S, Nq, Nkv):
         assert lib.last_kernel() == "kv_tile_kernel"
 
 
+@pytest.mark.parametrize("S, L", [(5, 4200), (12, 8300)])
+def test_drafts_over_many_codes(lib, cuda, S, L):
+    """More than 16 rows that stay with the kernel for few: several row tiles of a head, dealt out."""
+    rng = np.random.default_rng(S)
+    past = rng.integers(0, L - S + 1, 8)
+    past[0], past[5] = L - S, 0
+    for dtype, extra in (("bf16", {}), ("f16", dict(cap=8.0, alibi=True, prefix=700))):
+        a = _make(42, dtype, 8, S, 32, 8, 64, L, past.tolist(), True, **extra)
+        _check(lib, a, cuda, dtype)
+        assert lib.last_kernel() == "kv_token_kernel"
+
+
 @pytest.mark.parametrize("fp8", [False, True])
-def test_documents_of_a_long_row(lib, cuda, fp8):
+@pytest.mark.parametrize("B, S, Nq, Nkv, H, L", [(1, 1, 8, 8, 128, 4096), (2, 9, 12, 2, 64, 1000), (3, 4, 16, 1, 96, 130),
+                                                 (1, 16, 4, 2, 256, 300), (1, 1, 16, 1, 128, 65)])
+def test_clusters(lib, cuda, fp8, B, S, Nq, Nkv, H, L):
+    """Few problems, each split over a cluster: shares of no unit, of one, of many; rows of several tiles."""
+    for past in (0, 1, 63, 64, 100, L - S):
+        past = min(past, L - S)
+        for extra in ({}, dict(cap=6.0, docs=3), dict(alibi=True, prefix=50)):
+            a = _make(43, "bf16", B, S, Nq, Nkv, H, L, [past] * (B - 1) + [0], fp8, **extra)
+            first = _check(lib, a, cuda, f"{past} {extra}")
+            assert lib.last_kernel() == "kv_token_kernel"
+            assert torch.equal(_call(lib, a, cuda, workspace=torch.empty(0, dtype=torch.uint8, device=cuda)), first)
+
+
+@pytest.mark.parametrize("fp8, S", [(False, 24), (True, 24), (True, 72)])
+def test_documents_of_a_long_row(lib, cuda, fp8, S):
     """More key tiles than a CTA lists documents of (4096 of 128 keys), with a workspace for splits and without."""
-    S, L = 24, 4096 * 128 + 3000
+    L = 4096 * 128 + 3000
     a = _make(35, "f16", 1, S, 1, 1, 16, L, [L - S - 5], fp8)
     j = np.arange(L)
     ids = (j // 1000) % 40
@@ -70,7 +96,7 @@ def test_documents_of_a_long_row(lib, cuda, fp8):
     for room in (None, 16):
         ws = None if room is None else torch.empty(room, dtype=torch.uint8, device=cuda)
         got = _call(lib, a, cuda, workspace=ws)
-        assert lib.last_kernel() == "kv_tile_kernel"
+        assert lib.last_kernel() == ("kv_token_kernel" if fp8 and S == 24 else "kv_tile_kernel")
         ku.close(got, want, bound, str(room))
 
 
@@ -111,8 +137,9 @@ def test_codes_as_bytes_and_as_floats(lib, cuda, shape):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("shape, kernel", [("token", "kv_token_kernel"), ("few_group", "kv_tile_kernel"),
-                                           ("prompt", "kv_tile_kernel"), ("scalar", "kv_simple_kernel")])
+@pytest.mark.parametrize("shape, kernel", [("token", "kv_token_kernel"), ("few_group", "kv_token_kernel"),
+                                           ("chunk_mha", "kv_tile_kernel"), ("prompt", "kv_tile_kernel"),
+                                           ("scalar", "kv_simple_kernel")])
 def test_kernels_and_the_simt_variant(lib, cuda, fp8, shape, kernel):
     """Which kernel a call takes, and that the plain one agrees."""
     B, S, Nq, Nkv, H, L, past = SHAPES[shape]
