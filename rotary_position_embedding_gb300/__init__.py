@@ -659,7 +659,7 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
     if workspace is not None:
         _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
     if scale is None:
-        scale = H ** -0.5
+        scale = max(H, 1) ** -0.5
     if _elsewhere(torch, dev, stream):
         with _on(dev, stream):
             return _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, scale, softcap,
