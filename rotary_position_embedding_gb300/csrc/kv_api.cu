@@ -190,7 +190,8 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
     if (pl.cluster) return pl;
     // Many more problems than CTAs even out by themselves (2048 problems of 1 to 4096
     // keys in 8 bits on 608 places: 225 us one a CTA, 233 us dealt).
-    if (problems < 3 * kv_token_ctas(fp8, H, rt == 16) && B <= kKvDealMost && problems <= (1 << 20) && max_len > 64 && problems * units < (1ll << 31)) {
+    if (problems < 3 * kv_token_ctas(fp8, H, rt == 16) && B <= kKvDealMost && max_len > 64 &&
+        problems * units < (1ll << 31)) {
       pl.deal = kv_token_ctas(fp8, H, rt == 16);
       if (pl.deal > problems * units) pl.deal = (int)(problems * units);
       pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;

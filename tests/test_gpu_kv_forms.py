@@ -216,3 +216,33 @@ def test_a_captured_step_that_moves_on(lib, cuda, dtype):
         assert torch.equal(one, two)
     for one, two in zip(outs[0][1:], outs[1][1:]):
         assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_rows_past_32_bits(lib, cuda, fp8):
+    """Prompts over caches of more than 2^31 elements, by the kernel for many rows and the plain one."""
+    B, N, H, L, S, n = 2, 4, 128, 2200000, 40, 300
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn((B, S, 8 * H), generator=g).to(torch.bfloat16).to(cuda)
+    past = torch.tensor([n - S, 100], dtype=torch.int32, device=cuda)
+    x = [torch.randn((B, N, n, H), generator=g) for _ in range(2)]
+    if fp8:
+        kc, vc, ks, vs = lib.kv_cache_fp8(B, N, L, H, cuda)
+        for c, y, s in ((kc, x[0], ks), (vc, x[1], vs)):
+            c.view(torch.uint8)[:, :, :n] = torch.from_numpy(ku.e4m3(y.numpy() * 100)).to(cuda)
+            s.fill_(2.0 ** -7)
+        call = lambda: lib.kv_attention_fp8(q, kc, vc, ks, vs, past, num_heads=8)  # noqa: E731
+        kd, vd = (torch.from_numpy(ku.values(c[:, :, :304].view(torch.uint8).cpu().numpy(), s[:, :, :19].cpu().numpy())).to(cuda)
+                  for c, s in ((kc, ks), (vc, vs)))
+    else:
+        kc, vc = (torch.empty((B, N, L, H), dtype=torch.bfloat16, device=cuda) for _ in range(2))
+        for c, y in ((kc, x[0]), (vc, x[1])):
+            c[:, :, :n] = y.to(torch.bfloat16).to(cuda)
+        call = lambda: lib.kv_attention(q, kc, vc, past, num_heads=8)  # noqa: E731
+        kd, vd = kc[:, :, :n].double(), vc[:, :, :n].double()
+    want, bound = ku.attention(q.double(), kd, vd, past.cpu().numpy(), 8, H ** -0.5, weight_eps=2.0 ** -11 if fp8 else 2.0 ** -8)
+    ku.close(call(), want, bound)
+    assert lib.last_kernel() == "kv_tile_kernel"
+    with lib.variant("simt"):
+        ku.close(call(), want, bound)
+        assert lib.last_kernel() == "kv_simple_kernel"
