@@ -549,9 +549,9 @@ rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t n
  * (powers of two, as written there) of each block of ROPE_KV_SCALE_BLOCK rows,
  * and key or value row j is code * scale. Scales that are not powers of two are
  * outside the contract; a scale none of whose rows is visible may hold anything.
- * What is rounded to float16 is weight * (value scale / largest value scale that
- * the row has met so far), the row's largest weight being about 1 or more: to
- * within 2^-11, or to within 2^-25 where that is below 2^-14.
+ * What is rounded to float16 is weight * (value scale / largest value scale so far
+ * among the blocks of which the row sees a key), the row's largest weight being
+ * about 1 or more: to within 2^-11, or to within 2^-25 where that is below 2^-14.
  * Everything else as kv_attention.
  */
 rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,

@@ -19,8 +19,10 @@
 //   be zeros, by cp.async.
 //   8-bit caches: the bringing warps load codes and write float16 (exact); the
 //   key scale of each 16 keys multiplies scores, the value scale weights,
-//   relative to the largest value scale so far (powers of two); bfloat16 Q rows
-//   become float16 after scaling by a power of two that the scores undo.
+//   relative to the largest value scale that the row has seen so far (powers of
+//   two); bfloat16 Q rows become float16 after scaling by a power of two that the
+//   scores undo. A block of 16 keys none of which a row sees has no part in that
+//   row's reference, whatever its scale: the weights there are 0.
 // A softmax thread holds its 128 scores in registers from one TMEM load on
 // (32 at a time, read twice, the loads' latency was two thirds of a step: 3.3 us
 // a step of both row tiles): hence 192 registers a softmax thread, 88 a bringing
@@ -298,12 +300,13 @@ __device__ __forceinline__ float tile_max(const float (&x)[N]) {
 }
 
 // Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
-// vs[16-column block] * vinv over 8-bit caches); their sum.
+// vs[16-column block] / vref over 8-bit caches); their sum.
 // MODE 0: score = x * mult; 1: capped by the polynomial, mult = scale / cap; 2:
 // capped; 3: x itself. MASKED: some x are hidden.
 template <bool FP8, bool BF, int MODE, bool MASKED, int N>
 __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
-                                              const float* vs, float vinv) {
+                                              const float* vs, float vref) {
+  const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;  // 2^127 for vref = 0
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   float2 k0, k1, k2, k3;  // cap * tanh(mult * x) = x (k0 + x^2 (k1 + x^2 (k2 + x^2 k3)))
   if constexpr (MODE == 1) {
@@ -320,7 +323,8 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float2 fv = make_float2(1.0f, 1.0f);
-      if constexpr (FP8) fv.x = fv.y = vs[2 * q + h] * vinv;
+      // at most the reference: a larger one is of a block that the row does not see
+      if constexpr (FP8) fv.x = fv.y = fminf(vs[2 * q + h], vref) * vinv;
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
         const int i = 32 * q + 16 * h + k;
@@ -602,25 +606,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int i = 0; i < N; ++i) x[i] = __uint_as_float(c[i]);
         }
+        const float mag = general ? tile_scores<FP8, true, N>(x, tr, capped) : tile_scores<FP8, false, N>(x, tr, capped);
+        const bool masked = tr.part || tr.look;
         bool grown = false;
         float vmax = 0.0f;
         if constexpr (FP8) {
 #pragma unroll
           for (int i = 0; i < NB; ++i) vmax = fmaxf(vmax, vs[i]);
-          grown = vmax > vref;
+          grown = __any_sync(0xffffffffu, vmax > vref);
+          if (grown && masked) {  // what counts are the blocks that the row sees something of
+            vmax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              float top = x[16 * i];
+#pragma unroll
+              for (int k = 1; k < 16; ++k) top = fmaxf(top, x[16 * i + k]);
+              if (top != -CUDART_INF_F) vmax = fmaxf(vmax, vs[i]);
+            }
+          }
         }
-        const float mag = general ? tile_scores<FP8, true, N>(x, tr, capped) : tile_scores<FP8, false, N>(x, tr, capped);
-        const bool masked = tr.part || tr.look;
         // 2 log2(e) |y| with |y| <= 1/2; the last keeps the polynomial's powers finite
         const bool small = capped && !general && __all_sync(0xffffffffu, mag * mult <= kLog2e && mult < 1e4f);
         auto weights = [&]() {
           const float nb = m == -CUDART_INF_F ? 0.0f : -m;
-          const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
-          if (general) return tile_weights<FP8, BF, 3, false, N>(x, ts, tr, 1.0f, nb, vs, vinv);
-          if (!capped) return tile_weights<FP8, BF, 0, false, N>(x, ts, tr, mult, nb, vs, vinv);
-          if (masked) return tile_weights<FP8, BF, 2, true, N>(x, ts, tr, mult, nb, vs, vinv);
-          if (!small) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, mult, nb, vs, vinv);
-          return tile_weights<FP8, BF, 1, false, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vinv);
+          if (general) return tile_weights<FP8, BF, 3, false, N>(x, ts, tr, 1.0f, nb, vs, vref);
+          if (!capped) return tile_weights<FP8, BF, 0, false, N>(x, ts, tr, mult, nb, vs, vref);
+          if (masked) return tile_weights<FP8, BF, 2, true, N>(x, ts, tr, mult, nb, vs, vref);
+          if (!small) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, mult, nb, vs, vref);
+          return tile_weights<FP8, BF, 1, false, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
         };
         // Weights by the base so far, where every row has one; only where a row's sum
         // says that one may be too large (2^15 fits float16) is the maximum taken, the
@@ -639,7 +652,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           m = mn;
           l *= a;
           if constexpr (FP8) {
-            if (grown) {
+            if (vmax > vref) {
               a *= vref * __uint_as_float((254u << 23) - __float_as_uint(vmax));  // old / new, powers of two
               vref = vmax;
             }
@@ -857,7 +870,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int blk = me % NB;
         const float* s = me < NB ? p.ks : p.vs;
         float f = j0 + blk * 16 < hi ? __ldg(s + plane * p.nblk + j0 / kKvBlock + blk) : 0.0f;
-        if (!(f < CUDART_INF_F)) f = 0.0f;
+        if (!(f >= 0.0f && f < CUDART_INF_F)) f = 0.0f;  // of a block that no row sees
         reinterpret_cast<float*>(in + N * 4)[me] = f;
       }
       mbar_arrive(bar(&bars.info[step & 3]));

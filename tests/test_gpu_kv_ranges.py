@@ -1,0 +1,64 @@
+"""Attention over the caches on the GPU where numbers are far apart: value scales of blocks that a row does not
+see, caps of every size, infinite keys under a cap, small queries over large keys."""
+
+import pytest
+import torch
+
+import kv_util as ku
+from test_gpu_kv import _call, _make, _want
+
+pytestmark = pytest.mark.gpu
+
+# finite scales that no append writes: far too large, far too small, between powers of two, negative
+WILD = [2.0 ** 30, 1e30, 3.7e20, 2.0 ** 126, 3.4e38, 1e-40, 0.0, -1.0, -2.5e33, 1234.5]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S, G", [(1, 4), (5, 4), (5, 2), (100, 4), (300, 1)])
+@pytest.mark.parametrize("H", [64, 128, 256])
+@pytest.mark.parametrize("cap", [0.0, 6.0])
+def test_scales_that_no_row_sees(lib, cuda, dtype, S, G, H, cap):
+    """A padded front and a hole between documents, whose blocks' scales hold anything finite."""
+    B, N, L = 2, 2, 700
+    past = [L - S - 40, 333]
+    a = _make(51, dtype, B, S, G * N, N, H, L, past, True, cap=cap)
+    ids = torch.zeros((B, L), dtype=torch.int32)
+    ids[:, :48], ids[:, 160:208], ids[0, 272:288] = 7, 8, 9
+    a["docs"] = ids
+    want, bound = _want(a, cuda)
+    ku.close(_call(lib, a, cuda), want, bound)
+    hidden = [n for n in range(-(-L // 16)) if bool((ids[0, 16 * n:16 * n + 16] != 0).all())]
+    for turn in range(2):
+        for name in ("ks", "vs"):
+            for n, blk in enumerate(hidden):
+                a[name][0, :, blk] = WILD[(n + 3 * turn) % len(WILD)]
+                if blk != 17:  # the second sequence has no third hole
+                    a[name][1, :, blk] = WILD[(n + 3 * turn + 5) % len(WILD)]
+        ku.close(_call(lib, a, cuda), want, bound, f"turn {turn}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S, G", [(5, 4), (5, 1), (40, 2), (150, 4), (300, 1)])
+@pytest.mark.parametrize("up", [20, 30, 60])
+def test_value_scales_ahead_of_a_query(lib, cuda, dtype, S, G, up):
+    """Blocks of later tokens, of another document and behind a prefix have scales 2^up larger: rows that do not
+    see them keep their accuracy."""
+    B, N, H, L = 2, 2, 64, 500
+    past = [L - S - 3, 100 - S % 16 + 14]  # drafts that begin in one block and end in the next
+    for extra in ({}, dict(alibi=True), dict(prefix=30), dict(docs=3)):
+        a = _make(52, dtype, B, S, G * N, N, H, L, past, True, **extra)
+        if extra.get("docs"):
+            ids = torch.zeros((B, L), dtype=torch.int32)
+            ids[:, 64:128] = 3
+            for b in range(B):
+                ids[b, past[b] + S // 2:] = 4  # half of the rows see only each other
+            a["docs"] = ids
+            a["vs"][:, :, 4:8] *= 2.0 ** up
+            a["vs"][:, 0] = torch.where(torch.arange(a["vs"].shape[2]) < 4, 1.0, 2.0 ** -40) * a["vs"][:, 0]
+        for b in range(B):
+            last = (past[b] + S - 1) // 16
+            first = max(past[b] // 16 + 1, last - 3)
+            a["vs"][b, :, first:last + 1] *= 2.0 ** up
+        want, bound = _want(a, cuda)
+        keep = want.abs() + bound < (3e4 if dtype == "f16" else 1e38)  # what the output's type holds
+        ku.close(_call(lib, a, cuda)[keep], want[keep], bound[keep], str(extra))
