@@ -21,8 +21,8 @@
 //      two tokens' words are interleaved in registers into V^T fragments.
 // 8-bit caches: codes become float16 exactly on the way into the fragments; the
 // key scale of a unit (a block of 16 rows has one) multiplies its scores, the
-// value scale its weights, relative to the largest seen so far (a power of two,
-// so nothing is rounded). Q is float16 too, for bfloat16 after scaling each row
+// value scale its weights, relative to the largest that the row has seen so far (a
+// power of two, so nothing is rounded). Q is float16 too, for bfloat16 after scaling each row
 // by a power of two; the scores undo it.
 //
 // Softmax: the running maximum moves only where a score passes it by 8 (in
@@ -62,6 +62,9 @@ __device__ __forceinline__ float kv_rcp(float x) {
 // tanh(y) = 1 - 2 / (1 + e^(2y)) from y2 = 2 * log2(e) * y. Absolute error a
 // few 2^-24 (the score needs an absolute one: it goes into an exponent).
 __device__ __forceinline__ float kv_tanh_of(float y2) { return fmaf(-2.0f, kv_rcp(1.0f + kv_exp2(y2)), 1.0f); }
+
+// 1 / s for s = 2^e, -126 <= e <= 126, exactly; 0 and 2^127 become each other.
+__device__ __forceinline__ float kv_pow2_over(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 template <bool BF16>
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -480,7 +483,9 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
-    float vref = 0.0f;  // O is held in units of this value scale
+    float vinv[NB][2];  // one over the row's largest value scale so far, in whose units O is held
+#pragma unroll
+    for (int n = 0; n < NB; ++n) vinv[n][0] = vinv[n][1] = 0x1p127f;  // 0: none seen
     bool odd = false;   // an infinity or a NaN in a value that not every row sees
 
     int stage = 0, next = C::kStages - 1;
@@ -534,6 +539,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       if (dbase) d0 = reinterpret_cast<const int*>(meta)[g], d1 = reinterpret_cast<const int*>(meta)[g + 8];
       bool seen0 = false, seen1 = false;
       bool moved = false;
+      uint32_t larger = 0;  // rows whose value scale grows here
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -555,6 +561,9 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
             y = d ? y : -CUDART_INF_F;
             seen0 |= a;
             seen1 |= d;
+            if (FP8 && (__ballot_sync(0xffffffffu, a || d) >> c & 0x11111111u) && vs * vinv[n][e] > 1.0f) larger |= 1u << (2 * n + e);
+          } else if (FP8 && vs * vinv[n][e] > 1.0f) {
+            larger |= 1u << (2 * n + e);
           }
           s[n][e] = x;
           s[n][2 + e] = y;
@@ -565,13 +574,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
         any1 = __ballot_sync(0xffffffffu, seen1);
       }
       if (any0 | any1) {  // a unit that no row sees is left out
-        const bool grown = FP8 && vs > vref;
-        if (__any_sync(0xffffffffu, moved) || grown) {
-          float fv = 1.0f;
-          if (grown) {
-            fv = vref * __uint_as_float((254u << 23) - __float_as_uint(vs));  // old / new, powers of two
-            vref = vs;
-          }
+        if (__any_sync(0xffffffffu, moved || larger)) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -583,14 +586,19 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
               const float a = x == -CUDART_INF_F ? 1.0f : kv_exp2(m[n][e] - x);
               m[n][e] = x;
               l[n][e] *= a;
+              float f = a;
+              if (FP8 && (larger >> (2 * n + e) & 1u)) {
+                const float inv = kv_pow2_over(vs);
+                f *= kv_pow2_over(vinv[n][e]) * inv;  // old / new
+                vinv[n][e] = inv;
+              }
 #pragma unroll
               for (int t = 0; t < OT; ++t) {
-                acc[t][n][e] *= a * fv;
-                acc[t][n][2 + e] *= a * fv;
+                acc[t][n][e] *= f;
+                acc[t][n][2 + e] *= f;
               }
             }
         }
-        const float fp = FP8 ? vs * __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;
         uint32_t pf[NB][2];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -601,8 +609,12 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
             w[e] = kv_exp2(s[n][e] - base);
             w[2 + e] = kv_exp2(s[n][2 + e] - base);
             l[n][e] += w[e] + w[2 + e];
+            if constexpr (FP8) {  // (a scale above the row's is of a unit that it does not see)
+              const float fp = fminf(vs * vinv[n][e], 1.0f);
+              w[e] *= fp;
+              w[2 + e] *= fp;
+            }
           }
-          if constexpr (FP8) w[0] *= fp, w[1] *= fp, w[2] *= fp, w[3] *= fp;
           pf[n][0] = kv_transpose8(kv_pack2<BF>(w[0], w[1]));
           pf[n][1] = kv_transpose8(kv_pack2<BF>(w[2], w[3]));
         }
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
         const int r = n * 8 + 2 * c + e;
         if (g == 0) s_m[warp][r] = m[n][e], s_l[warp][r] = sum;
         float* o = so + (warp * NB * 8 + r) * LD;
-        const float f = FP8 ? vref : 1.0f;
+        const float f = FP8 ? kv_pow2_over(vinv[n][e]) : 1.0f;
 #pragma unroll
         for (int t = 0; t < OT; ++t) {
           // tile t: dims piece(t / (VD / 2)) + g * VD + 2 * (t % (VD / 2)) and the next

@@ -62,3 +62,23 @@ def test_value_scales_ahead_of_a_query(lib, cuda, dtype, S, G, up):
         want, bound = _want(a, cuda)
         keep = want.abs() + bound < (3e4 if dtype == "f16" else 1e38)  # what the output's type holds
         ku.close(_call(lib, a, cuda)[keep], want[keep], bound[keep], str(extra))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S, G", [(2, 4), (4, 4), (3, 4), (100, 1)])
+@pytest.mark.parametrize("up", [20, 30, 60])
+def test_value_scales_of_another_rows_document(lib, cuda, dtype, S, G, up):
+    """Two documents in turns along the cache, the second one's value scales 2^up larger; tokens of either."""
+    N, H, L = 2, 64, 8200
+    past = L - S - 60
+    a = _make(57, dtype, 1, S, G * N, N, H, L, [past], True)
+    ids = (torch.arange(L) // 64 % 4 == 1).int() * 4
+    ids[past:] = torch.arange(L - past) % 2 * 4
+    a["docs"] = ids[None].int()
+    second = (ids[::16] == 4) & (torch.arange(0, L, 16) + 16 <= past)
+    a["vs"] = torch.where(second, 2.0 ** up, 1.0) * a["vs"]
+    want, bound = _want(a, cuda)
+    keep = want.abs() + bound < (3e4 if dtype == "f16" else 1e38)
+    for room in (None, 0):
+        ws = None if room is None else torch.empty(room, dtype=torch.uint8, device=cuda)
+        ku.close(_call(lib, a, cuda, workspace=ws)[keep], want[keep], bound[keep], str(room))
