@@ -212,6 +212,7 @@ __device__ __forceinline__ void tile_tma(uint32_t dst, const CUtensorMap* map, i
 
 // What a softmax thread knows of its row, and the tile it is at.
 struct TileRow {
+  float unit;                   // of a bfloat16 Q row over 8-bit keys, see kv_row_shift
   float mult, slope, cap2;      // score factor; bias and cap in log2
   bool ahead;                   // some key of the tile is ahead of some row of the warp
   float dist;                   // the row's position less the tile's first key
@@ -231,18 +232,21 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
   if constexpr (FP8) {
 #pragma unroll
     for (int h = 0; h < N / 16; ++h) {
-      const float f = r.ks[h] * (GENERAL ? r.mult : 1.0f);
+      // to q.k first: queries may be as small as keys are large
+      const float f = fminf(r.ks[h] * r.unit, FLT_MAX);
 #pragma unroll
       for (int k = 16 * h; k < 16 * h + 16; k += 2) {
         const float2 y = __fmul2_rn(make_float2(x[k], x[k + 1]), make_float2(f, f));
         x[k] = y.x, x[k + 1] = y.y;
       }
     }
-  } else if constexpr (GENERAL) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] *= r.mult;
   }
   if constexpr (GENERAL) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(r.mult, r.mult));
+      x[i] = y.x, x[i + 1] = y.y;
+    }
     if (capped) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = kv_tanh_of(x[i]) * r.cap2;
@@ -566,8 +570,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tr.slope = 0.0f;
     if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + (rem0 + tid) % G) * kLog2e;
     const bool capped = KIND == kKvAnyScore && p.cap > 0.0f;
-    float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
-    if constexpr (FP8 && kIsBf16<T>) mult *= undo[tid % (NT * kTileRows)];
+    const float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    tr.unit = FP8 && kIsBf16<T> ? undo[tid % (NT * kTileRows)] : 1.0f;
     tr.mult = mult;
     tr.cap2 = p.cap * kLog2e;
     const bool general = KIND == kKvBiased || (KIND == kKvAnyScore && (p.slopes || !(p.scale > 0.0f)));

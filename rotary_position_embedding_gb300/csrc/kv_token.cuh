@@ -38,6 +38,8 @@
 // of it: the CTA then does its rows over again one by one (kv_careful_row).
 #pragma once
 
+#include <cfloat>
+
 #include "kv_careful.cuh"
 
 namespace rope_gb300 {
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
     }
 
     // the rows whose scores this lane holds: 2c and 2c + 1 of each column tile
-    float mult[NB][2], slope[NB][2], m[NB][2], l[NB][2];
+    float unit[NB][2], slope[NB][2], m[NB][2], l[NB][2];  // unit: of bfloat16 Q rows, see kv_row_shift
     int64_t pos[NB][2];
     int lim[NB][2], doc[NB][2];
     const float c1 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
         const int r = rows0 + n * 8 + 2 * c + e;
         const bool live = r < rows_all;
         const int tok = live ? kv_div(r, p.by_g) : 0;
-        mult[n][e] = c1 * __shfl_sync(0xffffffffu, undo[n], 4 * (2 * c + e));
+        unit[n][e] = __shfl_sync(0xffffffffu, undo[n], 4 * (2 * c + e));
         pos[n][e] = seq.past + tok;
         int64_t k = live ? kv_limit(seq, pos[n][e]) : 0;
         doc[n][e] = 0;
@@ -544,7 +546,12 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = s[n][e] * (mult[n][e] * ks), y = s[n][2 + e] * (mult[n][e] * ks);
+          float x = s[n][e], y = s[n][2 + e];
+          if constexpr (FP8) {  // to q.k first: queries may be as small as keys are large
+            const float f = kIsBf16<T> ? fminf(unit[n][e] * ks, FLT_MAX) : ks;
+            x *= f, y *= f;
+          }
+          x *= c1, y *= c1;
           if (p.cap > 0.0f) {
             x = kv_tanh_of(x) * c2;
             y = kv_tanh_of(y) * c2;

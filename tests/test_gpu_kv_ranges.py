@@ -82,3 +82,17 @@ def test_value_scales_of_another_rows_document(lib, cuda, dtype, S, G, up):
     for room in (None, 0):
         ws = None if room is None else torch.empty(room, dtype=torch.uint8, device=cuda)
         ku.close(_call(lib, a, cuda, workspace=ws)[keep], want[keep], bound[keep], str(room))
+
+
+@pytest.mark.parametrize("S", [1, 6, 70])
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+@pytest.mark.parametrize("down", [60, 100, 118])
+def test_small_queries_over_large_keys(lib, cuda, S, cap, down):
+    """bfloat16 queries near 2^-down over 8-bit keys near 2^down: the scores are a few units. And the other way."""
+    for sign in (-1, 1):
+        e = down if sign < 0 else min(down, 110)  # scales are 2^-120 at least
+        a = _make(56, "bf16", 1, S, 8, 2, 64, 300, [300 - S], True, cap=cap)
+        a["q"] = (a["q"].float() * 2.0 ** (sign * e)).to(torch.bfloat16)
+        a["ks"] = a["ks"] * 2.0 ** (-sign * e)
+        want, bound = _want(a, cuda, 0.3)
+        ku.close(_call(lib, a, cuda, scale=0.3), want, bound, str(sign))
