@@ -273,6 +273,10 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
     }
     mag = fmaxf(a0, a1);
   }
+  if (!GENERAL && capped && (r.part || r.look)) {  // -inf is for what is hidden
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = x[i] == -CUDART_INF_F ? -FLT_MAX : x[i];
+  }
   if (r.part) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = i < r.limit ? x[i] : -CUDART_INF_F;
@@ -345,7 +349,7 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
             const float2 t = __fmul2_rn(y, mul);
             y = __ffma2_rn(make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y)), c2, nb);
           }
-          if constexpr (MASKED) {  // a hidden score is -inf, not the cap's end
+          if constexpr (MASKED) {  // a hidden score is -inf, not the cap's end (nor is a seen one: tile_scores)
             y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
             y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
           }
@@ -649,8 +653,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           move = __any_sync(0xffffffffu, !(sum <= 32768.0f));
         }
         if (move) {
-          float mx = tile_max(x) * (general ? 1.0f : mult);
-          if (capped && !general) mx = mx == -CUDART_INF_F ? mx : kv_tanh_of(mx) * tr.cap2;
+          const float top = tile_max(x);
+          float mx = top * (general ? 1.0f : mult);
+          if (capped && !general) mx = masked && top == -CUDART_INF_F ? top : kv_tanh_of(mx) * tr.cap2;
           const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
           m = mn;

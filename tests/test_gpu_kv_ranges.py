@@ -84,6 +84,30 @@ def test_value_scales_of_another_rows_document(lib, cuda, dtype, S, G, up):
         ku.close(_call(lib, a, cuda, workspace=ws)[keep], want[keep], bound[keep], str(room))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S", [1, 6, 40, 130])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_infinite_keys_under_a_cap(lib, cuda, dtype, S, alibi):
+    """A visible key whose product with the query is -inf scores -softcap wherever it lies: in a key tile that
+    is partly hidden, in a whole tile, in a tile of nothing else; hidden ones stay hidden."""
+    L = 420
+    for bad in ([3], [3, 60, 130, 131, 390], list(range(128)), list(range(100, 280)), list(range(L))):
+        a = _make(55, dtype, 1, S, 2, 1, 64, L, [L - S - 5], False, cap=2.0, alibi=alibi)
+        a["q"] = a["q"].abs() + 0.1
+        b = dict(a, k=a["k"].clone())
+        b["k"][0, 0, bad] = -64.0  # a product far below -softcap
+        want, bound = _want(b, cuda)
+        a["k"][0, 0, bad] = float("-inf")
+        ku.close(_call(lib, a, cuda), want, bound, f"{len(bad)} keys")
+        docs = torch.zeros((1, L), dtype=torch.int32)
+        docs[0, bad[:len(bad) // 2]] = 1
+        docs[0, L - S - 5:] = 0
+        for x in (a, b):
+            x["docs"] = docs
+        want, bound = _want(b, cuda)
+        ku.close(_call(lib, a, cuda), want, bound, f"{len(bad)} keys, documents")
+
+
 @pytest.mark.parametrize("S", [1, 6, 70])
 @pytest.mark.parametrize("cap", [0.0, 3.0])
 @pytest.mark.parametrize("down", [60, 100, 118])
