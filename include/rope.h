@@ -515,7 +515,8 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
  * past_seq_lens device int32 (B). A query whose row i is outside the cache sets
  *           status bit 2; it sees the rows that its formula says (with
  *           documents: none).
- * scale     finite; usually 1 / sqrt(H). softcap finite, >= 0; 0: no cap.
+ * scale     at most 2^100 in magnitude; usually 1 / sqrt(H). softcap finite, >= 0;
+ *           0: no cap; above 2^112 it counts as 2^112.
  * alibi_slopes  NULL or device float32 (num_heads).
  * document_ids  NULL or device int32 (B, max_cache_len), by cache row.
  * prefix_lens   NULL or device int32 (B).

@@ -260,7 +260,7 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   set_last_error("");
   KV_TRY(check_dtype(dtype));
   KV_TRY(check_attention_sizes(batch, seq, num_heads, kv_num_heads, head_size, max_cache_len));
-  if (!std::isfinite(scale)) return fail(ROPE_ERR_INVALID_ARG, "scale must be finite");
+  if (!(std::fabs(scale) <= 0x1p100f)) return fail(ROPE_ERR_INVALID_ARG, "scale must be finite, at most 2^100 in magnitude");
   if (!(softcap >= 0.0f && softcap < INFINITY))
     return fail(ROPE_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
   if (workspace_bytes < 0) return fail(ROPE_ERR_INVALID_ARG, "workspace_bytes is negative");
@@ -334,7 +334,12 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   }
   p.vec = vec;
   p.scale = scale;
-  p.cap = softcap;
+  // A cap above 2^112 is as good as 2^112 (a score below 2^100 is capped by less than
+  // 2^-24 of it) and keeps scale / cap a normal number and cap * log2(e) finite. A
+  // steepness above 2^125 would be infinite with the kernels' factor, and 0 times it
+  // NaN; as |scale| <= 2^100, it comes with a cap, and scores, below 2^-25.
+  p.cap = fminf(softcap, 0x1p112f);
+  p.over = softcap > 0.0f ? fminf(fmaxf(scale / p.cap, -0x1p125f), 0x1p125f) : 0.0f;
 
   void* args[] = {&p};
   const int64_t gx = family == Family::kToken ? pl.tiles * kv_num_heads : pl.tiles * pl.splits;

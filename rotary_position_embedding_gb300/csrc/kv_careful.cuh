@@ -23,7 +23,7 @@ __device__ __noinline__ void kv_careful_row(const KvParams& p, const KvSeq& seq,
   if (p.docs && !kv_document(p, b, pos, &doc)) lim = 0;
   if (hi < lim) lim = hi;
   const float slope = p.slopes ? __ldg(p.slopes + kvh * p.G + row % p.G) * kLog2e : 0.0f;
-  const float c1 = p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e;
+  const float c1 = p.cap > 0.0f ? p.over : p.scale * kLog2e;
   const float c2 = p.cap * kLog2e;
   auto value = [&](const void* base, const float* scales, int64_t j, int d) -> float {
     const int64_t e = (plane * p.max_len + j) * p.H + d;

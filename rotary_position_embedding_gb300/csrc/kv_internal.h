@@ -48,6 +48,7 @@ struct KvParams {
   int32_t tma;             // kv_tile_kernel: the tensor maps are there
   float scale;             // factor of q.k
   float cap;               // 0: no cap
+  float over;              // scale / cap
 };
 
 // Kernel entry points for cudaLaunchKernel; each launch takes (KvParams).

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kKvSimpleThreads, NJ < 4 ? 2 : 1) kv_simple_ke
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[a][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    const float c1 = p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e;
+    const float c1 = p.cap > 0.0f ? p.over : p.scale * kLog2e;
     const float c2 = p.cap * kLog2e;
     const int32_t* docs = p.docs ? p.docs + (int64_t)b * p.max_len : nullptr;
     for (int64_t j0 = lo; j0 < hi; j0 += kSimpleCols) {

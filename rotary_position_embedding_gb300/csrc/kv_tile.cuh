@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tr.slope = 0.0f;
     if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + (rem0 + tid) % G) * kLog2e;
     const bool capped = KIND == kKvAnyScore && p.cap > 0.0f;
-    const float mult = capped ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    const float mult = capped ? 2.0f * kLog2e * p.over : p.scale * kLog2e;
     tr.unit = FP8 && kIsBf16<T> ? undo[tid % (NT * kTileRows)] : 1.0f;
     tr.mult = mult;
     tr.cap2 = p.cap * kLog2e;

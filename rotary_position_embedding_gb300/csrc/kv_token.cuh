@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kKvTokenThreads, TokenCfg<T, FP8, HD, NB>::kCt
     float unit[NB][2], slope[NB][2], m[NB][2], l[NB][2];  // unit: of bfloat16 Q rows, see kv_row_shift
     int64_t pos[NB][2];
     int lim[NB][2], doc[NB][2];
-    const float c1 = p.cap > 0.0f ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    const float c1 = p.cap > 0.0f ? 2.0f * kLog2e * p.over : p.scale * kLog2e;
     const float c2 = p.cap * kLog2e;
     int full = 0x7fffffff;  // keys below this are seen by every row
 #pragma unroll

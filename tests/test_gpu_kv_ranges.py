@@ -84,6 +84,37 @@ def test_value_scales_of_another_rows_document(lib, cuda, dtype, S, G, up):
         ku.close(_call(lib, a, cuda, workspace=ws)[keep], want[keep], bound[keep], str(room))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S", [1, 6, 70])
+@pytest.mark.parametrize("cap, scale", [(1e-38, 1.0), (1e-44, 1.0), (1e-30, 1e20), (2.0, 1.2e30), (2.0, -1.2e30), (0.0, 1e-45),
+                                        (3e38, 1e-45)])
+def test_caps_and_scales_at_the_ends_of_their_type(lib, cuda, dtype, fp8, S, cap, scale):
+    """Queries of zeros among others, whose score is 0 whatever the scale, and of 1e-3: a vanishing cap or scale
+    weighs all keys alike; with a vast scale a score is at either end of the cap."""
+    a = _make(54, dtype, 1, S, 8, 2, 64, 300, [300 - S - 9], fp8, cap=cap)
+    a["q"] = a["q"].view(1, S, 8, 64).clone()
+    a["q"][:, :, ::3] = 0
+    a["q"] = a["q"].view(1, S, -1)
+    got = _call(lib, a, cuda, scale=scale)
+    if abs(scale) < 2:  # all scores are within 1e-30 of 0
+        b = dict(a, q=torch.zeros_like(a["q"]), softcap=0.0)
+        want, bound = _want(b, cuda, 1.0)
+        ku.close(got, want, bound)
+        return
+    k = torch.from_numpy(ku.values(a["k"].numpy(), a["ks"].numpy())) if fp8 else a["k"].double()
+    v = torch.from_numpy(ku.values(a["v"].numpy(), a["vs"].numpy())) if fp8 else a["v"].double()
+    for s in range(S):
+        n = 300 - S - 9 + s + 1
+        for h in range(8):
+            y = k[0, h // 4, :n] @ a["q"][0, s, 64 * h:64 * h + 64].double()
+            assert not a["q"][0, s, 64 * h:64 * h + 64].any() or float(y.abs().min()) > 0
+            p = torch.softmax(cap * torch.sign(y) * (1.0 if scale > 0 else -1.0), -1)
+            want = p @ v[0, h // 4, :n]
+            limit = (2.0 ** -9 if dtype != "bf16" else 2.0 ** -6) * (p @ v[0, h // 4, :n].abs()) + n * 2.0 ** -24
+            assert ((got[0, s, 64 * h:64 * h + 64].double().cpu() - want).abs() <= limit).all(), (s, h)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("S", [1, 6, 40, 130])
 @pytest.mark.parametrize("alibi", [False, True])
