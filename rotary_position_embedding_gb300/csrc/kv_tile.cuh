@@ -28,7 +28,7 @@
 // a step of both row tiles): hence 192 registers a softmax thread, 88 a bringing
 // one, 40 a thread of the MMA warps. Where the scores only grow with q.k (no
 // bias), the maximum is taken before the cap, and where all of a warp's capped
-// scores have |y| <= 1/2, tanh(y) is a polynomial: 3 exponential-unit operations
+// scores have |y| <= 0.4, tanh(y) is a polynomial: 3 exponential-unit operations
 // a score become one.
 // Measured, a step of 128 keys and both row tiles at H = 128: 1.58 us (its MMAs
 // alone 1.22), biased 2.12, capped 2.47, over 8-bit caches 2.24, those capped 3.23;
@@ -82,10 +82,6 @@ struct TileCfg {
   static constexpr int kTail = 4 * kInfo + 2 * kTileListed / 8 + NT * kTileRows * 4 + 256;
   static constexpr int kSmem = 1024 + kQ + 4 * kStage + kTail;
 };
-
-// tanh(y) for |y| <= 1/2, off by at most 1.3e-7: the odd polynomial of degree 7
-// with the smallest largest error over [0, 1/2]. Coefficients of y, y^3, y^5, y^7.
-constexpr float kTanh0 = 0.999997675f, kTanh1 = -0.333206564f, kTanh2 = 0.131451532f, kTanh3 = -0.0433726683f;
 
 struct TileBars {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], info[4], q_full, drain;
@@ -223,13 +219,18 @@ struct TileRow {
   const float* ks;              // of each 16 columns
 };
 
-// N raw scores of a row -> scores in log2 (GENERAL), or raw scores times what
-// depends on the column; hidden ones -inf. Returns, for a cap, the largest
-// magnitude before masking.
-template <bool FP8, bool GENERAL, int N>
-__device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bool capped) {
-  float mag = 0.0f;
-  if constexpr (FP8) {
+// N raw scores of a row from TMEM; over 8-bit caches times what the codes of each 16
+// columns and the query row stand for.
+template <bool FP8, int N>
+__device__ __forceinline__ void tile_load(float (&x)[N], uint32_t ts, const TileRow& r, bool raw) {
+  uint32_t c[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 32) tc_ld32(c + i, ts + i);
+#pragma unroll
+  for (int i = 0; i < N; i += 32) tc_wait_ld32(c + i);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(c[i]);
+  if (FP8 && raw) {
 #pragma unroll
     for (int h = 0; h < N / 16; ++h) {
       // to q.k first: queries may be as small as keys are large
@@ -241,15 +242,56 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
       }
     }
   }
-  if constexpr (GENERAL) {
+}
+
+// Whether all of a warp's raw scores have |y| <= 0.4: then the cap is a polynomial.
+// The bounds of mult keep the polynomial's powers normal numbers.
+template <int N>
+__device__ __forceinline__ bool tile_small(const float (&x)[N], const TileRow& r) {
+  float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(r.mult, r.mult));
-      x[i] = y.x, x[i + 1] = y.y;
+  for (int i = 0; i < N; i += 4) {
+    a0 = fmaxf(a0, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+    a1 = fmaxf(a1, fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
+  }
+  return __all_sync(0xffffffffu, fmaxf(a0, a1) * r.mult <= 2.0f * kTanhEnd * kLog2e && r.mult > 1e-5f && r.mult < 1e4f);
+}
+
+// Other scores are capped where they lie in TMEM, 32 columns at a time: in registers,
+// code for N columns cost the common path 8 % (of 8-bit capped prompts).
+template <bool FP8, int N>
+__device__ __forceinline__ void tile_cap(uint32_t ts, const TileRow& r) {
+#pragma unroll 1
+  for (int q = 0; q < N; q += 32) {
+    uint32_t c[32];
+    tc_ld32(c, ts + q);
+    tc_wait_ld32(c);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float2 y = make_float2(__uint_as_float(c[k]), __uint_as_float(c[k + 1]));
+      if constexpr (FP8) {
+        const float f = fminf(r.ks[q / 16 + k / 16] * r.unit, FLT_MAX);
+        y = __fmul2_rn(y, make_float2(f, f));
+      }
+      y = kv_tanh_of(__fmul2_rn(y, make_float2(r.mult, r.mult)));
+      y = __fmul2_rn(y, make_float2(r.cap2, r.cap2));
+      c[k] = __float_as_uint(y.x), c[k + 1] = __float_as_uint(y.y);
     }
-    if (capped) {
+    tc_st32(ts + q, c);
+  }
+  tc_wait_st();
+}
+
+// BIAS: scores get their bias, raw ones their factor first. Hidden ones become -inf.
+template <bool BIAS, int N>
+__device__ __forceinline__ void tile_scores(float (&x)[N], const TileRow& r, bool raw) {
+  if constexpr (BIAS) {
+    if (raw) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = kv_tanh_of(x[i]) * r.cap2;
+      for (int i = 0; i < N; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(r.mult, r.mult));
+        x[i] = y.x, x[i + 1] = y.y;
+      }
     }
     if (r.ahead) {  // some key is ahead of its query (a prefix)
 #pragma unroll
@@ -263,19 +305,6 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
         x[i] = y.x, x[i + 1] = y.y;
       }
     }
-  }
-  if (!GENERAL && capped) {
-    float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      a0 = fmaxf(a0, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
-      a1 = fmaxf(a1, fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
-    }
-    mag = fmaxf(a0, a1);
-  }
-  if (!GENERAL && capped && (r.part || r.look)) {  // -inf is for what is hidden
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = x[i] == -CUDART_INF_F ? -FLT_MAX : x[i];
   }
   if (r.part) {
 #pragma unroll
@@ -291,7 +320,6 @@ __device__ __forceinline__ float tile_scores(float (&x)[N], const TileRow& r, bo
       x[i + 3] = d.w == r.doc ? x[i + 3] : -CUDART_INF_F;
     }
   }
-  return mag;
 }
 
 template <int N>
@@ -309,8 +337,8 @@ __device__ __forceinline__ float tile_max(const float (&x)[N]) {
 
 // Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
 // vs[16-column block] / vref over 8-bit caches); their sum.
-// MODE 0: score = x * mult; 1: capped by the polynomial, mult = scale / cap; 2:
-// capped; 3: x itself. MASKED: some x are hidden.
+// MODE 0: score = x * mult; 1: capped by kv_tanh_of's polynomial, mult = scale / cap;
+// 2: x itself. MASKED: some x are hidden.
 template <bool FP8, bool BF, int MODE, bool MASKED, int N>
 __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
                                               const float* vs, float vref) {
@@ -319,12 +347,12 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
   float2 k0, k1, k2, k3;  // cap * tanh(mult * x) = x (k0 + x^2 (k1 + x^2 (k2 + x^2 k3)))
   if constexpr (MODE == 1) {
     const float u = mult * mult, v = r.cap2 * mult;
-    k0 = make_float2(v * kTanh0, v * kTanh0);
+    k0 = make_float2(v, v);
     k1 = make_float2(v * u * kTanh1, v * u * kTanh1);
     k2 = make_float2(v * u * u * kTanh2, v * u * u * kTanh2);
     k3 = make_float2(v * u * u * u * kTanh3, v * u * u * u * kTanh3);
   }
-  const float2 mul = make_float2(mult, mult), nb = make_float2(nbase, nbase), c2 = make_float2(r.cap2, r.cap2);
+  const float2 mul = make_float2(mult, mult), nb = make_float2(nbase, nbase);
 #pragma unroll
   for (int q = 0; q < N / 32; ++q) {
     uint32_t w[16];
@@ -339,17 +367,12 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
         float2 y = make_float2(x[i], x[i + 1]);
         if constexpr (MODE == 0) {
           y = __ffma2_rn(y, mul, nb);
-        } else if constexpr (MODE == 3) {
+        } else if constexpr (MODE == 2) {
           y = __fadd2_rn(y, nb);
         } else {
-          if constexpr (MODE == 1) {
-            const float2 z = __fmul2_rn(y, y);
-            y = __ffma2_rn(y, __ffma2_rn(z, __ffma2_rn(z, __ffma2_rn(z, k3, k2), k1), k0), nb);
-          } else {
-            const float2 t = __fmul2_rn(y, mul);
-            y = __ffma2_rn(make_float2(kv_tanh_of(t.x), kv_tanh_of(t.y)), c2, nb);
-          }
-          if constexpr (MASKED) {  // a hidden score is -inf, not the cap's end (nor is a seen one: tile_scores)
+          const float2 z = __fmul2_rn(y, y);
+          y = __ffma2_rn(y, __ffma2_rn(z, __ffma2_rn(z, __ffma2_rn(z, k3, k2), k1), k0), nb);
+          if constexpr (MASKED) {
             y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
             y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
           }
@@ -605,16 +628,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         tc_after();
         float x[N];
-        {
-          uint32_t c[N];
-#pragma unroll
-          for (int i = 0; i < N; i += 32) tc_ld32(c + i, ts + i);
-#pragma unroll
-          for (int i = 0; i < N; i += 32) tc_wait_ld32(c + i);
-#pragma unroll
-          for (int i = 0; i < N; ++i) x[i] = __uint_as_float(c[i]);
+        tile_load<FP8, N>(x, ts, tr, true);
+        bool done = general;  // x holds scores in log2, not raw ones
+        if (capped && (general || !tile_small(x, tr))) {
+          // (an infinite product is at an end of the cap from here on: -inf means hidden)
+          tile_cap<FP8, N>(ts, tr);
+          tile_load<FP8, N>(x, ts, tr, false);
+          done = true;
         }
-        const float mag = general ? tile_scores<FP8, true, N>(x, tr, capped) : tile_scores<FP8, false, N>(x, tr, capped);
+        if (general)
+          tile_scores<true, N>(x, tr, !capped);
+        else
+          tile_scores<false, N>(x, tr, true);
         const bool masked = tr.part || tr.look;
         bool grown = false;
         float vmax = 0.0f;
@@ -633,14 +658,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
-        // 2 log2(e) |y| with |y| <= 1/2; the last keeps the polynomial's powers finite
-        const bool small = capped && !general && __all_sync(0xffffffffu, mag * mult <= kLog2e && mult < 1e4f);
         auto weights = [&]() {
           const float nb = m == -CUDART_INF_F ? 0.0f : -m;
-          if (general) return tile_weights<FP8, BF, 3, false, N>(x, ts, tr, 1.0f, nb, vs, vref);
+          if (done) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, 1.0f, nb, vs, vref);
           if (!capped) return tile_weights<FP8, BF, 0, false, N>(x, ts, tr, mult, nb, vs, vref);
-          if (masked) return tile_weights<FP8, BF, 2, true, N>(x, ts, tr, mult, nb, vs, vref);
-          if (!small) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, mult, nb, vs, vref);
+          if (masked) return tile_weights<FP8, BF, 1, true, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
           return tile_weights<FP8, BF, 1, false, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
         };
         // Weights by the base so far, where every row has one; only where a row's sum
@@ -654,8 +676,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (move) {
           const float top = tile_max(x);
-          float mx = top * (general ? 1.0f : mult);
-          if (capped && !general) mx = masked && top == -CUDART_INF_F ? top : kv_tanh_of(mx) * tr.cap2;
+          float mx = top * (done ? 1.0f : mult);
+          if (capped && !done) mx = top == -CUDART_INF_F ? top : kv_tanh_of(mx) * tr.cap2;
           const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
           m = mn;

@@ -1,6 +1,7 @@
 """Attention over the caches on the GPU where numbers are far apart: value scales of blocks that a row does not
 see, caps of every size, infinite keys under a cap, small queries over large keys."""
 
+import numpy as np
 import pytest
 import torch
 
@@ -82,6 +83,80 @@ def test_value_scales_of_another_rows_document(lib, cuda, dtype, S, G, up):
     for room in (None, 0):
         ws = None if room is None else torch.empty(room, dtype=torch.uint8, device=cuda)
         ku.close(_call(lib, a, cuda, workspace=ws)[keep], want[keep], bound[keep], str(room))
+
+
+def _tight(a, dev, scale):
+    """kv_util.attention's result with a bound whose share for the cap goes with the capped score, not with the
+    cap: tanh(y) for |y| <= 0.4 by a polynomial to 1.2e-7 of it, above as 1 - 2 / (1 + e^(2y)) by an exponential
+    to 2^-22 and a reciprocal to 2^-23, which is off by 2 / (1 + e) (e / (1 + e) 2^-22 + 3 * 2^-24) + 2^-25, at
+    most 4 * 2^-22 of tanh(y) (at y = -0.4); two more roundings for scaling. 10 * 2^-23 in all. A negative
+    exponential's result below 2^-126 counts as 0, which is 1e-38 of the cap's largest value, 1."""
+    out, old = _want(a, dev, scale)
+    cap = a["softcap"]
+    if "ks" in a:
+        k, v = (torch.from_numpy(ku.values(a[n].numpy(), a[n + "s"].numpy())).to(dev) for n in ("k", "v"))
+    else:
+        k, v = a["k"].double().to(dev), a["v"].double().to(dev)
+    q = a["q"].double().to(dev)
+    B, S, _ = q.shape
+    N, H, Nq = k.shape[1], k.shape[3], a["num_heads"]
+    G = Nq // N
+    t = a["q"].dtype
+    weight_eps = 2.0 ** -24 if t == torch.float32 else 2.0 ** -11 if "ks" in a else ku.EPS[t]
+    bound = torch.zeros((B, S, Nq, H), dtype=torch.float64, device=dev)
+    qh = q.view(B, S, Nq, H)
+    for b in range(B):
+        for s in range(S):
+            past = int(a["past"][b])
+            n = past + s + 1
+            for h in range(N):
+                kk, vv, rows = k[b, h, :n], v[b, h, :n], qh[b, s, h * G:(h + 1) * G]
+                d = (H + 8) * 2.0 ** -23 * (rows.abs() @ kk.abs().T) * abs(scale)
+                y = cap * torch.tanh(rows @ kk.T * scale / cap)
+                d = d + 10 * 2.0 ** -23 * y.abs()
+                if a["slopes"] is not None:
+                    bias = a["slopes"][h * G:(h + 1) * G, None].double().to(dev) * (past + s - torch.arange(n, device=dev))
+                    y, d = y - bias, d + 4 * 2.0 ** -23 * bias
+                d = d + 4 * 2.0 ** -23 * y.abs()
+                p = torch.softmax(y, -1)
+                off = p * torch.expm1(2 * d.clamp(max=50.0))
+                mean = p @ vv.abs()
+                total = (2 * weight_eps + (n + 16) * 2.0 ** -23) * mean + off @ vv.abs() + off.sum(-1, keepdim=True) * mean
+                if weight_eps > 2.0 ** -20:
+                    total = total + n * 2.0 ** -25 * vv.abs().amax()
+                bound[b, s, h * G:(h + 1) * G] = total
+    return out, bound.view(B, S, -1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("S, G", [(1, 4), (6, 4), (70, 4)])
+@pytest.mark.parametrize("cap", [0.05, 1.0, 50.0, 1e4, 1e5, 1e6, 1e9, 1e20, 3e38])
+def test_caps_of_every_size(lib, cuda, dtype, fp8, S, G, cap):
+    """Scores of a few units under caps from far below them to far above, next to keys whose scores are about
+    -cap / 2 where the storage type holds such: a large cap tends to none."""
+    N, H, L = 2, 64, 400
+    for alibi in (False, True):
+        a = _make(53, dtype, 1, S, G * N, N, H, L, [L - S - 30], fp8, cap=cap, alibi=alibi, qscale=0.3)
+        a["q"] = a["q"].view(1, S, G * N, H).clone()
+        a["q"][..., 0] = 1.0
+        a["q"] = a["q"].view(1, S, -1)
+        low = -min(cap / 2, 2.0 ** 15)  # of the first dimension, in a few keys
+        if fp8:
+            a["ks"][:] = 2.0 ** -6  # as _make's scale of the middle
+            a["k"][..., 0] = 0
+            e = max(-100.0, np.floor(np.log2(-low / 256)))
+            for blk in (3, 9, 20):  # whole blocks
+                a["ks"][:, :, blk] = 2.0 ** e
+                a["k"][:, :, 16 * blk:16 * blk + 16] = 0
+                a["k"][:, :, 16 * blk:16 * blk + 16, 0] = int(ku.e4m3(np.array(low / 2.0 ** e)))
+        else:
+            a["k"][..., 0] = 0
+            for j in (3, 50, 51, 200, 333):
+                a["k"][:, :, j, 1:] = 0
+                a["k"][:, :, j, 0] = low
+        want, bound = _tight(a, cuda, 1.0)
+        ku.close(_call(lib, a, cuda, scale=1.0), want, bound, str(alibi))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
