@@ -474,7 +474,8 @@ rope_status rope_apply_no_alloc(rope_dtype dtype, int32_t x_rank, const int64_t*
  * query .. value, positions, past_seq_lens (required), interleaved,
  * rotary_embedding_dim, norm weights (both or neither), epsilon, q_out,
  * status_flags, ownership and errors as rope_apply_qkv in cache mode and
- * rope_apply_qkv_rmsnorm; no scratch. max_cache_len is limited to 2^30.
+ * rope_apply_qkv_rmsnorm; no scratch. max_cache_len is limited to 2^30, the rows of
+ * Q (batch * seq * num_heads) and the blocks that are touched to about 2^31.
  */
 #define ROPE_KV_SCALE_BLOCK 16
 rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,

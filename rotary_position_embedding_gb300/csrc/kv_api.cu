@@ -538,16 +538,20 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
   const bool fast = p.rows == rows_wanted && p.U <= p.lanes;
   p.wide = head_size % 16 == 0 && aligned(k_cache, 16) && aligned(v_cache, 16);
   p.blocks = (seq + kKvBlock - 2) / kKvBlock + 1;
-  const int64_t q_rows = batch * seq * num_heads;
-  if (!sizes_fit({batch, kv_num_heads, p.blocks, (int64_t)1 << 31}) || batch * kv_num_heads * p.blocks >= (int64_t)1 << 31 ||
-      q_rows >= (int64_t)1 << 31)
-    return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 rows of Q or blocks of the caches");
-  p.kv_tasks = (int32_t)(batch * kv_num_heads * p.blocks);
-  const int per_cta = kKvAppendThreads / (p.lanes * p.rows);
-  p.kv_ctas = (p.kv_tasks + per_cta - 1) / per_cta;
+  // A CTA's first item is within its threads' reach of the last: with these limits
+  // the kernel's 32-bit counts do not pass 2^31 (nor does the grid: a CTA takes 8
+  // of them at least from Q, and fewer than 2^30 take blocks).
+  constexpr int64_t kMostItems = INT32_MAX - kKvAppendThreads;
   p.q_groups = (num_heads + kKvAppendHeads - 1) / kKvAppendHeads;
-  p.q_items = (int32_t)(batch * seq * p.q_groups);
+  const int64_t kv_tasks = sizes_fit({batch, kv_num_heads, p.blocks, 2}) ? batch * kv_num_heads * p.blocks : INT64_MAX;
+  const int64_t q_items = batch * seq * p.q_groups;
+  if (batch * seq * num_heads > INT32_MAX || q_items > kMostItems || kv_tasks > kMostItems)
+    return fail(ROPE_ERR_UNSUPPORTED, "2^31 rows of Q or blocks of the caches, or nearly so many");
+  const int per_cta = kKvAppendThreads / (p.lanes * p.rows);
   const int q_per_cta = kKvAppendThreads / p.lanes;
+  p.kv_tasks = (int32_t)kv_tasks;
+  p.q_items = (int32_t)q_items;
+  p.kv_ctas = (p.kv_tasks + per_cta - 1) / per_cta;
   const int64_t grid = p.kv_ctas + ((int64_t)p.q_items + q_per_cta - 1) / q_per_cta;
   p.by_q = div_of(p.q_groups);
   p.by_s = div_of(seq);
