@@ -75,8 +75,11 @@ struct KvTokenKernel {
 constexpr int kKvTokenThreads = 128;
 constexpr int kKvClusterMost = 8;
 constexpr int kKvDealMost = 1024;  // sequences whose units a CTA adds up
-// CTAs that the work is dealt to: what is resident on 152 SMs (see TokenCfg).
-constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) { return 152 * (H > 128 || two ? 2 : fp8 ? 4 : 3); }
+// CTAs that the work is dealt to: what is resident on 152 SMs (TokenCfg checks it;
+// 16-bit rows above H = 128 take 132 KB of shared memory, one CTA an SM).
+constexpr int kv_token_ctas(bool fp8, int64_t H, bool two) {
+  return 152 * (H > 128 && !fp8 ? 1 : H > 128 || two ? 2 : fp8 ? 4 : 3);
+}
 KvTokenKernel kv_token_kernel(int dtype, bool fp8, int H, bool two);
 
 // Many rows, 16-bit T, KvParams.vec: 256 rows of a (b, kvh) a CTA (128 above

@@ -275,6 +275,8 @@ struct TokenCfg {
   static constexpr int kMerge = kTokWarps * NB * 8 * (HD + 4) * 4;
   static constexpr int kRing = kStage * kStages * kTokWarps;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  // 228 KB an SM; a CTA holds about 4.5 KB statically, and 1 KB is reserved for it
+  static_assert(kv_token_ctas(FP8, HD, NB > 1) / 152 * (kSmem + 5632) <= 228 * 1024, "CTAs that are resident");
 };
 
 template <class T, bool FP8, int HD, int NB>
