@@ -324,7 +324,6 @@ rope_status attention_impl(rope_dtype dtype, bool fp8, int64_t batch, int64_t se
   if (family == Family::kToken) {
     p.by_g = div_of(p.G);
     p.by_tiles = div_of(p.tiles);
-    p.by_problems = div_of((int64_t)p.tiles * kv_num_heads);
   }
   if (pl.splits > 1 || pl.deal > 0) {
     const int64_t rows = pl.deal > 0 ? 2 * (int64_t)pl.deal * p.rt : batch * kv_num_heads * pl.splits * p.R;

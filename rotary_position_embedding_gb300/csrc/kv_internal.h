@@ -42,7 +42,7 @@ struct KvParams {
   int32_t splits;
   int32_t tiles, rt;       // kv_token_kernel: tiles of a (b, kvh), rows of a tile
   int32_t deal;            // CTAs that the work is dealt to, or 0: one problem a CTA
-  KvDiv by_g, by_tiles, by_problems;  // kv_token_kernel: by G, tiles, Nkv * tiles
+  KvDiv by_g, by_tiles;   // kv_token_kernel: by G, tiles
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   int32_t cluster;         // kv_token_kernel: CTAs of a problem that meet in shared memory (0: see deal)
   int32_t tma;             // kv_tile_kernel: the tensor maps are there
