@@ -257,8 +257,9 @@ __device__ __forceinline__ bool tile_small(const float (&x)[N], const TileRow& r
   return __all_sync(0xffffffffu, fmaxf(a0, a1) * r.mult <= 2.0f * kTanhEnd * kLog2e && r.mult > 1e-5f && r.mult < 1e4f);
 }
 
-// Other scores are capped where they lie in TMEM, 32 columns at a time: in registers,
-// code for N columns cost the common path 8 % (of 8-bit capped prompts).
+// Other scores, and those of tiles with hidden keys, are capped where they lie in
+// TMEM, 32 columns at a time: in registers, code for N columns that is seldom reached
+// cost the common path 10 % of 8-bit capped prompts.
 template <bool FP8, int N>
 __device__ __forceinline__ void tile_cap(uint32_t ts, const TileRow& r) {
 #pragma unroll 1
@@ -338,8 +339,8 @@ __device__ __forceinline__ float tile_max(const float (&x)[N]) {
 // Weights 2^(score - base), written to TMEM at `ts` as 16-bit values (times
 // vs[16-column block] / vref over 8-bit caches); their sum.
 // MODE 0: score = x * mult; 1: capped by kv_tanh_of's polynomial, mult = scale / cap;
-// 2: x itself. MASKED: some x are hidden.
-template <bool FP8, bool BF, int MODE, bool MASKED, int N>
+// 2: x itself.
+template <bool FP8, bool BF, int MODE, int N>
 __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, const TileRow& r, float mult, float nbase,
                                               const float* vs, float vref) {
   const float vinv = FP8 ? __uint_as_float((254u << 23) - __float_as_uint(vref)) : 1.0f;  // 2^127 for vref = 0
@@ -372,10 +373,6 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
         } else {
           const float2 z = __fmul2_rn(y, y);
           y = __ffma2_rn(y, __ffma2_rn(z, __ffma2_rn(z, __ffma2_rn(z, k3, k2), k1), k0), nb);
-          if constexpr (MASKED) {
-            y.x = x[i] == -CUDART_INF_F ? -CUDART_INF_F : y.x;
-            y.y = x[i + 1] == -CUDART_INF_F ? -CUDART_INF_F : y.y;
-          }
         }
         float2 e = make_float2(kv_exp2(y.x), kv_exp2(y.y));
         sum[h] = __fadd2_rn(sum[h], e);
@@ -630,7 +627,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         float x[N];
         tile_load<FP8, N>(x, ts, tr, true);
         bool done = general;  // x holds scores in log2, not raw ones
-        if (capped && (general || !tile_small(x, tr))) {
+        const bool masked = tr.part || tr.look;
+        if (capped && (general || masked || !tile_small(x, tr))) {
           // (an infinite product is at an end of the cap from here on: -inf means hidden)
           tile_cap<FP8, N>(ts, tr);
           tile_load<FP8, N>(x, ts, tr, false);
@@ -640,7 +638,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tile_scores<true, N>(x, tr, !capped);
         else
           tile_scores<false, N>(x, tr, true);
-        const bool masked = tr.part || tr.look;
         bool grown = false;
         float vmax = 0.0f;
         if constexpr (FP8) {
@@ -660,10 +657,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         auto weights = [&]() {
           const float nb = m == -CUDART_INF_F ? 0.0f : -m;
-          if (done) return tile_weights<FP8, BF, 2, false, N>(x, ts, tr, 1.0f, nb, vs, vref);
-          if (!capped) return tile_weights<FP8, BF, 0, false, N>(x, ts, tr, mult, nb, vs, vref);
-          if (masked) return tile_weights<FP8, BF, 1, true, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
-          return tile_weights<FP8, BF, 1, false, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
+          if (done) return tile_weights<FP8, BF, 2, N>(x, ts, tr, 1.0f, nb, vs, vref);
+          if (!capped) return tile_weights<FP8, BF, 0, N>(x, ts, tr, mult, nb, vs, vref);
+          return tile_weights<FP8, BF, 1, N>(x, ts, tr, mult * (0.5f / kLog2e), nb, vs, vref);
         };
         // Weights by the base so far, where every row has one; only where a row's sum
         // says that one may be too large (2^15 fits float16) is the maximum taken, the
@@ -677,7 +673,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (move) {
           const float top = tile_max(x);
           float mx = top * (done ? 1.0f : mult);
-          if (capped && !done) mx = top == -CUDART_INF_F ? top : kv_tanh_of(mx) * tr.cap2;
+          if (capped && !done) mx = kv_tanh_of(mx) * tr.cap2;
           const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
           m = mn;
