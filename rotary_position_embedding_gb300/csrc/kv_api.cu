@@ -189,10 +189,14 @@ Plan plan_attention(Family family, bool fp8, int64_t B, int64_t S, int64_t Nq, i
     pl.cluster = token_cluster(fp8, problems, H, R, max_len);
     if (pl.cluster) return pl;
     // Many more problems than CTAs even out by themselves (2048 problems of 1 to 4096
-    // keys in 8 bits on 608 places: 225 us one a CTA, 233 us dealt).
-    if (problems < 3 * kv_token_ctas(fp8, H, rt == 16) && B <= kKvDealMost && max_len > 64 &&
-        problems * units < (1ll << 31)) {
-      pl.deal = kv_token_ctas(fp8, H, rt == 16);
+    // keys in 8 bits on 608 places: 225 us one a CTA, 233 us dealt). Between three and
+    // six problems a place, one CTA an SM is dealt to twice: 512 problems of 8000
+    // 16-bit keys of 256 take 757 us so, 852 one a CTA (of 1 to 8190 keys 455 and 447;
+    // dealt to once 751 and 474).
+    const int places = kv_token_ctas(fp8, H, rt == 16);
+    const int rounds = places == kSms && problems >= 3 * places ? 2 : 1;
+    if (problems < 3 * rounds * places && B <= kKvDealMost && max_len > 64 && problems * units < (1ll << 31)) {
+      pl.deal = rounds * places;
       if (pl.deal > problems * units) pl.deal = (int)(problems * units);
       pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
     }
