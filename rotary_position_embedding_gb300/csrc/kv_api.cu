@@ -162,14 +162,19 @@ struct Plan {
 };
 
 // CTAs of a cluster that takes one problem of kToken, or 0. Few problems of short
-// caches need no second launch that way. One float16 sequence, 8 key/value heads of
-// 128: 778 keys 7.0 us, dealt out 12.7; 4000 keys 14.4 against 17.4; but 8000 keys
-// 23.3 against 18.9. In 8 bits 8000 keys 17.8 against 18.0; 7 such sequences 32.6
-// against 34.2.
+// caches need no second launch that way, as long as all clusters are resident. One
+// float16 sequence, 8 key/value heads of 128: 778 keys 7.0 us, dealt out 12.7; 4000
+// keys 14.4 against 17.4; but 8000 keys 23.3 against 18.9. In 8 bits 8000 keys 17.8
+// against 18.0; 7 such sequences 32.6 against 34.2. 12 sequences of 195 keys, in
+// clusters of 4: 7.6 against 11.2.
+// The lengths are on the device, so max_len stands for them here and in the plans
+// below, whose figures are of caches that are nearly full: 778 keys take 7.2 us in a
+// cache of 4096 rows and 13.0 in one of 4097 or 131072.
 int token_cluster(bool fp8, int64_t problems, int64_t H, int64_t R, int64_t max_len) {
-  if (max_len <= 64 || max_len * (fp8 ? 1 : 2) > 8192 || problems * kKvClusterMost > kv_token_ctas(fp8, H, R > 8)) return 0;
-  const int n = pow2_at_least((max_len + 63) / 64);
-  return n < kKvClusterMost ? n : kKvClusterMost;
+  if (max_len <= 64 || max_len * (fp8 ? 1 : 2) > 8192) return 0;
+  int n = pow2_at_least((max_len + 63) / 64);
+  if (n > kKvClusterMost) n = kKvClusterMost;
+  return problems * n <= kv_token_ctas(fp8, H, R > 8) ? n : 0;
 }
 
 // Row tiles and splits from the sizes alone: the lengths are on the device.
@@ -228,7 +233,9 @@ Family choose_family(bool matrix, bool fp8, int64_t B, int64_t S, int64_t G, int
   const bool grid = B <= 65535 && (R + kv_tile_rows(H) - 1) / kv_tile_rows(H) <= 65535;
   bool few = R <= 16;
   if (!few && R <= 64 && B <= 65535) {  // B * Nkv * max_len stays below 2^62
-    few = (max_len <= 4096 && token_cluster(fp8, B * Nkv * ((R + 15) / 16), H, R, max_len) > 0) ||
+    const int64_t problems = B * Nkv * ((R + 15) / 16);
+    few = (max_len <= 4096 && problems * kKvClusterMost <= kv_token_ctas(fp8, H, true) &&
+           token_cluster(fp8, problems, H, R, max_len) > 0) ||
           (fp8 && H <= 128 && R <= 48 && B * Nkv * max_len >= (R <= 32 ? 1 << 18 : 1 << 19));
   }
   if (!few && grid) return Family::kTile;
