@@ -507,9 +507,13 @@ rope_status rope_apply_qkv_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int
  * A row that sees no key (or whose largest score is -inf) gives 0. Keys and
  * values that a row does not see, and cache rows from total on, may hold
  * anything, NaN included. Products of 16-bit types are exact and summed in
- * float32, as are the softmax statistics; the weights are rounded to T (to
- * float16 over 8-bit caches) for the product with V. float32 keeps float32
- * products.
+ * float32, as are the softmax statistics; c is computed to 2^-20 of its value. The
+ * weights are rounded to T (to float16 over 8-bit caches) for the product with V:
+ * to within half a step, or in float16, where a weight is below 2^-14 of the row's
+ * largest, to within 2^-25 of that; the sum that they are divided by is of the
+ * unrounded ones. They are not divided before the product, and may be 2^15 where the
+ * largest of them would be 1: sums over values beyond 2^90 may overflow. float32
+ * keeps float32 products.
  *
  * query     device T (B, S, num_heads*H): the q_out of the Q/K operators.
  * k_cache, v_cache  device T (B, kv_num_heads, max_cache_len, H), read only.
@@ -554,6 +558,9 @@ rope_status kv_attention(rope_dtype dtype, int64_t batch, int64_t seq, int32_t n
  * What is rounded to float16 is weight * (value scale / largest value scale so far
  * among the blocks of which the row sees a key), the row's largest weight being
  * about 1 or more: to within 2^-11, or to within 2^-25 where that is below 2^-14.
+ * bfloat16 queries become float16 after scaling each row by a power of two: exact,
+ * but for elements below 2^-22 of the row's largest, which are off by up to 2^-33 of
+ * it.
  * Everything else as kv_attention.
  */
 rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32_t num_heads,

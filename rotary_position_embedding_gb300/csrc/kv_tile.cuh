@@ -26,15 +26,17 @@
 // A softmax thread holds its 128 scores in registers from one TMEM load on
 // (32 at a time, read twice, the loads' latency was two thirds of a step: 3.3 us
 // a step of both row tiles): hence 192 registers a softmax thread, 88 a bringing
-// one, 40 a thread of the MMA warps. Where the scores only grow with q.k (no
-// bias), the maximum is taken before the cap, and where all of a warp's capped
-// scores have |y| <= 0.4, tanh(y) is a polynomial: 3 exponential-unit operations
-// a score become one.
+// one, 40 a thread of the MMA warps. Where no bias is added, nothing is hidden and
+// all of a warp's capped scores have |y| <= 0.4, tanh(y) is a polynomial: 3
+// exponential-unit operations a score become one. Scores stay raw there, and the
+// maximum is taken before the cap.
 // Measured, a step of 128 keys and both row tiles at H = 128: 1.58 us (its MMAs
-// alone 1.22), biased 2.12, capped 2.47, over 8-bit caches 2.24, those capped 3.23;
-// 1.40 at H = 64, 0.94 for 64 keys and one row tile at H = 256. 4 x 2048 float16
-// tokens over up to 4095 keys, 32/8 heads, capped: 408 us, 0.36 of the measured
-// bfloat16 rate.
+// alone 1.22), biased 2.00, capped 2.53, over 8-bit caches 2.29, those capped 3.29;
+// 1.40 at H = 64, 0.95 for 64 keys and one row tile at H = 256. 4 x 2048 float16
+// tokens over up to 4095 keys, 32/8 heads, capped: 405 us, 0.36 of the measured
+// bfloat16 rate. Head sizes between run padded: 2 x 2048 bfloat16 tokens over up to
+// 4096 keys, 32/8 heads of 64 135 us, 80 148, 96 153, 112 156, 128 161, 160 332, 192
+// 339, 256 353.
 // Shared memory: Q, two stages of K and two of V, each as slabs of 64 elements
 // (128-byte rows, 128-byte swizzle): the K-major form for Q and K, and the same
 // bytes read MN-major for V.
@@ -389,7 +391,7 @@ __device__ __forceinline__ float tile_weights(const float (&x)[N], uint32_t ts, 
 // which shows in these unrolled rows: without one for plain scores, 2 x 2048
 // float16 tokens took 152 us for 140 (a row of documents 142 for 129), without
 // the biased one 3 x 1531 tokens 59.5 us for 55.7. An instance for capped scores
-// alone did not: the compiler spills there (61 -> 81 us).
+// alone did not: the compiler spilled there (61 -> 81 us).
 template <class T, bool FP8, int HD, int KIND>
 __global__ void __launch_bounds__(kTileThreads, 1)
     kv_tile_kernel_t(const KvParams p, const __grid_constant__ KvTileMaps maps) {

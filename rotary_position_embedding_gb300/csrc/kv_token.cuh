@@ -22,8 +22,9 @@
 // 8-bit caches: codes become float16 exactly on the way into the fragments; the
 // key scale of a unit (a block of 16 rows has one) multiplies its scores, the
 // value scale its weights, relative to the largest that the row has seen so far (a
-// power of two, so nothing is rounded). Q is float16 too, for bfloat16 after scaling each row
-// by a power of two; the scores undo it.
+// power of two, so nothing is rounded; rows of one CTA may see different blocks).
+// Q is float16 too, for bfloat16 after scaling each row by a power of two; the
+// scores undo it.
 //
 // Softmax: the running maximum moves only where a score passes it by 8 (in
 // log2), so weights stay below 2^8 (exact in float32, far from float16's end) and
@@ -31,7 +32,10 @@
 //
 // Measured: 64 sequences of 1 to 8190 bfloat16 keys (8 heads of 128, 32 query heads)
 // 214 us with the joining, 5.0 TB/s; 256 of 1 to 4096 keys in 8 bits 225 us, 4.8 TB/s;
-// one of 131001 keys in 8 bits 69.7 us. The copy rate's floors are 158, 159 and 40 us.
+// one of 131001 keys in 8 bits 68.5 us. The copy rate's floors are 158, 159 and 40 us.
+// Head sizes between run padded, and copy piece by piece: 64 sequences of up to 8190
+// bfloat16 keys, 8 heads of 64 114 us, 80 167, 96 172, 112 188, 128 205, 160 534, 192
+// 543, 256 454 (8 bits: 93, 140, 141, 143, 132, 278, 280, 254).
 //
 // A value that no row sees is zeroed before the product. Where one that only
 // some rows see is not finite, its zero weight in the others would make a NaN
@@ -159,9 +163,9 @@ __device__ __forceinline__ float kv_row_shift(float amax, float* factor) {
 // in the order of the problems, whatever the sequences' lengths: a problem that
 // one CTA has whole goes to the output, the others' parts to the workspace (2
 // slots a CTA: its first segment's, its last one's), with a word on the problem that
-// the CTA begins and leaves unfinished, for kv_join_kernel. Without (no workspace, or more sequences than fit) a CTA
-// takes one problem. Equal splits of ragged sequences left some SMs with 1.25
-// times the mean's work.
+// the CTA begins and leaves unfinished, for kv_join_kernel. Without (no workspace,
+// or more sequences than fit) a CTA takes one problem. Equal splits of ragged
+// sequences left some SMs with 1.25 times the mean's work.
 //
 // Few problems of caches that are not long (p.cluster CTAs a problem, a cluster):
 // each CTA takes its share of the problem's units, and the parts meet in the
