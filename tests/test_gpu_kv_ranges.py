@@ -10,8 +10,9 @@ from test_gpu_kv import _call, _make, _want
 
 pytestmark = pytest.mark.gpu
 
-# finite scales that no append writes: far too large, far too small, between powers of two, negative
-WILD = [2.0 ** 30, 1e30, 3.7e20, 2.0 ** 126, 3.4e38, 1e-40, 0.0, -1.0, -2.5e33, 1234.5]
+# scales that no append writes: far too large, far too small, between powers of two, negative, not finite
+WILD = [2.0 ** 30, 1e30, 3.7e20, 2.0 ** 126, 3.4e38, 1e-40, 0.0, -1.0, -2.5e33, 1234.5, float("nan"), float("inf"),
+        float("-inf")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -19,7 +20,7 @@ WILD = [2.0 ** 30, 1e30, 3.7e20, 2.0 ** 126, 3.4e38, 1e-40, 0.0, -1.0, -2.5e33, 
 @pytest.mark.parametrize("H", [64, 128, 256])
 @pytest.mark.parametrize("cap", [0.0, 6.0])
 def test_scales_that_no_row_sees(lib, cuda, dtype, S, G, H, cap):
-    """A padded front and a hole between documents, whose blocks' scales hold anything finite."""
+    """A padded front and a hole between documents, whose blocks' scales hold anything."""
     B, N, L = 2, 2, 700
     past = [L - S - 40, 333]
     a = _make(51, dtype, B, S, G * N, N, H, L, past, True, cap=cap)
@@ -29,7 +30,7 @@ def test_scales_that_no_row_sees(lib, cuda, dtype, S, G, H, cap):
     want, bound = _want(a, cuda)
     ku.close(_call(lib, a, cuda), want, bound)
     hidden = [n for n in range(-(-L // 16)) if bool((ids[0, 16 * n:16 * n + 16] != 0).all())]
-    for turn in range(2):
+    for turn in range(5):
         for name in ("ks", "vs"):
             for n, blk in enumerate(hidden):
                 a[name][0, :, blk] = WILD[(n + 3 * turn) % len(WILD)]
