@@ -578,6 +578,127 @@ rope_status kv_attention_fp8(rope_dtype dtype, int64_t batch, int64_t seq, int32
 int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, int32_t kv_num_heads,
                                int64_t head_size, int64_t max_cache_len);
 
+/*
+ * Caches held in pages. The three calls below take sequences of any number of new
+ * tokens each, one behind the other in one tensor of `tokens` rows, and caches whose
+ * rows lie in pages of a pool. They have no counterpart on the pages, like ROPE_BF16.
+ *
+ * query_starts  device int32 (batch + 1), ascending: sequence b has the tokens
+ *           [query_starts[b], query_starts[b+1]), none included. Tokens before the
+ *           first and behind the last sequence are nobody's: what the call writes for
+ *           tokens is left as it was there. NULL: every sequence has tokens / batch.
+ *           Values are clipped to [0, tokens].
+ * past_seq_lens device int32 (batch): token s of sequence b is at cache row
+ *           past_seq_lens[b] + s.
+ * k_pages, v_pages  device T: page p holds (kv_num_heads, page_size, head_size)
+ *           elements side by side from p * page_stride on (page_stride in elements, at
+ *           least their number; more where K and V share one tensor).
+ * page_table    device int32 (batch, max_pages): row j of sequence b is row j %
+ *           page_size of page page_table[b, j / page_size]. Pages may be shared where
+ *           they are only read. An entry outside [0, num_pages) where a row is written
+ *           takes nothing, where one is read it holds zeros; either sets status bit 2.
+ *           Entries behind a sequence's last row, and in front of a window, are not
+ *           looked at. Rows end at max_pages * page_size, at most 2^30.
+ * A contiguous cache (B, kv_num_heads, max_len, head_size) is one of B pages of max_len
+ * rows, sequence b holding page b.
+ */
+
+/*
+ * rope_apply_qkv_paged -- rope_apply_qkv (or, with both norm weights,
+ * rope_apply_qkv_rmsnorm) in cache mode with caches held in pages. Every Q, K and V
+ * head has the bits of those calls.
+ *
+ * query     device T (tokens, num_heads*H), or packed (tokens, (num_heads +
+ *           2*kv_num_heads)*H) with key and value NULL; key, value (tokens,
+ *           kv_num_heads*H).
+ * position_ids  device int64 (tokens), or NULL: the token's cache row. With a tree of
+ *           drafts the depth counts, not the row: past + depth.
+ * k_pages, v_pages  updated in place: the token's row of every key/value head. A row
+ *           outside [0, max_pages * page_size) or in a page outside the pool is not
+ *           stored (status bit 2). Two tokens' rows in one place (a page that two
+ *           sequences write to) give one of them.
+ * q_out     device T (tokens, num_heads*H); it may be query where that is not packed.
+ * Everything else, status bits 0 and 2 and errors as rope_apply_qkv and
+ * rope_apply_qkv_rmsnorm (a head of any number of units with the norm); no scratch.
+ * tokens is limited to 2^30.
+ */
+rope_status rope_apply_qkv_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int32_t num_heads,
+                                 int32_t kv_num_heads, int64_t head_size, const void* query,
+                                 const void* key, const void* value, const void* q_norm_weight,
+                                 const void* k_norm_weight, float epsilon, const void* cos_cache,
+                                 const void* sin_cache, int64_t cache_rows, const int64_t* position_ids,
+                                 const int32_t* past_seq_lens, const int32_t* query_starts,
+                                 const int32_t* page_table, int64_t max_pages, int32_t interleaved,
+                                 int32_t rotary_embedding_dim, void* q_out, void* k_pages, void* v_pages,
+                                 int64_t num_pages, int64_t page_size, int64_t page_stride,
+                                 int32_t* status_flags, rope_stream_t stream);
+
+/*
+ * kv_attention_paged -- kv_attention of each sequence's new tokens over caches held in
+ * pages, after rope_apply_qkv_paged with the same lengths and table. Token s of sequence
+ * b is at row i = past_seq_lens[b] + s, total = past_seq_lens[b] + its tokens (within
+ * [0, max_pages * page_size]), and key row j < total is visible if
+ *   j <= i and (window == 0 or j > i - window)              without tree_masks,
+ *   j < past_seq_lens[b], or bit j - past_seq_lens[b] of
+ *   tree_masks[token] is set                                with them;
+ * scores, cap, bias, softmax, sums and rounding as kv_attention. Keys and values that a
+ * row does not see, and rows from total on, may hold anything, NaN included.
+ *
+ * query     device T (tokens, num_heads*H): q_out of rope_apply_qkv_paged.
+ * max_query_len  at least the new tokens of the longest sequence, at most tokens. The
+ *           kernels and their split follow from it: 1 in a decode step. A longer
+ *           sequence is left out (its rows stay as they were) and sets status bit 2.
+ *           Without query_starts: tokens / batch.
+ * window    0, or how many keys a token sees, itself among them (above 2^30: all).
+ * tree_masks    NULL or device int64 (tokens): the new tokens are drafts, in any order,
+ *           and bit t of a token's word says that it sees new token t of its sequence
+ *           (a tree: itself and its ancestors). max_query_len is at most 64 then, and
+ *           neither window nor alibi_slopes are given.
+ * out       device T (tokens, num_heads*H); must not overlap an input.
+ * workspace NULL or workspace_bytes as for kv_attention; kv_attention_paged_workspace
+ *           says how much the planned split takes.
+ * Everything else as kv_attention. 16-bit types with head_size a multiple of 8,
+ * page_size a multiple of 8 and 16-byte aligned pages and tensors run on the tensor
+ * cores, others on CUDA cores.
+ */
+rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
+                               int32_t num_heads, int32_t kv_num_heads, int64_t head_size,
+                               const void* query, const void* k_pages, const void* v_pages,
+                               int64_t num_pages, int64_t page_size, int64_t page_stride,
+                               const int32_t* page_table, int64_t max_pages,
+                               const int32_t* past_seq_lens, const int32_t* query_starts, float scale,
+                               float softcap, int64_t window, const float* alibi_slopes,
+                               const int64_t* tree_masks, void* out, int32_t* status_flags,
+                               void* workspace, int64_t workspace_bytes, rope_stream_t stream);
+
+/* Bytes of workspace with which kv_attention_paged splits the keys of such a call as
+   planned; 0 where nothing is split, -1 for sizes that it refuses. A host function: no
+   CUDA call. */
+int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_query_len,
+                                     int32_t num_heads, int32_t kv_num_heads, int64_t head_size,
+                                     int64_t page_size, int64_t max_pages);
+
+/*
+ * kv_keep_paged -- after drafts were verified: of each sequence's new rows, the accepted
+ * ones move up behind the older ones, in K and V and for every key/value head. Row
+ * past_seq_lens[b] + kept[b, i] goes to past_seq_lens[b] + i, for i < kept_lens[b]; the
+ * caller's next past_seq_lens is that much larger.
+ *
+ * kept      device int32 (batch, max_kept): which new rows, ascending (a path of a tree
+ *           whose nodes come behind their parents).
+ * kept_lens device int32 (batch), at most max_kept.
+ * A sequence whose kept rows do not ascend, or lie outside its page table or in a page
+ * outside the pool, stays as it is and sets status bit 2, as does one whose count is
+ * negative or above max_kept.
+ * ROPE_ERR_INVALID_ARG as rope_apply_qkv_paged; batch * kv_num_heads * head_size is
+ * limited to 2^40, max_kept to 2^20.
+ */
+rope_status kv_keep_paged(rope_dtype dtype, int64_t batch, int32_t kv_num_heads, int64_t head_size,
+                          void* k_pages, void* v_pages, int64_t num_pages, int64_t page_size,
+                          int64_t page_stride, const int32_t* page_table, int64_t max_pages,
+                          const int32_t* past_seq_lens, const int32_t* kept, int64_t max_kept,
+                          const int32_t* kept_lens, int32_t* status_flags, rope_stream_t stream);
+
 /* Static name of a status code. */
 const char* rope_status_string(rope_status status);
 
@@ -592,8 +713,10 @@ const char* rope_last_error(void);
    "rope_qkv_heads_kernel" (SIMT Q/K, several heads of one role per thread),
    "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
    (8-bit append), "kv_token_kernel" (attention, few rows), "kv_tile_kernel"
-   (attention, many rows) or "kv_simple_kernel"
-   (attention on CUDA cores); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
+   (attention, many rows), "kv_simple_kernel"
+   (attention on CUDA cores), "paged_append_kernel", "paged_token_kernel", "paged_tile_kernel",
+   "paged_simple_kernel" or "paged_keep_kernel" (the same over pages; with both few rows and many the
+   last to be launched); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.
    The string is static; never free it. */
 const char* rope_last_kernel(void);

@@ -20,6 +20,7 @@ __all__ = [
     "mrope_apply_stream_map", "mrope_stream_map", "rope_apply_fused", "rope_cache_build",
     "rope_apply_qkv", "mrope_apply_qkv", "rope_apply_qkv_fp8", "kv_attention", "kv_attention_fp8",
     "kv_attention_workspace", "kv_cache_fp8",
+    "rope_apply_qkv_paged", "kv_attention_paged", "kv_attention_paged_workspace", "kv_keep_paged", "kv_cache_paged",
     "set_variant", "get_variant", "variant",
     "ROPE_OK", "ROPE_ERR_INVALID_ARG", "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_CUDA",
 ]
@@ -69,6 +70,12 @@ SIGNATURES = {
     "kv_attention_fp8": [_i32, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _f32, _f32, _vp,
                          _vp, _vp, _vp, _vp, _vp, _i64, _vp],
     "kv_attention_workspace": [_i64, _i64, _i32, _i32, _i64, _i64],
+    "rope_apply_qkv_paged": [_i32, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _i64, _vp,
+                             _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp],
+    "kv_attention_paged": [_i32, _i64, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
+                           _vp, _f32, _f32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+    "kv_attention_paged_workspace": [_i64, _i64, _i64, _i32, _i32, _i64, _i64, _i64],
+    "kv_keep_paged": [_i32, _i64, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp],
     "rope_set_variant": [_i32],
     "rope_get_variant": [],
     "rope_status_string": [_i32],
@@ -76,7 +83,8 @@ SIGNATURES = {
     "rope_last_kernel": [],
 }
 _RESTYPES = {"rope_status_string": ctypes.c_char_p, "rope_last_error": ctypes.c_char_p,
-             "rope_last_kernel": ctypes.c_char_p, "kv_attention_workspace": _i64}
+             "rope_last_kernel": ctypes.c_char_p, "kv_attention_workspace": _i64,
+             "kv_attention_paged_workspace": _i64}
 
 
 class RopeError(RuntimeError):
@@ -610,13 +618,14 @@ def kv_attention_workspace(batch, seq, num_heads, kv_num_heads, head_size, max_c
 _workspace_bytes = {}
 
 
-def _workspace(lib, key):
-    """kv_attention_workspace of a call's sizes, asked for once (it follows from them and the variant)."""
+def _workspace(fn, key):
+    """A call's workspace by its sizes, asked for once (it follows from them and the variant); each function
+    has keys of a length of its own."""
     n = _workspace_bytes.get(key)
     if n is None:
         if len(_workspace_bytes) > 4096:
             _workspace_bytes.clear()
-        n = _workspace_bytes[key] = lib.kv_attention_workspace(*key)
+        n = _workspace_bytes[key] = fn(*key)
     return n
 
 
@@ -667,7 +676,7 @@ def _attention(name, query, k_cache, v_cache, scales, past_seq_lens, num_heads, 
     if out is None:
         out = torch.empty_like(query)
     if workspace is None:
-        need = _workspace(lib, (B, S, num_heads, N, H, L))
+        need = _workspace(lib.kv_attention_workspace, (B, S, num_heads, N, H, L))
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     room = 0 if workspace is None else workspace.numel()
@@ -704,6 +713,218 @@ def kv_attention_fp8(query, k_cache, v_cache, k_scale, v_scale, past_seq_lens, *
     """kv_attention over the 8-bit caches and scales of rope_apply_qkv_fp8."""
     return _attention("kv_attention_fp8", query, k_cache, v_cache, (k_scale, v_scale), past_seq_lens, num_heads,
                       scale, softcap, alibi_slopes, document_ids, prefix_lens, out, status, workspace, stream)
+
+
+# --------------------------------------------------------------------------
+# Caches held in pages
+# --------------------------------------------------------------------------
+
+def kv_cache_paged(num_pages, kv_num_heads, page_size, head_size, dtype=None, device=None):
+    """Empty pages for rope_apply_qkv_paged: (k_pages, v_pages), each (num_pages, kv_num_heads, page_size,
+    head_size)."""
+    import torch
+
+    shape = (num_pages, kv_num_heads, page_size, head_size)
+    device = torch.device("cuda") if device is None else device
+    return tuple(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2))
+
+
+def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32):
+    """The shape of the pages and the elements between them; the table and the lengths checked."""
+    plane = k_pages.shape
+    if len(plane) != 4:
+        raise ValueError("k_pages must be (num_pages, kv_num_heads, page_size, head_size)")
+    B = page_table.shape[0] if page_table.dim() == 2 else -1
+    if at < 0 or not (_fits(k_pages, at, plane, T) and _fits(v_pages, at, plane, T)
+                      and _fits(past_seq_lens, at, (B,), i32) and _fits(page_table, at, page_table.shape, i32)):
+        if B < 0:
+            raise ValueError("page_table must be (B, max_pages)")
+        _shaped("page_table", page_table, query, page_table.shape, i32)
+        _shaped("past_seq_lens", past_seq_lens, query, (B,), i32)
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.shape != plane or t.dtype != T or not t.is_cuda or t.device != query.device:
+                raise ValueError(f"{name} must be a {T} tensor of shape {tuple(plane)} on {query.device}")
+            if t.numel() and not t[0].is_contiguous():
+                raise ValueError(f"{name} must be contiguous within a page")
+        if plane[0] > 1 and k_pages.stride(0) != v_pages.stride(0):
+            raise ValueError("k_pages and v_pages must have the same stride between pages")
+    within = plane[1] * plane[2] * plane[3]
+    stride = k_pages.stride(0) if plane[0] > 1 else within
+    if stride < within:
+        raise ValueError("pages must not overlap")
+    return plane, stride, B
+
+
+def _tokens_of(name, query, query_starts, B, at, i32):
+    """(tokens, hidden) of query: (tokens, hidden) with query_starts, (B, S, hidden) without."""
+    if query_starts is None:
+        if query.dim() != 3 or query.shape[0] != B:
+            raise ValueError(f"{name} must be (B, S, hidden) with the batch of page_table, or come with query_starts")
+        return B * query.shape[1], query.shape[2]
+    if query.dim() != 2:
+        raise ValueError(f"{name} must be (tokens, hidden) with query_starts")
+    if not _fits(query_starts, at, (B + 1,), i32):
+        _shaped("query_starts", query_starts, query, (B + 1,), i32)
+    return query.shape
+
+
+def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_heads, kv_num_heads, k_pages, v_pages,
+                         page_table, past_seq_lens, query_starts=None, key=None, value=None, interleaved=0,
+                         rotary_embedding_dim=0, q_out=None, status=None, q_norm_weight=None, k_norm_weight=None,
+                         epsilon=1e-6, stream=None):
+    """rope_apply_qkv in cache mode with caches held in pages (see ``rope_apply_qkv_paged`` in include/rope.h).
+
+    query is (tokens, num_heads*H) with query_starts (int32 (B + 1)), or (B, S, num_heads*H) without, packed
+    [Q|K|V] where key and value are None; position_ids has its leading dimensions. k_pages and v_pages
+    (num_pages, kv_num_heads, page_size, H) are updated in place; page_table is int32 (B, max_pages). Returns
+    q_out."""
+    lib = load_library()
+    T, dev, at = query.dtype, query.device, query.get_device()
+    torch, code = _torch_code(T)
+    i32 = torch.int32
+    (P, N, ps, H), stride, B = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
+    tokens, hidden = _tokens_of("query", query, query_starts, B, at, i32)
+    lead = query.shape[:-1]
+    packed = key is None and value is None
+    if N != kv_num_heads:
+        raise ValueError(f"k_pages hold {N} heads, kv_num_heads is {kv_num_heads}")
+    if hidden != (num_heads + (2 * kv_num_heads if packed else 0)) * H:
+        raise ValueError(f"query hidden size {hidden} is not that of the heads of {H}")
+    if cos_cache.dim() != 2:
+        raise ValueError("cos_cache must be (rows, rd/2)")
+    table = (cos_cache.shape[0], (rotary_embedding_dim or H) // 2)
+    if not (query.is_contiguous() and _fits(cos_cache, at, table, T) and _fits(sin_cache, at, table, T)):
+        _shaped("query", query, query, query.shape, T)
+        _shaped("cos_cache", cos_cache, query, table, T)
+        _shaped("sin_cache", sin_cache, query, table, T)
+    if not packed:
+        _shaped("key", key, query, (*lead, N * H), T)
+        _shaped("value", value, query, (*lead, N * H), T)
+    if q_norm_weight is not None or k_norm_weight is not None:
+        _shaped("q_norm_weight", q_norm_weight, query, (H,), T)
+        _shaped("k_norm_weight", k_norm_weight, query, (H,), T)
+    if position_ids is not None:
+        _shaped("position_ids", position_ids, query, lead, torch.int64)
+    if q_out is not None:
+        _shaped("q_out", q_out, query, (*lead, num_heads * H), T)
+    if status is not None:
+        _shaped("status", status, query, status.shape, i32)
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return rope_apply_qkv_paged(
+                query, cos_cache, sin_cache, position_ids, num_heads=num_heads, kv_num_heads=kv_num_heads,
+                k_pages=k_pages, v_pages=v_pages, page_table=page_table, past_seq_lens=past_seq_lens,
+                query_starts=query_starts, key=key, value=value, interleaved=interleaved,
+                rotary_embedding_dim=rotary_embedding_dim, q_out=q_out, status=status, q_norm_weight=q_norm_weight,
+                k_norm_weight=k_norm_weight, epsilon=epsilon)
+    if q_out is None:
+        q_out = torch.empty((*lead, num_heads * H), dtype=T, device=dev)
+    st = lib.rope_apply_qkv_paged(
+        code, B, tokens, num_heads, N, H, query.data_ptr(), _address(key), _address(value), _address(q_norm_weight),
+        _address(k_norm_weight), epsilon, cos_cache.data_ptr(), sin_cache.data_ptr(), table[0], _address(position_ids),
+        past_seq_lens.data_ptr(), _address(query_starts), page_table.data_ptr(), page_table.shape[1], int(interleaved),
+        rotary_embedding_dim, q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), P, ps, stride, _address(status),
+        torch._C._cuda_getCurrentRawStream(at))
+    if st:
+        _check("rope_apply_qkv_paged", st)
+    return q_out
+
+
+def kv_attention_paged_workspace(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size,
+                                 max_pages):
+    """Bytes of workspace that kv_attention_paged uses for such a call."""
+    n = load_library().kv_attention_paged_workspace(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size,
+                                                    page_size, max_pages)
+    if n < 0:
+        _check("kv_attention_paged_workspace", ROPE_ERR_INVALID_ARG)
+    return n
+
+
+def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, num_heads, query_starts=None,
+                       max_query_len=None, scale=None, softcap=0.0, window=0, alibi_slopes=None, tree_masks=None,
+                       out=None, status=None, workspace=None, stream=None):
+    """Attention of each sequence's new tokens over caches held in pages (see ``kv_attention_paged`` in
+    include/rope.h), after rope_apply_qkv_paged with the same lengths and table.
+
+    query is (tokens, num_heads*H) with query_starts (int32 (B + 1)), or (B, S, num_heads*H) without.
+    max_query_len: at least the longest sequence's new tokens; None: as many as there are tokens, which plans
+    worse (with 64 or more tokens tree_masks want it given). tree_masks: int64, one word a token, bit t: new token
+    t of its sequence is seen. scale: 1/sqrt(H) if None. workspace: uint8 device memory of
+    ``kv_attention_paged_workspace`` bytes, or None to take it from PyTorch's allocator. Returns out."""
+    lib = load_library()
+    T, dev, at = query.dtype, query.device, query.get_device()
+    torch, code = _torch_code(T)
+    i32 = torch.int32
+    (P, N, ps, H), stride, B = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
+    tokens, hidden = _tokens_of("query", query, query_starts, B, at, i32)
+    if hidden != num_heads * H or not query.is_contiguous():
+        _shaped("query", query, query, (*query.shape[:-1], num_heads * H), T)
+    if max_query_len is None or query_starts is None:
+        most = tokens if query_starts is not None else query.shape[1]
+        if max_query_len not in (None, most):
+            raise ValueError(f"max_query_len must be {most} without query_starts, got {max_query_len}")
+        max_query_len = most
+    if alibi_slopes is not None:
+        _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), torch.float32)
+    if tree_masks is not None:
+        _shaped("tree_masks", tree_masks, query, query.shape[:-1], torch.int64)
+    if out is not None:
+        _shaped("out", out, query, query.shape, T)
+    if status is not None:
+        _shaped("status", status, query, status.shape, i32)
+    if workspace is not None:
+        _shaped("workspace", workspace, query, workspace.shape, torch.uint8)
+    if scale is None:
+        scale = max(H, 1) ** -0.5
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, num_heads=num_heads,
+                                      query_starts=query_starts, max_query_len=max_query_len, scale=scale,
+                                      softcap=softcap, window=window, alibi_slopes=alibi_slopes, tree_masks=tree_masks,
+                                      out=out, status=status, workspace=workspace)
+    if out is None:
+        out = torch.empty_like(query)
+    wide = page_table.shape[1]
+    if workspace is None:
+        need = _workspace(lib.kv_attention_paged_workspace, (B, tokens, max_query_len, num_heads, N, H, ps, wide))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib.kv_attention_paged(
+        code, B, tokens, max_query_len, num_heads, N, H, query.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), P, ps,
+        stride, page_table.data_ptr(), wide, past_seq_lens.data_ptr(), _address(query_starts), scale, softcap, window,
+        _address(alibi_slopes), _address(tree_masks), out.data_ptr(), _address(status), _address(workspace),
+        0 if workspace is None else workspace.numel(), torch._C._cuda_getCurrentRawStream(at))
+    if st:
+        _check("kv_attention_paged", st)
+    return out
+
+
+def kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, *, status=None, stream=None):
+    """After drafts were verified: row past_seq_lens[b] + kept[b, i] of each sequence goes to past_seq_lens[b] + i
+    for i < kept_lens[b], in k_pages and v_pages (see ``kv_keep_paged`` in include/rope.h). kept is int32 (B,
+    max_kept), ascending; kept_lens int32 (B). The next past_seq_lens is past_seq_lens + kept_lens."""
+    lib = load_library()
+    T, dev, at = k_pages.dtype, k_pages.device, k_pages.get_device()
+    torch, code = _torch_code(T)
+    i32 = torch.int32
+    (P, N, ps, H), stride, B = _paged(k_pages, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
+    if kept.dim() != 2:
+        raise ValueError("kept must be (B, max_kept)")
+    wide = kept.shape[1]
+    if not (_fits(kept, at, (B, wide), i32) and _fits(kept_lens, at, (B,), i32)):
+        _shaped("kept", kept, k_pages, (B, wide), i32)
+        _shaped("kept_lens", kept_lens, k_pages, (B,), i32)
+    if status is not None:
+        _shaped("status", status, k_pages, status.shape, i32)
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, status=status)
+    st = lib.kv_keep_paged(
+        code, B, N, H, k_pages.data_ptr(), v_pages.data_ptr(), P, ps, stride, page_table.data_ptr(),
+        page_table.shape[1], past_seq_lens.data_ptr(), kept.data_ptr(), wide, kept_lens.data_ptr(), _address(status),
+        torch._C._cuda_getCurrentRawStream(at))
+    if st:
+        _check("kv_keep_paged", st)
 
 
 def set_variant(name):

@@ -1,0 +1,359 @@
+// C ABI of the operators over paged caches: rope_apply_qkv_paged,
+// kv_attention_paged and kv_keep_paged (include/rope.h). Argument checks, choice of
+// kernel, launch geometry. Nothing is allocated or kept, nothing waits, and every
+// check comes before any CUDA call.
+#include "kv_host.h"
+#include "kv_maps.h"
+#include "paged_internal.h"
+
+using namespace rope_gb300;
+
+namespace {
+
+rope_status check_heads(int64_t batch, int64_t tokens, int32_t num_heads, int32_t kv_num_heads) {
+  if (batch < 0 || tokens < 0) return fail(ROPE_ERR_INVALID_ARG, "batch and tokens must be >= 0");
+  if (batch > kMaxLen || tokens > kMaxLen) return fail(ROPE_ERR_UNSUPPORTED, "batch and tokens are limited to 2^30");
+  if (num_heads < 1 || kv_num_heads < 1)
+    return fail(ROPE_ERR_INVALID_ARG, "num_heads (%d) and kv_num_heads (%d) must be >= 1", num_heads, kv_num_heads);
+  if (num_heads % kv_num_heads)
+    return fail(ROPE_ERR_INVALID_ARG, "kv_num_heads %d does not divide num_heads %d", kv_num_heads, num_heads);
+  if (kv_num_heads > 65535) return fail(ROPE_ERR_UNSUPPORTED, "kv_num_heads is limited to 65535");
+  return ROPE_OK;
+}
+
+rope_status check_table(int64_t batch, int64_t page_size, int64_t max_pages) {
+  if (page_size < 1 || max_pages < 1) return fail(ROPE_ERR_INVALID_ARG, "page_size and max_pages must be >= 1");
+  if (page_size > kMaxLen || max_pages > kMaxLen || page_size * max_pages > kMaxLen)
+    return fail(ROPE_ERR_UNSUPPORTED, "max_pages * page_size is limited to 2^30");
+  if (!sizes_fit({batch, max_pages, 4})) return fail(ROPE_ERR_INVALID_ARG, "page_table is too large");
+  return ROPE_OK;
+}
+
+rope_status check_pages(int32_t kv_num_heads, int64_t head_size, int64_t num_pages, int64_t page_size,
+                        int64_t page_stride) {
+  if (num_pages < 1) return fail(ROPE_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if (num_pages > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "num_pages is limited to 2^31 - 1");
+  if (!sizes_fit({kv_num_heads, page_size, head_size}) || page_stride < (int64_t)kv_num_heads * page_size * head_size)
+    return fail(ROPE_ERR_INVALID_ARG, "page_stride is below kv_num_heads * page_size * head_size");
+  if (!sizes_fit({num_pages, page_stride, 8})) return fail(ROPE_ERR_INVALID_ARG, "the pages have more than 2^59 elements");
+  return ROPE_OK;
+}
+
+PagedBatch batch_of(int64_t batch, int64_t tokens, const int32_t* past, const int32_t* starts, const int32_t* table,
+                    int64_t max_pages, int64_t num_pages, int64_t page_size, int64_t page_stride, int32_t* status) {
+  PagedBatch s;
+  memset(&s, 0, sizeof(s));
+  s.starts = starts;
+  s.past = past;
+  s.table = table;
+  s.status = status;
+  s.T = tokens;
+  s.S = starts || batch == 0 ? 0 : tokens / batch;
+  s.page_stride = page_stride;
+  s.rows = max_pages * page_size;
+  s.B = (int32_t)batch;
+  s.max_pages = (int32_t)max_pages;
+  s.pages = (int32_t)num_pages;
+  s.ps = (int32_t)page_size;
+  s.most = INT32_MAX;
+  s.by_ps = div_of(page_size);
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+struct PagedPlan {
+  int64_t tiles = 0;        // row tiles of the longest sequence
+  bool few = false;         // 16 rows a tile
+  int splits = 1;
+  int64_t split_bytes = 0;  // workspace of one split
+  int64_t bytes = 0;
+};
+
+// From the sizes alone: the lengths are on the device.
+PagedPlan plan_simple(int64_t B, int64_t T, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
+  PagedPlan pl;
+  const int64_t G = Nq / Nkv, R = most * G;
+  pl.few = kv_simple_rows(R) == 16;
+  pl.tiles = (R + kv_simple_rows(R) - 1) / kv_simple_rows(R);
+  int64_t ctas = T * G / kv_simple_rows(R) + 1;  // tiles that have rows, at least
+  if (ctas < B && B <= T) ctas = B;
+  int64_t n = kv_simple_resident(H, R) * kSms / (ctas * Nkv);
+  if (n > (rows + 127) / 128) n = (rows + 127) / 128;
+  if (n > 128) n = 128;
+  pl.splits = n < 1 ? 1 : (int)n;
+  pl.split_bytes = T * Nq * (H * 4 + 8);
+  if (pl.splits > 1) pl.bytes = pl.splits * pl.split_bytes + kWorkspaceSlack;
+  return pl;
+}
+
+rope_status check_attention(int64_t batch, int64_t tokens, int64_t max_query_len, int32_t num_heads,
+                            int32_t kv_num_heads, int64_t head_size, int64_t page_size, int64_t max_pages) {
+  KV_TRY(check_heads(batch, tokens, num_heads, kv_num_heads));
+  if (head_size < 1) return fail(ROPE_ERR_INVALID_ARG, "head_size must be >= 1");
+  if (head_size > kKvMaxHead)
+    return fail(ROPE_ERR_UNSUPPORTED, "head_size %lld exceeds %d", (long long)head_size, kKvMaxHead);
+  KV_TRY(check_table(batch, page_size, max_pages));
+  if (max_query_len < 0 || max_query_len > tokens)
+    return fail(ROPE_ERR_INVALID_ARG, "max_query_len must be within [1, tokens]");
+  if (tokens > 0 && batch > 0 && max_query_len < 1)
+    return fail(ROPE_ERR_INVALID_ARG, "max_query_len must be within [1, tokens]");
+  if (!sizes_fit({tokens, num_heads, head_size, 1024})) return fail(ROPE_ERR_INVALID_ARG, "Q has more than 2^52 elements");
+  return ROPE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_query_len, int32_t num_heads,
+                                     int32_t kv_num_heads, int64_t head_size, int64_t page_size, int64_t max_pages) {
+  set_last_error("");
+  if (check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages) != ROPE_OK)
+    return -1;
+  if (batch == 0 || tokens == 0) return 0;
+  return plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size * max_pages).bytes;
+}
+
+rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
+                               int32_t num_heads, int32_t kv_num_heads, int64_t head_size, const void* query,
+                               const void* k_pages, const void* v_pages, int64_t num_pages, int64_t page_size,
+                               int64_t page_stride, const int32_t* page_table, int64_t max_pages,
+                               const int32_t* past_seq_lens, const int32_t* query_starts, float scale, float softcap,
+                               int64_t window, const float* alibi_slopes, const int64_t* tree_masks, void* out,
+                               int32_t* status_flags, void* workspace, int64_t workspace_bytes, rope_stream_t stream) {
+  set_last_error("");
+  KV_TRY(check_dtype(dtype));
+  KV_TRY(check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages));
+  KV_TRY(check_pages(kv_num_heads, head_size, num_pages, page_size, page_stride));
+  if (!query_starts && batch * max_query_len != tokens)
+    return fail(ROPE_ERR_INVALID_ARG, "without query_starts tokens must be batch * max_query_len");
+  if (!(std::fabs(scale) <= 0x1p100f)) return fail(ROPE_ERR_INVALID_ARG, "scale must be finite, at most 2^100 in magnitude");
+  if (!(softcap >= 0.0f && softcap < INFINITY))
+    return fail(ROPE_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
+  if (window < 0) return fail(ROPE_ERR_INVALID_ARG, "window must be >= 0 (0: none)");
+  if (tree_masks && (window > 0 || alibi_slopes))
+    return fail(ROPE_ERR_INVALID_ARG, "tree_masks go with neither window nor alibi_slopes");
+  if (tree_masks && max_query_len > 64) return fail(ROPE_ERR_INVALID_ARG, "tree_masks: max_query_len is at most 64");
+  if (workspace_bytes < 0) return fail(ROPE_ERR_INVALID_ARG, "workspace_bytes is negative");
+  if (batch == 0 || tokens == 0) return ROPE_OK;
+  const size_t es = dtype == ROPE_F32 ? 4 : 2;
+  KV_TRY(check_ptr(query, "query", es));
+  KV_TRY(check_ptr(k_pages, "k_pages", es));
+  KV_TRY(check_ptr(v_pages, "v_pages", es));
+  KV_TRY(check_ptr(page_table, "page_table", 4));
+  KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
+  KV_TRY(check_ptr(out, "out", es));
+  KV_TRY(check_optional(query_starts, "query_starts", 4));
+  KV_TRY(check_optional(alibi_slopes, "alibi_slopes", 4));
+  KV_TRY(check_optional(tree_masks, "tree_masks", 8));
+  KV_TRY(check_optional(status_flags, "status_flags", 4));
+  KV_TRY(check_optional(workspace, "workspace", 16));
+  if (out == query || out == k_pages || out == v_pages)
+    return fail(ROPE_ERR_INVALID_ARG, "out cannot alias query or the pages");
+
+  PagedParams p;
+  memset(&p, 0, sizeof(p));
+  p.s = batch_of(batch, tokens, past_seq_lens, query_starts, page_table, max_pages, num_pages, page_size, page_stride,
+                 status_flags);
+  p.s.most = (int32_t)max_query_len;
+  p.q = query;
+  p.k = k_pages;
+  p.v = v_pages;
+  p.out = out;
+  p.slopes = alibi_slopes;
+  p.masks = tree_masks;
+  p.Nq = num_heads;
+  p.Nkv = kv_num_heads;
+  p.G = num_heads / kv_num_heads;
+  p.H = (int32_t)head_size;
+  p.window = window > kMaxLen ? 0 : (int32_t)window;
+  p.by_g = div_of(p.G);
+  const int64_t per16 = 16 / (int64_t)es;
+  p.vec = head_size % per16 == 0 && page_stride % per16 == 0 && aligned(query, 16) && aligned(k_pages, 16) &&
+          aligned(v_pages, 16) && aligned(out, 16);
+  p.scale = scale;
+  // as kv_attention: a cap above 2^112 is as good as 2^112, a steepness above 2^125 as that
+  p.cap = fminf(softcap, 0x1p112f);
+  p.over = softcap > 0.0f ? fminf(fmaxf(scale / p.cap, -0x1p125f), 0x1p125f) : 0.0f;
+
+  PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, p.s.rows);
+  const int64_t fits =
+      workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
+  if (pl.splits > fits) pl.splits = fits > 1 ? (int)fits : 1;
+  p.splits = pl.splits;
+  if (pl.splits > 1) {
+    const int64_t rows = pl.splits * tokens * num_heads;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
+  }
+  void* args[] = {&p};
+  if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
+  const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, pl.few);
+  const dim3 grid((unsigned)(pl.tiles * pl.splits), kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
+  KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention_paged launch"));
+  if (pl.splits > 1) {
+    const int64_t rows = tokens * num_heads;
+    const int per = pl.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
+    int64_t gc = (rows + per - 1) / per;
+    if (gc > INT32_MAX) gc = INT32_MAX;
+    KV_TRY(launch(paged_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
+                  "kv_attention_paged launch (joining the splits)"));
+  }
+  set_last_kernel("paged_simple_kernel");
+  return ROPE_OK;
+}
+
+rope_status rope_apply_qkv_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int32_t num_heads,
+                                 int32_t kv_num_heads, int64_t head_size, const void* query, const void* key,
+                                 const void* value, const void* q_norm_weight, const void* k_norm_weight,
+                                 float epsilon, const void* cos_cache, const void* sin_cache, int64_t cache_rows,
+                                 const int64_t* position_ids, const int32_t* past_seq_lens,
+                                 const int32_t* query_starts, const int32_t* page_table, int64_t max_pages,
+                                 int32_t interleaved, int32_t rotary_embedding_dim, void* q_out, void* k_pages,
+                                 void* v_pages, int64_t num_pages, int64_t page_size, int64_t page_stride,
+                                 int32_t* status_flags, rope_stream_t stream) {
+  set_last_error("");
+  KV_TRY(check_dtype(dtype));
+  const bool norm = q_norm_weight || k_norm_weight;
+  if (norm && (!q_norm_weight || !k_norm_weight))
+    return fail(ROPE_ERR_INVALID_ARG, "RMSNorm needs both q_norm_weight and k_norm_weight");
+  if (norm && !(epsilon >= 0.0f && epsilon < INFINITY))
+    return fail(ROPE_ERR_INVALID_ARG, "epsilon must be finite and >= 0");
+  KV_TRY(check_heads(batch, tokens, num_heads, kv_num_heads));
+  if (head_size < 2 || head_size % 2) return fail(ROPE_ERR_INVALID_ARG, "head_size must be even and >= 2");
+  if (head_size > INT32_MAX / 4) return fail(ROPE_ERR_UNSUPPORTED, "head_size exceeds 2^29");
+  if (num_heads > INT32_MAX / 4) return fail(ROPE_ERR_UNSUPPORTED, "num_heads exceeds 2^29");
+  if (interleaved != 0 && interleaved != 1)
+    return fail(ROPE_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", interleaved);
+  if (cache_rows < 0) return fail(ROPE_ERR_INVALID_ARG, "cache_rows is negative");
+  const int64_t rd = rotary_embedding_dim ? rotary_embedding_dim : head_size;
+  if (rd < 2 || rd % 2 || rd > head_size)
+    return fail(ROPE_ERR_INVALID_ARG, "rotary_embedding_dim %d must be 0 or even, 0 < rd <= head size %lld",
+                rotary_embedding_dim, (long long)head_size);
+  KV_TRY(check_table(batch, page_size, max_pages));
+  KV_TRY(check_pages(kv_num_heads, head_size, num_pages, page_size, page_stride));
+  if (!query_starts && batch > 0 && tokens % batch)
+    return fail(ROPE_ERR_INVALID_ARG, "without query_starts batch must divide tokens");
+  const int64_t heads = (int64_t)num_heads + 2 * (int64_t)kv_num_heads;
+  if (!sizes_fit({tokens, heads, head_size, 8}) || !sizes_fit({cache_rows, rd, 8}))
+    return fail(ROPE_ERR_INVALID_ARG, "Q/K/V or the tables have more than 2^59 elements");
+  if (batch == 0 || tokens == 0) return ROPE_OK;
+  const bool packed = !key && !value;
+  if (!packed && (!key || !value)) return fail(ROPE_ERR_INVALID_ARG, "key and value come together (or packed in query)");
+  const size_t es = dtype == ROPE_F32 ? 4 : 2;
+  KV_TRY(check_ptr(query, "query", es));
+  if (!packed) {
+    KV_TRY(check_ptr(key, "key", es));
+    KV_TRY(check_ptr(value, "value", es));
+  }
+  KV_TRY(check_ptr(q_out, "q_out", es));
+  if (packed && q_out == query)
+    return fail(ROPE_ERR_INVALID_ARG, "q_out cannot alias a packed query (different row strides)");
+  KV_TRY(check_ptr(k_pages, "k_pages", es));
+  KV_TRY(check_ptr(v_pages, "v_pages", es));
+  KV_TRY(check_ptr(page_table, "page_table", 4));
+  KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
+  KV_TRY(check_optional(query_starts, "query_starts", 4));
+  if (cache_rows > 0) {
+    KV_TRY(check_ptr(cos_cache, "cos_cache", es));
+    KV_TRY(check_ptr(sin_cache, "sin_cache", es));
+  }
+  KV_TRY(check_optional(position_ids, "position_ids", 8));
+  KV_TRY(check_optional(status_flags, "status_flags", 4));
+  if (norm) {
+    KV_TRY(check_ptr(q_norm_weight, "q_norm_weight", es));
+    KV_TRY(check_ptr(k_norm_weight, "k_norm_weight", es));
+  }
+
+  const int64_t V16 = 16 / (int64_t)es;
+  bool vec = head_size % V16 == 0 && (rd / 2) % V16 == 0 && page_stride % V16 == 0;
+  for (const void* x : {query, key, value, (const void*)q_out, (const void*)k_pages, (const void*)v_pages, cos_cache,
+                        sin_cache, q_norm_weight, k_norm_weight})
+    vec = vec && aligned(x, 16);
+  const int64_t V = vec ? V16 : 1;
+  PagedAppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.s = batch_of(batch, tokens, past_seq_lens, query_starts, page_table, max_pages, num_pages, page_size, page_stride,
+                 status_flags);
+  p.q = query;
+  p.k = key;
+  p.v = value;
+  p.cos = cos_cache;
+  p.sin = sin_cache;
+  p.pos = position_ids;
+  p.qw = q_norm_weight;
+  p.kw = k_norm_weight;
+  p.q_out = q_out;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.cache_rows = cache_rows;
+  p.H = head_size;
+  p.Nq = num_heads;
+  p.Nkv = kv_num_heads;
+  p.packed = packed;
+  p.h = (int32_t)(rd / 2);
+  p.rd = (int32_t)rd;
+  p.nP = (int32_t)(p.h / V);
+  p.U = p.nP + (int32_t)((head_size - rd) / V);
+  p.lanes = p.U >= 32 ? 32 : pow2_at_least(p.U);
+  p.eps = epsilon;
+  const int64_t per = kPagedAppendThreads / p.lanes;
+  int64_t grid = (tokens * heads + per - 1) / per;
+  if (grid > INT32_MAX) grid = INT32_MAX;
+  void* args[] = {&p};
+  KV_TRY(launch(paged_append_kernel(dtype, vec, interleaved != 0, norm), dim3((unsigned)grid), kPagedAppendThreads, 0,
+                stream, args, "rope_apply_qkv_paged launch"));
+  set_last_kernel("paged_append_kernel");
+  return ROPE_OK;
+}
+
+rope_status kv_keep_paged(rope_dtype dtype, int64_t batch, int32_t kv_num_heads, int64_t head_size, void* k_pages,
+                          void* v_pages, int64_t num_pages, int64_t page_size, int64_t page_stride,
+                          const int32_t* page_table, int64_t max_pages, const int32_t* past_seq_lens,
+                          const int32_t* kept, int64_t max_kept, const int32_t* kept_lens, int32_t* status_flags,
+                          rope_stream_t stream) {
+  set_last_error("");
+  KV_TRY(check_dtype(dtype));
+  KV_TRY(check_heads(batch, 0, kv_num_heads, kv_num_heads));
+  if (head_size < 1) return fail(ROPE_ERR_INVALID_ARG, "head_size must be >= 1");
+  KV_TRY(check_table(batch, page_size, max_pages));
+  KV_TRY(check_pages(kv_num_heads, head_size, num_pages, page_size, page_stride));
+  if (max_kept < 0) return fail(ROPE_ERR_INVALID_ARG, "max_kept must be >= 0");
+  if (head_size > INT32_MAX / 4 || max_kept > 1 << 20 || !sizes_fit({batch, kv_num_heads, head_size, 1 << 22}))
+    return fail(ROPE_ERR_UNSUPPORTED, "batch * kv_num_heads * head_size is limited to 2^40, max_kept to 2^20");
+  if (batch == 0 || max_kept == 0) return ROPE_OK;
+  const size_t es = dtype == ROPE_F32 ? 4 : 2;
+  KV_TRY(check_ptr(k_pages, "k_pages", es));
+  KV_TRY(check_ptr(v_pages, "v_pages", es));
+  KV_TRY(check_ptr(page_table, "page_table", 4));
+  KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
+  KV_TRY(check_ptr(kept, "kept", 4));
+  KV_TRY(check_ptr(kept_lens, "kept_lens", 4));
+  KV_TRY(check_optional(status_flags, "status_flags", 4));
+
+  const int64_t per16 = 16 / (int64_t)es;
+  const bool vec = head_size % per16 == 0 && page_stride % per16 == 0 && aligned(k_pages, 16) && aligned(v_pages, 16);
+  const int64_t V = vec ? per16 : 1;
+  PagedKeepParams p;
+  memset(&p, 0, sizeof(p));
+  p.s = batch_of(batch, 0, past_seq_lens, nullptr, page_table, max_pages, num_pages, page_size, page_stride / V,
+                 status_flags);
+  p.k = k_pages;
+  p.v = v_pages;
+  p.kept = kept;
+  p.kept_lens = kept_lens;
+  p.width = (int32_t)max_kept;
+  p.Nkv = kv_num_heads;
+  p.units = head_size / V;
+  int64_t grid = (batch * 2 * kv_num_heads * p.units + kPagedKeepThreads - 1) / kPagedKeepThreads;
+  if (grid > INT32_MAX) grid = INT32_MAX;
+  void* args[] = {&p};
+  KV_TRY(launch(paged_keep_kernel(vec ? 16 : (int)es), dim3((unsigned)grid), kPagedKeepThreads, 0, stream, args,
+                "kv_keep_paged launch"));
+  set_last_kernel("paged_keep_kernel");
+  return ROPE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,89 @@
+// Internal interface between the C-ABI layer of the paged-cache operators
+// (paged_api.cu) and their kernels. Not installed; not part of the public ABI.
+#pragma once
+
+#include "kv_internal.h"
+
+namespace rope_gb300 {
+
+// A batch over caches held in pages. Sequence b has the tokens [starts[b],
+// starts[b + 1]) of T, or [b S, (b + 1) S); its row j is row j % ps of page
+// table[b, j / ps], a page holding (Nkv, ps, H) elements.
+struct PagedBatch {
+  const int32_t* starts;  // (B + 1), or null
+  const int32_t* past;    // (B)
+  const int32_t* table;   // (B, max_pages)
+  int32_t* status;
+  int64_t T, S;
+  int64_t page_stride;    // elements between pages
+  int64_t rows;           // max_pages * ps, below 2^30
+  int32_t B, max_pages, pages, ps;
+  int32_t most;           // longer sequences are left out (attention)
+  KvDiv by_ps;
+};
+
+// Attention. The G query heads of a key/value head and the n tokens of a sequence
+// are the n * G rows of one problem (b, kvh); a row of the batch is token * G + its
+// head in the group.
+struct PagedParams {
+  PagedBatch s;
+  const void* q;           // (T, Nq*H)
+  const void* k;           // pages
+  const void* v;
+  void* out;               // (T, Nq*H)
+  const float* slopes;     // (Nq), or null
+  const int64_t* masks;    // (T): bit t: new token t is seen; or null
+  float* ws_o;             // partial outputs, (Nkv, splits, T * G, H)
+  float2* ws_ml;           // and their (maximum, sum)
+  int32_t Nq, Nkv, G, H;
+  int32_t window;          // keys that a token sees, itself among them; 0: all
+  int32_t splits;
+  int32_t tiles;           // row tiles of the longest sequence (paged_simple_kernel)
+  int32_t vec;             // 16-byte loads of Q, K and V are aligned
+  KvDiv by_g;
+  float scale, cap, over;  // factor of q.k; 0: no cap; scale / cap
+};
+
+// Kernel entry points; each launch takes (PagedParams).
+KvSimpleKernel paged_simple_kernel(int dtype, int H, bool few);
+const void* paged_combine_kernel(int dtype);
+
+// Append: Q and K rotation, K and V to their pages.
+struct PagedAppendParams {
+  PagedBatch s;
+  const void* q;           // (T, Nq*H), or packed (T, (Nq + 2 Nkv)*H)
+  const void* k;           // (T, Nkv*H), or null when packed
+  const void* v;
+  const void* cos;         // (cache_rows, h)
+  const void* sin;
+  const int64_t* pos;      // (T), or null: the row of the cache
+  const void* qw;          // RMSNorm weights (H), or null
+  const void* kw;
+  void* q_out;             // (T, Nq*H)
+  void* k_pages;
+  void* v_pages;
+  int64_t cache_rows, H;
+  int32_t Nq, Nkv, packed;
+  int32_t h, rd;           // half rotary width, rotary width
+  int32_t U, nP;           // units of a head, pair units among them
+  int32_t lanes;           // threads that share a head (a power of two <= 32)
+  KvDiv by_rows;           // by Nq + 2 Nkv
+  float eps;
+};
+constexpr int kPagedAppendThreads = 256;
+const void* paged_append_kernel(int dtype, bool vec, bool interleaved, bool rms_norm);
+
+// Rows past + kept[b, i] of each sequence to past + i.
+struct PagedKeepParams {
+  PagedBatch s;
+  void* k;
+  void* v;
+  const int32_t* kept;       // (B, width)
+  const int32_t* kept_lens;  // (B)
+  int32_t width, Nkv;
+  int64_t units;             // of a row
+};
+constexpr int kPagedKeepThreads = 256;
+const void* paged_keep_kernel(int unit_bytes);
+
+}  // namespace rope_gb300
