@@ -3,8 +3,8 @@
 // kernel, launch geometry. Nothing is allocated or kept, nothing waits, and every
 // check comes before any CUDA call.
 #include "kv_host.h"
-#include "kv_maps.h"
 #include "paged_internal.h"
+#include "paged_maps.h"
 
 using namespace rope_gb300;
 
@@ -63,19 +63,22 @@ PagedBatch batch_of(int64_t batch, int64_t tokens, const int32_t* past, const in
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
+enum class PagedFamily { kSimple, kToken, kTile, kMixed };
+
 struct PagedPlan {
-  int64_t tiles = 0;        // row tiles of the longest sequence
-  bool few = false;         // 16 rows a tile
-  int splits = 1;
-  int64_t split_bytes = 0;  // workspace of one split
+  int64_t tiles = 0;        // kSimple, kTile: row tiles of the longest sequence
+  int64_t items = 0;        // kTile: row tiles of all sequences, at most
+  int splits = 1;           // kSimple, kTile: splits of the keys
+  int deal = 0, cluster = 0;  // kToken
+  int64_t split_bytes = 0;  // workspace of one split, or of one CTA that is dealt to
   int64_t bytes = 0;
 };
 
-// From the sizes alone: the lengths are on the device.
+// Everything from the sizes alone: the lengths are on the device.
+
 PagedPlan plan_simple(int64_t B, int64_t T, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
   PagedPlan pl;
   const int64_t G = Nq / Nkv, R = most * G;
-  pl.few = kv_simple_rows(R) == 16;
   pl.tiles = (R + kv_simple_rows(R) - 1) / kv_simple_rows(R);
   int64_t ctas = T * G / kv_simple_rows(R) + 1;  // tiles that have rows, at least
   if (ctas < B && B <= T) ctas = B;
@@ -86,6 +89,72 @@ PagedPlan plan_simple(int64_t B, int64_t T, int64_t most, int64_t Nq, int64_t Nk
   pl.split_bytes = T * Nq * (H * 4 + 8);
   if (pl.splits > 1) pl.bytes = pl.splits * pl.split_bytes + kWorkspaceSlack;
   return pl;
+}
+
+// Few problems of caches that are not long take a cluster of CTAs each, one launch
+// instead of two; else units of keys are dealt to as many CTAs as are resident.
+PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
+  PagedPlan pl;
+  const int64_t R = most * (Nq / Nkv), rt = R > 8 ? 16 : 8;
+  const int64_t problems = B * Nkv, units = (rows + 63) / 64;
+  pl.split_bytes = 2 * rt * (H * 4 + 8) + 16;
+  if (units > 1 && rows <= 4096) {
+    int n = pow2_at_least(units);
+    if (n > kKvClusterMost) n = kKvClusterMost;
+    if (problems * n <= kSms) pl.cluster = n;
+  }
+  if (!pl.cluster && units > 1 && B <= kKvDealMost && problems < (1ll << 31) / units) {
+    pl.deal = paged_token_ctas(H);
+    if (pl.deal > problems * units) pl.deal = (int)(problems * units);
+    pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
+  }
+  return pl;
+}
+
+// `lone`: every sequence is this kernel's.
+PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, bool lone, int64_t Nq, int64_t Nkv, int64_t H,
+                    int64_t rows) {
+  PagedPlan pl;
+  const int64_t G = Nq / Nkv, tr = kv_tile_rows(H);
+  pl.tiles = (most * G + tr - 1) / tr;
+  int64_t least;  // tiles that there are at least
+  if (ragged) {
+    // a sequence has one tile more than its rows fill, and more than kPagedFewRows rows
+    // where the others are paged_token_kernel's
+    const int64_t seqs = lone ? B : T * G / (kPagedFewRows + 1);
+    pl.items = T * G / tr + (seqs < B ? seqs : B);
+    if (pl.items > B * pl.tiles) pl.items = B * pl.tiles;
+    least = T * G / tr;
+    if (lone && least < B) least = B;
+  } else {
+    pl.items = least = B * pl.tiles;
+  }
+  int64_t n = kSms / ((least > 0 ? least : 1) * Nkv);
+  if (n > (rows + 511) / 512) n = (rows + 511) / 512;
+  if (n > 128) n = 128;
+  pl.splits = n < 1 ? 1 : (int)n;
+  pl.split_bytes = T * Nq * (H * 4 + 8);
+  if (pl.splits > 1) pl.bytes = pl.splits * pl.split_bytes + kWorkspaceSlack;
+  return pl;
+}
+
+// The matrix kernels take 16-bit types whose rows are 16-byte aligned, in pages that
+// TMA copies in boxes of 8 rows and more. Up to 16 rows of a problem go to the kernel
+// for few rows. Where some sequences may have no more than that and others do, both
+// kernels run, unless the short ones are so few that their CTAs of the kernel for many
+// rows fit beside the others', or the tokens are drafts, whose trees are much alike.
+PagedFamily choose_paged(bool matrix, int64_t B, int64_t T, int64_t most, bool ragged, bool trees, int64_t G, int64_t Nkv,
+                         int64_t H) {
+  if (!matrix || rope_get_variant() == ROPE_VARIANT_SIMT) return PagedFamily::kSimple;
+  const bool token = B * Nkv <= INT32_MAX / kKvClusterMost;
+  if (most * G <= kPagedFewRows) return token ? PagedFamily::kToken : PagedFamily::kSimple;
+  const int64_t tr = kv_tile_rows(H);
+  if (!sizes_fit({T * G / tr + B, Nkv * 128 * 2}) || (T * G / tr + B) * Nkv > INT32_MAX / 128) return PagedFamily::kSimple;
+  if (!ragged || B == 1 || trees || !token) return PagedFamily::kTile;
+  // T <= (B - s) most + s short for s sequences of `short` tokens
+  const int64_t shorts = kPagedFewRows / G < 1 ? 1 : kPagedFewRows / G;
+  const int64_t s = most > shorts ? (B * most - T) / (most - shorts) : B;
+  return s * Nkv <= kSms ? PagedFamily::kTile : PagedFamily::kMixed;
 }
 
 rope_status check_attention(int64_t batch, int64_t tokens, int64_t max_query_len, int32_t num_heads,
@@ -113,7 +182,15 @@ int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_
   if (check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages) != ROPE_OK)
     return -1;
   if (batch == 0 || tokens == 0) return 0;
-  return plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size * max_pages).bytes;
+  // whichever kernels the types, alignments and arguments make the call take
+  const int64_t rows = page_size * max_pages;
+  int64_t most = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes;
+  auto more = [&](int64_t n) { most = n > most ? n : most; };
+  if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
+    for (int i = 0; i < 3; ++i)
+      more(plan_tile(batch, tokens, max_query_len, i > 0, i == 1, num_heads, kv_num_heads, head_size, rows).bytes);
+  more(plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes);
+  return most;
 }
 
 rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
@@ -178,30 +255,90 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
   p.cap = fminf(softcap, 0x1p112f);
   p.over = softcap > 0.0f ? fminf(fmaxf(scale / p.cap, -0x1p125f), 0x1p125f) : 0.0f;
 
-  PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, p.s.rows);
-  const int64_t fits =
-      workspace && workspace_bytes > kWorkspaceSlack ? (workspace_bytes - kWorkspaceSlack) / pl.split_bytes : 0;
-  if (pl.splits > fits) pl.splits = fits > 1 ? (int)fits : 1;
-  p.splits = pl.splits;
-  if (pl.splits > 1) {
-    const int64_t rows = pl.splits * tokens * num_heads;
-    p.ws_o = static_cast<float*>(workspace);
-    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + rows * head_size + (rows * head_size & 1));
+  const bool ragged = query_starts != nullptr;
+  const int64_t rows = p.s.rows;
+  const int64_t room = workspace && workspace_bytes > kWorkspaceSlack ? workspace_bytes - kWorkspaceSlack : 0;
+  PagedMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  bool matrix = p.vec && dtype != ROPE_F32 && page_size % 8 == 0;
+  PagedFamily family =
+      choose_paged(matrix, batch, tokens, max_query_len, ragged, tree_masks != nullptr, p.G, kv_num_heads, head_size);
+  if (family != PagedFamily::kSimple) {
+    p.chunk = 8;
+    while (p.chunk < kPagedBox && page_size % (p.chunk * 2) == 0) p.chunk *= 2;
+    if (!encode_paged_map(&maps.k, dtype == ROPE_BF16, k_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, p.chunk) ||
+        !encode_paged_map(&maps.v, dtype == ROPE_BF16, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, p.chunk))
+      family = PagedFamily::kSimple;
   }
-  void* args[] = {&p};
-  if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
-  const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, pl.few);
-  const dim3 grid((unsigned)(pl.tiles * pl.splits), kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
-  KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention_paged launch"));
-  if (pl.splits > 1) {
-    const int64_t rows = tokens * num_heads;
-    const int per = pl.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
-    int64_t gc = (rows + per - 1) / per;
+  p.mixed = family == PagedFamily::kMixed;
+  void* args[] = {&p, &maps};
+  auto splits_of = [&](const PagedPlan& pl) {
+    const int64_t fits = room / pl.split_bytes;
+    p.splits = pl.splits <= fits ? pl.splits : fits > 1 ? (int)fits : 1;
+    if (p.splits > 1) {
+      const int64_t n = p.splits * tokens * num_heads;
+      p.ws_o = static_cast<float*>(workspace);
+      p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size + (n * head_size & 1));
+    }
+    p.tiles = (int32_t)pl.tiles;
+  };
+  auto combine = [&]() -> rope_status {
+    if (p.splits <= 1) return ROPE_OK;
+    const int64_t n = tokens * num_heads;
+    const int per = p.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
+    int64_t gc = (n + per - 1) / per;
     if (gc > INT32_MAX) gc = INT32_MAX;
-    KV_TRY(launch(paged_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
-                  "kv_attention_paged launch (joining the splits)"));
+    return launch(paged_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
+                  "kv_attention_paged launch (joining the splits)");
+  };
+  if (family == PagedFamily::kSimple) {
+    const PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows);
+    if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
+    splits_of(pl);
+    const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, kv_simple_rows(max_query_len * p.G) == 16);
+    const dim3 grid((unsigned)(pl.tiles * p.splits), kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
+    KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention_paged launch"));
+    KV_TRY(combine());
+    set_last_kernel("paged_simple_kernel");
+    return ROPE_OK;
   }
-  set_last_kernel("paged_simple_kernel");
+  if (family != PagedFamily::kToken) {
+    const PagedPlan pl = plan_tile(batch, tokens, max_query_len, ragged, !p.mixed, num_heads, kv_num_heads, head_size, rows);
+    splits_of(pl);
+    const int kind = softcap > 0.0f || !(scale > 0.0f) ? kKvAnyScore : alibi_slopes ? kKvBiased : kKvPlain;
+    const KvTileKernel k =
+        dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
+    KV_TRY(launch(k.fn, dim3((unsigned)(pl.items * kv_num_heads * p.splits)), kKvTileThreads, k.smem, stream, args,
+                  "kv_attention_paged launch (many rows)", kKvTileRegisters));
+    KV_TRY(combine());
+    set_last_kernel("paged_tile_kernel");
+  }
+  if (family != PagedFamily::kTile) {
+    const int64_t most = p.mixed ? kPagedFewRows / p.G < 1 ? 1 : kPagedFewRows / p.G : max_query_len;
+    const PagedPlan pl = plan_token(batch, most, num_heads, kv_num_heads, head_size, rows);
+    const int64_t fits = room / pl.split_bytes;
+    p.rt = most * p.G > 8 ? 16 : 8;
+    p.cluster = pl.cluster;
+    // half of the planned CTAs at least, or each its own problem
+    p.deal = pl.deal <= fits ? pl.deal : fits * 2 >= pl.deal ? (int)fits : 0;
+    if (p.deal > 0) {
+      const int64_t n = 2 * (int64_t)p.deal * p.rt;
+      p.ws_o = static_cast<float*>(workspace);
+      p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size);
+      p.ws_join = reinterpret_cast<int4*>(p.ws_ml + n);  // 16-byte aligned: n is a multiple of 16
+    }
+    const PagedTokenKernel k = paged_token_kernel(dtype, (int)head_size, p.rt == 8);
+    const int64_t grid = p.deal ? p.deal : batch * kv_num_heads * (p.cluster ? p.cluster : 1);
+    KV_TRY(launch(k.fn, dim3((unsigned)grid), kPagedTokenThreads, p.cluster ? k.cluster_smem : k.smem, stream, args,
+                  "kv_attention_paged launch (few rows)", 0, p.cluster));
+    if (p.deal) {
+      // few problems, each of many parts: a CTA a row
+      const unsigned n = batch * kv_num_heads * 8 <= p.deal ? (unsigned)p.rt : 1;
+      KV_TRY(launch(k.join, dim3((unsigned)p.deal, n), kKvTokenThreads, 0, stream, args,
+                    "kv_attention_paged launch (joining the parts)"));
+    }
+    set_last_kernel("paged_token_kernel");
+  }
   return ROPE_OK;
 }
 

@@ -34,11 +34,16 @@ struct PagedParams {
   const float* slopes;     // (Nq), or null
   const int64_t* masks;    // (T): bit t: new token t is seen; or null
   float* ws_o;             // partial outputs, (Nkv, splits, T * G, H)
-  float2* ws_ml;           // and their (maximum, sum)
+  float2* ws_ml;           // and their (maximum, sum); or (2 * deal, rt, H)
+  int4* ws_join;           // (deal): the problem that a CTA leaves unfinished
   int32_t Nq, Nkv, G, H;
   int32_t window;          // keys that a token sees, itself among them; 0: all
   int32_t splits;
-  int32_t tiles;           // row tiles of the longest sequence (paged_simple_kernel)
+  int32_t tiles;           // row tiles of the longest sequence
+  int32_t mixed;           // sequences of up to kPagedFewRows rows are paged_token_kernel's, longer ones paged_tile_kernel's
+  int32_t chunk;           // rows of a box: of a page, and of a unit or tile of keys
+  int32_t deal, cluster;   // paged_token_kernel: CTAs that the work is dealt to, or those of a cluster a problem
+  int32_t rt;              // and rows of a part in the workspace (8 or 16)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;
   float scale, cap, over;  // factor of q.k; 0: no cap; scale / cap
@@ -47,6 +52,26 @@ struct PagedParams {
 // Kernel entry points; each launch takes (PagedParams).
 KvSimpleKernel paged_simple_kernel(int dtype, int H, bool few);
 const void* paged_combine_kernel(int dtype);
+
+// Up to kPagedFewRows rows a problem, 16-bit T, PagedParams.vec, ps a multiple of 8.
+// `few`: up to 8 rows. Launches take (PagedParams, PagedMaps): grid (deal), or (B * Nkv *
+// cluster), or (B * Nkv); then, if dealt, join with (PagedParams), grid (deal, rows that
+// take a CTA).
+struct PagedTokenKernel {
+  const void* fn;
+  const void* join;
+  size_t smem, cluster_smem;  // without clusters, with them
+};
+constexpr int kPagedFewRows = 16;
+constexpr int kPagedTokenThreads = 160;
+constexpr int kPagedBox = 64;  // most rows of a box
+constexpr int paged_token_ctas(int64_t H) { return 152 * (H > 128 ? 1 : 2); }  // that are resident
+PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
+
+// Any number of rows, the same types: tiles of kv_tile_rows(H) rows, grid (tiles * Nkv *
+// splits); the launch takes (PagedParams, PagedMaps).
+KvTileKernel paged_tile_kernel_f16(int H, int kind);
+KvTileKernel paged_tile_kernel_bf16(int H, int kind);
 
 // Append: Q and K rotation, K and V to their pages.
 struct PagedAppendParams {

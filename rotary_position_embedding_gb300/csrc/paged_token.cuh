@@ -1,0 +1,696 @@
+// Attention over a paged cache for few rows (single tokens, short drafts): up to 16
+// rows n * G of a (b, kvh), 16-bit T.
+//
+// Every cached byte is used once for 8 or 16 rows, so the pages' bandwidth is the
+// bound. A fifth warp brings units of 64 keys into a ring by TMA, box by box (a box:
+// the rows of a unit that lie in one page, 64 elements wide), and runs ahead of the
+// four that compute, across problems too: nothing that those do between two
+// problems (queries, joining, output) leaves the memory idle while the ring is
+// filling. 96 KB of ring and two CTAs an SM; 192 KB and one above H = 128.
+//
+// Both products run on mma.m16n8k16 with the keys on the 16-row side, so that a
+// group of up to 8 query heads fills the 8-column side:
+//   S^T = K Q^T   (16 keys x 8 rows),   O^T += V^T P^T   (16 dims x 8 rows);
+// a warp takes 16 keys of each unit. K and V lie in shared memory as TMA's 128-byte
+// swizzle leaves them: ldmatrix reads both without bank conflicts, V transposed.
+// P^T fragments come from S^T by movmatrix. Softmax: the running maximum moves only
+// where a score passes it by 8 (in log2), so weights stay below 2^8 and the common
+// unit costs one vote.
+//
+// A value that no row sees is zeroed before the product. Where one that only some
+// rows see is not finite, its zero weight in the others would make a NaN of it: the
+// rows are then done over again one by one (paged_careful_row).
+//
+// Dealing. CTA i takes the units [i U / n, (i + 1) U / n) of all U in the order of the
+// problems (sequence, head), whatever the lengths: a problem that one CTA has whole
+// goes to the output, the others' parts to the workspace (2 slots a CTA: its first
+// segment's, its last one's), with a word on the problem that the CTA begins and
+// leaves unfinished, for paged_join_kernel_t. Without (no workspace, or more than
+// kKvDealMost sequences) a CTA takes one problem. Few problems of caches that are not
+// long: a cluster of CTAs each, whose parts meet in shared memory, so there is one
+// launch and no workspace.
+#pragma once
+
+#include "kv_token.cuh"
+#include "paged_careful.cuh"
+#include "paged_maps.h"
+#include "rope_tma.cuh"
+
+namespace rope_gb300 {
+
+constexpr int kPagedWarps = 4;                   // that compute
+constexpr int kPagedUnit = 16 * kPagedWarps;     // keys of a unit
+
+template <int HD, int NB>
+struct PagedTokenCfg {
+  static constexpr int SLABS = HD / 64;
+  static constexpr int kHalf = SLABS * kPagedUnit * 128;  // bytes of K, and of V, in a stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = HD <= 64 ? 6 : 3;
+  static constexpr int kCtas = HD <= 128 ? 2 : 1;  // on an SM
+  static constexpr int kParts = NB * HD / 64;      // passes in which the warps' outputs meet
+  static constexpr int kCols = HD / kParts;        // dims of a pass
+  static constexpr int kMerge = kPagedWarps * NB * 8 * (kCols + 4) * 4;
+  static constexpr int kRing = kStage * kStages;
+  static constexpr int kSmem = 1024 + kRing + kMerge;
+  static constexpr int kClusterPart = NB * 8 * (HD + 4) * 4;  // more, in clusters
+  // 228 KB an SM; a CTA holds about 5 KB statically, and 1 KB is reserved for it
+  static_assert(kCtas * (kSmem + 6144) <= 228 * 1024, "CTAs that are resident");
+  static_assert(kSmem + kClusterPart + 5120 <= 227 * 1024, "a CTA of a cluster fits");
+};
+
+__device__ __forceinline__ void paged_tma(uint32_t dst, const CUtensorMap* map, int x, int row, int kvh, int page,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(kvh), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void paged_ldsm(uint32_t (&a)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void paged_ldsm_t(uint32_t (&a)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(at)
+               : "memory");
+}
+
+// Barrier of the computing warps.
+__device__ __forceinline__ void paged_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool paged_sync_or(bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"((uint32_t)x)
+      : "memory");
+  return y != 0;
+}
+
+// Keys [lo, end) of a sequence's problems, lo at the start of a unit; no units where
+// the kernel for many rows takes it, or where it has no tokens.
+struct PagedSpan {
+  int lo, end;
+  __device__ __forceinline__ int units() const { return end > lo ? (end - lo + kPagedUnit - 1) / kPagedUnit : 1; }
+};
+__device__ __forceinline__ bool paged_token_mine(const PagedParams& p, const PagedSeq& q) {
+  return q.n > 0 && (int64_t)q.n * p.G <= kPagedFewRows;
+}
+__device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, const PagedSeq& q) {
+  PagedSpan s;
+  s.lo = paged_first(p, q.past) / kPagedUnit * kPagedUnit;
+  s.end = paged_limit(p, q, (int64_t)q.past + q.n - 1);
+  return s;
+}
+
+struct PagedDeal {
+  const int32_t* before;  // units of one problem of the sequences before b, for each b, and of all
+  int total;              // units of all problems, below 2^31
+  __device__ __forceinline__ int first(const PagedParams& p, int cta) const {
+    return (int)((uint64_t)(uint32_t)cta * (uint32_t)total / (uint32_t)p.deal);
+  }
+  __device__ __forceinline__ int owner(const PagedParams& p, int unit) const {
+    return (int)((((uint64_t)(uint32_t)unit + 1) * (uint32_t)p.deal - 1) / (uint32_t)total);
+  }
+};
+
+// The units before each sequence, in shared memory; all threads come here.
+__device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* before, int32_t* warp_sum) {
+  constexpr int PER = kKvDealMost / 128;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int u[PER], sum = 0, pre = 0;
+  if (warp < kPagedWarps) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = tid * PER + i;
+      u[i] = 0;
+      if (b < p.s.B) {
+        const PagedSeq q = paged_seq(p.s, b);
+        if (paged_token_mine(p, q)) u[i] = paged_span(p, q).units();
+      }
+      sum += u[i];
+    }
+    pre = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    if (lane == 31) warp_sum[warp] = pre;
+  }
+  __syncthreads();
+  if (warp < kPagedWarps) {
+    int at = pre - sum;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (tid * PER + i <= p.s.B) before[tid * PER + i] = at;
+      at += u[i];
+    }
+    if (tid == 127 && p.s.B == kKvDealMost) before[p.s.B] = at;
+  }
+  __syncthreads();
+  PagedDeal d;
+  d.before = before;
+  d.total = before[p.s.B] * p.Nkv;
+  return d;
+}
+
+// The problems of a CTA, one after the other, and its units of each.
+struct PagedWork {
+  int at, last;      // units left (dealt)
+  int b, kvh, u0, u1;
+  PagedSeq seq;
+  PagedSpan span;
+  bool whole;        // all of the problem
+  __device__ __forceinline__ bool next(const PagedParams& p, const PagedDeal& d, int segment) {
+    if (p.deal > 0) {
+      if (at >= last) return false;
+      int x = 0, y = p.s.B;  // the sequence of unit `at`: before[x] <= . < before[y]
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (d.before[mid] * p.Nkv <= at)
+          x = mid;
+        else
+          y = mid;
+      }
+      b = x;
+      const int units = d.before[b + 1] - d.before[b], in = at - d.before[b] * p.Nkv;
+      kvh = (int)((uint32_t)in / (uint32_t)units);
+      u0 = in - kvh * units;
+      u1 = u0 + (last - at) < units ? u0 + (last - at) : units;
+      whole = u0 == 0 && u1 == units;
+      at += u1 - u0;
+      seq = paged_seq(p.s, b);
+      span = paged_span(p, seq);
+      return true;
+    }
+    if (segment > 0) return false;
+    const int ranks = p.cluster > 1 ? p.cluster : 1;
+    const int problem = (int)blockIdx.x / ranks, rank = (int)blockIdx.x - problem * ranks;
+    b = problem / p.Nkv;
+    kvh = problem - b * p.Nkv;
+    seq = paged_seq(p.s, b);
+    span = paged_span(p, seq);
+    const int units = paged_token_mine(p, seq) ? span.units() : 0;
+    u0 = (int)((int64_t)units * rank / ranks);
+    u1 = (int)((int64_t)units * (rank + 1) / ranks);
+    whole = ranks == 1;
+    return units > 0;
+  }
+};
+
+template <class T, int HD, int NB>
+__global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCtas)
+    paged_token_kernel_t(const PagedParams p, const __grid_constant__ PagedMaps maps) {
+  using C = PagedTokenCfg<HD, NB>;
+  using bits = typename Elem<T>::bits;
+  constexpr bool BF = kIsBf16<T>;
+  constexpr int KB = HD / 16;  // 16-dim blocks
+  extern __shared__ uint8_t paged_smem[];
+  __shared__ float s_m[kPagedWarps][NB * 8], s_l[kPagedWarps][NB * 8];
+  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kPagedWarps];
+  __shared__ float2 s_part[NB * 8];
+  __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
+  const uint32_t ring = (kv_smem(paged_smem) + 1023u) & ~1023u;
+  float* const merge = reinterpret_cast<float*>(paged_smem + (ring - kv_smem(paged_smem)) + C::kRing);
+  float* const part_smem = merge + C::kMerge / 4;  // in clusters
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(kv_smem(&s_full[i]), 1);
+      mbar_init(kv_smem(&s_empty[i]), kPagedWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == kPagedWarps * 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  PagedDeal deal;
+  deal.before = s_before;
+  deal.total = 0;
+  PagedWork work;
+  work.at = work.last = 0;
+  if (p.deal > 0) {
+    deal = paged_deal(p, s_before, s_sum);
+    if (deal.total > 0) {
+      work.at = deal.first(p, blockIdx.x);
+      work.last = deal.first(p, blockIdx.x + 1);
+    }
+    if (work.at >= work.last && tid < NB * 8) {
+      // no units: nothing begins here, and nothing of this CTA's counts where a
+      // problem's CTAs lie on both sides of it
+      if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+      p.ws_ml[2 * (int64_t)blockIdx.x * (NB * 8) + tid] = make_float2(-CUDART_INF_F, 0.0f);
+    }
+  } else {
+    __syncthreads();
+  }
+  // every sequence's lengths are looked at once
+  if (p.s.status)
+    for (int64_t b = (int64_t)blockIdx.x * kPagedTokenThreads + tid; b < p.s.B; b += (int64_t)gridDim.x * kPagedTokenThreads)
+      paged_flag_seq(p.s, (int)b, paged_seq(p.s, (int)b));
+  const int ranks = p.cluster > 1 ? p.cluster : 1;
+  bool ok = true;
+
+  if (warp == kPagedWarps) {
+    // ------------------------------------------------------------ K and V
+    const int chunks = kPagedUnit / p.chunk;         // boxes of a slab in a unit
+    const int mine = lane & (chunks - 1);            // this lane's rows of a unit
+    const int boxes = chunks * C::SLABS * 2;
+    int it = 0;
+    bool bad = false;
+    for (int segment = 0; ok && work.next(p, deal, segment); ++segment) {
+      const int base = work.span.lo + mine * p.chunk;
+      const int end = work.span.end;
+      const int32_t* table = p.s.table + (int64_t)work.b * p.s.max_pages;
+      const int seen = paged_first(p, work.seq.past);  // keys before this are nobody's
+      auto page_of = [&](int u, int* row) {
+        const int j = base + u * kPagedUnit;
+        if (u >= work.u1 || j >= end) return -2;
+        const int i = kv_div(j, p.s.by_ps);
+        *row = j - i * p.s.ps;
+        if (j + p.chunk <= seen) return -1;
+        const int page = __ldg(table + i);
+        if ((uint32_t)page < (uint32_t)p.s.pages) return page;
+        bad = true;
+        return -1;  // outside the pool: TMA fills in zeros
+      };
+      int row = 0, row_next = 0;
+      int page = page_of(work.u0, &row);
+      for (int u = work.u0; u < work.u1; ++u, ++it) {
+        const int page_next = page_of(u + 1, &row_next);
+        const int st = it % C::kStages;
+        if (it >= C::kStages) ok = mbar_wait(kv_smem(&s_empty[st]), (it / C::kStages - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t full = kv_smem(&s_full[st]);
+        // rows behind the keys are not copied: what lies there is nobody's
+        const int live = (end - (work.span.lo + u * kPagedUnit) + p.chunk - 1) / p.chunk;
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, (uint32_t)(live < 0 ? 0 : live < chunks ? live : chunks) * C::SLABS * 2 * p.chunk * 128);
+        __syncwarp();
+        if (page > -2) {
+          const uint32_t dst = ring + st * C::kStage + mine * p.chunk * 128;
+          for (int i = lane; i < boxes; i += 32) {
+            const int part = i / chunks;  // K's slabs, then V's
+            const int slab = part < C::SLABS ? part : part - C::SLABS;
+            paged_tma(dst + part * (kPagedUnit * 128), part < C::SLABS ? &maps.k : &maps.v, slab * 64, row, work.kvh, page, full);
+          }
+        }
+        page = page_next;
+        row = row_next;
+      }
+    }
+    if (bad && p.s.status) atomicOr(p.s.status, 4);
+    if (!ok) {  // what is on its way has to land before shared memory goes
+      for (int i = it - C::kStages < 0 ? 0 : it - C::kStages; i < it; ++i)
+        mbar_wait(kv_smem(&s_full[i % C::kStages]), (i / C::kStages) & 1);
+    }
+  } else {
+    const int g = lane >> 2, c = lane & 3;
+    // ldmatrix: this lane's row and 16-byte piece of a 16 x 16 block, swizzled
+    const int krow = (lane & 7) + (lane >> 3 & 1) * 8, vrow = (lane & 7) + (lane >> 4) * 8;
+    const uint32_t kat = (uint32_t)(warp * 16 + krow) * 128, kx = (uint32_t)((lane >> 4) ^ (lane & 7));
+    const uint32_t vat = (uint32_t)(warp * 16 + vrow) * 128 + C::kHalf, vx = (uint32_t)((lane >> 3 & 1) ^ (lane & 7));
+    int it = 0;
+    for (int segment = 0; ok && work.next(p, deal, segment); ++segment) {
+      const int b = work.b, kvh = work.kvh;
+      const PagedSeq& seq = work.seq;
+      const int rows_all = seq.n * p.G;
+      const int end = work.span.end;
+      // the one problem that may begin in this CTA and go on in others: paged_join_kernel_t's
+      if (p.deal > 0 && work.at >= work.last && tid == 0) {
+        const bool open = work.u0 == 0 && !work.whole;  // a problem that began before is another CTA's
+        const int units = work.span.units();
+        const int parts = open ? deal.owner(p, work.at - work.u1 + units - 1) - (int)blockIdx.x : 0;
+        p.ws_join[blockIdx.x] = make_int4(b, kvh, 0, 2 * parts + (segment > 0 ? 1 : 0));
+      }
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
+      const int part_ld = ranks > 1 ? HD + 4 : p.H;
+      float* const part_o = work.whole ? nullptr : ranks > 1 ? part_smem : p.ws_o + slot * (NB * 8) * p.H;
+      float2* const part_ml = work.whole ? nullptr : ranks > 1 ? s_part : p.ws_ml + slot * (NB * 8);
+      auto row_of = [&](int r) {
+        const int tok = kv_div(r, p.by_g);
+        return ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+      };
+      uint32_t qf[NB][KB][2];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int r = n * 8 + g;
+        const bits* src = static_cast<const bits*>(p.q) + (r < rows_all ? row_of(r) : 0);
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int d = k * 16 + h * 8 + 2 * c;
+            qf[n][k][h] = 0;
+            if (r < rows_all && d < p.H) qf[n][k][h] = __ldg(reinterpret_cast<const uint32_t*>(src + d));
+          }
+      }
+      // the rows whose scores this lane holds: 2c and 2c + 1 of each column tile
+      float slope[NB][2], m[NB][2], l[NB][2];
+      int pos[NB][2], lim[NB][2], from[NB][2];
+      uint64_t word[NB][2];
+      const float c1 = p.cap > 0.0f ? 2.0f * kLog2e * p.over : p.scale * kLog2e;
+      const float c2 = p.cap * kLog2e;
+      int full = 0x7fffffff, below = 0;  // keys in [below, full) are seen by every row
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = n * 8 + 2 * c + e;
+          const bool live = r < rows_all;
+          const int tok = live ? kv_div(r, p.by_g) : 0;
+          pos[n][e] = seq.past + tok;
+          lim[n][e] = live ? paged_limit(p, seq, pos[n][e]) : 0;
+          from[n][e] = paged_first(p, pos[n][e]);
+          word[n][e] = p.masks && live ? (uint64_t)__ldg(p.masks + seq.t0 + tok) : ~0ull;
+          slope[n][e] = p.slopes && live ? __ldg(p.slopes + kvh * p.G + (r - tok * p.G)) * kLog2e : 0.0f;
+          if (live) {
+            const int f = p.masks && seq.past < lim[n][e] ? seq.past : lim[n][e];
+            full = f < full ? f : full;
+            below = from[n][e] > below ? from[n][e] : below;
+          }
+          m[n][e] = -CUDART_INF_F;
+          l[n][e] = 0.0f;
+        }
+#pragma unroll
+      for (int o = 1; o <= 2; o *= 2) {
+        const int x = __shfl_xor_sync(0xffffffffu, full, o), y = __shfl_xor_sync(0xffffffffu, below, o);
+        full = x < full ? x : full;
+        below = y > below ? y : below;
+      }
+      float acc[KB][NB][4];
+#pragma unroll
+      for (int t = 0; t < KB; ++t)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
+      bool odd = false;  // an infinity or a NaN in a value that not every row sees
+
+      for (int u = work.u0; u < work.u1; ++u, ++it) {
+        const int st = it % C::kStages;
+        const int j0 = work.span.lo + u * kPagedUnit + warp * 16;
+        ok = mbar_wait(kv_smem(&s_full[st]), (it / C::kStages) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (j0 < end) {
+          const uint32_t at = ring + st * C::kStage;
+          float s[NB][4], s2[NB][4];  // two sums: half as long a chain of dependent products
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < KB; ++k) {
+            uint32_t a[4];
+            paged_ldsm(a, at + kat + (k >> 2) * (kPagedUnit * 128) + ((((2 * k) & 7) ^ kx) << 4));
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+              kv_mma<BF>(k & 1 ? s2[n] : s[n], a[0], a[1], a[2], a[3], qf[n][k][0], qf[n][k][1]);
+          }
+          const bool whole = j0 >= below && j0 + 16 <= full;  // uniform over the warp
+          uint32_t any0 = 0xffffffffu, any1 = 0xffffffffu;
+          bool seen0 = false, seen1 = false, moved = false;
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = (s[n][e] + s2[n][e]) * c1, y = (s[n][2 + e] + s2[n][2 + e]) * c1;
+              if (p.cap > 0.0f) {
+                x = kv_tanh_of(x) * c2;
+                y = kv_tanh_of(y) * c2;
+              }
+              if (p.slopes) {
+                const float dist = (float)(pos[n][e] - j0 - g);
+                x = fmaf(-slope[n][e], fabsf(dist), x);
+                y = fmaf(-slope[n][e], fabsf(dist - 8.0f), y);
+              }
+              if (!whole) {
+                auto see = [&](int j) {
+                  bool on = j >= from[n][e] && j < lim[n][e];
+                  if (p.masks && j >= seq.past) on = on && j - seq.past < 64 && (word[n][e] >> (j - seq.past) & 1);
+                  return on;
+                };
+                const bool a = see(j0 + g), d = see(j0 + g + 8);
+                x = a ? x : -CUDART_INF_F;
+                y = d ? y : -CUDART_INF_F;
+                seen0 |= a;
+                seen1 |= d;
+              }
+              s[n][e] = x;
+              s[n][2 + e] = y;
+              moved |= fmaxf(x, y) > m[n][e] + 8.0f;
+            }
+          if (!whole) {
+            any0 = __ballot_sync(0xffffffffu, seen0);
+            any1 = __ballot_sync(0xffffffffu, seen1);
+          }
+          if (any0 | any1) {  // keys that no row sees are left out
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float x = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+                  for (int o = 4; o <= 16; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                  x = fmaxf(m[n][e], x);
+                  const float a = x == -CUDART_INF_F ? 1.0f : kv_exp2(m[n][e] - x);
+                  m[n][e] = x;
+                  l[n][e] *= a;
+#pragma unroll
+                  for (int t = 0; t < KB; ++t) {
+                    acc[t][n][e] *= a;
+                    acc[t][n][2 + e] *= a;
+                  }
+                }
+            }
+            uint32_t pf[NB][2];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float base = m[n][e] == -CUDART_INF_F ? 0.0f : m[n][e];
+                w[e] = kv_exp2(s[n][e] - base);
+                w[2 + e] = kv_exp2(s[n][2 + e] - base);
+                l[n][e] += w[e] + w[2 + e];
+              }
+              pf[n][0] = kv_transpose8(kv_pack2<BF>(w[0], w[1]));
+              pf[n][1] = kv_transpose8(kv_pack2<BF>(w[2], w[3]));
+            }
+            // keys 2c, 2c + 1 (low, high half) and 2c + 8, 2c + 9: whether some row sees them
+            const uint32_t on0 = ((any0 >> (8 * c)) & 15u ? 0xffffu : 0u) | ((any0 >> (8 * c + 4)) & 15u ? 0xffff0000u : 0u);
+            const uint32_t on1 = ((any1 >> (8 * c)) & 15u ? 0xffffu : 0u) | ((any1 >> (8 * c + 4)) & 15u ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int t = 0; t < KB; ++t) {
+              uint32_t a[4];
+              paged_ldsm_t(a, at + vat + (t >> 2) * (kPagedUnit * 128) + ((((2 * t) & 7) ^ vx) << 4));
+              if (!whole) {
+                a[0] &= on0, a[1] &= on0, a[2] &= on1, a[3] &= on1;
+                if (seq.n > 1) odd |= kv_odd2<BF>(a[0]) || kv_odd2<BF>(a[1]) || kv_odd2<BF>(a[2]) || kv_odd2<BF>(a[3]);
+              }
+#pragma unroll
+              for (int n = 0; n < NB; ++n) kv_mma<BF>(acc[t][n], a[0], a[1], a[2], a[3], pf[n][0], pf[n][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_smem(&s_empty[st]));
+      }
+      if (paged_sync_or(!ok)) {
+        ok = false;
+        break;
+      }
+      const int lo = work.span.lo + work.u0 * kPagedUnit;
+      const int hi = work.span.lo + work.u1 * kPagedUnit < end ? work.span.lo + work.u1 * kPagedUnit : end;
+      if (paged_sync_or(odd)) {
+#pragma unroll 1
+        for (int r = warp; r < rows_all; r += kPagedWarps)
+          paged_careful_row<T>(p, seq, b, kvh, r, lo, hi, part_o ? part_o + r * part_ld : nullptr, part_ml + r, lane);
+      } else {
+        // join the warps: their O and statistics meet in shared memory, some dims at a time
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float sum = l[n][e];
+#pragma unroll
+            for (int o = 4; o <= 16; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (g == 0) s_m[warp][n * 8 + 2 * c + e] = m[n][e], s_l[warp][n * 8 + 2 * c + e] = sum;
+          }
+        constexpr int LD = C::kCols + 4, PT = C::kCols / 16;
+#pragma unroll
+        for (int part = 0; part < C::kParts; ++part) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float* o = merge + (warp * NB * 8 + n * 8 + 2 * c + e) * LD;
+#pragma unroll
+              for (int t = 0; t < PT; ++t) {
+                o[t * 16 + g] = acc[part * PT + t][n][e];
+                o[t * 16 + g + 8] = acc[part * PT + t][n][2 + e];
+              }
+            }
+          paged_sync();
+          for (int i = tid; i < NB * 8 * (C::kCols / 4); i += kPagedWarps * 32) {
+            const int r = i / (C::kCols / 4), in = (i % (C::kCols / 4)) * 4, d = part * C::kCols + in;
+            if (r >= rows_all || d >= p.H) continue;
+            float M = s_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kPagedWarps; ++w) M = fmaxf(M, s_m[w][r]);
+            float L = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kPagedWarps; ++w) {
+              const float lw = s_l[w][r];
+              if (s_m[w][r] == -CUDART_INF_F && lw == 0.0f) continue;
+              const float f = kv_exp2(s_m[w][r] - (M == -CUDART_INF_F ? 0.0f : M));
+              const float4 x = *reinterpret_cast<const float4*>(merge + (w * NB * 8 + r) * LD + in);
+              L = fmaf(lw, f, L);
+              o0 = fmaf(x.x, f, o0), o1 = fmaf(x.y, f, o1), o2 = fmaf(x.z, f, o2), o3 = fmaf(x.w, f, o3);
+            }
+            if (part_o) {
+              if (d == 0) part_ml[r] = make_float2(M, L);
+              *reinterpret_cast<float4*>(part_o + r * part_ld + d) = make_float4(o0, o1, o2, o3);
+            } else {
+              const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+              VecT<T, 4> y;
+              y.v[0] = Elem<T>::fromf(o0 * inv), y.v[1] = Elem<T>::fromf(o1 * inv);
+              y.v[2] = Elem<T>::fromf(o2 * inv), y.v[3] = Elem<T>::fromf(o3 * inv);
+              *reinterpret_cast<VecT<T, 4>*>(static_cast<bits*>(p.out) + row_of(r) + d) = y;
+            }
+          }
+          paged_sync();
+        }
+      }
+    }
+  }
+  if (!ok && p.s.status) atomicOr(p.s.status, 2);
+  if (ranks > 1) {
+    // the cluster's parts: each thread takes four dims of a row from all of them
+    const int problem = (int)blockIdx.x / ranks, rank = (int)blockIdx.x - problem * ranks;
+    const int b = problem / p.Nkv, kvh = problem - b * p.Nkv;
+    const PagedSeq seq = paged_seq(p.s, b);
+    const int rows_all = paged_token_mine(p, seq) ? seq.n * p.G : 0;
+    constexpr int LD = HD + 4;
+    __syncthreads();
+    kv_cluster_sync();
+    for (int i = rank * kPagedTokenThreads + tid; i < rows_all * (HD / 4); i += ranks * kPagedTokenThreads) {
+      const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
+      if (d >= p.H) continue;
+      const uint32_t at_ml = kv_smem(s_part + r), at_o = kv_smem(part_smem + r * LD + d);
+      float M = -CUDART_INF_F;
+      for (int n = 0; n < ranks; ++n) M = fmaxf(M, kv_cluster_ld2(kv_cluster_at(at_ml, n)).x);
+      const float base = M == -CUDART_INF_F ? 0.0f : M;
+      float L = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+      for (int n = 0; n < ranks; ++n) {
+        const float2 ml = kv_cluster_ld2(kv_cluster_at(at_ml, n));
+        const float4 x = kv_cluster_ld4(kv_cluster_at(at_o, n));
+        if (ml.x == -CUDART_INF_F && ml.y == 0.0f) continue;
+        const float f = kv_exp2(ml.x - base);
+        L = fmaf(ml.y, f, L);
+        o0 = fmaf(x.x, f, o0), o1 = fmaf(x.y, f, o1), o2 = fmaf(x.z, f, o2), o3 = fmaf(x.w, f, o3);
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      VecT<T, 4> y;
+      y.v[0] = Elem<T>::fromf(o0 * inv), y.v[1] = Elem<T>::fromf(o1 * inv);
+      y.v[2] = Elem<T>::fromf(o2 * inv), y.v[3] = Elem<T>::fromf(o3 * inv);
+      const int tok = kv_div(r, p.by_g);
+      const int64_t at = ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+      *reinterpret_cast<VecT<T, 4>*>(static_cast<bits*>(p.out) + at + d) = y;
+    }
+    kv_cluster_sync();  // no CTA leaves before its part has been read
+  }
+}
+
+// Joins the parts of the problems that paged_token_kernel_t dealt to several CTAs.
+// CTA (x, y): the problem that begins in CTA x there and goes on in others, if there
+// is one; its rows y, y + gridDim.y, ..; with more than 8 parts the four warps share
+// a row, else each takes rows of its own.
+template <class T>
+__global__ void __launch_bounds__(kKvTokenThreads) paged_join_kernel_t(const PagedParams p) {
+  using bits = typename Elem<T>::bits;
+  __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
+  pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 what = p.ws_join[blockIdx.x];  // b, kvh, -, 2 * further CTAs + slot
+  if (what.w < 2) return;
+  const int b = what.x, kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x;
+  // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
+  const bool shared_row = parts > 8;
+  const PagedSeq seq = paged_seq(p.s, b);
+  const int rows = seq.n * p.G;
+  const int dr = shared_row ? gridDim.y : gridDim.y * kTokWarps;
+  const int n0 = shared_row ? warp : 0, dn = shared_row ? kTokWarps : 1;
+  auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
+  for (int r = shared_row ? (int)blockIdx.y : (int)blockIdx.y * kTokWarps + warp; r < rows; r += dr) {
+    float M = -CUDART_INF_F;
+    for (int n = lane; n < parts; n += 32) M = fmaxf(M, p.ws_ml[slot_of(n) * p.rt + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -CUDART_INF_F ? 0.0f : M;
+    float L = 0.0f, acc[kKvMaxHead / 32];
+#pragma unroll
+    for (int j = 0; j < kKvMaxHead / 32; ++j) acc[j] = 0.0f;
+#pragma unroll 8
+    for (int n = n0; n < parts; n += dn) {
+      const int64_t s = slot_of(n);
+      const float2 ml = p.ws_ml[s * p.rt + r];
+      const float* o = p.ws_o + (s * p.rt + r) * p.H;
+      const float f = exp2f(ml.x - base);
+      L = fmaf(ml.y, f, L);
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+        if (lane * 4 + 128 * j < p.H) {
+          float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
+          if (ml.x == -CUDART_INF_F && ml.y == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // never written where a CTA had no units
+          acc[4 * j] = fmaf(x.x, f, acc[4 * j]);
+          acc[4 * j + 1] = fmaf(x.y, f, acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(x.z, f, acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(x.w, f, acc[4 * j + 3]);
+        }
+    }
+    const int tok = kv_div(r, p.by_g);
+    bits* y = static_cast<bits*>(p.out) + ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+    if (shared_row) {
+      __syncthreads();  // the previous row's sums have been read
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (lane * 4 + 128 * j < p.H) s_o[warp][lane * 4 + 128 * j + i] = acc[4 * j + i];
+      if (lane == 0) s_l[warp] = L;
+      __syncthreads();
+      L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      for (int d = threadIdx.x; d < p.H; d += kKvTokenThreads)
+        y[d] = Elem<T>::fromf(((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) * inv);
+    } else {
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+      for (int j = 0; j < kKvMaxHead / 128; ++j)
+        if (lane * 4 + 128 * j < p.H) {
+          VecT<T, 4> v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v.v[i] = Elem<T>::fromf(acc[4 * j + i] * inv);
+          *reinterpret_cast<VecT<T, 4>*>(y + lane * 4 + 128 * j) = v;
+        }
+    }
+  }
+}
+
+}  // namespace rope_gb300

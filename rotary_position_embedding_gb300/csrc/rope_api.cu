@@ -28,6 +28,7 @@
 
 #include "rope.h"
 #include "kv_maps.h"
+#include "paged_maps.h"
 #include "rope_internal.h"
 #include "rope_qkv_tma.cuh"
 #include "rope_tma.cuh"
@@ -959,6 +960,20 @@ bool rope_gb300::encode_kv_map(CUtensorMap* m, bool bf16, const void* base, int6
   const cuuint64_t strides[2] = {(cuuint64_t)H * 2, (cuuint64_t)(H * len * 2)};
   const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
   return encode_tiled()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rope_gb300::encode_paged_map(CUtensorMap* m, bool bf16, const void* base, int64_t H, int64_t ps, int64_t Nkv,
+                                  int64_t num, int64_t stride, int rows) {
+  if (!encode_tiled() || ps >= (1ll << 32) || num >= (1ll << 32) || H * ps * Nkv * 2 >= (1ll << 40) ||
+      stride * 2 >= (1ll << 40))
+    return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)H, (cuuint64_t)ps, (cuuint64_t)Nkv, (cuuint64_t)num};
+  const cuuint64_t strides[3] = {(cuuint64_t)H * 2, (cuuint64_t)(H * ps * 2), (cuuint64_t)stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return encode_tiled()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
