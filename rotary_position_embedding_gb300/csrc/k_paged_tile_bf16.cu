@@ -3,6 +3,6 @@
 
 namespace rope_gb300 {
 
-KvTileKernel paged_tile_kernel_bf16(int H, int kind) { return paged_tile_pick<__nv_bfloat16>(H, kind); }
+PagedTileKernel paged_tile_kernel_bf16(int H, int kind) { return paged_tile_pick<__nv_bfloat16>(H, kind); }
 
 }  // namespace rope_gb300

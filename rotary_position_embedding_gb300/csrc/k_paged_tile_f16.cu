@@ -3,6 +3,6 @@
 
 namespace rope_gb300 {
 
-KvTileKernel paged_tile_kernel_f16(int H, int kind) { return paged_tile_pick<__half>(H, kind); }
+PagedTileKernel paged_tile_kernel_f16(int H, int kind) { return paged_tile_pick<__half>(H, kind); }
 
 }  // namespace rope_gb300

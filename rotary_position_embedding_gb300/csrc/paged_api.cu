@@ -66,10 +66,10 @@ PagedBatch batch_of(int64_t batch, int64_t tokens, const int32_t* past, const in
 enum class PagedFamily { kSimple, kToken, kTile, kMixed };
 
 struct PagedPlan {
-  int64_t tiles = 0;        // kSimple, kTile: row tiles of the longest sequence
+  int64_t tiles = 0;        // kSimple: row tiles of the longest sequence
   int64_t items = 0;        // kTile: row tiles of all sequences, at most
-  int splits = 1;           // kSimple, kTile: splits of the keys
-  int deal = 0, cluster = 0;  // kToken
+  int splits = 1;           // kSimple: splits of the keys
+  int deal = 0, cluster = 0;  // kToken, kTile: CTAs that are dealt to; kToken: or those of a cluster
   int64_t split_bytes = 0;  // workspace of one split, or of one CTA that is dealt to
   int64_t bytes = 0;
 };
@@ -111,30 +111,20 @@ PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H
   return pl;
 }
 
-// `lone`: every sequence is this kernel's.
-PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, bool lone, int64_t Nq, int64_t Nkv, int64_t H,
-                    int64_t rows) {
+// One CTA an SM is dealt to, as long as the items fit its tables.
+PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
   PagedPlan pl;
-  const int64_t G = Nq / Nkv, tr = kv_tile_rows(H);
-  pl.tiles = (most * G + tr - 1) / tr;
-  int64_t least;  // tiles that there are at least
-  if (ragged) {
-    // a sequence has one tile more than its rows fill, and more than kPagedFewRows rows
-    // where the others are paged_token_kernel's
-    const int64_t seqs = lone ? B : T * G / (kPagedFewRows + 1);
-    pl.items = T * G / tr + (seqs < B ? seqs : B);
-    if (pl.items > B * pl.tiles) pl.items = B * pl.tiles;
-    least = T * G / tr;
-    if (lone && least < B) least = B;
-  } else {
-    pl.items = least = B * pl.tiles;
+  const int64_t G = Nq / Nkv, tr = kv_tile_rows(H), tiles = (most * G + tr - 1) / tr;
+  // a sequence has one tile more than its rows fill
+  pl.items = B * tiles;
+  if (ragged && pl.items > T * G / tr + B) pl.items = T * G / tr + B;
+  pl.split_bytes = 2 * tr * (H * 4 + 8) + 16;
+  const int64_t units = (rows + kv_tile_keys(H) - 1) / kv_tile_keys(H);  // of an item
+  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 31) / units) {
+    pl.deal = kSms;
+    if (pl.deal > pl.items * Nkv * units) pl.deal = (int)(pl.items * Nkv * units);
+    pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
   }
-  int64_t n = kSms / ((least > 0 ? least : 1) * Nkv);
-  if (n > (rows + 511) / 512) n = (rows + 511) / 512;
-  if (n > 128) n = 128;
-  pl.splits = n < 1 ? 1 : (int)n;
-  pl.split_bytes = T * Nq * (H * 4 + 8);
-  if (pl.splits > 1) pl.bytes = pl.splits * pl.split_bytes + kWorkspaceSlack;
   return pl;
 }
 
@@ -152,7 +142,7 @@ PagedFamily choose_paged(bool matrix, int64_t B, int64_t T, int64_t most, bool r
   if (!sizes_fit({T * G / tr + B, Nkv * 128 * 2}) || (T * G / tr + B) * Nkv > INT32_MAX / 128) return PagedFamily::kSimple;
   if (!ragged || B == 1 || trees || !token) return PagedFamily::kTile;
   // T <= (B - s) most + s short for s sequences of `short` tokens
-  const int64_t shorts = kPagedFewRows / G < 1 ? 1 : kPagedFewRows / G;
+  const int64_t shorts = G >= 8 ? 1 : 8 / G;
   const int64_t s = most > shorts ? (B * most - T) / (most - shorts) : B;
   return s * Nkv <= kSms ? PagedFamily::kTile : PagedFamily::kMixed;
 }
@@ -187,8 +177,9 @@ int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_
   int64_t most = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes;
   auto more = [&](int64_t n) { most = n > most ? n : most; };
   if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
-    for (int i = 0; i < 3; ++i)
-      more(plan_tile(batch, tokens, max_query_len, i > 0, i == 1, num_heads, kv_num_heads, head_size, rows).bytes);
+    more(plan_tile(batch, tokens, max_query_len, false, num_heads, kv_num_heads, head_size, rows).bytes);
+  if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
+    more(plan_tile(batch, tokens, max_query_len, true, num_heads, kv_num_heads, head_size, rows).bytes);
   more(plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes);
   return most;
 }
@@ -270,63 +261,72 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
         !encode_paged_map(&maps.v, dtype == ROPE_BF16, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, p.chunk))
       family = PagedFamily::kSimple;
   }
-  p.mixed = family == PagedFamily::kMixed;
+  // In a mixed batch sequences of up to 8 rows go to the kernel for few rows: its
+  // instance for 16 does the arithmetic of 16 for each (95 single tokens of 5 rows beside
+  // a prompt, capped: 212 us).
+  constexpr int kMixedRows = 8;
+  if (family == PagedFamily::kMixed && p.G > kMixedRows) family = PagedFamily::kTile;
+  p.mixed = family == PagedFamily::kMixed ? kMixedRows : 0;
   void* args[] = {&p, &maps};
-  auto splits_of = [&](const PagedPlan& pl) {
+  // Parts in the workspace, `rt` rows each, two a CTA; half of the planned CTAs at least
+  // are dealt to, or each takes its own problem.
+  auto deal_of = [&](const PagedPlan& pl, int64_t rt) {
+    const int64_t fits = room / pl.split_bytes;
+    p.deal = pl.deal <= fits ? pl.deal : fits * 2 >= pl.deal ? (int)fits : 0;
+    if (p.deal > 0) {
+      const int64_t n = 2 * (int64_t)p.deal * rt;
+      p.ws_o = static_cast<float*>(workspace);
+      p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size);
+      p.ws_join = reinterpret_cast<int4*>(p.ws_ml + n);  // 16-byte aligned: n is a multiple of 16
+    }
+  };
+  if (family == PagedFamily::kSimple) {
+    const PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows);
+    if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
     const int64_t fits = room / pl.split_bytes;
     p.splits = pl.splits <= fits ? pl.splits : fits > 1 ? (int)fits : 1;
+    p.tiles = (int32_t)pl.tiles;
     if (p.splits > 1) {
       const int64_t n = p.splits * tokens * num_heads;
       p.ws_o = static_cast<float*>(workspace);
       p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size + (n * head_size & 1));
     }
-    p.tiles = (int32_t)pl.tiles;
-  };
-  auto combine = [&]() -> rope_status {
-    if (p.splits <= 1) return ROPE_OK;
-    const int64_t n = tokens * num_heads;
-    const int per = p.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
-    int64_t gc = (n + per - 1) / per;
-    if (gc > INT32_MAX) gc = INT32_MAX;
-    return launch(paged_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
-                  "kv_attention_paged launch (joining the splits)");
-  };
-  if (family == PagedFamily::kSimple) {
-    const PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows);
-    if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
-    splits_of(pl);
     const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, kv_simple_rows(max_query_len * p.G) == 16);
     const dim3 grid((unsigned)(pl.tiles * p.splits), kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
     KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention_paged launch"));
-    KV_TRY(combine());
+    if (p.splits > 1) {
+      const int64_t n = tokens * num_heads;
+      const int per = p.splits > kKvCombineWarpSplits ? 1 : kKvCombineThreads / 32;
+      int64_t gc = (n + per - 1) / per;
+      if (gc > INT32_MAX) gc = INT32_MAX;
+      KV_TRY(launch(paged_combine_kernel(dtype), dim3((unsigned)gc), kKvCombineThreads, 0, stream, args,
+                    "kv_attention_paged launch (joining the splits)"));
+    }
     set_last_kernel("paged_simple_kernel");
     return ROPE_OK;
   }
   if (family != PagedFamily::kToken) {
-    const PagedPlan pl = plan_tile(batch, tokens, max_query_len, ragged, !p.mixed, num_heads, kv_num_heads, head_size, rows);
-    splits_of(pl);
+    const PagedPlan pl = plan_tile(batch, tokens, max_query_len, ragged, num_heads, kv_num_heads, head_size, rows);
     const int kind = softcap > 0.0f || !(scale > 0.0f) ? kKvAnyScore : alibi_slopes ? kKvBiased : kKvPlain;
-    const KvTileKernel k =
+    const PagedTileKernel k =
         dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
-    KV_TRY(launch(k.fn, dim3((unsigned)(pl.items * kv_num_heads * p.splits)), kKvTileThreads, k.smem, stream, args,
+    int tr = kv_tile_rows(head_size);
+    deal_of(pl, tr);
+    KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kKvTileThreads, k.smem, stream, args,
                   "kv_attention_paged launch (many rows)", kKvTileRegisters));
-    KV_TRY(combine());
+    if (p.deal) {
+      void* jargs[] = {&p, &tr};
+      KV_TRY(launch(k.join, dim3((unsigned)p.deal, 16), kKvTokenThreads, 0, stream, jargs,
+                    "kv_attention_paged launch (joining the parts)"));
+    }
     set_last_kernel("paged_tile_kernel");
   }
   if (family != PagedFamily::kTile) {
-    const int64_t most = p.mixed ? kPagedFewRows / p.G < 1 ? 1 : kPagedFewRows / p.G : max_query_len;
+    const int64_t most = p.mixed ? kMixedRows / p.G : max_query_len;
     const PagedPlan pl = plan_token(batch, most, num_heads, kv_num_heads, head_size, rows);
-    const int64_t fits = room / pl.split_bytes;
     p.rt = most * p.G > 8 ? 16 : 8;
     p.cluster = pl.cluster;
-    // half of the planned CTAs at least, or each its own problem
-    p.deal = pl.deal <= fits ? pl.deal : fits * 2 >= pl.deal ? (int)fits : 0;
-    if (p.deal > 0) {
-      const int64_t n = 2 * (int64_t)p.deal * p.rt;
-      p.ws_o = static_cast<float*>(workspace);
-      p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size);
-      p.ws_join = reinterpret_cast<int4*>(p.ws_ml + n);  // 16-byte aligned: n is a multiple of 16
-    }
+    deal_of(pl, p.rt);
     const PagedTokenKernel k = paged_token_kernel(dtype, (int)head_size, p.rt == 8);
     const int64_t grid = p.deal ? p.deal : batch * kv_num_heads * (p.cluster ? p.cluster : 1);
     KV_TRY(launch(k.fn, dim3((unsigned)grid), kPagedTokenThreads, p.cluster ? k.cluster_smem : k.smem, stream, args,

@@ -40,9 +40,9 @@ struct PagedParams {
   int32_t window;          // keys that a token sees, itself among them; 0: all
   int32_t splits;
   int32_t tiles;           // row tiles of the longest sequence
-  int32_t mixed;           // sequences of up to kPagedFewRows rows are paged_token_kernel's, longer ones paged_tile_kernel's
+  int32_t mixed;           // sequences of up to so many rows are paged_token_kernel's, longer ones paged_tile_kernel's (0: all one's)
   int32_t chunk;           // rows of a box: of a page, and of a unit or tile of keys
-  int32_t deal, cluster;   // paged_token_kernel: CTAs that the work is dealt to, or those of a cluster a problem
+  int32_t deal, cluster;   // CTAs that the work is dealt to; paged_token_kernel: or those of a cluster a problem
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;
@@ -68,10 +68,18 @@ constexpr int kPagedBox = 64;  // most rows of a box
 constexpr int paged_token_ctas(int64_t H) { return 152 * (H > 128 ? 1 : 2); }  // that are resident
 PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
 
-// Any number of rows, the same types: tiles of kv_tile_rows(H) rows, grid (tiles * Nkv *
-// splits); the launch takes (PagedParams, PagedMaps).
-KvTileKernel paged_tile_kernel_f16(int H, int kind);
-KvTileKernel paged_tile_kernel_bf16(int H, int kind);
+// Any number of rows, the same types: tiles of kv_tile_rows(H) rows; the launch takes
+// (PagedParams, PagedMaps), grid (deal), and is followed by join with (PagedParams, rows
+// of a tile), grid (deal, any); or, with more than kPagedItems tiles or no workspace,
+// grid (tiles * Nkv).
+struct PagedTileKernel {
+  const void* fn;
+  const void* join;
+  size_t smem;
+};
+constexpr int kPagedItems = 1024;
+PagedTileKernel paged_tile_kernel_f16(int H, int kind);
+PagedTileKernel paged_tile_kernel_bf16(int H, int kind);
 
 // Append: Q and K rotation, K and V to their pages.
 struct PagedAppendParams {

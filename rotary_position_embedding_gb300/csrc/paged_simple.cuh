@@ -318,8 +318,7 @@ __global__ void __launch_bounds__(kKvCombineThreads) paged_combine_kernel_t(cons
     const int64_t kvh = w / R, row = w - kvh * R;
     int b;
     if (!paged_find(p.s, row / p.G, &b)) continue;  // nobody's row
-    const int n_tok = paged_seq(p.s, b).n;
-    if (n_tok == 0 || (p.mixed && (int64_t)n_tok * p.G <= kPagedFewRows)) continue;  // another kernel's
+    if (paged_seq(p.s, b).n == 0) continue;  // left out
     const int64_t at = kvh * p.splits * R + row;
     float M = -CUDART_INF_F;
     for (int n = lane; n < p.splits; n += 32) M = fmaxf(M, p.ws_ml[at + n * R].x);

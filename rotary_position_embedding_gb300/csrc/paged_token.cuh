@@ -101,7 +101,7 @@ struct PagedSpan {
   __device__ __forceinline__ int units() const { return end > lo ? (end - lo + kPagedUnit - 1) / kPagedUnit : 1; }
 };
 __device__ __forceinline__ bool paged_token_mine(const PagedParams& p, const PagedSeq& q) {
-  return q.n > 0 && (int64_t)q.n * p.G <= kPagedFewRows;
+  return q.n > 0 && (int64_t)q.n * p.G <= (p.mixed ? p.mixed : kPagedFewRows);
 }
 __device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, const PagedSeq& q) {
   PagedSpan s;
