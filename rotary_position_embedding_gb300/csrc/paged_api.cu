@@ -114,13 +114,14 @@ PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H
 // One CTA an SM is dealt to, as long as the items fit its tables.
 PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
   PagedPlan pl;
-  const int64_t G = Nq / Nkv, tr = kv_tile_rows(H), tiles = (most * G + tr - 1) / tr;
-  // a sequence has one tile more than its rows fill
+  const int64_t G = Nq / Nkv, tr = kv_tile_rows(H);
+  const int64_t tpi = G < tr ? tr / G : 1, tiles = (most + tpi - 1) / tpi;
+  // a sequence has one item more than its tokens fill
   pl.items = B * tiles;
-  if (ragged && pl.items > T * G / tr + B) pl.items = T * G / tr + B;
+  if (ragged && pl.items > T / tpi + B) pl.items = T / tpi + B;
   pl.split_bytes = 2 * tr * (H * 4 + 8) + 16;
   const int64_t units = (rows + kv_tile_keys(H) - 1) / kv_tile_keys(H);  // of an item
-  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 31) / units) {
+  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 31) / (units + 8)) {
     pl.deal = kSms;
     if (pl.deal > pl.items * Nkv * units) pl.deal = (int)(pl.items * Nkv * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -139,7 +140,8 @@ PagedFamily choose_paged(bool matrix, int64_t B, int64_t T, int64_t most, bool r
   const bool token = B * Nkv <= INT32_MAX / kKvClusterMost;
   if (most * G <= kPagedFewRows) return token ? PagedFamily::kToken : PagedFamily::kSimple;
   const int64_t tr = kv_tile_rows(H);
-  if (!sizes_fit({T * G / tr + B, Nkv * 128 * 2}) || (T * G / tr + B) * Nkv > INT32_MAX / 128) return PagedFamily::kSimple;
+  if (G > tr || most * G > INT32_MAX || tr * G * Nkv * H > INT32_MAX || (T * G / (tr / 2) + B) * Nkv > INT32_MAX)
+    return PagedFamily::kSimple;
   if (!ragged || B == 1 || trees || !token) return PagedFamily::kTile;
   // T <= (B - s) most + s short for s sequences of `short` tokens
   const int64_t shorts = G >= 8 ? 1 : 8 / G;
@@ -266,6 +268,18 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
   // a prompt, capped: 212 us).
   constexpr int kMixedRows = 8;
   if (family == PagedFamily::kMixed && p.G > kMixedRows) family = PagedFamily::kTile;
+  PagedTileMaps tile_maps;
+  if (family == PagedFamily::kTile || family == PagedFamily::kMixed) {
+    memset(&tile_maps, 0, sizeof(tile_maps));
+    const bool bf = dtype == ROPE_BF16;
+    p.tpi = kv_tile_rows(head_size) / p.G;
+    tile_maps.k = maps.k;
+    tile_maps.v = maps.v;
+    if (!encode_paged_map(&tile_maps.k_row, bf, k_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 1) ||
+        !encode_paged_map(&tile_maps.v_row, bf, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 1) ||
+        !encode_paged_q_map(&tile_maps.q, bf, query, head_size, num_heads, tokens, p.G, p.tpi))
+      family = PagedFamily::kSimple;
+  }
   p.mixed = family == PagedFamily::kMixed ? kMixedRows : 0;
   void* args[] = {&p, &maps};
   // Parts in the workspace, `rt` rows each, two a CTA; half of the planned CTAs at least
@@ -312,11 +326,12 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
         dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
     int tr = kv_tile_rows(head_size);
     deal_of(pl, tr);
-    KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kKvTileThreads, k.smem, stream, args,
-                  "kv_attention_paged launch (many rows)", kKvTileRegisters));
+    void* targs[] = {&p, &tile_maps};
+    KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kPagedTileBlock, k.smem, stream, targs,
+                  "kv_attention_paged launch (many rows)", kPagedTileRegisters));
     if (p.deal) {
       void* jargs[] = {&p, &tr};
-      KV_TRY(launch(k.join, dim3((unsigned)p.deal, 16), kKvTokenThreads, 0, stream, jargs,
+      KV_TRY(launch(k.join, dim3((unsigned)p.deal, tr / 16), kKvTokenThreads, 0, stream, jargs,
                     "kv_attention_paged launch (joining the parts)"));
     }
     set_last_kernel("paged_tile_kernel");

@@ -9,10 +9,11 @@
 namespace rope_gb300 {
 
 // Row `row` of (b, kvh) over the keys [lo, hi): the output, or with `part_o` (H
-// values) a partial one and its (maximum, sum) at `part_ml`.
+// values, each 4 of them part_ld apart) a partial one and its (maximum, sum) at `part_ml`.
 template <class T>
 __device__ __noinline__ void paged_careful_row(const PagedParams& p, const PagedSeq& seq, int b, int kvh, int64_t row,
-                                               int lo, int hi, float* part_o, float2* part_ml, int lane) {
+                                               int lo, int hi, float* part_o, int part_ld, float2* part_ml,
+                                               int lane) {
   using bits = typename Elem<T>::bits;
   constexpr int ND = kKvMaxHead / 32;
   const int64_t tok = row / p.G;
@@ -65,7 +66,7 @@ __device__ __noinline__ void paged_careful_row(const PagedParams& p, const Paged
     const int d = lane + 32 * i;
     if (d >= p.H) continue;
     if (part_o)
-      part_o[d] = o[i];
+      part_o[(d >> 2) * part_ld + (d & 3)] = o[i];
     else
       static_cast<bits*>(p.out)[at_row + d] = Elem<T>::fromf(o[i] * inv);
   }

@@ -44,6 +44,7 @@ struct PagedParams {
   int32_t chunk;           // rows of a box: of a page, and of a unit or tile of keys
   int32_t deal, cluster;   // CTAs that the work is dealt to; paged_token_kernel: or those of a cluster a problem
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
+  int32_t tpi;             // paged_tile_kernel: tokens of an item
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;
   float scale, cap, over;  // factor of q.k; 0: no cap; scale / cap
@@ -68,16 +69,21 @@ constexpr int kPagedBox = 64;  // most rows of a box
 constexpr int paged_token_ctas(int64_t H) { return 152 * (H > 128 ? 1 : 2); }  // that are resident
 PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
 
-// Any number of rows, the same types: tiles of kv_tile_rows(H) rows; the launch takes
-// (PagedParams, PagedMaps), grid (deal), and is followed by join with (PagedParams, rows
-// of a tile), grid (deal, any); or, with more than kPagedItems tiles or no workspace,
-// grid (tiles * Nkv).
+// Any number of rows, the same types, G up to kv_tile_rows(H): items of PagedParams.tpi
+// tokens; the launch takes (PagedParams, PagedTileMaps), grid (deal), and is followed by
+// join with (PagedParams, kv_tile_rows(H)), grid (deal, a sixteenth of that); or, with more
+// than kPagedItems items or no workspace, grid (items * Nkv).
 struct PagedTileKernel {
   const void* fn;
   const void* join;
   size_t smem;
 };
-constexpr int kPagedItems = 1024;
+constexpr int kPagedItems = 768;
+constexpr int kPagedTileBlock = 384;
+// The kernel deals its registers out again (setmaxnreg): 256 x 208 + 128 x 88 = 384 x 168,
+// so it must have been launched with 168 a thread.
+constexpr int kPagedTileRegisters = 168;
+static_assert(256 * 208 + 128 * 88 <= kPagedTileBlock * kPagedTileRegisters, "registers of paged_tile_kernel");
 PagedTileKernel paged_tile_kernel_f16(int H, int kind);
 PagedTileKernel paged_tile_kernel_bf16(int H, int kind);
 

@@ -4,22 +4,28 @@
 // of 128 rows take turns on the tensor cores, S and O in TMEM, P = 2^(x - m) by the
 // threads that own the rows, the base moved only where a tile's weights ask for it.
 //
-// One CTA an SM stays for the whole call. The work is the key tiles of all items (a
-// sequence's tile of rows) and heads, and CTA i takes the key tiles [i U / n, (i + 1) U / n)
-// of all U: sequences of any lengths, few long ones and many short ones, even out, and
+// One CTA an SM stays for the whole call. The work is the key tiles of all items (up to
+// ROWS rows of a sequence, whole tokens) and heads, and CTA i takes the part [i W / n, (i +
+// 1) W / n) of their weight W, an item's being its key tiles and kPagedOver for its beginning
+// and its output: sequences of any lengths, few long ones and many short ones, even out, and
 // nothing is split where it need not be. An item that one CTA has whole goes to the
 // output, the others' parts to the workspace (2 slots a CTA), where
 // paged_tile_join_kernel_t adds them up. The roles run through a CTA's segments
 // without meeting: while the last tile of one is with the softmax threads and its
 // output is on its way, K, V and Q of the next come in and its first products run.
-//   Warps (16): 0-3 and 4-7 softmax and output of row tile 0 and 1; 8-11 bring K and V,
-//   by TMA in boxes (the rows of a key tile that lie in one page x 64 elements), one
-//   thread a box, each with the next tile's page looked up a step ahead; the tile that
-//   holds the last key by cp.async, rows behind it zeros; 12 issues every MMA; 13-15
-//   bring Q as soon as the last product of the segment before has read its own.
+//   Warps (12): 0-3 and 4-7 softmax and output of row tile 0 and 1, a thread a row; 8 and 9
+//   bring K and V by TMA in boxes (the rows of a key tile that lie in one page x 64
+//   elements), a lane a box, the next tile's pages looked up a step ahead; 10 brings Q as
+//   soon as the last product of the segment before has read its own; 11 issues every MMA.
+// V's rows behind the last key have to be zeros (their weights are, and 0 * NaN is not):
+// boxes of such rows are asked for in a page that does not exist, and the box that holds
+// the last key is brought row by row.
 // A row sees keys from its window on; of a draft tree's new keys those whose bit its
 // mask holds. Only key tiles that some row does not see whole are looked at key by key,
 // as bits of four words.
+// Outputs leave in rows of 128 bytes, turned among 8 lanes by shuffles (a thread's own
+// row, 16 bytes of 32 rows at a time, took 3 us an item); parts lie in the workspace with
+// the same 4 dims of all rows side by side.
 // Bound by the tensor cores for prompts; trees, whose rows are two tiles or less, by the
 // softmax between the products of a key tile.
 //
@@ -31,30 +37,42 @@
 
 namespace rope_gb300 {
 
-constexpr int kPagedQThreads = 96;  // that bring Q
+constexpr int kPagedTileThreads = kPagedTileBlock;
+constexpr int kPagedOver = 2;  // what an item weighs beside its key tiles
 
 struct PagedTileBars {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], q_full, q_free, drain;
 };
 
-// The key tiles' range of an item: keys [start, end), start at the beginning of a tile.
-// Its units are those tiles, at least one, so that its output is written.
-__device__ __forceinline__ int4 paged_item(const PagedParams& p, const PagedSeq& q, int b, int tile, int rows, int keys) {
-  const int64_t rows0 = (int64_t)tile * rows, R = (int64_t)q.n * p.G;
-  const int64_t last = rows0 + rows < R ? rows0 + rows : R;
-  int4 it;
-  it.x = b;
-  it.y = tile;
-  it.z = paged_first(p, q.past + rows0 / p.G) / keys * keys;
-  it.w = paged_limit(p, q, q.past + (last - 1) / p.G);
+// An item: tokens [tok0, tok0 + ntok) of sequence b, which are the batch's [g0, ..) and at
+// rows [pos0, ..). Its keys are [start, end), start at the beginning of a key tile.
+struct alignas(16) PagedItem {
+  int b, tok0, start, end;
+  int g0, ntok, pos0, total;  // total: rows of the sequence
+  __device__ __forceinline__ PagedSeq seq() const {
+    PagedSeq q;
+    q.t0 = g0 - tok0;
+    q.n = tok0 + ntok;
+    q.past = pos0 - tok0;
+    q.total = total;
+    return q;
+  }
+};
+__device__ __forceinline__ PagedItem paged_item(const PagedParams& p, const PagedSeq& q, int b, int tile, int keys) {
+  PagedItem it;
+  it.b = b;
+  it.tok0 = tile * p.tpi;
+  it.ntok = q.n - it.tok0 < p.tpi ? q.n - it.tok0 : p.tpi;
+  it.g0 = (int)q.t0 + it.tok0;
+  it.pos0 = q.past + it.tok0;
+  it.total = q.total;
+  it.start = paged_first(p, it.pos0) / keys * keys;
+  it.end = paged_limit(p, q, it.pos0 + it.ntok - 1);
   return it;
 }
-__device__ __forceinline__ int paged_item_units(int4 it, int keys) { return it.w > it.z ? (it.w - it.z + keys - 1) / keys : 1; }
-
-// Tiles of rows of sequence b that are this kernel's.
-__device__ __forceinline__ int paged_tiles(const PagedParams& p, const PagedSeq& q, int rows) {
-  const int64_t R = (int64_t)q.n * p.G;
-  return p.mixed && R <= p.mixed ? 0 : (int)((R + rows - 1) / rows);
+// Its key tiles; one where there are no keys, so that its output is written.
+__device__ __forceinline__ int paged_item_tiles(const PagedItem& it, int keys) {
+  return it.end > it.start ? (it.end - it.start + keys - 1) / keys : 1;
 }
 
 // An inclusive sum over the CTA's threads, and the sum of all.
@@ -70,7 +88,7 @@ __device__ __forceinline__ int paged_scan(int n, int* s_sum, int* all) {
   __syncthreads();
   int a = 0;
 #pragma unroll
-  for (int w = 0; w < kTileThreads / 32; ++w) {
+  for (int w = 0; w < kPagedTileThreads / 32; ++w) {
     const int x = s_sum[w];
     if (w < warp) n += x;
     a += x;
@@ -79,29 +97,27 @@ __device__ __forceinline__ int paged_scan(int n, int* s_sum, int* all) {
   return n;
 }
 
-// The items of the batch and the units of one head of those before each, in shared
+// The items of the batch and the weight of one head of those before each, in shared
 // memory; their number. Not dealt: only item number `only`, or none. All threads come
 // here, and the tables hold when it returns.
-__device__ __forceinline__ int paged_items(const PagedParams& p, int only, int rows, int keys, int4* items, int32_t* before,
+__device__ __forceinline__ int paged_items(const PagedParams& p, int only, int keys, PagedItem* items, int32_t* before,
                                            int* s_sum) {
   const int tid = threadIdx.x;
   int count = 0;
-  for (int b0 = 0; b0 < p.s.B; b0 += kTileThreads) {
+  for (int b0 = 0; b0 < p.s.B; b0 += kPagedTileThreads) {
     const int b = b0 + tid;
     PagedSeq q;
     int n = 0, all;
     if (b < p.s.B) {
       q = paged_seq(p.s, b);
-      n = paged_tiles(p, q, rows);
+      if (!(p.mixed && (int64_t)q.n * p.G <= p.mixed)) n = (q.n + p.tpi - 1) / p.tpi;
     }
     const int first = paged_scan(n, s_sum, &all) - n + count;
     if (p.deal > 0) {
       // (more than planned for only where query_starts does not ascend)
-      for (int t = 0; t < n && first + t < kPagedItems; ++t) items[first + t] = make_int4(b, t, 0, 0);
+      for (int t = 0; t < n && first + t < kPagedItems; ++t) items[first + t].b = b, items[first + t].tok0 = t;
     } else if (only >= first && only < first + n) {
-      items[0] = paged_item(p, q, b, first + n - 1 - only, rows, keys);  // the longest rows first
-      before[0] = 0;
-      before[1] = paged_item_units(items[0], keys);
+      items[0] = paged_item(p, q, b, first + n - 1 - only, keys);  // the longest rows first
     }
     count += all;
     if (p.deal == 0 && only < count) break;  // the same for all threads
@@ -110,13 +126,14 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int r
   if (p.deal == 0) return only < count ? 1 : 0;
   if (count > kPagedItems) count = kPagedItems;
   int sum = 0;
-  for (int i0 = 0; i0 < count; i0 += kTileThreads) {
+  for (int i0 = 0; i0 < count; i0 += kPagedTileThreads) {
     const int i = i0 + tid;
     int n = 0, all;
     if (i < count) {
-      const int4 it = items[i];
-      items[i] = paged_item(p, paged_seq(p.s, it.x), it.x, it.y, rows, keys);
-      n = paged_item_units(items[i], keys);
+      const int b = items[i].b;
+      const PagedItem it = paged_item(p, paged_seq(p.s, b), b, items[i].tok0, keys);
+      items[i] = it;
+      n = paged_item_tiles(it, keys) + kPagedOver;
     }
     const int upto = paged_scan(n, s_sum, &all) + sum;
     if (i < count) before[i] = upto - n;
@@ -127,9 +144,9 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int r
   return count;
 }
 
-// The segments of a CTA, one after the other.
+// The segments of a CTA, one after the other: key tiles [u0, u1) of an item and head.
 struct PagedTileWork {
-  int at, last;     // units left
+  int at, last;     // weight left
   int item, kvh, u0, u1;
   bool whole;       // all of the item
   __device__ __forceinline__ bool next(const PagedParams& p, const int32_t* before, int count) {
@@ -151,16 +168,44 @@ struct PagedTileWork {
       else
         y = mid;
     }
+    // an item's weight: kPagedOver of nothing, then a tile each
+    int weight = before[x + 1] - before[x], in = at - before[x] * p.Nkv;
+    kvh = (int)((uint32_t)in / (uint32_t)weight);
+    in -= kvh * weight;
+    if (in < kPagedOver) {
+      at += kPagedOver - in;
+      in = kPagedOver;
+      if (at >= last) return false;
+    }
     item = x;
-    const int units = before[x + 1] - before[x], in = at - before[x] * p.Nkv;
-    kvh = (int)((uint32_t)in / (uint32_t)units);
-    u0 = in - kvh * units;
-    u1 = u0 + (last - at) < units ? u0 + (last - at) : units;
-    whole = u0 == 0 && u1 == units;
+    u0 = in - kPagedOver;
+    u1 = u0 + (last - at) < weight - kPagedOver ? u0 + (last - at) : weight - kPagedOver;
+    whole = u0 == 0 && u1 == weight - kPagedOver;
     at += u1 - u0;
     return true;
   }
 };
+
+// 8 pieces of 16 bytes of each of 8 lanes, turned: piece j of lane i becomes piece i of lane j.
+__device__ __forceinline__ void paged_turn(uint4 (&v)[8], int lane) {
+#pragma unroll
+  for (int s = 1; s < 8; s *= 2) {
+    const bool high = lane & s;
+#pragma unroll
+    for (int a = 0; a < 8; ++a) {
+      if (a & s) continue;
+      uint4 x = high ? v[a] : v[a | s];
+      x.x = __shfl_xor_sync(0xffffffffu, x.x, s);
+      x.y = __shfl_xor_sync(0xffffffffu, x.y, s);
+      x.z = __shfl_xor_sync(0xffffffffu, x.z, s);
+      x.w = __shfl_xor_sync(0xffffffffu, x.w, s);
+      if (high)
+        v[a] = x;
+      else
+        v[a | s] = x;
+    }
+  }
+}
 
 // Scores of the tile at j0 that the row does not see become -inf.
 template <int N>
@@ -181,8 +226,8 @@ __device__ __forceinline__ void paged_hide(float (&x)[N], int j0, int from, int 
 }
 
 template <class T, int HD, int KIND>
-__global__ void __launch_bounds__(kTileThreads, 1)
-    paged_tile_kernel_t(const PagedParams p, const __grid_constant__ PagedMaps maps) {
+__global__ void __launch_bounds__(kPagedTileThreads, 1)
+    paged_tile_kernel_t(const PagedParams p, const __grid_constant__ PagedTileMaps maps) {
   using C = TileCfg<false, HD>;
   using bits = typename Elem<T>::bits;
   constexpr bool BF = kIsBf16<T>;
@@ -190,81 +235,79 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ uint8_t kv_tiles[];
   __shared__ PagedTileBars bars;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_sum[kTileThreads / 32];
+  __shared__ int s_sum[kPagedTileThreads / 32];
   uint8_t* base = kv_tiles + ((1024 - (kv_smem(kv_tiles) & 1023)) & 1023);
   const uint32_t sq = kv_smem(base), sk = sq + C::kQ, sv = sk + 2 * C::kStage;
-  int4* const items = reinterpret_cast<int4*>(base + C::kQ + 4 * C::kStage);
+  PagedItem* const items = reinterpret_cast<PagedItem*>(base + C::kQ + 4 * C::kStage);
   int32_t* const before = reinterpret_cast<int32_t*>(items + kPagedItems);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](uint64_t* b) { return kv_smem(b); };
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(&bars.k_full[i]), kTileBring);
-      mbar_init(bar(&bars.v_full[i]), kTileBring);
+      mbar_init(bar(&bars.k_full[i]), 1);
+      mbar_init(bar(&bars.v_full[i]), 1);
       mbar_init(bar(&bars.k_free[i]), 1);
       mbar_init(bar(&bars.v_free[i]), 1);
       mbar_init(bar(&bars.s_full[i]), 1);
       mbar_init(bar(&bars.p_full[i]), kTileRows);
       mbar_init(bar(&bars.o_full[i]), 1);
     }
-    mbar_init(bar(&bars.q_full), kPagedQThreads);
+    mbar_init(bar(&bars.q_full), 1);
     mbar_init(bar(&bars.q_free), 1);
     mbar_init(bar(&bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 256) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
-  }
-  if (warp == 12) {
+  if (warp == 8 && lane < 5)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + lane * sizeof(CUtensorMap)) : "memory");
+  if (warp == 11) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem(&s_tmem)), "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // rows of Q that no token fills: nobody's, but numbers
+  const int q_rows = p.tpi * p.G;
+  for (int i = tid; i < (ROWS - q_rows) * (HD / 8); i += kPagedTileThreads) {
+    const int r = q_rows + i / (HD / 8), piece = i % (HD / 8);
+    *reinterpret_cast<uint4*>(base + tile_at(ROWS, r, piece)) = make_uint4(0, 0, 0, 0);
+  }
+  tc_fence_smem();
   pdl_launch_dependents();
   pdl_wait();
 
   tc_before();
-  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), ROWS, N, items, before, s_sum);
+  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), N, items, before, s_sum);
   tc_after();
   const uint32_t tmem = s_tmem;
   PagedTileWork work;
   work.at = work.last = 0;
-  if (count > 0) {
-    const uint32_t total = (uint32_t)before[count] * (p.deal > 0 ? p.Nkv : 1);  // below 2^31
-    work.last = (int)total;
-    if (p.deal > 0) {
-      work.at = (int)((uint64_t)blockIdx.x * total / (uint32_t)p.deal);
-      work.last = (int)((uint64_t)(blockIdx.x + 1) * total / (uint32_t)p.deal);
-    }
-  }
-  if (p.deal > 0 && work.at >= work.last && tid < ROWS) {
-    // no units: nothing begins here, and nothing of this CTA's counts where an item's
-    // CTAs lie on both sides of it
+  const uint32_t total = p.deal > 0 ? (uint32_t)before[count] * (uint32_t)p.Nkv : 0u;  // below 2^31
+  if (p.deal > 0) {
+    work.at = (int)((uint64_t)blockIdx.x * total / (uint32_t)p.deal);
+    work.last = (int)((uint64_t)(blockIdx.x + 1) * total / (uint32_t)p.deal);
+    // so far nothing begins here that goes on elsewhere, and nothing of this CTA's counts
+    // where an item's CTAs lie on both sides of it
     if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
-    p.ws_ml[2 * (int64_t)blockIdx.x * ROWS + tid] = make_float2(-CUDART_INF_F, 0.0f);
+    if (work.at >= work.last && tid < ROWS) p.ws_ml[2 * (int64_t)blockIdx.x * ROWS + tid] = make_float2(-CUDART_INF_F, 0.0f);
+  } else if (count > 0) {
+    work.last = paged_item_tiles(items[0], N);
   }
   // every sequence's lengths are looked at once, where the other kernel has not
   if (p.s.status && !p.mixed)
-    for (int64_t i = (int64_t)blockIdx.x * kTileThreads + tid; i < p.s.B; i += (int64_t)gridDim.x * kTileThreads)
+    for (int64_t i = (int64_t)blockIdx.x * kPagedTileThreads + tid; i < p.s.B; i += (int64_t)gridDim.x * kPagedTileThreads)
       paged_flag_seq(p.s, (int)i, paged_seq(p.s, (int)i));
-  // keys of a segment
-  auto keys_of = [&](const int4& it, int& lo, int& hi) {
-    lo = it.z + work.u0 * N;
-    hi = it.z + work.u1 * N < it.w ? it.z + work.u1 * N : it.w;
-    return hi > lo ? (hi - lo + N - 1) / N : 0;  // key tiles
+  // keys of a segment, and its key tiles
+  auto keys_of = [&](const PagedItem& it, int& lo, int& hi) {
+    lo = it.start + work.u0 * N;
+    hi = it.start + work.u1 * N < it.end ? it.start + work.u1 * N : it.end;
+    return hi > lo ? (hi - lo + N - 1) / N : 0;
   };
-  auto rows_of = [&](const PagedSeq& seq, const int4& it) {
-    const int64_t left = (int64_t)seq.n * p.G - (int64_t)it.y * ROWS;
-    return left < ROWS ? (int)left : ROWS;  // at least 1
-  };
-  // 512 threads x 128 registers, dealt out again: see kKvTileRegisters
+  // 384 threads x 168 registers, dealt out again: see kPagedTileRegisters
   bool ok = true;
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes of TMEM a warp
     const uint32_t to = tmem + lanes + 256 + (NT == 2 ? t * 128 : 0);
@@ -279,32 +322,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tr.cap2 = p.cap * kLog2e;
     int done_steps = 0, done_segments = 0;  // of this row tile
     for (int segment = 0; ok && t < NT && work.next(p, before, count); ++segment) {
-      const int4 it = items[work.item];
-      const PagedSeq seq = paged_seq(p.s, it.x);
+      const PagedItem& it = items[work.item];
       int lo, hi;
       const int steps = keys_of(it, lo, hi);
-      const int nrows = rows_of(seq, it);
-      // the one item that may begin in this CTA and go on in others: paged_tile_join_kernel_t's
-      if (p.deal > 0 && work.at >= work.last && tid == 0) {
-        const bool open = work.u0 == 0 && !work.whole;  // an item that began before is another CTA's
-        const uint32_t total = (uint32_t)before[count] * p.Nkv;
-        const int upto = work.at - work.u1 + paged_item_units(it, N);  // its last unit, and one
-        const int parts =
-            open ? (int)(((uint64_t)(uint32_t)upto * (uint32_t)p.deal - 1) / total) - (int)blockIdx.x : 0;
-        p.ws_join[blockIdx.x] = make_int4(it.x, work.kvh, it.y, 2 * parts + (segment > 0 ? 1 : 0));
+      const int nrows = it.ntok * p.G;
+      const int kvh = work.kvh;
+      const bool whole = work.whole;
+      // the one item that begins in this CTA and goes on in others: paged_tile_join_kernel_t's
+      if (tid == 0 && work.u0 == 0 && !whole) {
+        const uint32_t upto = (uint32_t)(work.at - work.u1 + paged_item_tiles(it, N));  // its last tile, and one
+        const int parts = (int)(((uint64_t)upto * (uint32_t)p.deal - 1) / total) - (int)blockIdx.x;
+        p.ws_join[blockIdx.x] = make_int4(it.g0, kvh, nrows, 2 * parts + (segment > 0 ? 1 : 0));
       }
       if (t * kTileRows >= nrows) continue;
       const bool live = tid < nrows;  // row tid of the item: TMEM lane tid % 128 of row tile t
-      const int kvh = work.kvh;
-      const bool whole = work.whole;
-      const int64_t row = (int64_t)it.y * ROWS + (live ? tid : nrows - 1);
-      const int64_t tok = row / p.G;
-      const int head = (int)(row - tok * p.G);
-      const int64_t pos = seq.past + tok;
-      const int lim = live ? paged_limit(p, seq, pos) : 0, from = paged_first(p, pos);
-      const uint64_t word = p.masks && live ? (uint64_t)__ldg(p.masks + seq.t0 + tok) : ~0ull;
+      const int past = it.pos0 - it.tok0;
+      const int tok = kv_div(live ? tid : nrows - 1, p.by_g), head = (live ? tid : nrows - 1) - tok * p.G;
+      const int pos = it.pos0 + tok;
+      int lim = 0;
+      if (live && pos >= 0) lim = p.masks || pos + 1 > it.total ? it.total : pos + 1;
+      const int from = paged_first(p, pos);
+      const uint64_t word = p.masks && live ? (uint64_t)__ldg(p.masks + it.g0 + tok) : ~0ull;
       // keys in [below, full) are seen by every row of the warp
-      const int full = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : p.masks && seq.past < lim ? seq.past : lim);
+      const int full = __reduce_min_sync(0xffffffffu, !live ? 0x7fffffff : p.masks && past < lim ? past : lim);
       const int below = __reduce_max_sync(0xffffffffu, live ? from : 0);
       tr.slope = 0.0f;
       if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + head) * kLog2e;
@@ -332,7 +372,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           done = true;
         }
         if (general) tile_scores<true, N>(x, tr, !capped);
-        if (masked) paged_hide<N>(x, j0, from, lim, p.masks != nullptr, seq.past, word);
+        if (masked) paged_hide<N>(x, j0, from, lim, p.masks != nullptr, past, word);
         auto weights = [&]() {
           const float nb = m == -CUDART_INF_F ? 0.0f : -m;
           if (done) return tile_weights<false, BF, 2, N>(x, ts, tr, 1.0f, nb, nullptr, 1.0f);
@@ -390,52 +430,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const float f = whole ? inv : 1.0f;
         const bool empty = m == -CUDART_INF_F && l == 0.0f;  // nothing seen (TMEM may never have been written)
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0)) * ROWS;
-        bits* dst = static_cast<bits*>(p.out) + ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + head) * p.H;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
+        float4* const part = reinterpret_cast<float4*>(p.ws_o) + slot * (p.H / 4) * ROWS + tid;
+        bits* const out = static_cast<bits*>(p.out) + ((int64_t)it.g0 * p.Nq + (int64_t)kvh * p.G) * p.H;
+        const int at = live ? (tok * p.Nq + head) * p.H : -1;  // of the row, from `out` on
         bool odd = false;
-        if (live && !whole) p.ws_ml[slot + tid] = make_float2(m, l);
-        constexpr int OC = HD < 128 ? HD : 128;  // columns at once
+        if (live && !whole) p.ws_ml[slot * ROWS + tid] = make_float2(m, l);
 #pragma unroll 1
-        for (int i0 = 0; i0 < HD; i0 += OC) {
-          uint32_t all[OC];
+        for (int i0 = 0; i0 < HD; i0 += 64) {
+          uint32_t o[64];
+          tc_ld32(o, to + i0);
+          tc_ld32(o + 32, to + i0 + 32);
+          tc_wait_ld32(o);
+          tc_wait_ld32(o + 32);
+          float y[64];
 #pragma unroll
-          for (int i = 0; i < OC; i += 32) tc_ld32(all + i, to + i0 + i);
-#pragma unroll
-          for (int i = 0; i < OC; i += 32) tc_wait_ld32(all + i);
-#pragma unroll
-          for (int i1 = 0; i1 < OC; i1 += 32) {
-            const int i = i0 + i1;
-            const uint32_t* o = all + i1;
-            float y[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
-              odd |= !(fabsf(y[k]) < CUDART_INF_F) && i + k < p.H;
-            }
-            if (!live) continue;
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              if (i + k >= p.H) continue;
-              if (!whole) {
-                float* part = p.ws_o + (slot + tid) * p.H + i + k;
-                *reinterpret_cast<float4*>(part) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                *reinterpret_cast<float4*>(part + 4) = make_float4(y[k + 4], y[k + 5], y[k + 6], y[k + 7]);
-              } else {
-                VecT<T, 8> v;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v.v[q] = Elem<T>::fromf(y[k + q]);
-                *reinterpret_cast<VecT<T, 8>*>(dst + i + k) = v;
-              }
-            }
-        }
+          for (int k = 0; k < 64; ++k) {
+            y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
+            odd |= !(fabsf(y[k]) < CUDART_INF_F) && i0 + k < p.H;
           }
+          if (!whole) {
+#pragma unroll
+            for (int k = 0; k < 64; k += 4)
+              if (live && i0 + k < p.H) part[(int64_t)((i0 + k) / 4) * ROWS] = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+          } else {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = make_uint4(kv_pack2<BF>(y[8 * k], y[8 * k + 1]), kv_pack2<BF>(y[8 * k + 2], y[8 * k + 3]),
+                                kv_pack2<BF>(y[8 * k + 4], y[8 * k + 5]), kv_pack2<BF>(y[8 * k + 6], y[8 * k + 7]));
+            paged_turn(v, lane);
+            const int d = i0 + 8 * (lane & 7);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int to_row = __shfl_sync(0xffffffffu, at, (lane & ~7) | k);
+              if (to_row >= 0 && d < p.H) *reinterpret_cast<uint4*>(out + to_row + d) = v[k];
+            }
+          }
+        }
         // An infinity or a NaN may have come from a value that the row does not see
         uint32_t again = __ballot_sync(0xffffffffu, odd && live);
         if (again) {
           bool found = false;  // in a value that some row of the warp does not see and its key tile holds
           auto look = [&](int from_key, int to_key) {
             for (int j = from_key; j < to_key; ++j) {
-              const int64_t e = paged_row(p.s, it.x, kvh, j, p.H);
+              const int64_t e = paged_row(p.s, it.b, kvh, j, p.H);
               for (int d = lane; d < p.H; d += 32)
                 found |= e >= 0 && !(fabsf(Elem<T>::tof(static_cast<const bits*>(p.v)[e + d])) < CUDART_INF_F);
             }
@@ -448,16 +487,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         while (again) {
           const int r = __ffs(again) - 1;
           again &= again - 1;
-          const int64_t w = slot + warp * 32 + r;
-          paged_careful_row<T>(p, seq, it.x, kvh, (int64_t)it.y * ROWS + (warp * 32 + r), lo, hi,
-                               whole ? nullptr : p.ws_o + w * p.H, p.ws_ml + w, lane);
+          const int row = warp * 32 + r;
+          paged_careful_row<T>(p, it.seq(), it.b, kvh, (int64_t)it.tok0 * p.G + row, lo, hi,
+                               whole ? nullptr : p.ws_o + (slot * (p.H / 4) * ROWS + row) * 4, 4 * ROWS,
+                               p.ws_ml + slot * ROWS + row, lane);
         }
       }
     }
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------------ MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 12) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 11) {
+      // ---------------------------------------------------------------- MMA
       // The whole warp walks the steps, so that what an MMA takes stays in uniform
       // registers; one lane issues.
       const uint32_t iqk = tc_idesc(BF, N, false), ipv = tc_idesc(BF, HD, true);
@@ -472,12 +512,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (tc_elect()) tc_commit(bar(w));
       };
       auto qk = [&](int t, int stage, uint32_t d) {
-        const uint32_t a = dq + t * (kTileRows * HD * 2 / 16), c = dk + stage * (C::kStage / 16);
+        const uint32_t a = dq + t * (kTileRows * 128 / 16), c = dk + stage * (C::kStage / 16);
         if (tc_elect()) {
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k)
             if (k < steps)
-              tc_mma_ss(d, a + ((k >> 2) * (kTileRows * 128) + (k & 3) * 32) / 16,
+              tc_mma_ss(d, a + ((k >> 2) * (ROWS * 128) + (k & 3) * 32) / 16,
                         c + ((k >> 2) * (N * 128) + (k & 3) * 32) / 16, iqk, k > 0);
         }
       };
@@ -491,11 +531,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       int gs = 0, c0 = 0, c1 = 0, segments = 0;  // key tiles; of each row tile; segments with any
       while (ok && work.next(p, before, count)) {
-        const int4 it = items[work.item];
+        const PagedItem& it = items[work.item];
         int lo, hi;
         const int n = keys_of(it, lo, hi);
         if (n == 0) continue;
-        const int live_tiles = NT == 2 && rows_of(paged_seq(p.s, it.x), it) > kTileRows ? 2 : 1;
+        const int live_tiles = NT == 2 && it.ntok * p.G > kTileRows ? 2 : 1;
         wait(&bars.q_full, segments & 1);
         wait(&bars.k_full[gs & 1], (gs >> 1) & 1);
         if (!ok) break;
@@ -565,185 +605,147 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         commit(&bars.drain);
         mbar_wait(bar(&bars.drain), 0);
       }
-    } else {
+    } else if (warp == 10) {
       // ---------------------------------------------------------------- Q
-      const int me = tid - 13 * 32;
-      constexpr int PPR = HD / 8;  // 16-byte pieces of a row
       int segments = 0;
       while (ok && work.next(p, before, count)) {
-        const int4 it = items[work.item];
+        const PagedItem& it = items[work.item];
         int lo, hi;
         if (keys_of(it, lo, hi) == 0) continue;
-        const PagedSeq seq = paged_seq(p.s, it.x);
-        const int nrows = rows_of(seq, it);
-        const int64_t tok0 = (int64_t)it.y * ROWS / p.G;
-        const int rem0 = (int)((int64_t)it.y * ROWS - tok0 * p.G);
-        const bits* q0 = static_cast<const bits*>(p.q) + ((seq.t0 + tok0) * p.Nq + (int64_t)work.kvh * p.G) * p.H;
         if (segments > 0) ok = mbar_wait(bar(&bars.q_free), (segments - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         ++segments;
-        const int upto = nrows > kTileRows ? ROWS : kTileRows;
-#pragma unroll 8
-        for (int i = me; i < upto * PPR; i += kPagedQThreads) {
-          const int r = i / PPR, piece = i % PPR;
-          const bool on = r < nrows && piece * 8 < p.H;
-          const int d = kv_div(rem0 + r, p.by_g);  // token from tok0 on; head rem0 + r - d G
-          const int64_t at = (int64_t)d * p.Nq * p.H + (int64_t)(rem0 + r - d * p.G) * p.H + piece * 8;
-          kv_cp<16>(sq + (r / kTileRows) * (kTileRows * HD * 2) + tile_at(kTileRows, r % kTileRows, piece),
-                    on ? q0 + at : static_cast<const bits*>(p.q), on);
-        }
-        kv_cp_commit();
-        kv_cp_wait<0>();
-        tc_fence_smem();
-        mbar_arrive(bar(&bars.q_full));
+        if (lane == 0) mbar_arrive_expect_tx(bar(&bars.q_full), C::SLABS * q_rows * 128);
+        __syncwarp();
+        if (lane < C::SLABS)
+          tile_tma(sq + lane * (ROWS * 128), &maps.q, lane * 64, work.kvh * p.G, it.g0, bar(&bars.q_full));
       }
-    }
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------------ K and V
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    const int me = tid - 256;
-    constexpr int PPR = HD / 8;              // 16-byte pieces of a row in shared memory
-    // a box: p.chunk rows (of one page) x 64 elements; this thread's rows and slab of a tile
-    const int chunks = N / p.chunk, boxes = chunks * C::SLABS;
-    const int my_row = (me & (chunks - 1)) * p.chunk, my_slab = me / chunks;
-    bool bad = false;
-    int gs = 0, nk = 0, nv = 0;  // key tiles; those of K and of V whose loads have begun
-    while (ok && work.next(p, before, count)) {
-      const int4 it = items[work.item];
-      int lo, hi;
-      const int n = keys_of(it, lo, hi);
-      if (n == 0) continue;
-      const int b = it.x, kvh = work.kvh;
-      const PagedSeq seq = paged_seq(p.s, b);
-      const int seen = paged_first(p, seq.past + (int64_t)it.y * ROWS / p.G);  // keys before this are nobody's
-      const int32_t* table = p.s.table + (int64_t)b * p.s.max_pages;
-      // (row in the page, page) of this thread's box of the tile at j0; -1: zeros
-      auto box_of = [&](int j0) {
-        const int j = j0 + my_row;
-        int2 at = make_int2(0, -1);
-        if (me >= boxes || j0 < lo || j0 + N > hi || j + p.chunk <= seen) return at;
-        const int i = kv_div(j, p.s.by_ps);
-        at.x = j - i * p.s.ps;
-        at.y = __ldg(table + i);
-        if ((uint32_t)at.y >= (uint32_t)p.s.pages) bad = true, at.y = -1;
-        return at;
-      };
-      auto bring = [&](uint32_t dst, const void* src, const CUtensorMap* map, int j0, int2 box, uint32_t full) {
-        if (j0 + N <= hi) {
-          if (me == 0)
-            mbar_arrive_expect_tx(full, C::kStage);
-          else
-            mbar_arrive(full);
-          if (me < boxes)
-            paged_tma(dst + my_slab * (N * 128) + my_row * 128, map, my_slab * 64, box.x, kvh, box.y, full);
-          return;
+      // what is on its way has to land before shared memory goes
+      if (segments > 0 && !ok) mbar_wait(bar(&bars.q_full), (segments - 1) & 1);
+    } else {
+      // ---------------------------------------------------------------- K (warp 8) and V
+      const bool is_k = warp == 8;
+      uint64_t* const full = is_k ? bars.k_full : bars.v_full;
+      uint64_t* const free_ = is_k ? bars.k_free : bars.v_free;
+      const CUtensorMap* const map = is_k ? &maps.k : &maps.v;
+      const CUtensorMap* const row_map = is_k ? &maps.k_row : &maps.v_row;
+      const uint32_t stage0 = is_k ? sk : sv;
+      // a box: p.chunk rows (of one page) x 64 elements; this lane's rows and slab of a tile
+      const int chunks = N / p.chunk;
+      const int my_row = (lane & (chunks - 1)) * p.chunk, my_slab = lane / chunks;
+      bool bad = false;
+      int gs = 0;  // key tiles
+      while (ok && work.next(p, before, count)) {
+        const PagedItem& it = items[work.item];
+        int lo, hi;
+        const int n = keys_of(it, lo, hi);
+        if (n == 0) continue;
+        const int kvh = work.kvh, seen = paged_first(p, it.pos0);  // keys before `seen` are nobody's
+        const int32_t* table = p.s.table + (int64_t)it.b * p.s.max_pages;
+        // (row in its page, page) of key j, -1: zeros; for keys that nobody sees, and pages outside the pool
+        auto place = [&](int j, int upto) {
+          int2 at = make_int2(0, -1);
+          if (j >= hi || upto <= seen) return at;
+          const int i = kv_div(j, p.s.by_ps);
+          at.x = j - i * p.s.ps;
+          at.y = __ldg(table + i);
+          if ((uint32_t)at.y >= (uint32_t)p.s.pages) bad = true, at.y = -1;
+          return at;
+        };
+        auto box_of = [&](int j0) {
+          return j0 >= lo ? place(j0 + my_row, j0 + my_row + p.chunk) : make_int2(0, -1);
+        };
+        int2 box = box_of(lo + (n - 1) * N);
+        for (int tile = n - 1; tile >= 0; --tile, ++gs) {
+          const int st = gs & 1, j0 = lo + tile * N;
+          const int2 after = box_of(j0 - N);
+          if (gs >= 2) ok = mbar_wait(bar(&free_[st]), ((gs >> 1) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t dst = stage0 + st * C::kStage, done = bar(&full[st]);
+          if (lane == 0) mbar_arrive_expect_tx(done, C::kStage);
+          __syncwarp();
+          // the box that holds the last key and rows behind it
+          const int cut = hi < j0 + N ? (hi - j0) & ~(p.chunk - 1) : N;
+          const bool cut_box = cut < N && cut + j0 < hi;
+          if (my_slab < C::SLABS && !(cut_box && my_row == cut))
+            paged_tma(dst + my_slab * (N * 128) + my_row * 128, map, my_slab * 64, box.x, kvh, box.y, done);
+          if (cut_box)
+            for (int i = lane; i < p.chunk * C::SLABS; i += 32) {
+              const int r = cut + (i & (p.chunk - 1)), slab = i / p.chunk;
+              const int2 at = place(j0 + r, j0 + r + 1);
+              paged_tma(dst + slab * (N * 128) + r * 128, row_map, slab * 64, at.x, kvh, at.y, done);
+            }
+          box = after;
         }
-        // the last tile: rows behind the keys have to be zeros
-#pragma unroll 4
-        for (int i = me; i < N * PPR; i += kTileBring) {
-          const int r = i / PPR, piece = i % PPR;
-          int64_t at = -1;
-          if (j0 + r < hi && j0 + r >= seen && piece * 8 < p.H) {
-            at = paged_row(p.s, b, kvh, j0 + r, p.H);
-            bad |= at < 0;
-          }
-          kv_cp<16>(dst + tile_at(N, r, piece), static_cast<const bits*>(src) + (at >= 0 ? at + piece * 8 : 0), at >= 0);
-        }
-        kv_cp_commit();
-        kv_cp_wait<0>();
-        tc_fence_smem();
-        mbar_arrive(full);
-      };
-      int2 box = box_of(lo + (n - 1) * N);
-      for (int tile = n - 1; tile >= 0; --tile, ++gs) {
-        const int st = gs & 1, j0 = lo + tile * N;
-        const int2 after = box_of(j0 - N);
-        if (gs >= 2) ok = mbar_wait(bar(&bars.k_free[st]), ((gs >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        bring(sk + st * C::kStage, p.k, &maps.k, j0, box, bar(&bars.k_full[st]));
-        ++nk;
-        if (gs >= 2) ok = mbar_wait(bar(&bars.v_free[st]), ((gs >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        bring(sv + st * C::kStage, p.v, &maps.v, j0, box, bar(&bars.v_full[st]));
-        ++nv;
-        box = after;
       }
-    }
-    if (bad && p.s.status) atomicOr(p.s.status, 4);
-    if (!ok) {  // what TMA still brings has to land before shared memory goes
-      for (int i = nk - 2; i < nk; ++i)
-        if (i >= 0) mbar_wait(bar(&bars.k_full[i & 1]), (i >> 1) & 1);
-      for (int i = nv - 2; i < nv; ++i)
-        if (i >= 0) mbar_wait(bar(&bars.v_full[i & 1]), (i >> 1) & 1);
+      if (bad && p.s.status) atomicOr(p.s.status, 4);
+      if (!ok)  // what is on its way has to land before shared memory goes
+        for (int i = gs - 2; i < gs; ++i)
+          if (i >= 0) mbar_wait(bar(&full[i & 1]), (i >> 1) & 1);
     }
   }
   if (!ok && p.s.status) atomicOr(p.s.status, 2);
   tc_before();
   __syncthreads();
-  if (warp == 12)
+  if (warp == 11)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
 // Joins the parts of the items that paged_tile_kernel_t dealt to several CTAs. CTA (x,
-// y): the item that begins in CTA x there and goes on in others, if there is one; a warp
-// a row, rows 4 y + warp, + 4 gridDim.y, ... `rows`: of a slot.
+// y): the item that begins in CTA x there and goes on in others, if there is one; its
+// rows 16 y .., 16 threads side by side for the same dims of 16 rows. `rows`: of a slot.
 template <class T>
 __global__ void __launch_bounds__(kKvTokenThreads) paged_tile_join_kernel_t(const PagedParams p, int rows) {
-  using bits = typename Elem<T>::bits;
+  constexpr int PIECES = kKvMaxHead / 4 / 8;  // of 4 dims, a thread
   pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int4 what = p.ws_join[blockIdx.x];  // b, kvh, tile of rows, 2 * further CTAs + slot
-  if (what.w < 2) return;
-  const int kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x;
-  const PagedSeq seq = paged_seq(p.s, what.x);
-  const int64_t row0 = (int64_t)what.z * rows, left = (int64_t)seq.n * p.G - row0;
-  const int n_rows = left < rows ? (int)left : rows;
+  const int4 what = p.ws_join[blockIdx.x];  // first token, kvh, rows, 2 * further CTAs + slot
+  const int r = (int)blockIdx.y * 16 + (threadIdx.x & 15), piece0 = threadIdx.x >> 4;
+  if (what.w < 2 || r >= what.z) return;
+  const int kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x, pieces = p.H / 4;
   // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
   auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
-  for (int r = (int)blockIdx.y * kTokWarps + warp; r < n_rows; r += gridDim.y * kTokWarps) {
-    float M = -CUDART_INF_F;
-    for (int n = lane; n < parts; n += 32) M = fmaxf(M, p.ws_ml[slot_of(n) * rows + r].x);
+  float M = -CUDART_INF_F;
+#pragma unroll 8
+  for (int n = 0; n < parts; ++n) M = fmaxf(M, p.ws_ml[slot_of(n) * rows + r].x);
+  const float base = M == -CUDART_INF_F ? 0.0f : M;
+  float L = 0.0f;
+  float4 acc[PIECES];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -CUDART_INF_F ? 0.0f : M;
-    float L = 0.0f, acc[kKvMaxHead / 32];
-#pragma unroll
-    for (int j = 0; j < kKvMaxHead / 32; ++j) acc[j] = 0.0f;
+  for (int j = 0; j < PIECES; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int n = 0; n < parts; ++n) {
-      const int64_t s = slot_of(n) * rows + r;
-      const float2 ml = p.ws_ml[s];
-      const float* o = p.ws_o + s * p.H;
-      const float f = exp2f(ml.x - base);
-      L = fmaf(ml.y, f, L);
+  for (int n = 0; n < parts; ++n) {
+    const int64_t slot = slot_of(n);
+    const float2 ml = p.ws_ml[slot * rows + r];
+    const float f = exp2f(ml.x - base);
+    const bool on = !(ml.x == -CUDART_INF_F && ml.y == 0.0f);  // else nothing was written, or zeros
+    L = fmaf(ml.y, f, L);
+    const float4* o = reinterpret_cast<const float4*>(p.ws_o) + slot * pieces * rows + r;
 #pragma unroll
-      for (int j = 0; j < kKvMaxHead / 128; ++j)
-        if (lane * 4 + 128 * j < p.H) {
-          float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
-          if (ml.x == -CUDART_INF_F && ml.y == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // never written where a CTA had no units
-          acc[4 * j] = fmaf(x.x, f, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(x.y, f, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(x.z, f, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(x.w, f, acc[4 * j + 3]);
-        }
-    }
-    const int64_t row = row0 + r, tok = row / p.G;
-    bits* y = static_cast<bits*>(p.out) + ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (row - tok * p.G)) * p.H;
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-    for (int j = 0; j < kKvMaxHead / 128; ++j)
-      if (lane * 4 + 128 * j < p.H) {
-        VecT<T, 4> v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v.v[i] = Elem<T>::fromf(acc[4 * j + i] * inv);
-        *reinterpret_cast<VecT<T, 4>*>(y + lane * 4 + 128 * j) = v;
+    for (int j = 0; j < PIECES; ++j)
+      if (on && piece0 + 8 * j < pieces) {
+        const float4 x = o[(int64_t)(piece0 + 8 * j) * rows];
+        acc[j].x = fmaf(x.x, f, acc[j].x);
+        acc[j].y = fmaf(x.y, f, acc[j].y);
+        acc[j].z = fmaf(x.z, f, acc[j].z);
+        acc[j].w = fmaf(x.w, f, acc[j].w);
       }
   }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int tok = kv_div(r, p.by_g);
+  typename Elem<T>::bits* y = static_cast<typename Elem<T>::bits*>(p.out) +
+                              (((int64_t)what.x + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j)
+    if (piece0 + 8 * j < pieces) {
+      VecT<T, 4> v;
+      v.v[0] = Elem<T>::fromf(acc[j].x * inv);
+      v.v[1] = Elem<T>::fromf(acc[j].y * inv);
+      v.v[2] = Elem<T>::fromf(acc[j].z * inv);
+      v.v[3] = Elem<T>::fromf(acc[j].w * inv);
+      *reinterpret_cast<VecT<T, 4>*>(y + 4 * (piece0 + 8 * j)) = v;
+    }
 }
 
 template <class T, int HD>
@@ -752,7 +754,7 @@ PagedTileKernel paged_tile_of(int kind) {
   const void* fn = kind == kKvPlain    ? (const void*)paged_tile_kernel_t<T, HD, kKvPlain>
                    : kind == kKvBiased ? (const void*)paged_tile_kernel_t<T, HD, kKvBiased>
                                        : (const void*)paged_tile_kernel_t<T, HD, kKvAnyScore>;
-  return {fn, (const void*)paged_tile_join_kernel_t<T>, 1024 + C::kQ + 4 * C::kStage + kPagedItems * 20 + 16};
+  return {fn, (const void*)paged_tile_join_kernel_t<T>, 1024 + C::kQ + 4 * C::kStage + kPagedItems * (sizeof(PagedItem) + 4) + 16};
 }
 
 template <class T>

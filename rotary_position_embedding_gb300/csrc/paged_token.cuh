@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
       if (paged_sync_or(odd)) {
 #pragma unroll 1
         for (int r = warp; r < rows_all; r += kPagedWarps)
-          paged_careful_row<T>(p, seq, b, kvh, r, lo, hi, part_o ? part_o + r * part_ld : nullptr, part_ml + r, lane);
+          paged_careful_row<T>(p, seq, b, kvh, r, lo, hi, part_o ? part_o + r * part_ld : nullptr, 4, part_ml + r,
+                              lane);
       } else {
         // join the warps: their O and statistics meet in shared memory, some dims at a time
 #pragma unroll

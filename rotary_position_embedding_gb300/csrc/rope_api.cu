@@ -979,6 +979,18 @@ bool rope_gb300::encode_paged_map(CUtensorMap* m, bool bf16, const void* base, i
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool rope_gb300::encode_paged_q_map(CUtensorMap* m, bool bf16, const void* base, int64_t H, int64_t Nq, int64_t T, int G,
+                                    int tokens) {
+  if (!encode_tiled() || Nq >= (1ll << 32) || T >= (1ll << 32) || Nq * H * 2 >= (1ll << 40)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)H, (cuuint64_t)Nq, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)H * 2, (cuuint64_t)(Nq * H * 2)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens}, estr[3] = {1, 1, 1};
+  return encode_tiled()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" {
 
 rope_status rope_apply(rope_dtype dtype, int32_t x_rank, const int64_t* x_shape, const void* x,
