@@ -714,7 +714,7 @@ const char* rope_last_error(void);
    "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
    (8-bit append), "kv_token_kernel" (attention, few rows), "kv_tile_kernel"
    (attention, many rows), "kv_simple_kernel"
-   (attention on CUDA cores), "paged_append_kernel", "paged_token_kernel", "paged_tile_kernel",
+   (attention on CUDA cores), "paged_append_kernel", "paged_append_heads_kernel" (several heads a thread), "paged_token_kernel", "paged_tile_kernel",
    "paged_simple_kernel" or "paged_keep_kernel" (the same over pages; with both few rows and many the
    last to be launched); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.

@@ -25,7 +25,7 @@ SOURCES = ["rope_api.cu", "k_rope.cu", "k_mrope.cu", "k_fused.cu", "k_tma.cu", "
            "k_paged_keep.cu"]
 HEADERS = ["rope_kernels.cuh", "rope_internal.h", "rope_tma.cuh", "rope_qkv.cuh", "rope_qkv_tma.cuh", "rope_packed.cuh", "rope_fused.cuh",
            "rope_mrope_heads.cuh", "rope_qkv_heads.cuh", "kv_internal.h", "kv_common.cuh", "kv_append.cuh", "kv_simple.cuh", "kv_careful.cuh", "kv_token.cuh", "kv_tile.cuh", "kv_maps.h", "kv_host.h",
-           "paged_internal.h", "paged_common.cuh", "paged_append.cuh", "paged_simple.cuh", "paged_careful.cuh", "paged_token.cuh",
+           "paged_internal.h", "paged_common.cuh", "paged_append.cuh", "paged_append_heads.cuh", "paged_simple.cuh", "paged_careful.cuh", "paged_token.cuh",
            "paged_tile.cuh", "paged_maps.h", "paged_keep.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -9,8 +9,10 @@
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
+#include <map>
 #include <mutex>
 #include <set>
+#include <tuple>
 #include <utility>
 
 #include "kv_internal.h"
@@ -116,6 +118,24 @@ inline rope_status allow_smem(const void* fn, size_t smem, int registers) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
   g_raised.insert(std::make_pair(dev, fn));
+  return ROPE_OK;
+}
+
+// CTAs of `threads` threads without dynamic shared memory that an SM holds, asked for once.
+inline std::map<std::tuple<int, const void*, int>, int> g_resident;
+inline rope_status resident_ctas(const void* fn, int threads, int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(g_mu);
+  int& held = g_resident[std::make_tuple(dev, fn, threads)];
+  if (held == 0) {
+    int b = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, 0);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+    held = b < 1 ? 1 : b;
+  }
+  *n = held;
   return ROPE_OK;
 }
 

@@ -93,12 +93,12 @@ PagedPlan plan_simple(int64_t B, int64_t T, int64_t most, int64_t Nq, int64_t Nk
 
 // Few problems of caches that are not long take a cluster of CTAs each, one launch
 // instead of two; else units of keys are dealt to as many CTAs as are resident.
-PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
+PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows, bool mixed) {
   PagedPlan pl;
   const int64_t R = most * (Nq / Nkv), rt = R > 8 ? 16 : 8;
   const int64_t problems = B * Nkv, units = (rows + 63) / 64;
   pl.split_bytes = 2 * rt * (H * 4 + 8) + 16;
-  if (units > 1 && rows <= 4096) {
+  if (!mixed && units > 1 && rows <= 4096) {
     int n = pow2_at_least(units);
     if (n > kKvClusterMost) n = kKvClusterMost;
     if (problems * n <= kSms) pl.cluster = n;
@@ -177,13 +177,15 @@ int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_
   // whichever kernels the types, alignments and arguments make the call take
   const int64_t rows = page_size * max_pages;
   int64_t most = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes;
-  auto more = [&](int64_t n) { most = n > most ? n : most; };
+  int64_t tile = 0;
   if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
-    more(plan_tile(batch, tokens, max_query_len, false, num_heads, kv_num_heads, head_size, rows).bytes);
-  if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
-    more(plan_tile(batch, tokens, max_query_len, true, num_heads, kv_num_heads, head_size, rows).bytes);
-  more(plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes);
-  return most;
+    tile = plan_tile(batch, tokens, max_query_len, batch * max_query_len != tokens, num_heads, kv_num_heads, head_size, rows).bytes;
+  int64_t token = 0;
+  for (bool mixed : {false, true}) {
+    const int64_t n = plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows, mixed && tile > 0).bytes;
+    token = n > token ? n : token;
+  }
+  return tile + token > most ? tile + token : most;
 }
 
 rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
@@ -284,16 +286,26 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
   void* args[] = {&p, &maps};
   // Parts in the workspace, `rt` rows each, two a CTA; half of the planned CTAs at least
   // are dealt to, or each takes its own problem.
-  auto deal_of = [&](const PagedPlan& pl, int64_t rt) {
-    const int64_t fits = room / pl.split_bytes;
+  auto deal_of = [&](const PagedPlan& pl, int64_t rt, int64_t from) {
+    const int64_t fits = (room - from) / pl.split_bytes;
     p.deal = pl.deal <= fits ? pl.deal : fits * 2 >= pl.deal ? (int)fits : 0;
     if (p.deal > 0) {
       const int64_t n = 2 * (int64_t)p.deal * rt;
-      p.ws_o = static_cast<float*>(workspace);
+      p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + from);
       p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size);
       p.ws_join = reinterpret_cast<int4*>(p.ws_ml + n);  // 16-byte aligned: n is a multiple of 16
     }
   };
+  // The two kernels of a mixed batch run at a time where both are dealt to with a
+  // workspace of their own.
+  int64_t token_at = 0;  // where paged_token_kernel's begins
+  const int64_t token_most = p.mixed ? kMixedRows / p.G : max_query_len;
+  if (p.mixed) {
+    const PagedPlan tile = plan_tile(batch, tokens, max_query_len, ragged, num_heads, kv_num_heads, head_size, rows);
+    const PagedPlan token = plan_token(batch, token_most, num_heads, kv_num_heads, head_size, rows, true);
+    p.shared = tile.deal == kSms && token.deal == paged_token_ctas(head_size) && tile.bytes + token.bytes <= room + kWorkspaceSlack;
+    if (p.shared) token_at = tile.bytes;
+  }
   if (family == PagedFamily::kSimple) {
     const PagedPlan pl = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows);
     if (pl.tiles * pl.splits > INT32_MAX) return fail(ROPE_ERR_UNSUPPORTED, "more than 2^31 row tiles");
@@ -319,33 +331,39 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     set_last_kernel("paged_simple_kernel");
     return ROPE_OK;
   }
+  PagedParams tile_p = p;
+  const void* tile_join = nullptr;
+  auto join_tiles = [&]() -> rope_status {
+    if (!tile_p.deal) return ROPE_OK;
+    int tr = kv_tile_rows(head_size);
+    void* jargs[] = {&tile_p, &tr};
+    return launch(tile_join, dim3((unsigned)tile_p.deal, tr / 16), kKvTokenThreads, 0, stream, jargs,
+                  "kv_attention_paged launch (joining the parts)");
+  };
   if (family != PagedFamily::kToken) {
     const PagedPlan pl = plan_tile(batch, tokens, max_query_len, ragged, num_heads, kv_num_heads, head_size, rows);
     const int kind = softcap > 0.0f || !(scale > 0.0f) ? kKvAnyScore : alibi_slopes ? kKvBiased : kKvPlain;
     const PagedTileKernel k =
         dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
-    int tr = kv_tile_rows(head_size);
-    deal_of(pl, tr);
+    deal_of(pl, kv_tile_rows(head_size), 0);
     void* targs[] = {&p, &tile_maps};
     KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kPagedTileBlock, k.smem, stream, targs,
                   "kv_attention_paged launch (many rows)", kPagedTileRegisters));
-    if (p.deal) {
-      void* jargs[] = {&p, &tr};
-      KV_TRY(launch(k.join, dim3((unsigned)p.deal, tr / 16), kKvTokenThreads, 0, stream, jargs,
-                    "kv_attention_paged launch (joining the parts)"));
-    }
+    tile_p = p;
+    tile_join = k.join;
+    if (!p.shared) KV_TRY(join_tiles());
     set_last_kernel("paged_tile_kernel");
   }
   if (family != PagedFamily::kTile) {
-    const int64_t most = p.mixed ? kMixedRows / p.G : max_query_len;
-    const PagedPlan pl = plan_token(batch, most, num_heads, kv_num_heads, head_size, rows);
-    p.rt = most * p.G > 8 ? 16 : 8;
+    const PagedPlan pl = plan_token(batch, token_most, num_heads, kv_num_heads, head_size, rows, p.mixed != 0);
+    p.rt = token_most * p.G > 8 ? 16 : 8;
     p.cluster = pl.cluster;
-    deal_of(pl, p.rt);
+    deal_of(pl, p.rt, token_at);
     const PagedTokenKernel k = paged_token_kernel(dtype, (int)head_size, p.rt == 8);
     const int64_t grid = p.deal ? p.deal : batch * kv_num_heads * (p.cluster ? p.cluster : 1);
     KV_TRY(launch(k.fn, dim3((unsigned)grid), kPagedTokenThreads, p.cluster ? k.cluster_smem : k.smem, stream, args,
                   "kv_attention_paged launch (few rows)", 0, p.cluster));
+    if (p.shared) KV_TRY(join_tiles());
     if (p.deal) {
       // few problems, each of many parts: a CTA a row
       const unsigned n = batch * kv_num_heads * 8 <= p.deal ? (unsigned)p.rt : 1;
@@ -451,10 +469,30 @@ rope_status rope_apply_qkv_paged(rope_dtype dtype, int64_t batch, int64_t tokens
   p.U = p.nP + (int32_t)((head_size - rd) / V);
   p.lanes = p.U >= 32 ? 32 : pow2_at_least(p.U);
   p.eps = epsilon;
+  p.width = (float)head_size;
+  void* args[] = {&p};
+  // Several heads of one role a thread where a token's threads fit a CTA: 4 on 16-bit
+  // data from 4096 tokens on, else 2 (more, smaller CTAs), as rope_apply_qkv.
+  const bool whole_groups = !norm || p.U == p.lanes;  // a head's sum is taken by U lanes side by side
+  const int hpt = norm || es == 4 || tokens < 4096 ? 2 : 4;
+  const int64_t groups = (num_heads + hpt - 1) / hpt + 2 * ((kv_num_heads + hpt - 1) / hpt);
+  if (vec && p.U <= 32 && whole_groups && groups * p.U <= kPagedHeadsThreads) {
+    const int per_tok = (int)groups * p.U;
+    p.groups = (int32_t)groups;
+    p.tokens = per_tok >= 256 ? 1 : 256 / per_tok;
+    const int threads = (p.tokens * per_tok + 31) / 32 * 32;
+    const void* fn = paged_append_heads_kernel(dtype, interleaved != 0, norm, hpt);
+    int resident = 0;
+    KV_TRY(resident_ctas(fn, threads, &resident));
+    int64_t n = (tokens + p.tokens - 1) / p.tokens;
+    if (n > resident * kSms) n = resident * kSms;  // one wave: a thread goes from token to token
+    KV_TRY(launch(fn, dim3((unsigned)n), threads, 0, stream, args, "rope_apply_qkv_paged launch"));
+    set_last_kernel("paged_append_heads_kernel");
+    return ROPE_OK;
+  }
   const int64_t per = kPagedAppendThreads / p.lanes;
   int64_t grid = (tokens * heads + per - 1) / per;
   if (grid > INT32_MAX) grid = INT32_MAX;
-  void* args[] = {&p};
   KV_TRY(launch(paged_append_kernel(dtype, vec, interleaved != 0, norm), dim3((unsigned)grid), kPagedAppendThreads, 0,
                 stream, args, "rope_apply_qkv_paged launch"));
   set_last_kernel("paged_append_kernel");
@@ -499,7 +537,8 @@ rope_status kv_keep_paged(rope_dtype dtype, int64_t batch, int32_t kv_num_heads,
   p.width = (int32_t)max_kept;
   p.Nkv = kv_num_heads;
   p.units = head_size / V;
-  int64_t grid = (batch * 2 * kv_num_heads * p.units + kPagedKeepThreads - 1) / kPagedKeepThreads;
+  p.lanes = p.units >= 32 ? 32 : pow2_at_least(p.units);
+  int64_t grid = (batch * 2 * kv_num_heads + kPagedKeepThreads / 32 - 1) / (kPagedKeepThreads / 32);
   if (grid > INT32_MAX) grid = INT32_MAX;
   void* args[] = {&p};
   KV_TRY(launch(paged_keep_kernel(vec ? 16 : (int)es), dim3((unsigned)grid), kPagedKeepThreads, 0, stream, args,

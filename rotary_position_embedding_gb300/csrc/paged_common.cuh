@@ -97,4 +97,53 @@ __device__ __forceinline__ int paged_first(const PagedParams& p, int64_t i) {
   return f <= 0 ? 0 : f < (1 << 30) ? (int)f : 1 << 30;
 }
 
+// Keys [lo, end) of a sequence for the kernel for few rows, lo at the start of a unit; a
+// unit where there are none, so that its output is written.
+constexpr int kPagedUnit = 64;  // keys of a unit
+struct PagedSpan {
+  int lo, end;
+  __device__ __forceinline__ int units() const { return end > lo ? (end - lo + kPagedUnit - 1) / kPagedUnit : 1; }
+};
+__device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, const PagedSeq& q) {
+  PagedSpan s;
+  s.lo = paged_first(p, q.past) / kPagedUnit * kPagedUnit;
+  s.end = paged_limit(p, q, (int64_t)q.past + q.n - 1);
+  return s;
+}
+// Whether a sequence is the kernel's for few rows.
+__device__ __forceinline__ bool paged_few(const PagedParams& p, const PagedSeq& q) {
+  return q.n > 0 && (int64_t)q.n * p.G <= (p.mixed ? p.mixed : kPagedFewRows);
+}
+
+// A mixed batch: prompts are bound by the tensor cores, single tokens by the memory, so
+// paged_tile_kernel_t and paged_token_kernel_t run at a time, the first on `n` SMs, the
+// second on the others: about 100 of them take what the memory gives (62 GB/s an SM).
+// Both work n out of the lengths in whole numbers, each sequence's time (ns of an SM)
+// added up in any order. A mixed step of a capped prompt of 2048 tokens and 95 single
+// tokens over up to 4000 keys: one after the other 255 us.
+constexpr int kPagedOver = 3;  // what an item of paged_tile_kernel_t weighs beside its key tiles
+struct PagedTimes {
+  unsigned long long tile, token;
+};
+__device__ __forceinline__ void paged_time(const PagedParams& p, const PagedSeq& q, PagedTimes* t) {
+  if (q.n == 0) return;
+  if (paged_few(p, q)) {
+    t->token += (unsigned long long)paged_span(p, q).units() * (unsigned)p.H * 4u;
+  } else {
+    const int keys = p.H <= 128 ? 128 : 64, step = p.H <= 64 ? 1400 : p.H <= 128 ? 1600 : 1000;
+    int64_t span = (int64_t)q.past + q.n / 2;
+    if (p.window > 0 && span > p.window + p.tpi) span = p.window + p.tpi;
+    if (span < 0) span = 0;
+    const int64_t items = (q.n + p.tpi - 1) / p.tpi;
+    t->tile += (unsigned long long)(items * (span / keys + 1 + kPagedOver)) * (unsigned)(p.cap > 0.0f ? step + 900 : step);
+  }
+}
+__device__ __forceinline__ int paged_shares(const PagedTimes& t) {
+  const unsigned long long all = t.tile + t.token;
+  if (t.tile == 0 || all == 0) return 0;
+  int n = (int)(152.0 * ((double)t.tile / (double)all) + 0.5);
+  if (n < 1) n = 1;
+  return t.token > 0 && n > 151 ? 151 : n > 152 ? 152 : n;
+}
+
 }  // namespace rope_gb300

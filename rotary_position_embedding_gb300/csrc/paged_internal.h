@@ -45,6 +45,7 @@ struct PagedParams {
   int32_t deal, cluster;   // CTAs that the work is dealt to; paged_token_kernel: or those of a cluster a problem
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
   int32_t tpi;             // paged_tile_kernel: tokens of an item
+  int32_t shared;          // both kernels run at a time, each on its share of the SMs (see paged_shares)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;
   float scale, cap, over;  // factor of q.k; 0: no cap; scale / cap
@@ -64,7 +65,7 @@ struct PagedTokenKernel {
   size_t smem, cluster_smem;  // without clusters, with them
 };
 constexpr int kPagedFewRows = 16;
-constexpr int kPagedTokenThreads = 160;
+constexpr int kPagedTokenThreads = 192;
 constexpr int kPagedBox = 64;  // most rows of a box
 constexpr int paged_token_ctas(int64_t H) { return 152 * (H > 128 ? 1 : 2); }  // that are resident
 PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
@@ -106,11 +107,15 @@ struct PagedAppendParams {
   int32_t h, rd;           // half rotary width, rotary width
   int32_t U, nP;           // units of a head, pair units among them
   int32_t lanes;           // threads that share a head (a power of two <= 32)
-  KvDiv by_rows;           // by Nq + 2 Nkv
-  float eps;
+  int32_t groups, tokens;  // paged_append_heads_kernel: groups of heads of a token, tokens of a CTA at a time
+  float eps, width;        // width: H
 };
 constexpr int kPagedAppendThreads = 256;
 const void* paged_append_kernel(int dtype, bool vec, bool interleaved, bool rms_norm);
+// The same on the 128-bit path for heads of at most 32 units, `hpt` heads of one role a
+// thread (4 or 2, with the norm 2; null for others); PagedAppendParams.groups, tokens.
+const void* paged_append_heads_kernel(int dtype, bool interleaved, bool rms_norm, int hpt);
+constexpr int kPagedHeadsThreads = 512;  // of a CTA at most
 
 // Rows past + kept[b, i] of each sequence to past + i.
 struct PagedKeepParams {
@@ -120,6 +125,7 @@ struct PagedKeepParams {
   const int32_t* kept;       // (B, width)
   const int32_t* kept_lens;  // (B)
   int32_t width, Nkv;
+  int32_t lanes;             // that share a row (a power of two <= 32)
   int64_t units;             // of a row
 };
 constexpr int kPagedKeepThreads = 256;

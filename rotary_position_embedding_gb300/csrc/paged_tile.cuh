@@ -38,7 +38,6 @@
 namespace rope_gb300 {
 
 constexpr int kPagedTileThreads = kPagedTileBlock;
-constexpr int kPagedOver = 2;  // what an item weighs beside its key tiles
 
 struct PagedTileBars {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], q_full, q_free, drain;
@@ -98,19 +97,22 @@ __device__ __forceinline__ int paged_scan(int n, int* s_sum, int* all) {
 }
 
 // The items of the batch and the weight of one head of those before each, in shared
-// memory; their number. Not dealt: only item number `only`, or none. All threads come
-// here, and the tables hold when it returns.
+// memory; their number. Not dealt: only item number `only`, or none. With p.shared none
+// where the CTA is beyond this kernel's share, `ctas`. All threads come here, and the
+// tables hold when it returns.
 __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int keys, PagedItem* items, int32_t* before,
-                                           int* s_sum) {
+                                           int* s_sum, PagedTimes* times, uint32_t* ctas) {
   const int tid = threadIdx.x;
   int count = 0;
+  PagedTimes t_all = {0, 0};
   for (int b0 = 0; b0 < p.s.B; b0 += kPagedTileThreads) {
     const int b = b0 + tid;
     PagedSeq q;
     int n = 0, all;
     if (b < p.s.B) {
       q = paged_seq(p.s, b);
-      if (!(p.mixed && (int64_t)q.n * p.G <= p.mixed)) n = (q.n + p.tpi - 1) / p.tpi;
+      if (!(p.mixed && paged_few(p, q))) n = (q.n + p.tpi - 1) / p.tpi;
+      if (p.shared) paged_time(p, q, &t_all);
     }
     const int first = paged_scan(n, s_sum, &all) - n + count;
     if (p.deal > 0) {
@@ -122,7 +124,17 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
     count += all;
     if (p.deal == 0 && only < count) break;  // the same for all threads
   }
+  if (p.shared) {
+    if (t_all.tile) atomicAdd(&times->tile, t_all.tile);
+    if (t_all.token) atomicAdd(&times->token, t_all.token);
+  }
   __syncthreads();
+  *ctas = (uint32_t)p.deal;
+  if (p.shared) {
+    const uint32_t n = (uint32_t)paged_shares(*times);
+    *ctas = n < 1 ? 1 : n < *ctas ? n : *ctas;
+    if (blockIdx.x >= *ctas) return 0;
+  }
   if (p.deal == 0) return only < count ? 1 : 0;
   if (count > kPagedItems) count = kPagedItems;
   int sum = 0;
@@ -236,6 +248,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   __shared__ PagedTileBars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_sum[kPagedTileThreads / 32];
+  __shared__ PagedTimes s_times;
   uint8_t* base = kv_tiles + ((1024 - (kv_smem(kv_tiles) & 1023)) & 1023);
   const uint32_t sq = kv_smem(base), sk = sq + C::kQ, sv = sk + 2 * C::kStage;
   PagedItem* const items = reinterpret_cast<PagedItem*>(base + C::kQ + 4 * C::kStage);
@@ -244,6 +257,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   auto bar = [&](uint64_t* b) { return kv_smem(b); };
 
   if (tid == 0) {
+    s_times.tile = s_times.token = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&bars.k_full[i]), 1);
       mbar_init(bar(&bars.v_full[i]), 1);
@@ -272,19 +286,30 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
     *reinterpret_cast<uint4*>(base + tile_at(ROWS, r, piece)) = make_uint4(0, 0, 0, 0);
   }
   tc_fence_smem();
-  pdl_launch_dependents();
+  if (!p.shared) pdl_launch_dependents();
   pdl_wait();
+  if (p.shared) pdl_launch_dependents();  // paged_token_kernel_t does not wait for what came before
+  __syncthreads();
 
   tc_before();
-  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), N, items, before, s_sum);
+  uint32_t ctas;  // that the work is dealt to
+  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), N, items, before, s_sum, &s_times, &ctas);
   tc_after();
   const uint32_t tmem = s_tmem;
+  if (p.shared && blockIdx.x >= ctas) {  // an SM of the other kernel's
+    if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == 11)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+    return;
+  }
   PagedTileWork work;
   work.at = work.last = 0;
-  const uint32_t total = p.deal > 0 ? (uint32_t)before[count] * (uint32_t)p.Nkv : 0u;  // below 2^31
+  const uint32_t total = p.deal > 0 && count > 0 ? (uint32_t)before[count] * (uint32_t)p.Nkv : 0u;  // below 2^31
   if (p.deal > 0) {
-    work.at = (int)((uint64_t)blockIdx.x * total / (uint32_t)p.deal);
-    work.last = (int)((uint64_t)(blockIdx.x + 1) * total / (uint32_t)p.deal);
+    if (blockIdx.x < ctas) {
+      work.at = (int)((uint64_t)blockIdx.x * total / ctas);
+      work.last = (int)((uint64_t)(blockIdx.x + 1) * total / ctas);
+    }
     // so far nothing begins here that goes on elsewhere, and nothing of this CTA's counts
     // where an item's CTAs lie on both sides of it
     if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -331,7 +356,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
       // the one item that begins in this CTA and goes on in others: paged_tile_join_kernel_t's
       if (tid == 0 && work.u0 == 0 && !whole) {
         const uint32_t upto = (uint32_t)(work.at - work.u1 + paged_item_tiles(it, N));  // its last tile, and one
-        const int parts = (int)(((uint64_t)upto * (uint32_t)p.deal - 1) / total) - (int)blockIdx.x;
+        const int parts = (int)(((uint64_t)upto * ctas - 1) / total) - (int)blockIdx.x;
         p.ws_join[blockIdx.x] = make_int4(it.g0, kvh, nrows, 2 * parts + (segment > 0 ? 1 : 0));
       }
       if (t * kTileRows >= nrows) continue;
@@ -434,7 +459,8 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
         float4* const part = reinterpret_cast<float4*>(p.ws_o) + slot * (p.H / 4) * ROWS + tid;
         bits* const out = static_cast<bits*>(p.out) + ((int64_t)it.g0 * p.Nq + (int64_t)kvh * p.G) * p.H;
         const int at = live ? (tok * p.Nq + head) * p.H : -1;  // of the row, from `out` on
-        bool odd = false;
+        float2 sums = make_float2(0.0f, 0.0f);  // of 0 times each output: NaN where one is not finite
+        const float2 f2 = make_float2(f, f), zero2 = make_float2(0.0f, 0.0f);
         if (live && !whole) p.ws_ml[slot * ROWS + tid] = make_float2(m, l);
 #pragma unroll 1
         for (int i0 = 0; i0 < HD; i0 += 64) {
@@ -445,9 +471,11 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
           tc_wait_ld32(o + 32);
           float y[64];
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            y[k] = empty ? 0.0f : __uint_as_float(o[k]) * f;
-            odd |= !(fabsf(y[k]) < CUDART_INF_F) && i0 + k < p.H;
+          for (int k = 0; k < 64; k += 2) {
+            const float2 z = __fmul2_rn(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), f2);
+            y[k] = empty ? 0.0f : z.x;
+            y[k + 1] = empty ? 0.0f : z.y;
+            sums = __ffma2_rn(make_float2(y[k], y[k + 1]), zero2, sums);
           }
           if (!whole) {
 #pragma unroll
@@ -469,7 +497,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
           }
         }
         // An infinity or a NaN may have come from a value that the row does not see
-        uint32_t again = __ballot_sync(0xffffffffu, odd && live);
+        uint32_t again = __ballot_sync(0xffffffffu, live && !(sums.x == 0.0f && sums.y == 0.0f));
         if (again) {
           bool found = false;  // in a value that some row of the warp does not see and its key tile holds
           auto look = [&](int from_key, int to_key) {
@@ -643,23 +671,21 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
         if (n == 0) continue;
         const int kvh = work.kvh, seen = paged_first(p, it.pos0);  // keys before `seen` are nobody's
         const int32_t* table = p.s.table + (int64_t)it.b * p.s.max_pages;
-        // (row in its page, page) of key j, -1: zeros; for keys that nobody sees, and pages outside the pool
-        auto place = [&](int j, int upto) {
-          int2 at = make_int2(0, -1);
-          if (j >= hi || upto <= seen) return at;
-          const int i = kv_div(j, p.s.by_ps);
-          at.x = j - i * p.s.ps;
-          at.y = __ldg(table + i);
-          if ((uint32_t)at.y >= (uint32_t)p.s.pages) bad = true, at.y = -1;
-          return at;
+        // The table's entry for key j, looked at a tile later; -1 for keys that nobody sees,
+        // as for pages outside the pool: TMA fills in zeros.
+        auto entry = [&](int j, int upto) {
+          return j < hi && upto > seen && j >= lo ? __ldg(table + kv_div(j, p.s.by_ps)) : -1;
         };
-        auto box_of = [&](int j0) {
-          return j0 >= lo ? place(j0 + my_row, j0 + my_row + p.chunk) : make_int2(0, -1);
+        auto bring = [&](const CUtensorMap* m, uint32_t dst, int slab, int j, int upto, int page, uint32_t done) {
+          const bool in_pool = (uint32_t)page < (uint32_t)p.s.pages;
+          bad |= !in_pool && j < hi && upto > seen;
+          paged_tma(dst, m, slab * 64, j - kv_div(j, p.s.by_ps) * p.s.ps, kvh, in_pool ? page : -1, done);
         };
-        int2 box = box_of(lo + (n - 1) * N);
+        auto box_entry = [&](int j0) { return entry(j0 + my_row, j0 + my_row + p.chunk); };
+        int page = box_entry(lo + (n - 1) * N);
         for (int tile = n - 1; tile >= 0; --tile, ++gs) {
           const int st = gs & 1, j0 = lo + tile * N;
-          const int2 after = box_of(j0 - N);
+          const int page_after = box_entry(j0 - N);
           if (gs >= 2) ok = mbar_wait(bar(&free_[st]), ((gs >> 1) - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -670,14 +696,15 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
           const int cut = hi < j0 + N ? (hi - j0) & ~(p.chunk - 1) : N;
           const bool cut_box = cut < N && cut + j0 < hi;
           if (my_slab < C::SLABS && !(cut_box && my_row == cut))
-            paged_tma(dst + my_slab * (N * 128) + my_row * 128, map, my_slab * 64, box.x, kvh, box.y, done);
-          if (cut_box)
+            bring(map, dst + my_slab * (N * 128) + my_row * 128, my_slab, j0 + my_row, j0 + my_row + p.chunk, page, done);
+          if (cut_box) {
+            const int cut_page = entry(j0 + cut, j0 + cut + p.chunk);
             for (int i = lane; i < p.chunk * C::SLABS; i += 32) {
-              const int r = cut + (i & (p.chunk - 1)), slab = i / p.chunk;
-              const int2 at = place(j0 + r, j0 + r + 1);
-              paged_tma(dst + slab * (N * 128) + r * 128, row_map, slab * 64, at.x, kvh, at.y, done);
+              const int r = cut + (i & (p.chunk - 1)), slab = i / p.chunk, j = j0 + r;
+              bring(row_map, dst + slab * (N * 128) + r * 128, slab, j, j + 1, j < hi && j >= seen ? cut_page : -1, done);
             }
-          box = after;
+          }
+          page = page_after;
         }
       }
       if (bad && p.s.status) atomicOr(p.s.status, 4);
@@ -696,10 +723,11 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
 // Joins the parts of the items that paged_tile_kernel_t dealt to several CTAs. CTA (x,
 // y): the item that begins in CTA x there and goes on in others, if there is one; its
 // rows 16 y .., 16 threads side by side for the same dims of 16 rows. `rows`: of a slot.
-template <class T>
+template <class T, int HD>
 __global__ void __launch_bounds__(kKvTokenThreads) paged_tile_join_kernel_t(const PagedParams p, int rows) {
-  constexpr int PIECES = kKvMaxHead / 4 / 8;  // of 4 dims, a thread
-  pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
+  constexpr int PIECES = HD / 4 / 8;  // of 4 dims, a thread
+  pdl_wait();  // it lets nothing start early (the next call's CTAs would take places unevenly)
+  if (p.shared) pdl_launch_dependents();  // but the other kernel's joining
   const int4 what = p.ws_join[blockIdx.x];  // first token, kvh, rows, 2 * further CTAs + slot
   const int r = (int)blockIdx.y * 16 + (threadIdx.x & 15), piece0 = threadIdx.x >> 4;
   if (what.w < 2 || r >= what.z) return;
@@ -714,7 +742,7 @@ __global__ void __launch_bounds__(kKvTokenThreads) paged_tile_join_kernel_t(cons
   float4 acc[PIECES];
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll(HD > 128 ? 2 : 4)
   for (int n = 0; n < parts; ++n) {
     const int64_t slot = slot_of(n);
     const float2 ml = p.ws_ml[slot * rows + r];
@@ -724,8 +752,9 @@ __global__ void __launch_bounds__(kKvTokenThreads) paged_tile_join_kernel_t(cons
     const float4* o = reinterpret_cast<const float4*>(p.ws_o) + slot * pieces * rows + r;
 #pragma unroll
     for (int j = 0; j < PIECES; ++j)
-      if (on && piece0 + 8 * j < pieces) {
-        const float4 x = o[(int64_t)(piece0 + 8 * j) * rows];
+      if (piece0 + 8 * j < pieces) {
+        float4 x = o[(int64_t)(piece0 + 8 * j) * rows];  // (loaded in any case: no load waits for another)
+        if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         acc[j].x = fmaf(x.x, f, acc[j].x);
         acc[j].y = fmaf(x.y, f, acc[j].y);
         acc[j].z = fmaf(x.z, f, acc[j].z);
@@ -754,7 +783,7 @@ PagedTileKernel paged_tile_of(int kind) {
   const void* fn = kind == kKvPlain    ? (const void*)paged_tile_kernel_t<T, HD, kKvPlain>
                    : kind == kKvBiased ? (const void*)paged_tile_kernel_t<T, HD, kKvBiased>
                                        : (const void*)paged_tile_kernel_t<T, HD, kKvAnyScore>;
-  return {fn, (const void*)paged_tile_join_kernel_t<T>, 1024 + C::kQ + 4 * C::kStage + kPagedItems * (sizeof(PagedItem) + 4) + 16};
+  return {fn, (const void*)paged_tile_join_kernel_t<T, HD>, 1024 + C::kQ + 4 * C::kStage + kPagedItems * (sizeof(PagedItem) + 4) + 16};
 }
 
 template <class T>

@@ -2,8 +2,8 @@
 // rows n * G of a (b, kvh), 16-bit T.
 //
 // Every cached byte is used once for 8 or 16 rows, so the pages' bandwidth is the
-// bound. A fifth warp brings units of 64 keys into a ring by TMA, box by box (a box:
-// the rows of a unit that lie in one page, 64 elements wide), and runs ahead of the
+// bound. Two warps bring units of 64 keys into a ring by TMA, box by box (a box:
+// the rows of a unit that lie in one page, 64 elements wide), and run ahead of the
 // four that compute, across problems too: nothing that those do between two
 // problems (queries, joining, output) leaves the memory idle while the ring is
 // filling. 96 KB of ring and two CTAs an SM; 192 KB and one above H = 128.
@@ -39,7 +39,7 @@
 namespace rope_gb300 {
 
 constexpr int kPagedWarps = 4;                   // that compute
-constexpr int kPagedUnit = 16 * kPagedWarps;     // keys of a unit
+static_assert(kPagedUnit == 16 * kPagedWarps, "keys of a unit");
 
 template <int HD, int NB>
 struct PagedTokenCfg {
@@ -94,38 +94,25 @@ __device__ __forceinline__ bool paged_sync_or(bool x) {
   return y != 0;
 }
 
-// Keys [lo, end) of a sequence's problems, lo at the start of a unit; no units where
-// the kernel for many rows takes it, or where it has no tokens.
-struct PagedSpan {
-  int lo, end;
-  __device__ __forceinline__ int units() const { return end > lo ? (end - lo + kPagedUnit - 1) / kPagedUnit : 1; }
-};
-__device__ __forceinline__ bool paged_token_mine(const PagedParams& p, const PagedSeq& q) {
-  return q.n > 0 && (int64_t)q.n * p.G <= (p.mixed ? p.mixed : kPagedFewRows);
-}
-__device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, const PagedSeq& q) {
-  PagedSpan s;
-  s.lo = paged_first(p, q.past) / kPagedUnit * kPagedUnit;
-  s.end = paged_limit(p, q, (int64_t)q.past + q.n - 1);
-  return s;
-}
-
 struct PagedDeal {
   const int32_t* before;  // units of one problem of the sequences before b, for each b, and of all
   int total;              // units of all problems, below 2^31
-  __device__ __forceinline__ int first(const PagedParams& p, int cta) const {
-    return (int)((uint64_t)(uint32_t)cta * (uint32_t)total / (uint32_t)p.deal);
+  int ctas;               // that they are dealt to
+  __device__ __forceinline__ int first(int cta) const {
+    return cta < ctas ? (int)((uint64_t)(uint32_t)cta * (uint32_t)total / (uint32_t)ctas) : total;
   }
-  __device__ __forceinline__ int owner(const PagedParams& p, int unit) const {
-    return (int)((((uint64_t)(uint32_t)unit + 1) * (uint32_t)p.deal - 1) / (uint32_t)total);
+  __device__ __forceinline__ int owner(int unit) const {
+    return (int)((((uint64_t)(uint32_t)unit + 1) * (uint32_t)ctas - 1) / (uint32_t)total);
   }
 };
 
 // The units before each sequence, in shared memory; all threads come here.
-__device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* before, int32_t* warp_sum) {
+__device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* before, int32_t* warp_sum,
+                                                PagedTimes* times) {
   constexpr int PER = kKvDealMost / 128;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int u[PER], sum = 0, pre = 0;
+  PagedTimes t = {0, 0};
   if (warp < kPagedWarps) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -133,7 +120,8 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
       u[i] = 0;
       if (b < p.s.B) {
         const PagedSeq q = paged_seq(p.s, b);
-        if (paged_token_mine(p, q)) u[i] = paged_span(p, q).units();
+        if (paged_few(p, q)) u[i] = paged_span(p, q).units();
+        if (p.shared) paged_time(p, q, &t);
       }
       sum += u[i];
     }
@@ -144,6 +132,10 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
       if (lane >= o) pre += x;
     }
     if (lane == 31) warp_sum[warp] = pre;
+    if (p.shared) {
+      if (t.tile) atomicAdd(&times->tile, t.tile);
+      if (t.token) atomicAdd(&times->token, t.token);
+    }
   }
   __syncthreads();
   if (warp < kPagedWarps) {
@@ -160,6 +152,11 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
   PagedDeal d;
   d.before = before;
   d.total = before[p.s.B] * p.Nkv;
+  d.ctas = p.deal;
+  if (p.shared) {  // those of the SMs that the other kernel leaves
+    d.ctas = p.deal * (152 - paged_shares(*times)) / 152;
+    if (d.ctas < 1) d.ctas = 1;
+  }
   return d;
 }
 
@@ -199,7 +196,7 @@ struct PagedWork {
     kvh = problem - b * p.Nkv;
     seq = paged_seq(p.s, b);
     span = paged_span(p, seq);
-    const int units = paged_token_mine(p, seq) ? span.units() : 0;
+    const int units = paged_few(p, seq) ? span.units() : 0;
     u0 = (int)((int64_t)units * rank / ranks);
     u1 = (int)((int64_t)units * (rank + 1) / ranks);
     whole = ranks == 1;
@@ -219,13 +216,15 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kPagedWarps];
   __shared__ float2 s_part[NB * 8];
   __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
+  __shared__ PagedTimes s_times;
   const uint32_t ring = (kv_smem(paged_smem) + 1023u) & ~1023u;
   float* const merge = reinterpret_cast<float*>(paged_smem + (ring - kv_smem(paged_smem)) + C::kRing);
   float* const part_smem = merge + C::kMerge / 4;  // in clusters
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+    s_times.tile = s_times.token = 0;
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(kv_smem(&s_full[i]), 1);
+      mbar_init(kv_smem(&s_full[i]), 2);
       mbar_init(kv_smem(&s_empty[i]), kPagedWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -235,17 +234,22 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
   pdl_launch_dependents();
-  pdl_wait();
+  // Beside paged_tile_kernel_t, which begins after all that came before and lets this
+  // kernel start then, its end is waited for at this one's.
+  if (!p.shared)
+    pdl_wait();
+  else
+    __syncthreads();
   PagedDeal deal;
   deal.before = s_before;
-  deal.total = 0;
+  deal.total = deal.ctas = 0;
   PagedWork work;
   work.at = work.last = 0;
   if (p.deal > 0) {
-    deal = paged_deal(p, s_before, s_sum);
+    deal = paged_deal(p, s_before, s_sum, &s_times);
     if (deal.total > 0) {
-      work.at = deal.first(p, blockIdx.x);
-      work.last = deal.first(p, blockIdx.x + 1);
+      work.at = deal.first(blockIdx.x);
+      work.last = deal.first(blockIdx.x + 1);
     }
     if (work.at >= work.last && tid < NB * 8) {
       // no units: nothing begins here, and nothing of this CTA's counts where a
@@ -263,11 +267,13 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   const int ranks = p.cluster > 1 ? p.cluster : 1;
   bool ok = true;
 
-  if (warp == kPagedWarps) {
-    // ------------------------------------------------------------ K and V
+  if (warp >= kPagedWarps) {
+    // ------------------------------------------------------------ K, V: a warp each
+    const bool is_k = warp == kPagedWarps;
+    const CUtensorMap* const map = is_k ? &maps.k : &maps.v;
+    const uint32_t half = ring + (is_k ? 0 : C::kHalf);
     const int chunks = kPagedUnit / p.chunk;         // boxes of a slab in a unit
-    const int mine = lane & (chunks - 1);            // this lane's rows of a unit
-    const int boxes = chunks * C::SLABS * 2;
+    const int mine = lane & (chunks - 1), slab = lane / chunks;  // this lane's rows and slab
     int it = 0;
     bool bad = false;
     for (int segment = 0; ok && work.next(p, deal, segment); ++segment) {
@@ -275,21 +281,15 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
       const int end = work.span.end;
       const int32_t* table = p.s.table + (int64_t)work.b * p.s.max_pages;
       const int seen = paged_first(p, work.seq.past);  // keys before this are nobody's
-      auto page_of = [&](int u, int* row) {
+      // The table's entry for this lane's rows of unit u. It is looked at two units later:
+      // waiting for each (1000 clocks) kept an SM below 42 GB/s.
+      auto entry = [&](int u) {
         const int j = base + u * kPagedUnit;
-        if (u >= work.u1 || j >= end) return -2;
-        const int i = kv_div(j, p.s.by_ps);
-        *row = j - i * p.s.ps;
-        if (j + p.chunk <= seen) return -1;
-        const int page = __ldg(table + i);
-        if ((uint32_t)page < (uint32_t)p.s.pages) return page;
-        bad = true;
-        return -1;  // outside the pool: TMA fills in zeros
+        return u < work.u1 && j < end && j + p.chunk > seen ? __ldg(table + kv_div(j, p.s.by_ps)) : -1;
       };
-      int row = 0, row_next = 0;
-      int page = page_of(work.u0, &row);
+      int page = entry(work.u0), page1 = entry(work.u0 + 1);
       for (int u = work.u0; u < work.u1; ++u, ++it) {
-        const int page_next = page_of(u + 1, &row_next);
+        const int page2 = entry(u + 2);
         const int st = it % C::kStages;
         if (it >= C::kStages) ok = mbar_wait(kv_smem(&s_empty[st]), (it / C::kStages - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -298,18 +298,18 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
         // rows behind the keys are not copied: what lies there is nobody's
         const int live = (end - (work.span.lo + u * kPagedUnit) + p.chunk - 1) / p.chunk;
         if (lane == 0)
-          mbar_arrive_expect_tx(full, (uint32_t)(live < 0 ? 0 : live < chunks ? live : chunks) * C::SLABS * 2 * p.chunk * 128);
+          mbar_arrive_expect_tx(full, (uint32_t)(live < 0 ? 0 : live < chunks ? live : chunks) * C::SLABS * p.chunk * 128);
         __syncwarp();
-        if (page > -2) {
-          const uint32_t dst = ring + st * C::kStage + mine * p.chunk * 128;
-          for (int i = lane; i < boxes; i += 32) {
-            const int part = i / chunks;  // K's slabs, then V's
-            const int slab = part < C::SLABS ? part : part - C::SLABS;
-            paged_tma(dst + part * (kPagedUnit * 128), part < C::SLABS ? &maps.k : &maps.v, slab * 64, row, work.kvh, page, full);
-          }
+        const int j = base + u * kPagedUnit;
+        if (slab < C::SLABS && j < end) {
+          const bool in_pool = (uint32_t)page < (uint32_t)p.s.pages;
+          bad |= !in_pool && j + p.chunk > seen;
+          // (in a page that does not exist TMA fills in zeros)
+          paged_tma(half + st * C::kStage + slab * (kPagedUnit * 128) + mine * p.chunk * 128, map, slab * 64,
+                    j - kv_div(j, p.s.by_ps) * p.s.ps, work.kvh, in_pool ? page : -1, full);
         }
-        page = page_next;
-        row = row_next;
+        page = page1;
+        page1 = page2;
       }
     }
     if (bad && p.s.status) atomicOr(p.s.status, 4);
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
       if (p.deal > 0 && work.at >= work.last && tid == 0) {
         const bool open = work.u0 == 0 && !work.whole;  // a problem that began before is another CTA's
         const int units = work.span.units();
-        const int parts = open ? deal.owner(p, work.at - work.u1 + units - 1) - (int)blockIdx.x : 0;
+        const int parts = open ? deal.owner(work.at - work.u1 + units - 1) - (int)blockIdx.x : 0;
         p.ws_join[blockIdx.x] = make_int4(b, kvh, 0, 2 * parts + (segment > 0 ? 1 : 0));
       }
       const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
     const int problem = (int)blockIdx.x / ranks, rank = (int)blockIdx.x - problem * ranks;
     const int b = problem / p.Nkv, kvh = problem - b * p.Nkv;
     const PagedSeq seq = paged_seq(p.s, b);
-    const int rows_all = paged_token_mine(p, seq) ? seq.n * p.G : 0;
+    const int rows_all = paged_few(p, seq) ? seq.n * p.G : 0;
     constexpr int LD = HD + 4;
     __syncthreads();
     kv_cluster_sync();
@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
     }
     kv_cluster_sync();  // no CTA leaves before its part has been read
   }
+  if (p.shared && blockIdx.x == 0) pdl_wait();  // this kernel does not end before the other
 }
 
 // Joins the parts of the problems that paged_token_kernel_t dealt to several CTAs.
@@ -626,7 +627,13 @@ template <class T>
 __global__ void __launch_bounds__(kKvTokenThreads) paged_join_kernel_t(const PagedParams p) {
   using bits = typename Elem<T>::bits;
   __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
-  pdl_wait();  // it lets nothing start early: the next call's CTAs would take places unevenly
+  // It lets nothing start early: the next call's CTAs would take places unevenly. Behind
+  // paged_tile_join_kernel_t, which begins after all parts are there, that one's end is
+  // waited for at this one's.
+  if (!p.shared)
+    pdl_wait();
+  else if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32)
+    pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 what = p.ws_join[blockIdx.x];  // b, kvh, -, 2 * further CTAs + slot
   if (what.w < 2) return;

@@ -89,6 +89,9 @@ SHAPES = {
     "prompt": (4, 1, 128, 32, [0], [300]),
     "mixed": (8, 2, 128, 16, [100, 0, 77, 511, 3], [1, 260, 1, 2, 75]),
     "mixed_small": (12, 2, 64, 8, [300, 20, 0], [1, 33, 130]),
+    "mixed_many": (8, 2, 128, 16, [7 * i % 400 for i in range(100)], [1] * 40 + [150] + [2] * 58 + [33]),
+    "mixed_wide": (4, 4, 256, 32, [11 * i % 300 for i in range(60)], [90] + [2] * 59),
+    "mixed_narrow": (6, 6, 64, 8, [5 * i % 200 for i in range(50)], [3] * 20 + [300, 40] + [1] * 28),
     "scalar": (4, 2, 19, 16, [3, 51], [9, 1]),
     "tiny_head": (4, 4, 2, 16, [3, 33], [33, 2]),
     "tiny_page": (8, 2, 64, 1, [30, 0], [3, 50]),
@@ -288,7 +291,7 @@ def test_contiguous_cache_is_pages(lib, cuda, dtype):
 @pytest.mark.parametrize("room", [None, 0, 4096, 200_000])
 def test_workspaces(lib, cuda, dtype, room):
     """Less workspace than planned splits less; its contents do not matter."""
-    for shape in ("token_long", "mixed", "one"):
+    for shape in ("token_long", "mixed", "one", "mixed_many", "prompt"):
         a = _make(14, dtype, *SHAPES[shape])
         ws = None if room is None else torch.full((room,), 255, dtype=torch.uint8, device=cuda)
         _check(lib, a, cuda, shape, workspace=ws)
@@ -623,8 +626,17 @@ def test_two_graphs_share_a_workspace(lib, cuda):
             assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("shape,kernel", [
+    ("one", "token"), ("few", "token"), ("chunk", "tile"), ("mixed", "tile"), ("mixed_many", "token"), ("odd_page", "simple"),
+    ("token_page", "token")])
+def test_kernels_are_the_ones_meant(lib, cuda, shape, kernel):
+    for dtype in ("f16", "bf16"):
+        _call(lib, _make(65, dtype, *SHAPES[shape]), cuda)
+        assert lib.last_kernel() == f"paged_{kernel}_kernel"
+
+
 def test_same_call_same_bits(lib, cuda):
-    for shape in ("token_long", "mixed", "chunk"):
+    for shape in ("token_long", "mixed", "chunk", "mixed_many"):
         a = _make(64, "bf16", *SHAPES[shape])
         want = _call(lib, a, cuda)
         for _ in range(5):
