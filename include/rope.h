@@ -674,9 +674,9 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
 /* Bytes of workspace with which kv_attention_paged splits the keys of such a call as
    planned; 0 where nothing is split, -1 for sizes that it refuses. A host function: no
    CUDA call. */
-int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_query_len,
-                                     int32_t num_heads, int32_t kv_num_heads, int64_t head_size,
-                                     int64_t page_size, int64_t max_pages);
+int64_t kv_attention_paged_workspace(rope_dtype dtype, int64_t batch, int64_t tokens,
+                                     int64_t max_query_len, int32_t num_heads, int32_t kv_num_heads,
+                                     int64_t head_size, int64_t page_size, int64_t max_pages);
 
 /*
  * kv_keep_paged -- after drafts were verified: of each sequence's new rows, the accepted

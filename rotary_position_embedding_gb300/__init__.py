@@ -74,7 +74,7 @@ SIGNATURES = {
                              _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp],
     "kv_attention_paged": [_i32, _i64, _i64, _i64, _i32, _i32, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp,
                            _vp, _f32, _f32, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
-    "kv_attention_paged_workspace": [_i64, _i64, _i64, _i32, _i32, _i64, _i64, _i64],
+    "kv_attention_paged_workspace": [_i32, _i64, _i64, _i64, _i32, _i32, _i64, _i64, _i64],
     "kv_keep_paged": [_i32, _i64, _i32, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp],
     "rope_set_variant": [_i32],
     "rope_get_variant": [],
@@ -729,18 +729,22 @@ def kv_cache_paged(num_pages, kv_num_heads, page_size, head_size, dtype=None, de
     return tuple(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2))
 
 
-def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32):
-    """The shape of the pages and the elements between them; the table and the lengths checked."""
-    plane = k_pages.shape
-    if len(plane) != 4:
-        raise ValueError("k_pages must be (num_pages, kv_num_heads, page_size, head_size)")
-    B = page_table.shape[0] if page_table.dim() == 2 else -1
-    if at < 0 or not (_fits(k_pages, at, plane, T) and _fits(v_pages, at, plane, T)
-                      and _fits(past_seq_lens, at, (B,), i32) and _fits(page_table, at, page_table.shape, i32)):
-        if B < 0:
+def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32):
+    """(shape of the pages, elements between them, sequences, entries of a row of the table), checked together
+    with the lengths."""
+    plane, table = k_pages.shape, page_table.shape
+    if not (at >= 0 and len(plane) == 4 and len(table) == 2 and k_pages.dtype is T and v_pages.dtype is T
+            and page_table.dtype is i32 and past_seq_lens.dtype is i32 and v_pages.shape == plane
+            and past_seq_lens.shape == table[:1] and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and page_table.is_contiguous() and past_seq_lens.is_contiguous() and k_pages.get_device() == at
+            and v_pages.get_device() == at and page_table.get_device() == at and past_seq_lens.get_device() == at):
+        if len(plane) != 4:
+            raise ValueError("k_pages must be (num_pages, kv_num_heads, page_size, head_size)")
+        if len(table) != 2:
             raise ValueError("page_table must be (B, max_pages)")
-        _shaped("page_table", page_table, query, page_table.shape, i32)
-        _shaped("past_seq_lens", past_seq_lens, query, (B,), i32)
+        _shaped("query", query, query, query.shape, T)
+        _shaped("page_table", page_table, query, table, i32)
+        _shaped("past_seq_lens", past_seq_lens, query, table[:1], i32)
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             if t.shape != plane or t.dtype != T or not t.is_cuda or t.device != query.device:
                 raise ValueError(f"{name} must be a {T} tensor of shape {tuple(plane)} on {query.device}")
@@ -752,20 +756,23 @@ def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32):
     stride = k_pages.stride(0) if plane[0] > 1 else within
     if stride < within:
         raise ValueError("pages must not overlap")
-    return plane, stride, B
+    if query_starts is not None and not (
+            query_starts.dtype is i32 and query_starts.shape == (table[0] + 1,) and query_starts.is_contiguous()
+            and query_starts.get_device() == at):
+        _shaped("query_starts", query_starts, query, (table[0] + 1,), i32)
+    return plane, stride, table[0], table[1]
 
 
-def _tokens_of(name, query, query_starts, B, at, i32):
+def _tokens_of(query, query_starts, B):
     """(tokens, hidden) of query: (tokens, hidden) with query_starts, (B, S, hidden) without."""
+    shape = query.shape
     if query_starts is None:
-        if query.dim() != 3 or query.shape[0] != B:
-            raise ValueError(f"{name} must be (B, S, hidden) with the batch of page_table, or come with query_starts")
-        return B * query.shape[1], query.shape[2]
-    if query.dim() != 2:
-        raise ValueError(f"{name} must be (tokens, hidden) with query_starts")
-    if not _fits(query_starts, at, (B + 1,), i32):
-        _shaped("query_starts", query_starts, query, (B + 1,), i32)
-    return query.shape
+        if len(shape) != 3 or shape[0] != B:
+            raise ValueError("query must be (B, S, hidden) with the batch of page_table, or come with query_starts")
+        return B * shape[1], shape[2]
+    if len(shape) != 2:
+        raise ValueError("query must be (tokens, hidden) with query_starts")
+    return shape
 
 
 def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_heads, kv_num_heads, k_pages, v_pages,
@@ -782,8 +789,8 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
     T, dev, at = query.dtype, query.device, query.get_device()
     torch, code = _torch_code(T)
     i32 = torch.int32
-    (P, N, ps, H), stride, B = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
-    tokens, hidden = _tokens_of("query", query, query_starts, B, at, i32)
+    (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
+    tokens, hidden = _tokens_of(query, query_starts, B)
     lead = query.shape[:-1]
     packed = key is None and value is None
     if N != kv_num_heads:
@@ -822,7 +829,7 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
     st = lib.rope_apply_qkv_paged(
         code, B, tokens, num_heads, N, H, query.data_ptr(), _address(key), _address(value), _address(q_norm_weight),
         _address(k_norm_weight), epsilon, cos_cache.data_ptr(), sin_cache.data_ptr(), table[0], _address(position_ids),
-        past_seq_lens.data_ptr(), _address(query_starts), page_table.data_ptr(), page_table.shape[1], int(interleaved),
+        past_seq_lens.data_ptr(), _address(query_starts), page_table.data_ptr(), wide, int(interleaved),
         rotary_embedding_dim, q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), P, ps, stride, _address(status),
         torch._C._cuda_getCurrentRawStream(at))
     if st:
@@ -830,11 +837,11 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
     return q_out
 
 
-def kv_attention_paged_workspace(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size,
+def kv_attention_paged_workspace(dtype, batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size,
                                  max_pages):
     """Bytes of workspace that kv_attention_paged uses for such a call."""
-    n = load_library().kv_attention_paged_workspace(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size,
-                                                    page_size, max_pages)
+    n = load_library().kv_attention_paged_workspace(_torch_code(dtype)[1], batch, tokens, max_query_len, num_heads,
+                                                    kv_num_heads, head_size, page_size, max_pages)
     if n < 0:
         _check("kv_attention_paged_workspace", ROPE_ERR_INVALID_ARG)
     return n
@@ -855,8 +862,8 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
     T, dev, at = query.dtype, query.device, query.get_device()
     torch, code = _torch_code(T)
     i32 = torch.int32
-    (P, N, ps, H), stride, B = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
-    tokens, hidden = _tokens_of("query", query, query_starts, B, at, i32)
+    (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
+    tokens, hidden = _tokens_of(query, query_starts, B)
     if hidden != num_heads * H or not query.is_contiguous():
         _shaped("query", query, query, (*query.shape[:-1], num_heads * H), T)
     if max_query_len is None or query_starts is None:
@@ -884,9 +891,8 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
                                       out=out, status=status, workspace=workspace)
     if out is None:
         out = torch.empty_like(query)
-    wide = page_table.shape[1]
     if workspace is None:
-        need = _workspace(lib.kv_attention_paged_workspace, (B, tokens, max_query_len, num_heads, N, H, ps, wide))
+        need = _workspace(lib.kv_attention_paged_workspace, (code, B, tokens, max_query_len, num_heads, N, H, ps, wide))
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib.kv_attention_paged(
@@ -907,12 +913,12 @@ def kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, 
     T, dev, at = k_pages.dtype, k_pages.device, k_pages.get_device()
     torch, code = _torch_code(T)
     i32 = torch.int32
-    (P, N, ps, H), stride, B = _paged(k_pages, T, at, k_pages, v_pages, page_table, past_seq_lens, i32)
+    (P, N, ps, H), stride, B, wide = _paged(k_pages, T, at, k_pages, v_pages, page_table, past_seq_lens, None, i32)
     if kept.dim() != 2:
         raise ValueError("kept must be (B, max_kept)")
-    wide = kept.shape[1]
-    if not (_fits(kept, at, (B, wide), i32) and _fits(kept_lens, at, (B,), i32)):
-        _shaped("kept", kept, k_pages, (B, wide), i32)
+    most = kept.shape[1]
+    if not (_fits(kept, at, (B, most), i32) and _fits(kept_lens, at, (B,), i32)):
+        _shaped("kept", kept, k_pages, (B, most), i32)
         _shaped("kept_lens", kept_lens, k_pages, (B,), i32)
     if status is not None:
         _shaped("status", status, k_pages, status.shape, i32)
@@ -920,8 +926,8 @@ def kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, 
         with _on(dev, stream):
             return kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, status=status)
     st = lib.kv_keep_paged(
-        code, B, N, H, k_pages.data_ptr(), v_pages.data_ptr(), P, ps, stride, page_table.data_ptr(),
-        page_table.shape[1], past_seq_lens.data_ptr(), kept.data_ptr(), wide, kept_lens.data_ptr(), _address(status),
+        code, B, N, H, k_pages.data_ptr(), v_pages.data_ptr(), P, ps, stride, page_table.data_ptr(), wide,
+        past_seq_lens.data_ptr(), kept.data_ptr(), most, kept_lens.data_ptr(), _address(status),
         torch._C._cuda_getCurrentRawStream(at))
     if st:
         _check("kv_keep_paged", st)

@@ -63,6 +63,11 @@ PagedBatch batch_of(int64_t batch, int64_t tokens, const int32_t* past, const in
 // ---------------------------------------------------------------------------
 // Attention
 // ---------------------------------------------------------------------------
+// In a mixed batch sequences of up to so many rows go to the kernel for few rows: its
+// instance for 16 does the arithmetic of 16 for each (95 single tokens of 5 rows beside a
+// prompt, capped: 212 us for 139).
+constexpr int kMixedRows = 8;
+
 enum class PagedFamily { kSimple, kToken, kTile, kMixed };
 
 struct PagedPlan {
@@ -168,24 +173,26 @@ rope_status check_attention(int64_t batch, int64_t tokens, int64_t max_query_len
 
 extern "C" {
 
-int64_t kv_attention_paged_workspace(int64_t batch, int64_t tokens, int64_t max_query_len, int32_t num_heads,
-                                     int32_t kv_num_heads, int64_t head_size, int64_t page_size, int64_t max_pages) {
+int64_t kv_attention_paged_workspace(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
+                                     int32_t num_heads, int32_t kv_num_heads, int64_t head_size, int64_t page_size,
+                                     int64_t max_pages) {
   set_last_error("");
-  if (check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages) != ROPE_OK)
+  if (check_dtype(dtype) != ROPE_OK ||
+      check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages) != ROPE_OK)
     return -1;
   if (batch == 0 || tokens == 0) return 0;
-  // whichever kernels the types, alignments and arguments make the call take
-  const int64_t rows = page_size * max_pages;
-  int64_t most = plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes;
-  int64_t tile = 0;
-  if (max_query_len * (num_heads / kv_num_heads) > kPagedFewRows)
-    tile = plan_tile(batch, tokens, max_query_len, batch * max_query_len != tokens, num_heads, kv_num_heads, head_size, rows).bytes;
-  int64_t token = 0;
-  for (bool mixed : {false, true}) {
-    const int64_t n = plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows, mixed && tile > 0).bytes;
-    token = n > token ? n : token;
-  }
-  return tile + token > most ? tile + token : most;
+  // what the sizes make the call take (tensors that are not 16-byte aligned split less)
+  const int64_t rows = page_size * max_pages, G = num_heads / kv_num_heads;
+  const bool matrix = dtype != ROPE_F32 && head_size % 8 == 0 && page_size % 8 == 0;
+  const bool ragged = batch * max_query_len != tokens;
+  const PagedFamily family = choose_paged(matrix, batch, tokens, max_query_len, ragged, false, G, kv_num_heads, head_size);
+  if (family == PagedFamily::kSimple)
+    return plan_simple(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, rows).bytes;
+  if (family == PagedFamily::kToken) return plan_token(batch, max_query_len, num_heads, kv_num_heads, head_size, rows, false).bytes;
+  int64_t n = plan_tile(batch, tokens, max_query_len, ragged, num_heads, kv_num_heads, head_size, rows).bytes;
+  if (family == PagedFamily::kMixed && G <= kMixedRows)
+    n += plan_token(batch, kMixedRows / G, num_heads, kv_num_heads, head_size, rows, true).bytes;
+  return n;
 }
 
 rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, int64_t max_query_len,
@@ -265,10 +272,6 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
         !encode_paged_map(&maps.v, dtype == ROPE_BF16, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, p.chunk))
       family = PagedFamily::kSimple;
   }
-  // In a mixed batch sequences of up to 8 rows go to the kernel for few rows: its
-  // instance for 16 does the arithmetic of 16 for each (95 single tokens of 5 rows beside
-  // a prompt, capped: 212 us).
-  constexpr int kMixedRows = 8;
   if (family == PagedFamily::kMixed && p.G > kMixedRows) family = PagedFamily::kTile;
   PagedTileMaps tile_maps;
   if (family == PagedFamily::kTile || family == PagedFamily::kMixed) {

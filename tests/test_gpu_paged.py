@@ -605,7 +605,7 @@ def test_two_graphs_share_a_workspace(lib, cuda):
         args = dict(q=a["q"].to(cuda), k=a["k"].to(cuda), v=a["v"].to(cuda), t=_i32(a["table"], cuda), p=_i32(a["past"], cuda),
                     s=_i32(a["starts"], cuda))
         tokens, (_, N, ps, H) = args["q"].shape[0], a["k"].shape
-        need = max(need, lib.kv_attention_paged_workspace(len(a["past"]), tokens, a["most"], a["Nq"], N, H, ps,
+        need = max(need, lib.kv_attention_paged_workspace(args["q"].dtype, len(a["past"]), tokens, a["most"], a["Nq"], N, H, ps,
                                                           args["t"].shape[1]))
         calls.append((a, args))
     ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device=cuda)

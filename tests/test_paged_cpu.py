@@ -112,11 +112,15 @@ def test_empty_calls_launch_nothing(lib):
 
 
 def test_workspace_is_a_host_function(lib):
-    assert lib.kv_attention_paged_workspace(0, 0, 0, 8, 2, 64, 16, 8) == 0
-    assert lib.kv_attention_paged_workspace(1, 1, 1, 8, 2, 64, 16, 4096) > 0
-    for bad in ((1, 1, 1, 8, 3, 64, 16, 8), (1, 1, 1, 8, 2, 257, 16, 8), (1, 1, 2, 8, 2, 64, 16, 8), (1, 1, 1, 8, 2, 64, 0, 8)):
-        with pytest.raises(lib.RopeError):
-            lib.kv_attention_paged_workspace(*bad)
+    for t in (torch.float32, torch.float16, torch.bfloat16):
+        assert lib.kv_attention_paged_workspace(t, 0, 0, 0, 8, 2, 64, 16, 8) == 0
+        assert lib.kv_attention_paged_workspace(t, 1, 1, 1, 8, 2, 64, 16, 4096) > 0
+        for bad in ((1, 1, 1, 8, 3, 64, 16, 8), (1, 1, 1, 8, 2, 257, 16, 8), (1, 1, 2, 8, 2, 64, 16, 8),
+                    (1, 1, 1, 8, 2, 64, 0, 8)):
+            with pytest.raises(lib.RopeError):
+                lib.kv_attention_paged_workspace(t, *bad)
+    with pytest.raises(lib.RopeError):
+        lib.kv_attention_paged_workspace(torch.float64, 1, 1, 1, 8, 2, 64, 16, 8)
 
 
 def test_binding_refuses(lib):
