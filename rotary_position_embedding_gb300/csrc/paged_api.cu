@@ -108,7 +108,7 @@ PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H
     if (n > kKvClusterMost) n = kKvClusterMost;
     if (problems * n <= kSms) pl.cluster = n;
   }
-  if (!pl.cluster && units > 1 && B <= kKvDealMost && problems < (1ll << 31) / units) {
+  if (!pl.cluster && units > 1 && B <= kKvDealMost && problems < (1ll << 31) / (units + 2)) {
     pl.deal = paged_token_ctas(H);
     if (pl.deal > problems * units) pl.deal = (int)(problems * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -127,7 +127,7 @@ PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq,
   pl.split_bytes = 2 * tr * (H * 4 + 8) + 16;
   const int64_t units = (rows + kv_tile_keys(H) - 1) / kv_tile_keys(H);  // of an item
   if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 31) / (units + 8)) {
-    pl.deal = kSms;
+    pl.deal = kPagedTileCtas;
     if (pl.deal > pl.items * Nkv * units) pl.deal = (int)(pl.items * Nkv * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
   }
@@ -340,7 +340,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     if (!tile_p.deal) return ROPE_OK;
     int tr = kv_tile_rows(head_size);
     void* jargs[] = {&tile_p, &tr};
-    return launch(tile_join, dim3((unsigned)tile_p.deal, tr / 16), kKvTokenThreads, 0, stream, jargs,
+    return launch(tile_join, dim3((unsigned)tile_p.deal, tr / 16), kPagedJoinThreads, 0, stream, jargs,
                   "kv_attention_paged launch (joining the parts)");
   };
   if (family != PagedFamily::kToken) {

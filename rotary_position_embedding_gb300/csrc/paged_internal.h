@@ -81,6 +81,8 @@ struct PagedTileKernel {
 };
 constexpr int kPagedItems = 768;
 constexpr int kPagedTileBlock = 384;
+constexpr int kPagedTileCtas = 152;  // most that are dealt to
+constexpr int kPagedJoinThreads = 256;
 // The kernel deals its registers out again (setmaxnreg): 256 x 208 + 128 x 88 = 384 x 168,
 // so it must have been launched with 168 a thread.
 constexpr int kPagedTileRegisters = 168;

@@ -720,60 +720,97 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
+// A load that stays where it stands, ahead of what decides whether it counts.
+__device__ __forceinline__ float4 paged_load4(const float4* at) {
+  float4 x;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(at) : "memory");
+  return x;
+}
+
 // Joins the parts of the items that paged_tile_kernel_t dealt to several CTAs. CTA (x,
 // y): the item that begins in CTA x there and goes on in others, if there is one; its
-// rows 16 y .., 16 threads side by side for the same dims of 16 rows. `rows`: of a slot.
+// rows 16 y .., 16 threads side by side for the same dims of 16 rows. What each part
+// counts is worked out first, for all parts at a time, so that the loads of the parts wait
+// for nothing. `rows`: of a slot.
 template <class T, int HD>
-__global__ void __launch_bounds__(kKvTokenThreads) paged_tile_join_kernel_t(const PagedParams p, int rows) {
-  constexpr int PIECES = HD / 4 / 8;  // of 4 dims, a thread
-  pdl_wait();  // it lets nothing start early (the next call's CTAs would take places unevenly)
-  if (p.shared) pdl_launch_dependents();  // but the other kernel's joining
+__global__ void __launch_bounds__(kPagedJoinThreads) paged_tile_join_kernel_t(const PagedParams p, int rows) {
+  constexpr int SIDE = kPagedJoinThreads / 16, PIECES = HD / 4 / SIDE;  // of 4 dims, a thread
+  constexpr int DEEP = PIECES <= 2 ? 8 : 4;                             // parts at a time
+  __shared__ float s_f[kPagedTileCtas + DEEP][16], s_max[SIDE][16], s_sum[SIDE][16];
+  const int r0 = threadIdx.x & 15, side = threadIdx.x >> 4, r = (int)blockIdx.y * 16 + r0;
+  pdl_wait();
+  pdl_launch_dependents();
   const int4 what = p.ws_join[blockIdx.x];  // first token, kvh, rows, 2 * further CTAs + slot
-  const int r = (int)blockIdx.y * 16 + (threadIdx.x & 15), piece0 = threadIdx.x >> 4;
-  if (what.w < 2 || r >= what.z) return;
+  if (what.w < 2 || (int)blockIdx.y * 16 >= what.z) return;
   const int kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x, pieces = p.H / 4;
   // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
   auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
   float M = -CUDART_INF_F;
-#pragma unroll 8
-  for (int n = 0; n < parts; ++n) M = fmaxf(M, p.ws_ml[slot_of(n) * rows + r].x);
+#pragma unroll 4
+  for (int n = side; n < parts; n += SIDE) {
+    const float m = p.ws_ml[slot_of(n) * rows + r].x;
+    s_f[n][r0] = m;
+    M = fmaxf(M, m);
+  }
+  s_max[side][r0] = M;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < SIDE; ++k) M = fmaxf(M, s_max[k][r0]);
   const float base = M == -CUDART_INF_F ? 0.0f : M;
   float L = 0.0f;
+#pragma unroll 4
+  for (int n = side; n < parts; n += SIDE) {
+    const float f = exp2f(s_f[n][r0] - base);
+    L = fmaf(p.ws_ml[slot_of(n) * rows + r].y, f, L);
+    s_f[n][r0] = f;
+  }
+  for (int n = parts + side; n < parts + DEEP; n += SIDE) s_f[n][r0] = 0.0f;
+  s_sum[side][r0] = L;
+  __syncthreads();
+  L = 0.0f;
+#pragma unroll
+  for (int k = 0; k < SIDE; ++k) L += s_sum[k][r0];
   float4 acc[PIECES];
 #pragma unroll
   for (int j = 0; j < PIECES; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll(HD > 128 ? 2 : 4)
-  for (int n = 0; n < parts; ++n) {
-    const int64_t slot = slot_of(n);
-    const float2 ml = p.ws_ml[slot * rows + r];
-    const float f = exp2f(ml.x - base);
-    const bool on = !(ml.x == -CUDART_INF_F && ml.y == 0.0f);  // else nothing was written, or zeros
-    L = fmaf(ml.y, f, L);
-    const float4* o = reinterpret_cast<const float4*>(p.ws_o) + slot * pieces * rows + r;
+  const float4* const from = reinterpret_cast<const float4*>(p.ws_o) + r;
+  for (int n0 = 0; n0 < parts; n0 += DEEP) {
+    float4 x[DEEP][PIECES];
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j)
-      if (piece0 + 8 * j < pieces) {
-        float4 x = o[(int64_t)(piece0 + 8 * j) * rows];  // (loaded in any case: no load waits for another)
-        if (!on) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        acc[j].x = fmaf(x.x, f, acc[j].x);
-        acc[j].y = fmaf(x.y, f, acc[j].y);
-        acc[j].z = fmaf(x.z, f, acc[j].z);
-        acc[j].w = fmaf(x.w, f, acc[j].w);
+    for (int k = 0; k < DEEP; ++k)
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        const int piece = side + SIDE * j;
+        const int64_t at = slot_of(n0 + k < parts ? n0 + k : 0) * pieces * rows + (int64_t)(piece < pieces ? piece : 0) * rows;
+        x[k][j] = paged_load4(from + at);
       }
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) {
+      const float f = s_f[n0 + k][r0];  // 0 behind the last, and where a CTA had no part and wrote nothing
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) {
+        if (f == 0.0f) x[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        acc[j].x = fmaf(x[k][j].x, f, acc[j].x);
+        acc[j].y = fmaf(x[k][j].y, f, acc[j].y);
+        acc[j].z = fmaf(x[k][j].z, f, acc[j].z);
+        acc[j].w = fmaf(x[k][j].w, f, acc[j].w);
+      }
+    }
   }
+  if (r >= what.z) return;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const int tok = kv_div(r, p.by_g);
   typename Elem<T>::bits* y = static_cast<typename Elem<T>::bits*>(p.out) +
                               (((int64_t)what.x + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
 #pragma unroll
   for (int j = 0; j < PIECES; ++j)
-    if (piece0 + 8 * j < pieces) {
+    if (side + SIDE * j < pieces) {
       VecT<T, 4> v;
       v.v[0] = Elem<T>::fromf(acc[j].x * inv);
       v.v[1] = Elem<T>::fromf(acc[j].y * inv);
       v.v[2] = Elem<T>::fromf(acc[j].z * inv);
       v.v[3] = Elem<T>::fromf(acc[j].w * inv);
-      *reinterpret_cast<VecT<T, 4>*>(y + 4 * (piece0 + 8 * j)) = v;
+      *reinterpret_cast<VecT<T, 4>*>(y + 4 * (side + SIDE * j)) = v;
     }
 }
 

@@ -21,8 +21,8 @@
 // rows see is not finite, its zero weight in the others would make a NaN of it: the
 // rows are then done over again one by one (paged_careful_row).
 //
-// Dealing. CTA i takes the units [i U / n, (i + 1) U / n) of all U in the order of the
-// problems (sequence, head), whatever the lengths: a problem that one CTA has whole
+// Dealing. CTA i takes the part [i W / n, (i + 1) W / n) of the problems' weight W (their
+// units, and what each costs beside) in the order of the problems (sequence, head): a problem that one CTA has whole
 // goes to the output, the others' parts to the workspace (2 slots a CTA: its first
 // segment's, its last one's), with a word on the problem that the CTA begins and
 // leaves unfinished, for paged_join_kernel_t. Without (no workspace, or more than
@@ -94,10 +94,15 @@ __device__ __forceinline__ bool paged_sync_or(bool x) {
   return y != 0;
 }
 
+// What a problem weighs beside its units: queries, joining, output. Without it the CTA that
+// had the shortest sequences' problems ended 15 to 40 us behind the others.
+template <int NB>
+constexpr int kPagedTokenOver = NB;
+
 struct PagedDeal {
-  const int32_t* before;  // units of one problem of the sequences before b, for each b, and of all
-  int total;              // units of all problems, below 2^31
-  int ctas;               // that they are dealt to
+  const int32_t* before;  // weight of one problem of the sequences before b, for each b, and of all
+  int total;              // weight of all problems, below 2^31
+  int ctas;               // that it is dealt to
   __device__ __forceinline__ int first(int cta) const {
     return cta < ctas ? (int)((uint64_t)(uint32_t)cta * (uint32_t)total / (uint32_t)ctas) : total;
   }
@@ -106,7 +111,8 @@ struct PagedDeal {
   }
 };
 
-// The units before each sequence, in shared memory; all threads come here.
+// The weight before each sequence, in shared memory; all threads come here.
+template <int NB>
 __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* before, int32_t* warp_sum,
                                                 PagedTimes* times) {
   constexpr int PER = kKvDealMost / 128;
@@ -120,7 +126,7 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
       u[i] = 0;
       if (b < p.s.B) {
         const PagedSeq q = paged_seq(p.s, b);
-        if (paged_few(p, q)) u[i] = paged_span(p, q).units();
+        if (paged_few(p, q)) u[i] = paged_span(p, q).units() + kPagedTokenOver<NB>;
         if (p.shared) paged_time(p, q, &t);
       }
       sum += u[i];
@@ -161,8 +167,9 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
 }
 
 // The problems of a CTA, one after the other, and its units of each.
+template <int NB>
 struct PagedWork {
-  int at, last;      // units left (dealt)
+  int at, last;      // weight left (dealt)
   int b, kvh, u0, u1;
   PagedSeq seq;
   PagedSpan span;
@@ -170,7 +177,7 @@ struct PagedWork {
   __device__ __forceinline__ bool next(const PagedParams& p, const PagedDeal& d, int segment) {
     if (p.deal > 0) {
       if (at >= last) return false;
-      int x = 0, y = p.s.B;  // the sequence of unit `at`: before[x] <= . < before[y]
+      int x = 0, y = p.s.B;  // the sequence of `at`: before[x] <= . < before[y]
       while (y - x > 1) {
         const int mid = (x + y) >> 1;
         if (d.before[mid] * p.Nkv <= at)
@@ -178,12 +185,21 @@ struct PagedWork {
         else
           y = mid;
       }
+      // a problem's weight: kPagedTokenOver of nothing, then a unit each
+      constexpr int OVER = kPagedTokenOver<NB>;
+      const int weight = d.before[x + 1] - d.before[x];
+      int in = at - d.before[x] * p.Nkv;
       b = x;
-      const int units = d.before[b + 1] - d.before[b], in = at - d.before[b] * p.Nkv;
-      kvh = (int)((uint32_t)in / (uint32_t)units);
-      u0 = in - kvh * units;
-      u1 = u0 + (last - at) < units ? u0 + (last - at) : units;
-      whole = u0 == 0 && u1 == units;
+      kvh = (int)((uint32_t)in / (uint32_t)weight);
+      in -= kvh * weight;
+      if (in < OVER) {
+        at += OVER - in;
+        in = OVER;
+        if (at >= last) return false;
+      }
+      u0 = in - OVER;
+      u1 = u0 + (last - at) < weight - OVER ? u0 + (last - at) : weight - OVER;
+      whole = u0 == 0 && u1 == weight - OVER;
       at += u1 - u0;
       seq = paged_seq(p.s, b);
       span = paged_span(p, seq);
@@ -243,20 +259,19 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   PagedDeal deal;
   deal.before = s_before;
   deal.total = deal.ctas = 0;
-  PagedWork work;
+  PagedWork<NB> work;
   work.at = work.last = 0;
   if (p.deal > 0) {
-    deal = paged_deal(p, s_before, s_sum, &s_times);
+    deal = paged_deal<NB>(p, s_before, s_sum, &s_times);
     if (deal.total > 0) {
       work.at = deal.first(blockIdx.x);
       work.last = deal.first(blockIdx.x + 1);
     }
-    if (work.at >= work.last && tid < NB * 8) {
-      // no units: nothing begins here, and nothing of this CTA's counts where a
-      // problem's CTAs lie on both sides of it
-      if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // so far nothing begins here that goes on elsewhere, and nothing of this CTA's counts
+    // where a problem's CTAs lie on both sides of it
+    if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (work.at >= work.last && tid < NB * 8)
       p.ws_ml[2 * (int64_t)blockIdx.x * (NB * 8) + tid] = make_float2(-CUDART_INF_F, 0.0f);
-    }
   } else {
     __syncthreads();
   }
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
     const CUtensorMap* const map = is_k ? &maps.k : &maps.v;
     const uint32_t half = ring + (is_k ? 0 : C::kHalf);
     const int chunks = kPagedUnit / p.chunk;         // boxes of a slab in a unit
-    const int mine = lane & (chunks - 1), slab = lane / chunks;  // this lane's rows and slab
+    const int mine = lane & (chunks - 1), slab = lane / chunks;  // this lane's rows and slab, or unit of a batch
     int it = 0;
     bool bad = false;
     for (int segment = 0; ok && work.next(p, deal, segment); ++segment) {
@@ -281,15 +296,22 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
       const int end = work.span.end;
       const int32_t* table = p.s.table + (int64_t)work.b * p.s.max_pages;
       const int seen = paged_first(p, work.seq.past);  // keys before this are nobody's
-      // The table's entry for this lane's rows of unit u. It is looked at two units later:
-      // waiting for each (1000 clocks) kept an SM below 42 GB/s.
+      // The table's entries of `batch` units at a time, a lane each, and those of the batch
+      // behind it on their way: a load that was waited for at each unit (1000 clocks) kept an
+      // SM below 42 GB/s.
       auto entry = [&](int u) {
         const int j = base + u * kPagedUnit;
         return u < work.u1 && j < end && j + p.chunk > seen ? __ldg(table + kv_div(j, p.s.by_ps)) : -1;
       };
-      int page = entry(work.u0), page1 = entry(work.u0 + 1);
-      for (int u = work.u0; u < work.u1; ++u, ++it) {
-        const int page2 = entry(u + 2);
+      const int batch = 32 / chunks;
+      int pages = entry(work.u0 + slab), pages_next = entry(work.u0 + batch + slab);
+      for (int u = work.u0, in = 0; u < work.u1; ++u, ++it, ++in) {
+        if (in == batch) {
+          in = 0;
+          pages = pages_next;
+          pages_next = entry(u + batch + slab);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, in * chunks + mine);
         const int st = it % C::kStages;
         if (it >= C::kStages) ok = mbar_wait(kv_smem(&s_empty[st]), (it / C::kStages - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -308,8 +330,6 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
           paged_tma(half + st * C::kStage + slab * (kPagedUnit * 128) + mine * p.chunk * 128, map, slab * 64,
                     j - kv_div(j, p.s.by_ps) * p.s.ps, work.kvh, in_pool ? page : -1, full);
         }
-        page = page1;
-        page1 = page2;
       }
     }
     if (bad && p.s.status) atomicOr(p.s.status, 4);
@@ -329,11 +349,9 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
       const PagedSeq& seq = work.seq;
       const int rows_all = seq.n * p.G;
       const int end = work.span.end;
-      // the one problem that may begin in this CTA and go on in others: paged_join_kernel_t's
-      if (p.deal > 0 && work.at >= work.last && tid == 0) {
-        const bool open = work.u0 == 0 && !work.whole;  // a problem that began before is another CTA's
-        const int units = work.span.units();
-        const int parts = open ? deal.owner(work.at - work.u1 + units - 1) - (int)blockIdx.x : 0;
+      // the one problem that begins in this CTA and goes on in others: paged_join_kernel_t's
+      if (p.deal > 0 && work.u0 == 0 && !work.whole && tid == 0) {
+        const int parts = deal.owner(work.at - work.u1 + work.span.units() - 1) - (int)blockIdx.x;
         p.ws_join[blockIdx.x] = make_int4(b, kvh, 0, 2 * parts + (segment > 0 ? 1 : 0));
       }
       const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0 ? 1 : 0);
@@ -400,6 +418,26 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
           for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
       bool odd = false;  // an infinity or a NaN in a value that not every row sees
 
+      // The products of a unit's keys with Q, two sums: half as long a chain of dependent ones.
+      auto scores = [&](int stage, float (&s)[NB][4]) {
+        const uint32_t at = ring + stage * C::kStage;
+        float t[NB][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][i] = t[n][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          uint32_t a[4];
+          paged_ldsm(a, at + kat + (k >> 2) * (kPagedUnit * 128) + ((((2 * k) & 7) ^ kx) << 4));
+#pragma unroll
+          for (int n = 0; n < NB; ++n) kv_mma<BF>(k & 1 ? t[n] : s[n], a[0], a[1], a[2], a[3], qf[n][k][0], qf[n][k][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[n][i] += t[n][i];
+      };
       for (int u = work.u0; u < work.u1; ++u, ++it) {
         const int st = it % C::kStages;
         const int j0 = work.span.lo + u * kPagedUnit + warp * 16;
@@ -408,19 +446,8 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
         if (!ok) break;
         if (j0 < end) {
           const uint32_t at = ring + st * C::kStage;
-          float s[NB][4], s2[NB][4];  // two sums: half as long a chain of dependent products
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < KB; ++k) {
-            uint32_t a[4];
-            paged_ldsm(a, at + kat + (k >> 2) * (kPagedUnit * 128) + ((((2 * k) & 7) ^ kx) << 4));
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-              kv_mma<BF>(k & 1 ? s2[n] : s[n], a[0], a[1], a[2], a[3], qf[n][k][0], qf[n][k][1]);
-          }
+          float s[NB][4];
+          scores(st, s);
           const bool whole = j0 >= below && j0 + 16 <= full;  // uniform over the warp
           uint32_t any0 = 0xffffffffu, any1 = 0xffffffffu;
           bool seen0 = false, seen1 = false, moved = false;
@@ -428,7 +455,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = (s[n][e] + s2[n][e]) * c1, y = (s[n][2 + e] + s2[n][2 + e]) * c1;
+              float x = s[n][e] * c1, y = s[n][2 + e] * c1;
               if (p.cap > 0.0f) {
                 x = kv_tanh_of(x) * c2;
                 y = kv_tanh_of(y) * c2;
