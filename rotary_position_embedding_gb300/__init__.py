@@ -13,7 +13,7 @@ import ctypes
 import os
 import threading
 
-from .build import LIB_PATH, build_library  # noqa: F401
+from .build import BINDING_PATH, LIB_PATH, build_library  # noqa: F401
 
 __all__ = [
     "RopeError", "load_library", "build_library", "rope_apply", "mrope_apply",
@@ -34,6 +34,7 @@ _UNSUPPORTED_DTYPE = 99  # passed through so the library reports ROPE_ERR_UNSUPP
 
 _lock = threading.Lock()
 _lib = None
+_short = None  # csrc/binding.cpp once it was asked for, or False
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -117,6 +118,35 @@ def load_library(path=None):
         if path is None:
             _lib = lib
         return lib
+
+
+def _short_way():
+    """csrc/binding.cpp's module, bound to the library, or False where it was not compiled."""
+    global _short
+    if _short is None:
+        lib = load_library()
+        with _lock:
+            if _short is None:
+                module = False
+                if os.path.exists(BINDING_PATH):
+                    import importlib.machinery
+                    import importlib.util
+
+                    import torch  # noqa: F401  (its libraries are what the module links to)
+
+                    name = __name__ + "._binding"
+                    loader = importlib.machinery.ExtensionFileLoader(name, BINDING_PATH)
+                    spec = importlib.util.spec_from_file_location(name, BINDING_PATH, loader=loader)
+                    try:
+                        module = importlib.util.module_from_spec(spec)
+                        loader.exec_module(module)
+                        module.bind(*[ctypes.cast(getattr(lib, fn), _vp).value for fn in (
+                            "rope_apply_qkv_paged", "kv_attention_paged", "kv_attention_paged_workspace",
+                            "kv_keep_paged")])
+                    except ImportError:  # compiled for another PyTorch or machine
+                        module = False
+                _short = module
+    return _short
 
 
 def _check(fn, status):
@@ -785,9 +815,18 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
     [Q|K|V] where key and value are None; position_ids has its leading dimensions. k_pages and v_pages
     (num_pages, kv_num_heads, page_size, H) are updated in place; page_table is int32 (B, max_pages). Returns
     q_out."""
-    lib = load_library()
-    T, dev, at = query.dtype, query.device, query.get_device()
+    T, at = query.dtype, query.get_device()
     torch, code = _torch_code(T)
+    short = _short or _short_way()
+    if short and stream is None and at >= 0 and at == torch._C._cuda_getDevice():
+        done = short.append(at, torch._C._cuda_getCurrentRawStream(at), query, cos_cache, sin_cache, position_ids,
+                            num_heads, kv_num_heads, k_pages, v_pages, page_table, past_seq_lens, query_starts, key, value,
+                            interleaved, rotary_embedding_dim, q_out, status, q_norm_weight, k_norm_weight, epsilon)
+        if done is not None:
+            if done.__class__ is int:
+                _check("rope_apply_qkv_paged", done)
+            return done
+    lib, dev = load_library(), query.device
     i32 = torch.int32
     (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
     tokens, hidden = _tokens_of(query, query_starts, B)
@@ -858,9 +897,18 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
     worse (with 64 or more tokens tree_masks want it given). tree_masks: int64, one word a token, bit t: new token
     t of its sequence is seen. scale: 1/sqrt(H) if None. workspace: uint8 device memory of
     ``kv_attention_paged_workspace`` bytes, or None to take it from PyTorch's allocator. Returns out."""
-    lib = load_library()
-    T, dev, at = query.dtype, query.device, query.get_device()
+    T, at = query.dtype, query.get_device()
     torch, code = _torch_code(T)
+    short = _short or _short_way()
+    if short and stream is None and at >= 0 and at == torch._C._cuda_getDevice():
+        done = short.attention(at, torch._C._cuda_getCurrentRawStream(at), query, k_pages, v_pages, page_table,
+                               past_seq_lens, num_heads, query_starts, max_query_len, scale, softcap, window, alibi_slopes,
+                               tree_masks, out, status, workspace)
+        if done is not None:
+            if done.__class__ is int:
+                _check("kv_attention_paged", done)
+            return done
+    lib, dev = load_library(), query.device
     i32 = torch.int32
     (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
     tokens, hidden = _tokens_of(query, query_starts, B)
@@ -909,9 +957,17 @@ def kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, 
     """After drafts were verified: row past_seq_lens[b] + kept[b, i] of each sequence goes to past_seq_lens[b] + i
     for i < kept_lens[b], in k_pages and v_pages (see ``kv_keep_paged`` in include/rope.h). kept is int32 (B,
     max_kept), ascending; kept_lens int32 (B). The next past_seq_lens is past_seq_lens + kept_lens."""
-    lib = load_library()
-    T, dev, at = k_pages.dtype, k_pages.device, k_pages.get_device()
+    T, at = k_pages.dtype, k_pages.get_device()
     torch, code = _torch_code(T)
+    short = _short or _short_way()
+    if short and stream is None and at >= 0 and at == torch._C._cuda_getDevice():
+        done = short.keep(at, torch._C._cuda_getCurrentRawStream(at), k_pages, v_pages, page_table, past_seq_lens, kept,
+                          kept_lens, status)
+        if done is not None:
+            if done.__class__ is int:
+                _check("kv_keep_paged", done)
+            return
+    lib, dev = load_library(), k_pages.device
     i32 = torch.int32
     (P, N, ps, H), stride, B, wide = _paged(k_pages, T, at, k_pages, v_pages, page_table, past_seq_lens, None, i32)
     if kept.dim() != 2:

@@ -6,10 +6,12 @@ loads on a machine without a GPU driver (every entry point then fails with
 ROPE_ERR_CUDA once it reaches a CUDA call; argument checks still run).
 """
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +29,8 @@ HEADERS = ["rope_kernels.cuh", "rope_internal.h", "rope_tma.cuh", "rope_qkv.cuh"
            "rope_mrope_heads.cuh", "rope_qkv_heads.cuh", "kv_internal.h", "kv_common.cuh", "kv_append.cuh", "kv_simple.cuh", "kv_careful.cuh", "kv_token.cuh", "kv_tile.cuh", "kv_maps.h", "kv_host.h",
            "paged_internal.h", "paged_common.cuh", "paged_append.cuh", "paged_append_heads.cuh", "paged_simple.cuh", "paged_careful.cuh", "paged_token.cuh",
            "paged_tile.cuh", "paged_maps.h", "paged_keep.cuh"]
+BINDING = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(OUT_DIR, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,6 +48,32 @@ def _inputs():
     return files
 
 
+def build_binding(force=False):
+    """Compile (if needed) the short way into the library for calls with PyTorch tensors, csrc/binding.cpp, and
+    return its path; None where it cannot be compiled (calls then go through ctypes)."""
+    header = os.path.join(INCLUDE, "rope.h")
+    if not force and os.path.exists(BINDING_PATH) and all(
+            os.path.getmtime(f) <= os.path.getmtime(BINDING_PATH) for f in (BINDING, header)):
+        return BINDING_PATH
+    try:
+        torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+        os.makedirs(OUT_DIR, exist_ok=True)
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1",
+               "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include/torch/csrc/api/include"),
+               "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-I", cuda, BINDING, "-o", tmp,
+               "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr)
+        os.replace(tmp, BINDING_PATH)
+        return BINDING_PATH
+    except Exception as e:  # no PyTorch, no Python.h, no g++: the library works without it
+        sys.stderr.write(f"binding.cpp was not compiled, calls go through ctypes: {e}\n")
+        return None
+
+
 def up_to_date(path=LIB_PATH):
     if not os.path.exists(path):
         return False
@@ -54,7 +84,10 @@ def up_to_date(path=LIB_PATH):
 def build_library(force=False, extra_flags=(), out_path=None, verbose=False):
     """Compile (if needed) and return the path of the shared library."""
     out_path = out_path or LIB_PATH
+    binding = out_path == LIB_PATH
     if not force and not extra_flags and up_to_date(out_path):
+        if binding:
+            build_binding()
         return out_path
     nvcc = nvcc_path()
     obj_dir = os.path.join(os.path.dirname(out_path), f"_obj{os.getpid()}")
@@ -72,7 +105,9 @@ def build_library(force=False, extra_flags=(), out_path=None, verbose=False):
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        if binding:
+            ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
     if verbose:
         for _, log in results:

@@ -72,6 +72,7 @@ enum class PagedFamily { kSimple, kToken, kTile, kMixed };
 
 struct PagedPlan {
   int64_t tiles = 0;        // kSimple: row tiles of the longest sequence
+  bool few = false;         // kSimple: of 16 rows, not 64
   int64_t items = 0;        // kTile: row tiles of all sequences, at most
   int splits = 1;           // kSimple: splits of the keys
   int deal = 0, cluster = 0;  // kToken, kTile: CTAs that are dealt to; kToken: or those of a cluster
@@ -84,10 +85,14 @@ struct PagedPlan {
 PagedPlan plan_simple(int64_t B, int64_t T, int64_t most, int64_t Nq, int64_t Nkv, int64_t H, int64_t rows) {
   PagedPlan pl;
   const int64_t G = Nq / Nkv, R = most * G;
-  pl.tiles = (R + kv_simple_rows(R) - 1) / kv_simple_rows(R);
-  int64_t ctas = T * G / kv_simple_rows(R) + 1;  // tiles that have rows, at least
+  // 64 rows a CTA, or 16 where there are no more (16 for more CTAs: 537 float32 tokens of 8
+  // heads of 64 53 us instead of 34)
+  pl.few = kv_simple_rows(R) == 16;
+  const int64_t per = pl.few ? 16 : 64;
+  pl.tiles = (R + per - 1) / per;
+  int64_t ctas = T * G / per + 1;  // tiles that have rows, at least
   if (ctas < B && B <= T) ctas = B;
-  int64_t n = kv_simple_resident(H, R) * kSms / (ctas * Nkv);
+  int64_t n = kv_simple_resident(H, pl.few ? 16 : R) * kSms / (ctas * Nkv);
   if (n > (rows + 127) / 128) n = (rows + 127) / 128;
   if (n > 128) n = 128;
   pl.splits = n < 1 ? 1 : (int)n;
@@ -320,7 +325,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
       p.ws_o = static_cast<float*>(workspace);
       p.ws_ml = reinterpret_cast<float2*>(p.ws_o + n * head_size + (n * head_size & 1));
     }
-    const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, kv_simple_rows(max_query_len * p.G) == 16);
+    const KvSimpleKernel k = paged_simple_kernel(dtype, (int)head_size, pl.few);
     const dim3 grid((unsigned)(pl.tiles * p.splits), kv_num_heads, (unsigned)(batch < 65535 ? batch : 65535));
     KV_TRY(launch(k.fn, grid, kKvSimpleThreads, k.smem, stream, args, "kv_attention_paged launch"));
     if (p.splits > 1) {

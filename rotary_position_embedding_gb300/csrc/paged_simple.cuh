@@ -1,8 +1,9 @@
 // Attention over a paged cache on CUDA cores: every storage type, head size,
 // alignment, page size and mask; float32 keeps 32-bit products throughout.
 //
-// The arithmetic, tiles and copies are kv_simple_kernel_t's (kv_simple.cuh); what
-// differs is where a row of K or V lies, looked up for each, and what a row sees.
+// The tiles and copies are kv_simple_kernel_t's (kv_simple.cuh); what differs is where a
+// row of K or V lies, looked up for each, what a row sees, and that two products go in
+// one instruction.
 #pragma once
 
 #include "kv_simple.cuh"
@@ -153,11 +154,12 @@ __global__ void __launch_bounds__(kKvSimpleThreads, NJ < 4 ? 2 : 1) paged_simple
       const bool more = j0 + kSimpleCols < hi;
       kv_cp_wait<1>();  // K; V may still be on its way
       __syncthreads();
-      float s[RA][4];
+      // sums over even and odd dims side by side: two products an instruction
+      float2 two[RA][4];
 #pragma unroll
       for (int a = 0; a < RA; ++a)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[a][c] = 0.0f;
+        for (int c = 0; c < 4; ++c) two[a][c] = make_float2(0.0f, 0.0f);
       const float* qr = sq + ty * HP;
       const float* kr = sk + tx * HP;
       int d = 0;
@@ -171,9 +173,15 @@ __global__ void __launch_bounds__(kKvSimpleThreads, NJ < 4 ? 2 : 1) paged_simple
           const float4 q = *reinterpret_cast<const float4*>(qr + 16 * a * HP + d);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            s[a][c] = fmaf(q.x, k4[c].x, fmaf(q.y, k4[c].y, fmaf(q.z, k4[c].z, fmaf(q.w, k4[c].w, s[a][c]))));
+            two[a][c] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k4[c].x, k4[c].y),
+                                   __ffma2_rn(make_float2(q.z, q.w), make_float2(k4[c].z, k4[c].w), two[a][c]));
         }
       }
+      float s[RA][4];
+#pragma unroll
+      for (int a = 0; a < RA; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[a][c] = two[a][c].x + two[a][c].y;
       for (; d < H; ++d)
 #pragma unroll
         for (int a = 0; a < RA; ++a)
@@ -230,10 +238,10 @@ __global__ void __launch_bounds__(kKvSimpleThreads, NJ < 4 ? 2 : 1) paged_simple
         constexpr bool kCareful = decltype(careful)::value;
         auto fma4 = [&](float4& o, float w, const float4& v) {
           if (kCareful && w == 0.0f) return;  // a hidden key's weight is exactly 0, and its value is not touched
-          o.x = fmaf(w, v.x, o.x);
-          o.y = fmaf(w, v.y, o.y);
-          o.z = fmaf(w, v.z, o.z);
-          o.w = fmaf(w, v.w, o.w);
+          const float2 ww = make_float2(w, w);
+          const float2 lo = __ffma2_rn(ww, make_float2(v.x, v.y), make_float2(o.x, o.y));
+          const float2 hi = __ffma2_rn(ww, make_float2(v.z, v.w), make_float2(o.z, o.w));
+          o = make_float4(lo.x, lo.y, hi.x, hi.y);
         };
         for (int c = 0; c < n; c += 4) {
           float4 w[RA];

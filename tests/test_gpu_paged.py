@@ -641,3 +641,43 @@ def test_same_call_same_bits(lib, cuda):
         want = _call(lib, a, cuda)
         for _ in range(5):
             assert torch.equal(_call(lib, a, cuda), want)
+
+
+def test_short_way_and_ctypes_agree(lib, cuda, monkeypatch):
+    """Calls through csrc/binding.cpp and through ctypes: the same results, refusals and streams."""
+    assert lib._short_way()
+    a = _make(70, "bf16", *SHAPES["mixed"], lead=1, behind=2)
+    b = _append_case(71, "f16", *APPENDS["odd_heads"], norm=True, positions=True)
+    for name in ("attention", "append", "keep"):
+        results = []
+        for short in (lib._short_way(), False):
+            monkeypatch.setattr(lib, "_short", short)
+            if not short:
+                monkeypatch.setattr(lib, "_short_way", lambda: False)
+            if name == "attention":
+                out = torch.zeros_like(a["q"]).to(cuda)
+                assert _call(lib, a, cuda, out=out) is out
+                results.append([out])
+                with pytest.raises(lib.RopeError):
+                    _call(lib, dict(a, window=-1), cuda)
+                with pytest.raises(ValueError):
+                    _call(lib, a, cuda, workspace=torch.zeros(64, device=cuda))
+                with pytest.raises(ValueError):
+                    _call(lib, dict(a, q=a["q"].t()), cuda)
+            elif name == "append":
+                k, v = b["k"].to(cuda), b["v"].to(cuda)
+                results.append([_append(lib, b, cuda, k, v), k, v])
+                with pytest.raises(lib.RopeError):
+                    _append(lib, dict(b, inter=3), cuda, k, v)
+                with pytest.raises(ValueError):
+                    _append(lib, b, cuda, k.float(), v)
+            else:
+                g = torch.Generator().manual_seed(2)
+                k, v = (torch.randn((6, 2, 16, 64), generator=g).half().to(cuda) for _ in range(2))
+                _keep(lib, cuda, k, v, [[0, 3], [5, 1]], [4, 10], [[1, 5], [0, 2, 9]])
+                results.append([k, v])
+                with pytest.raises(ValueError):
+                    _keep(lib, cuda, k, v.float(), [[0, 3], [5, 1]], [4, 10], [[1, 5], [0, 2, 9]])
+            monkeypatch.undo()
+        for x, y in zip(*results):
+            assert torch.equal(x, y)

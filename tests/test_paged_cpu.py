@@ -136,6 +136,25 @@ def test_binding_refuses(lib):
                                  v_pages=k, page_table=i, past_seq_lens=i[:, 0], query_starts=i[:, 0])
 
 
+def test_short_way_leaves_the_rest_to_the_binding(lib):
+    """The compiled short way declines what is not all as it should be, without an error of its own."""
+    short = lib._short_way()
+    if not short:
+        pytest.skip("binding.cpp is not compiled here")
+    q = torch.zeros((3, 64), dtype=torch.float16)
+    k = torch.zeros((4, 1, 16, 64), dtype=torch.float16)
+    i = torch.zeros((3, 1), dtype=torch.int32)
+    p, s = i[:, 0].contiguous(), torch.zeros(4, dtype=torch.int32)
+    for fn, args in ((short.attention, (0, 0, q, k, k, i, p, 1, s, 1, None, 0.0, 0, None, None, None, None, None)),
+                     (short.keep, (0, 0, k, k, i, p, i, p, None)),
+                     (short.append, (0, 0, q, q, q, None, 1, 1, k, k, i, p, s, q, q, 0, 0, None, None, None, None, 1e-6))):
+        assert fn(*args) is None                    # CPU tensors
+        for n in range(len(args)):
+            for bad in ("x", None, 1.5, 2 ** 70):
+                assert fn(*args[:n], bad, *args[n + 1:]) is None
+        assert fn(*args[:-1]) is None and fn() is None
+
+
 # --------------------------------------------------------------------------
 # the definitions
 # --------------------------------------------------------------------------
