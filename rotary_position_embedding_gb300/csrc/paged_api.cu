@@ -131,7 +131,7 @@ PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq,
   if (ragged && pl.items > T / tpi + B) pl.items = T / tpi + B;
   pl.split_bytes = 2 * tr * (H * 4 + 8) + 16;
   const int64_t units = (rows + kv_tile_keys(H) - 1) / kv_tile_keys(H);  // of an item
-  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 31) / (units + 8)) {
+  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 30) / (units + 8)) {
     pl.deal = kPagedTileCtas;
     if (pl.deal > pl.items * Nkv * units) pl.deal = (int)(pl.items * Nkv * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -283,6 +283,10 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     memset(&tile_maps, 0, sizeof(tile_maps));
     const bool bf = dtype == ROPE_BF16;
     p.tpi = kv_tile_rows(head_size) / p.G;
+    // in key tiles, which take 1.6 us, capped 2.4 (and hidden keys of capped tiles 2 more):
+    // an item 4.5 to 6.5 us, joining 13 us where every SM has parts
+    p.over_item = softcap > 0.0f ? 4 : 3;
+    p.over_join = softcap > 0.0f ? 5 : 8;
     tile_maps.k = maps.k;
     tile_maps.v = maps.v;
     if (!encode_paged_map(&tile_maps.k_row, bf, k_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 1) ||

@@ -121,7 +121,6 @@ __device__ __forceinline__ bool paged_few(const PagedParams& p, const PagedSeq& 
 // Both work n out of the lengths in whole numbers, each sequence's time (ns of an SM)
 // added up in any order. A mixed step of a capped prompt of 2048 tokens and 95 single
 // tokens over up to 4000 keys: one after the other 255 us.
-constexpr int kPagedOver = 3;  // what an item of paged_tile_kernel_t weighs beside its key tiles
 struct PagedTimes {
   unsigned long long tile, token;
 };
@@ -135,7 +134,7 @@ __device__ __forceinline__ void paged_time(const PagedParams& p, const PagedSeq&
     if (p.window > 0 && span > p.window + p.tpi) span = p.window + p.tpi;
     if (span < 0) span = 0;
     const int64_t items = (q.n + p.tpi - 1) / p.tpi;
-    t->tile += (unsigned long long)(items * (span / keys + 1 + kPagedOver)) * (unsigned)(p.cap > 0.0f ? step + 900 : step);
+    t->tile += (unsigned long long)(items * (span / keys + 1 + p.over_item)) * (unsigned)(p.cap > 0.0f ? step + 900 : step);
   }
 }
 __device__ __forceinline__ int paged_shares(const PagedTimes& t) {

@@ -45,6 +45,7 @@ struct PagedParams {
   int32_t deal, cluster;   // CTAs that the work is dealt to; paged_token_kernel: or those of a cluster a problem
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
   int32_t tpi;             // paged_tile_kernel: tokens of an item
+  int32_t over_item, over_join;  // what an item weighs beside its key tiles, what joining parts is worth
   int32_t shared;          // both kernels run at a time, each on its share of the SMs (see paged_shares)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;

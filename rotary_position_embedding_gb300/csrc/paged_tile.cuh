@@ -6,7 +6,7 @@
 //
 // One CTA an SM stays for the whole call. The work is the key tiles of all items (up to
 // ROWS rows of a sequence, whole tokens) and heads, and CTA i takes the part [i W / n, (i +
-// 1) W / n) of their weight W, an item's being its key tiles and kPagedOver for its beginning
+// 1) W / n) of their weight W, an item's being its key tiles and over_item for its beginning
 // and its output: sequences of any lengths, few long ones and many short ones, even out, and
 // nothing is split where it need not be. An item that one CTA has whole goes to the
 // output, the others' parts to the workspace (2 slots a CTA), where
@@ -137,15 +137,29 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
   }
   if (p.deal == 0) return only < count ? 1 : 0;
   if (count > kPagedItems) count = kPagedItems;
+  // Items of one length lie side by side; they are strewn (i -> i s mod count, s a prime
+  // above count / 2 or coprime to it), so that each CTA has some of every kind: a prompt's
+  // shortest items, each of masked tiles alone, cost more than they weigh.
+  static_assert(kPagedItems == 2 * kPagedTileThreads, "two items a thread");
+  const uint32_t n389 = 389u % (uint32_t)(count > 0 ? count : 1), n241 = 241u % (uint32_t)(count > 0 ? count : 1);
+  auto far = [&](uint32_t r) { return r < count - r ? r : count - r; };
+  const uint32_t s = count % 389 == 0 || (count % 241 != 0 && far(n241) > far(n389)) ? 241u : 389u;
+  int2 mine[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t i = tid + k * kPagedTileThreads;
+    if (i < (uint32_t)count) mine[k] = make_int2(items[i * s % count].b, items[i * s % count].tok0);
+  }
+  __syncthreads();
   int sum = 0;
-  for (int i0 = 0; i0 < count; i0 += kPagedTileThreads) {
-    const int i = i0 + tid;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = k * kPagedTileThreads + tid;
     int n = 0, all;
     if (i < count) {
-      const int b = items[i].b;
-      const PagedItem it = paged_item(p, paged_seq(p.s, b), b, items[i].tok0, keys);
+      const PagedItem it = paged_item(p, paged_seq(p.s, mine[k].x), mine[k].x, mine[k].y, keys);
       items[i] = it;
-      n = paged_item_tiles(it, keys) + kPagedOver;
+      n = paged_item_tiles(it, keys) + p.over_item;
     }
     const int upto = paged_scan(n, s_sum, &all) + sum;
     if (i < count) before[i] = upto - n;
@@ -154,6 +168,35 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
   if (tid == 0) before[count] = sum;
   __syncthreads();
   return count;
+}
+
+// The weight dealt out: CTA i has [first(i), first(i + 1)).
+struct PagedTileShares {
+  uint32_t per, more;  // each has `per`, the first `more` of them one more
+  __device__ __forceinline__ void set(uint32_t total, uint32_t ctas) {
+    per = total / ctas;
+    more = total - per * ctas;
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t cta) const { return cta * per + (cta < more ? cta : more); }
+  __device__ __forceinline__ uint32_t owner(uint32_t at) const {
+    const uint32_t upto = more * (per + 1);
+    return at < upto ? at / (per + 1) : more + (at - upto) / per;
+  }
+};
+
+// The beginning of an item and head, or the end of the last, that is nearest to `at`.
+__device__ __forceinline__ int paged_nearest(const PagedParams& p, int at, const int32_t* before, int count) {
+  if (count == 0) return 0;
+  int x = 0, y = count;
+  while (y - x > 1) {
+    const int mid = (x + y) >> 1;
+    if (before[mid] * p.Nkv <= at)
+      x = mid;
+    else
+      y = mid;
+  }
+  const int weight = before[x + 1] - before[x], in = at - before[x] * p.Nkv;
+  return at - in + (int)((uint32_t)(2 * in + weight) / (uint32_t)(2 * weight)) * weight;
 }
 
 // The segments of a CTA, one after the other: key tiles [u0, u1) of an item and head.
@@ -180,19 +223,20 @@ struct PagedTileWork {
       else
         y = mid;
     }
-    // an item's weight: kPagedOver of nothing, then a tile each
+    // an item's weight: p.over_item of nothing, then a tile each
     int weight = before[x + 1] - before[x], in = at - before[x] * p.Nkv;
     kvh = (int)((uint32_t)in / (uint32_t)weight);
     in -= kvh * weight;
-    if (in < kPagedOver) {
-      at += kPagedOver - in;
-      in = kPagedOver;
+    if (in < p.over_item) {
+      at += p.over_item - in;
+      in = p.over_item;
       if (at >= last) return false;
     }
     item = x;
-    u0 = in - kPagedOver;
-    u1 = u0 + (last - at) < weight - kPagedOver ? u0 + (last - at) : weight - kPagedOver;
-    whole = u0 == 0 && u1 == weight - kPagedOver;
+    const int tiles = weight - p.over_item;
+    u0 = in - p.over_item;
+    u1 = u0 + (last - at) < tiles ? u0 + (last - at) : tiles;
+    whole = u0 == 0 && u1 == tiles;
     at += u1 - u0;
     return true;
   }
@@ -249,6 +293,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_sum[kPagedTileThreads / 32];
   __shared__ PagedTimes s_times;
+  __shared__ int s_ends[kPagedTileCtas + 1];
   uint8_t* base = kv_tiles + ((1024 - (kv_smem(kv_tiles) & 1023)) & 1023);
   const uint32_t sq = kv_smem(base), sk = sq + C::kQ, sv = sk + 2 * C::kStage;
   PagedItem* const items = reinterpret_cast<PagedItem*>(base + C::kQ + 4 * C::kStage);
@@ -304,11 +349,19 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   }
   PagedTileWork work;
   work.at = work.last = 0;
-  const uint32_t total = p.deal > 0 && count > 0 ? (uint32_t)before[count] * (uint32_t)p.Nkv : 0u;  // below 2^31
+  PagedTileShares shares;
   if (p.deal > 0) {
+    shares.set(count > 0 ? (uint32_t)before[count] * (uint32_t)p.Nkv : 0u, ctas);  // below 2^31
+    // Whole items, if that costs less than joining: each CTA's ends moved to the nearest
+    // item's. 288 items of 6 key tiles on 152 SMs 43.5 us split, 37 so.
+    const int cta = tid <= (int)ctas ? tid : (int)ctas;
+    s_ends[cta] = paged_nearest(p, (int)shares.first((uint32_t)cta), before, count);
+    __syncthreads();
+    const int load = s_ends[cta < (int)ctas ? cta + 1 : cta] - s_ends[cta];
+    const bool split = __syncthreads_or(load > (int)shares.per + p.over_join);
     if (blockIdx.x < ctas) {
-      work.at = (int)((uint64_t)blockIdx.x * total / ctas);
-      work.last = (int)((uint64_t)(blockIdx.x + 1) * total / ctas);
+      work.at = split ? (int)shares.first(blockIdx.x) : s_ends[blockIdx.x];
+      work.last = split ? (int)shares.first(blockIdx.x + 1) : s_ends[blockIdx.x + 1];
     }
     // so far nothing begins here that goes on elsewhere, and nothing of this CTA's counts
     // where an item's CTAs lie on both sides of it
@@ -355,8 +408,8 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
       const bool whole = work.whole;
       // the one item that begins in this CTA and goes on in others: paged_tile_join_kernel_t's
       if (tid == 0 && work.u0 == 0 && !whole) {
-        const uint32_t upto = (uint32_t)(work.at - work.u1 + paged_item_tiles(it, N));  // its last tile, and one
-        const int parts = (int)(((uint64_t)upto * ctas - 1) / total) - (int)blockIdx.x;
+        const uint32_t its_last = (uint32_t)(work.at - work.u1 + paged_item_tiles(it, N) - 1);
+        const int parts = (int)shares.owner(its_last) - (int)blockIdx.x;
         p.ws_join[blockIdx.x] = make_int4(it.g0, kvh, nrows, 2 * parts + (segment > 0 ? 1 : 0));
       }
       if (t * kTileRows >= nrows) continue;
