@@ -113,7 +113,7 @@ PagedPlan plan_token(int64_t B, int64_t most, int64_t Nq, int64_t Nkv, int64_t H
     if (n > kKvClusterMost) n = kKvClusterMost;
     if (problems * n <= kSms) pl.cluster = n;
   }
-  if (!pl.cluster && units > 1 && B <= kKvDealMost && problems < (1ll << 31) / (units + 2)) {
+  if (!pl.cluster && units > 1 && B <= kKvDealMost && problems < (1ll << 30) / (units + 8)) {
     pl.deal = paged_token_ctas(H);
     if (pl.deal > problems * units) pl.deal = (int)(problems * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -131,7 +131,7 @@ PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq,
   if (ragged && pl.items > T / tpi + B) pl.items = T / tpi + B;
   pl.split_bytes = 2 * tr * (H * 4 + 8) + 16;
   const int64_t units = (rows + kv_tile_keys(H) - 1) / kv_tile_keys(H);  // of an item
-  if (pl.items <= kPagedItems && pl.items * Nkv < (1ll << 30) / (units + 8)) {
+  if (B <= pl.items && pl.items <= kPagedItems && pl.items * Nkv < (1ll << 30) / (units + 8)) {
     pl.deal = kPagedTileCtas;
     if (pl.deal > pl.items * Nkv * units) pl.deal = (int)(pl.items * Nkv * units);
     pl.bytes = pl.deal * pl.split_bytes + kWorkspaceSlack;
@@ -289,7 +289,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     p.over_join = softcap > 0.0f ? 5 : 8;
     tile_maps.k = maps.k;
     tile_maps.v = maps.v;
-    if (!encode_paged_map(&tile_maps.k_row, bf, k_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 1) ||
+    if (!encode_paged_map(&tile_maps.v_eight, bf, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 8) ||
         !encode_paged_map(&tile_maps.v_row, bf, v_pages, head_size, page_size, kv_num_heads, num_pages, page_stride, 1) ||
         !encode_paged_q_map(&tile_maps.q, bf, query, head_size, num_heads, tokens, p.G, p.tpi))
       family = PagedFamily::kSimple;
@@ -349,7 +349,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     if (!tile_p.deal) return ROPE_OK;
     int tr = kv_tile_rows(head_size);
     void* jargs[] = {&tile_p, &tr};
-    return launch(tile_join, dim3((unsigned)tile_p.deal, tr / 16), kPagedJoinThreads, 0, stream, jargs,
+    return launch(tile_join, dim3(kSms * kPagedJoinCtas), kPagedJoinThreads, 0, stream, jargs,
                   "kv_attention_paged launch (joining the parts)");
   };
   if (family != PagedFamily::kToken) {
@@ -358,6 +358,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     const PagedTileKernel k =
         dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
     deal_of(pl, kv_tile_rows(head_size), 0);
+    p.items = p.deal ? (int32_t)pl.items : 0;
     void* targs[] = {&p, &tile_maps};
     KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kPagedTileBlock, k.smem, stream, targs,
                   "kv_attention_paged launch (many rows)", kPagedTileRegisters));
@@ -435,6 +436,8 @@ rope_status rope_apply_qkv_paged(rope_dtype dtype, int64_t batch, int64_t tokens
     return fail(ROPE_ERR_INVALID_ARG, "q_out cannot alias a packed query (different row strides)");
   KV_TRY(check_ptr(k_pages, "k_pages", es));
   KV_TRY(check_ptr(v_pages, "v_pages", es));
+  if (k_pages == v_pages || k_pages == q_out || v_pages == q_out)
+    return fail(ROPE_ERR_INVALID_ARG, "q_out, k_pages and v_pages cannot alias");
   KV_TRY(check_ptr(page_table, "page_table", 4));
   KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
   KV_TRY(check_optional(query_starts, "query_starts", 4));
@@ -529,6 +532,7 @@ rope_status kv_keep_paged(rope_dtype dtype, int64_t batch, int32_t kv_num_heads,
   const size_t es = dtype == ROPE_F32 ? 4 : 2;
   KV_TRY(check_ptr(k_pages, "k_pages", es));
   KV_TRY(check_ptr(v_pages, "v_pages", es));
+  if (k_pages == v_pages) return fail(ROPE_ERR_INVALID_ARG, "k_pages and v_pages are the same");
   KV_TRY(check_ptr(page_table, "page_table", 4));
   KV_TRY(check_ptr(past_seq_lens, "past_seq_lens", 4));
   KV_TRY(check_ptr(kept, "kept", 4));

@@ -44,7 +44,7 @@ struct PagedParams {
   int32_t chunk;           // rows of a box: of a page, and of a unit or tile of keys
   int32_t deal, cluster;   // CTAs that the work is dealt to; paged_token_kernel: or those of a cluster a problem
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
-  int32_t tpi;             // paged_tile_kernel: tokens of an item
+  int32_t tpi, items;      // paged_tile_kernel: tokens of an item; items of the batch, at most
   int32_t over_item, over_join;  // what an item weighs beside its key tiles, what joining parts is worth
   int32_t shared;          // both kernels run at a time, each on its share of the SMs (see paged_shares)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
@@ -73,7 +73,7 @@ PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
 
 // Any number of rows, the same types, G up to kv_tile_rows(H): items of PagedParams.tpi
 // tokens; the launch takes (PagedParams, PagedTileMaps), grid (deal), and is followed by
-// join with (PagedParams, kv_tile_rows(H)), grid (deal, a sixteenth of that); or, with more
+// join with (PagedParams, kv_tile_rows(H)), grid (kPagedJoinCtas an SM); or, with more
 // than kPagedItems items or no workspace, grid (items * Nkv).
 struct PagedTileKernel {
   const void* fn;
@@ -83,7 +83,7 @@ struct PagedTileKernel {
 constexpr int kPagedItems = 768;
 constexpr int kPagedTileBlock = 384;
 constexpr int kPagedTileCtas = 152;  // most that are dealt to
-constexpr int kPagedJoinThreads = 256;
+constexpr int kPagedJoinThreads = 256, kPagedJoinCtas = 2;  // of the join kernel; its CTAs an SM
 // The kernel deals its registers out again (setmaxnreg): 256 x 208 + 128 x 88 = 384 x 168,
 // so it must have been launched with 168 a thread.
 constexpr int kPagedTileRegisters = 168;

@@ -10,10 +10,10 @@ struct PagedMaps {
   CUtensorMap k, v;
 };
 
-// K and V in boxes of several rows and of one; Q (T, Nq, H) in boxes of the heads of a
-// group and the tokens of an item.
+// K and V in boxes of several rows, V of 8 and of one too; Q (T, Nq, H) in boxes of the
+// heads of a group and the tokens of an item.
 struct PagedTileMaps {
-  CUtensorMap k, v, k_row, v_row, q;
+  CUtensorMap k, v, v_eight, v_row, q;
 };
 
 // Map of pages (num, Nkv, ps, H) of 16-bit elements, `stride` elements apart, in

@@ -19,7 +19,8 @@
 //   soon as the last product of the segment before has read its own; 11 issues every MMA.
 // V's rows behind the last key have to be zeros (their weights are, and 0 * NaN is not):
 // boxes of such rows are asked for in a page that does not exist, and the box that holds
-// the last key is brought row by row.
+// the last key is brought in boxes of 8 rows and of one (all rows one by one, for K too,
+// a segment began 4 us later with pages of 64). What K has there only hidden scores get.
 // A row sees keys from its window on; of a draft tree's new keys those whose bit its
 // mask holds. Only key tiles that some row does not see whole are looked at key by key,
 // as bits of four words.
@@ -116,8 +117,7 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
     }
     const int first = paged_scan(n, s_sum, &all) - n + count;
     if (p.deal > 0) {
-      // (more than planned for only where query_starts does not ascend)
-      for (int t = 0; t < n && first + t < kPagedItems; ++t) items[first + t].b = b, items[first + t].tok0 = t;
+      if (b < p.s.B) before[b] = first;  // for now; there are at least as many items planned as sequences
     } else if (only >= first && only < first + n) {
       items[0] = paged_item(p, q, b, first + n - 1 - only, keys);  // the longest rows first
     }
@@ -136,7 +136,7 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
     if (blockIdx.x >= *ctas) return 0;
   }
   if (p.deal == 0) return only < count ? 1 : 0;
-  if (count > kPagedItems) count = kPagedItems;
+  if (count > p.items) count = p.items;  // more than planned for only where query_starts does not ascend
   // Items of one length lie side by side; they are strewn (i -> i s mod count, s a prime
   // above count / 2 or coprime to it), so that each CTA has some of every kind: a prompt's
   // shortest items, each of masked tiles alone, cost more than they weigh.
@@ -144,26 +144,31 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
   const uint32_t n389 = 389u % (uint32_t)(count > 0 ? count : 1), n241 = 241u % (uint32_t)(count > 0 ? count : 1);
   auto far = [&](uint32_t r) { return r < count - r ? r : count - r; };
   const uint32_t s = count % 389 == 0 || (count % 241 != 0 && far(n241) > far(n389)) ? 241u : 389u;
-  int2 mine[2];
+  PagedItem mine[2];
+  int n[2] = {0, 0}, sum;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint32_t i = tid + k * kPagedTileThreads;
-    if (i < (uint32_t)count) mine[k] = make_int2(items[i * s % count].b, items[i * s % count].tok0);
-  }
-  __syncthreads();
-  int sum = 0;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int i = k * kPagedTileThreads + tid;
-    int n = 0, all;
-    if (i < count) {
-      const PagedItem it = paged_item(p, paged_seq(p.s, mine[k].x), mine[k].x, mine[k].y, keys);
-      items[i] = it;
-      n = paged_item_tiles(it, keys) + p.over_item;
+    const uint32_t i = 2 * tid + k;
+    if (i >= (uint32_t)count) continue;
+    const int at = (int)(i * s % (uint32_t)count);
+    int x = 0, y = p.s.B;  // its sequence
+    while (y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (before[mid] <= at)
+        x = mid;
+      else
+        y = mid;
     }
-    const int upto = paged_scan(n, s_sum, &all) + sum;
-    if (i < count) before[i] = upto - n;
-    sum += all;
+    mine[k] = paged_item(p, paged_seq(p.s, x), x, at - before[x], keys);
+    n[k] = paged_item_tiles(mine[k], keys) + p.over_item;
+  }
+  const int first = paged_scan(n[0] + n[1], s_sum, &sum) - n[0] - n[1];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * tid + k;
+    if (i >= count) continue;
+    items[i] = mine[k];
+    before[i] = first + (k > 0 ? n[0] : 0);
   }
   if (tid == 0) before[count] = sum;
   __syncthreads();
@@ -710,7 +715,6 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
       uint64_t* const full = is_k ? bars.k_full : bars.v_full;
       uint64_t* const free_ = is_k ? bars.k_free : bars.v_free;
       const CUtensorMap* const map = is_k ? &maps.k : &maps.v;
-      const CUtensorMap* const row_map = is_k ? &maps.k_row : &maps.v_row;
       const uint32_t stage0 = is_k ? sk : sv;
       // a box: p.chunk rows (of one page) x 64 elements; this lane's rows and slab of a tile
       const int chunks = N / p.chunk;
@@ -745,16 +749,23 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
           const uint32_t dst = stage0 + st * C::kStage, done = bar(&full[st]);
           if (lane == 0) mbar_arrive_expect_tx(done, C::kStage);
           __syncwarp();
-          // the box that holds the last key and rows behind it
-          const int cut = hi < j0 + N ? (hi - j0) & ~(p.chunk - 1) : N;
+          // the box of V that holds the last key and rows behind it
+          const int cut = !is_k && hi < j0 + N ? (hi - j0) & ~(p.chunk - 1) : N;
           const bool cut_box = cut < N && cut + j0 < hi;
           if (my_slab < C::SLABS && !(cut_box && my_row == cut))
             bring(map, dst + my_slab * (N * 128) + my_row * 128, my_slab, j0 + my_row, j0 + my_row + p.chunk, page, done);
           if (cut_box) {
             const int cut_page = entry(j0 + cut, j0 + cut + p.chunk);
-            for (int i = lane; i < p.chunk * C::SLABS; i += 32) {
-              const int r = cut + (i & (p.chunk - 1)), slab = i / p.chunk, j = j0 + r;
-              bring(row_map, dst + slab * (N * 128) + r * 128, slab, j, j + 1, j < hi && j >= seen ? cut_page : -1, done);
+            // 8 rows at a time, those with the last key one by one; zeros behind it
+            const int eights = p.chunk / 8 - 1, copies = eights + 8, last8 = (hi - j0) & ~7;
+            for (int i = lane; i < copies * C::SLABS; i += 32) {
+              const int slab = i / copies, n8 = i - slab * copies;
+              const bool one = n8 >= eights;
+              int r = one ? last8 + n8 - eights : cut + 8 * n8;
+              if (!one && r >= last8) r += 8;  // (where hi ends a box of 8, the one behind goes row by row)
+              const int j = j0 + r, upto = j + (one ? 1 : 8);
+              bring(one ? &maps.v_row : &maps.v_eight, dst + slab * (N * 128) + r * 128, slab, j, upto,
+                    j < hi && upto > seen ? cut_page : -1, done);
             }
           }
           page = page_after;
@@ -773,98 +784,143 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-// A load that stays where it stands, ahead of what decides whether it counts.
+// Loads that stay where they stand, ahead of what decides whether they count. Each value
+// is read once, so L1 is passed by.
 __device__ __forceinline__ float4 paged_load4(const float4* at) {
   float4 x;
-  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(at) : "memory");
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 paged_load2(const float2* at) {
+  float2 x;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(at) : "memory");
   return x;
 }
 
-// Joins the parts of the items that paged_tile_kernel_t dealt to several CTAs. CTA (x,
-// y): the item that begins in CTA x there and goes on in others, if there is one; its
-// rows 16 y .., 16 threads side by side for the same dims of 16 rows. What each part
-// counts is worked out first, for all parts at a time, so that the loads of the parts wait
-// for nothing. `rows`: of a slot.
-template <class T, int HD>
-__global__ void __launch_bounds__(kPagedJoinThreads) paged_tile_join_kernel_t(const PagedParams p, int rows) {
-  constexpr int SIDE = kPagedJoinThreads / 16, PIECES = HD / 4 / SIDE;  // of 4 dims, a thread
-  constexpr int DEEP = PIECES <= 2 ? 8 : 4;                             // parts at a time
-  __shared__ float s_f[kPagedTileCtas + DEEP][16], s_max[SIDE][16], s_sum[SIDE][16];
-  const int r0 = threadIdx.x & 15, side = threadIdx.x >> 4, r = (int)blockIdx.y * 16 + r0;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int4 what = p.ws_join[blockIdx.x];  // first token, kvh, rows, 2 * further CTAs + slot
-  if (what.w < 2 || (int)blockIdx.y * 16 >= what.z) return;
-  const int kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x, pieces = p.H / 4;
-  // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
-  auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
-  float M = -CUDART_INF_F;
-#pragma unroll 4
-  for (int n = side; n < parts; n += SIDE) {
-    const float m = p.ws_ml[slot_of(n) * rows + r].x;
-    s_f[n][r0] = m;
-    M = fmaxf(M, m);
-  }
-  s_max[side][r0] = M;
-  __syncthreads();
+// 4 dims of `RW` rows of one item, kRows apart, from its parts: slots c0 * 2 + (what.w & 1)
+// and the first ones of the CTAs behind. The loads of 8 / RW parts of all rows are in flight
+// together, what they count beside them.
+template <class T, int RW>
+__device__ __forceinline__ void paged_tile_join_rows(const PagedParams& p, const int4& what, int c0, int first_row,
+                                                     int apart, int piece, int rows) {
+  constexpr int DEEP = 8 / RW;
+  const int parts = (what.w >> 1) + 1, pieces = p.H / 4;
+  const float4* const from = reinterpret_cast<const float4*>(p.ws_o) + piece * rows;
+  float M[RW], L[RW];
+  float4 acc[RW];
 #pragma unroll
-  for (int k = 0; k < SIDE; ++k) M = fmaxf(M, s_max[k][r0]);
-  const float base = M == -CUDART_INF_F ? 0.0f : M;
-  float L = 0.0f;
-#pragma unroll 4
-  for (int n = side; n < parts; n += SIDE) {
-    const float f = exp2f(s_f[n][r0] - base);
-    L = fmaf(p.ws_ml[slot_of(n) * rows + r].y, f, L);
-    s_f[n][r0] = f;
-  }
-  for (int n = parts + side; n < parts + DEEP; n += SIDE) s_f[n][r0] = 0.0f;
-  s_sum[side][r0] = L;
-  __syncthreads();
-  L = 0.0f;
-#pragma unroll
-  for (int k = 0; k < SIDE; ++k) L += s_sum[k][r0];
-  float4 acc[PIECES];
-#pragma unroll
-  for (int j = 0; j < PIECES; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float4* const from = reinterpret_cast<const float4*>(p.ws_o) + r;
+  for (int i = 0; i < RW; ++i) M[i] = -CUDART_INF_F, L[i] = 0.0f, acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int n0 = 0; n0 < parts; n0 += DEEP) {
-    float4 x[DEEP][PIECES];
-#pragma unroll
-    for (int k = 0; k < DEEP; ++k)
-#pragma unroll
-      for (int j = 0; j < PIECES; ++j) {
-        const int piece = side + SIDE * j;
-        const int64_t at = slot_of(n0 + k < parts ? n0 + k : 0) * pieces * rows + (int64_t)(piece < pieces ? piece : 0) * rows;
-        x[k][j] = paged_load4(from + at);
-      }
+    float4 o[DEEP][RW];
+    float2 ml[DEEP][RW];
 #pragma unroll
     for (int k = 0; k < DEEP; ++k) {
-      const float f = s_f[n0 + k][r0];  // 0 behind the last, and where a CTA had no part and wrote nothing
+      const int n = n0 + k;
+      // (offsets are below 2 kPagedTileCtas slots of 256 rows x 64 pieces, 2^23)
+      const uint32_t slot = 2 * (c0 + n) + (n == 0 ? what.w & 1 : 0);
 #pragma unroll
-      for (int j = 0; j < PIECES; ++j) {
-        if (f == 0.0f) x[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        acc[j].x = fmaf(x[k][j].x, f, acc[j].x);
-        acc[j].y = fmaf(x[k][j].y, f, acc[j].y);
-        acc[j].z = fmaf(x[k][j].z, f, acc[j].z);
-        acc[j].w = fmaf(x[k][j].w, f, acc[j].w);
+      for (int i = 0; i < RW; ++i) {
+        const int r = first_row + i * apart;
+        ml[k][i] = make_float2(-CUDART_INF_F, 0.0f);
+        o[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (n < parts && r < what.z) {
+          ml[k][i] = paged_load2(p.ws_ml + (slot * rows + r));
+          o[k][i] = paged_load4(from + (slot * pieces * rows + r));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      float m = M[i];
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k) m = fmaxf(m, ml[k][i].x);
+      const float base = m == -CUDART_INF_F ? 0.0f : m, a = exp2f(M[i] - base);
+      M[i] = m;
+      L[i] *= a;
+      acc[i].x *= a, acc[i].y *= a, acc[i].z *= a, acc[i].w *= a;
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k) {
+        const float f = exp2f(ml[k][i].x - base);
+        if (f == 0.0f) o[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // where a CTA had no part it wrote nothing
+        L[i] = fmaf(ml[k][i].y, f, L[i]);
+        acc[i].x = fmaf(o[k][i].x, f, acc[i].x);
+        acc[i].y = fmaf(o[k][i].y, f, acc[i].y);
+        acc[i].z = fmaf(o[k][i].z, f, acc[i].z);
+        acc[i].w = fmaf(o[k][i].w, f, acc[i].w);
       }
     }
   }
-  if (r >= what.z) return;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  const int tok = kv_div(r, p.by_g);
-  typename Elem<T>::bits* y = static_cast<typename Elem<T>::bits*>(p.out) +
-                              (((int64_t)what.x + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
 #pragma unroll
-  for (int j = 0; j < PIECES; ++j)
-    if (side + SIDE * j < pieces) {
-      VecT<T, 4> v;
-      v.v[0] = Elem<T>::fromf(acc[j].x * inv);
-      v.v[1] = Elem<T>::fromf(acc[j].y * inv);
-      v.v[2] = Elem<T>::fromf(acc[j].z * inv);
-      v.v[3] = Elem<T>::fromf(acc[j].w * inv);
-      *reinterpret_cast<VecT<T, 4>*>(y + 4 * (side + SIDE * j)) = v;
+  for (int i = 0; i < RW; ++i) {
+    const int r = first_row + i * apart;
+    if (r >= what.z) continue;
+    const float inv = L[i] == 0.0f ? 0.0f : 1.0f / L[i];
+    const int tok = kv_div(r, p.by_g);
+    VecT<T, 4> v;
+    v.v[0] = Elem<T>::fromf(acc[i].x * inv);
+    v.v[1] = Elem<T>::fromf(acc[i].y * inv);
+    v.v[2] = Elem<T>::fromf(acc[i].z * inv);
+    v.v[3] = Elem<T>::fromf(acc[i].w * inv);
+    *reinterpret_cast<VecT<T, 4>*>(static_cast<typename Elem<T>::bits*>(p.out) +
+                                   (((int64_t)what.x + tok) * p.Nq + (int64_t)what.y * p.G + (r - tok * p.G)) * p.H +
+                                   4 * piece) = v;
+  }
+}
+
+// Joins the parts of the items that paged_tile_kernel_t dealt to several CTAs. The rows of
+// all such items, a group at a time, go around the CTAs, which are as many as are resident
+// (one for each CTA dealt to and 16 rows, most of them with nothing to join, came in waves);
+// a thread has 4 dims of a row, or of 2 or 4 rows where there are few parts.
+template <class T, int HD>
+__global__ void __launch_bounds__(kPagedJoinThreads, kPagedJoinCtas) paged_tile_join_kernel_t(const PagedParams p, int rows) {
+  constexpr int PIECES = HD / 4, kRows = kPagedJoinThreads / PIECES;
+  __shared__ int4 s_what[kPagedTileCtas];
+  __shared__ int s_first[kPagedTileCtas + 1], s_cta[kPagedTileCtas], s_count[2][kPagedJoinThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto side_by_side = [](const int4& what) { return what.w < 4 ? 4 : what.w < 8 ? 2 : 1; };  // rows of a thread
+  pdl_wait();
+  pdl_launch_dependents();
+  // the items that have parts, and the groups of rows before each
+  int4 what = make_int4(0, 0, 0, 0);  // first token, kvh, rows, 2 * further CTAs + slot
+  if (tid < p.deal) what = p.ws_join[tid];
+  const int group = kRows * side_by_side(what), mine = what.w < 2 ? 0 : (what.z + group - 1) / group;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+  if (lane == 31) s_count[0][warp] = upto, s_count[1][warp] = __popc(some);
+  __syncthreads();
+  int before = upto - mine, at = __popc(some & ((1u << lane) - 1u)), total = 0, count = 0;
+#pragma unroll
+  for (int w = 0; w < kPagedJoinThreads / 32; ++w) {
+    if (w < warp) before += s_count[0][w], at += s_count[1][w];
+    total += s_count[0][w], count += s_count[1][w];
+  }
+  if (mine > 0) s_what[at] = what, s_first[at] = before, s_cta[at] = tid;
+  __syncthreads();
+  const int r0 = tid % kRows, piece = tid / kRows;
+  if (piece >= p.H / 4) return;
+  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+    int x = 0, y = count;
+    while (y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (s_first[mid] <= w)
+        x = mid;
+      else
+        y = mid;
     }
+    what = s_what[x];
+    const int n = side_by_side(what), row = (w - s_first[x]) * kRows * n + r0;
+    if (n == 4)
+      paged_tile_join_rows<T, 4>(p, what, s_cta[x], row, kRows, piece, rows);
+    else if (n == 2)
+      paged_tile_join_rows<T, 2>(p, what, s_cta[x], row, kRows, piece, rows);
+    else
+      paged_tile_join_rows<T, 1>(p, what, s_cta[x], row, kRows, piece, rows);
+  }
 }
 
 template <class T, int HD>

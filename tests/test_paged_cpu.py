@@ -14,12 +14,13 @@ F32, F16, BF16 = 0, 1, 2
 OK, INVALID, UNSUPPORTED = 0, 1, 2
 A = ctypes.c_void_p(0x10000)      # never dereferenced
 B = ctypes.c_void_p(0x90000)
+C = ctypes.c_void_p(0xd0000)
 ODD = ctypes.c_void_p(0x10001)
 
 
 def _append(so, **kw):
     a = dict(dtype=F16, B=2, tokens=6, Nq=8, Nkv=2, H=64, q=A, k=None, v=None, qw=None, kw=None, eps=1e-6, cos=A, sin=A,
-             rows=32, pos=None, past=A, starts=None, table=A, width=4, inter=0, rd=0, qo=B, kp=A, vp=A, pages=9, ps=16,
+             rows=32, pos=None, past=A, starts=None, table=A, width=4, inter=0, rd=0, qo=B, kp=A, vp=C, pages=9, ps=16,
              stride=2 * 16 * 64, st=None, stream=None)
     a.update(kw)
     return so.rope_apply_qkv_paged(*a.values())
@@ -34,7 +35,7 @@ def _attend(so, **kw):
 
 
 def _keep(so, **kw):
-    a = dict(dtype=F16, B=2, Nkv=2, H=64, kp=A, vp=A, pages=9, ps=16, stride=2 * 16 * 64, table=A, width=4, past=A, kept=A,
+    a = dict(dtype=F16, B=2, Nkv=2, H=64, kp=A, vp=C, pages=9, ps=16, stride=2 * 16 * 64, table=A, width=4, past=A, kept=A,
              most=5, lens=A, st=None, stream=None)
     a.update(kw)
     return so.kv_keep_paged(*a.values())
@@ -99,6 +100,12 @@ def test_out_is_no_input(lib):
         at.update({name: B, "out": B})
         assert _attend(so, **at) == INVALID
         assert b"alias" in so.rope_last_error()
+
+
+def test_pages_that_are_written_are_two(lib):
+    so = lib.load_library()
+    for call, kw in ((_append, dict(vp=A)), (_append, dict(qo=C)), (_append, dict(kp=B)), (_keep, dict(vp=A))):
+        assert call(so, **kw) == INVALID
 
 
 def test_empty_calls_launch_nothing(lib):
