@@ -606,7 +606,7 @@ int64_t kv_attention_workspace(int64_t batch, int64_t seq, int32_t num_heads, in
 /*
  * rope_apply_qkv_paged -- rope_apply_qkv (or, with both norm weights,
  * rope_apply_qkv_rmsnorm) in cache mode with caches held in pages. Every Q, K and V
- * head has the bits of those calls.
+ * head has the bits of those calls on tensors of the same alignment.
  *
  * query     device T (tokens, num_heads*H), or packed (tokens, (num_heads +
  *           2*kv_num_heads)*H) with key and value NULL; key, value (tokens,
@@ -713,10 +713,11 @@ const char* rope_last_error(void);
    "rope_qkv_heads_kernel" (SIMT Q/K, several heads of one role per thread),
    "rope_qkv_tma_kernel" (TMA pipeline), "rope_cache_build_kernel", "kv_append_kernel"
    (8-bit append), "kv_token_kernel" (attention, few rows), "kv_tile_kernel"
-   (attention, many rows), "kv_simple_kernel"
-   (attention on CUDA cores), "paged_append_kernel", "paged_append_heads_kernel" (several heads a thread), "paged_token_kernel", "paged_tile_kernel",
-   "paged_simple_kernel" or "paged_keep_kernel" (the same over pages; with both few rows and many the
-   last to be launched); "" before the first launch. Calls that fail or launch nothing (empty X) leave it unchanged.
+   (attention, many rows), "kv_simple_kernel" (attention on CUDA cores); over pages
+   "paged_append_kernel", "paged_append_heads_kernel" (several heads a thread),
+   "paged_token_kernel", "paged_tile_kernel", "paged_simple_kernel" (with few rows and
+   many in one call the last to be launched) or "paged_keep_kernel"; "" before the first
+   launch. Calls that fail or launch nothing (empty X) leave it unchanged.
    A diagnostic for profilers and benchmarks: the pages have no counterpart.
    The string is static; never free it. */
 const char* rope_last_kernel(void);
