@@ -6,6 +6,7 @@ loads on a machine without a GPU driver (every entry point then fails with
 ROPE_ERR_CUDA once it reaches a CUDA call; argument checks still run).
 """
 
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -30,7 +31,17 @@ HEADERS = ["rope_kernels.cuh", "rope_internal.h", "rope_tma.cuh", "rope_qkv.cuh"
            "paged_internal.h", "paged_common.cuh", "paged_append.cuh", "paged_append_heads.cuh", "paged_simple.cuh", "paged_careful.cuh", "paged_token.cuh",
            "paged_tile.cuh", "paged_maps.h", "paged_keep.cuh"]
 BINDING = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(OUT_DIR, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def _torch_version():
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "none"
+
+
+# what was compiled for another PyTorch is not loaded: its classes may be laid out differently
+BINDING_PATH = os.path.join(OUT_DIR, f"_binding-torch{_torch_version()}" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

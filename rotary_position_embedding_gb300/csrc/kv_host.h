@@ -117,7 +117,10 @@ inline rope_status allow_smem(const void* fn, size_t smem, int registers) {
   if (most < (int)smem) return fail(ROPE_ERR_UNSUPPORTED, "needs %zu bytes of shared memory", smem);
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
-  g_raised.insert(std::make_pair(dev, fn));
+  try {
+    g_raised.insert(std::make_pair(dev, fn));
+  } catch (...) {  // no memory: asked for again by the next call
+  }
   return ROPE_OK;
 }
 
@@ -128,14 +131,20 @@ inline rope_status resident_ctas(const void* fn, int threads, int* n) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lk(g_mu);
-  int& held = g_resident[std::make_tuple(dev, fn, threads)];
-  if (held == 0) {
-    int b = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, 0);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-    held = b < 1 ? 1 : b;
+  const auto key = std::make_tuple(dev, fn, threads);
+  const auto held = g_resident.find(key);
+  if (held != g_resident.end()) {
+    *n = held->second;
+    return ROPE_OK;
   }
-  *n = held;
+  int b = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fn, threads, 0);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  *n = b < 1 ? 1 : b;
+  try {
+    g_resident.emplace(key, *n);
+  } catch (...) {  // no memory: asked for again by the next call
+  }
   return ROPE_OK;
 }
 

@@ -6,7 +6,7 @@
 // stores. As kept ascends, kept[i] >= i: what a batch overwrites lies before every row
 // that a later one reads. Warps share nothing, so nothing is waited for. Bound by the
 // latency of four dependent loads (length, index, page, row): a thread that walked its
-// path by itself took 18 us for 40 rows.
+// path by itself took 18 us for 40 rows, this 5.5 (paths of 1 to 7 rows of 64 sequences 3.4).
 #pragma once
 
 #include "paged_common.cuh"

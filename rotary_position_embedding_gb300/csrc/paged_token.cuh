@@ -2,7 +2,9 @@
 // rows n * G of a (b, kvh), 16-bit T.
 //
 // Every cached byte is used once for 8 or 16 rows, so the pages' bandwidth is the
-// bound. Two warps bring units of 64 keys into a ring by TMA, box by box (a box:
+// bound: 64 single bfloat16 tokens over 1 to 8190 keys of 8 heads of 128, 167 us, 6.4
+// TB/s; 256 over up to 2000, 173 us, 6.1; 8 over up to 8190, 30 us. One token over 778 keys
+// takes 7.5 us, over 30000 29: there the start, the joining and a second launch count. Two warps bring units of 64 keys into a ring by TMA, box by box (a box:
 // the rows of a unit that lie in one page, 64 elements wide), and run ahead of the
 // four that compute, across problems too: nothing that those do between two
 // problems (queries, joining, output) leaves the memory idle while the ring is
@@ -22,10 +24,10 @@
 // rows are then done over again one by one (paged_careful_row).
 //
 // Dealing. CTA i takes the part [i W / n, (i + 1) W / n) of the problems' weight W (their
-// units, and what each costs beside) in the order of the problems (sequence, head): a problem that one CTA has whole
-// goes to the output, the others' parts to the workspace (2 slots a CTA: its first
-// segment's, its last one's), with a word on the problem that the CTA begins and
-// leaves unfinished, for paged_join_kernel_t. Without (no workspace, or more than
+// units, and what each costs beside) in the order of the problems (sequence, head): a
+// problem that one CTA has whole goes to the output, the others' parts to the workspace (2
+// slots a CTA: its first segment's, its last one's), with a word on the problem that the
+// CTA begins and leaves unfinished, for paged_join_kernel_t. Without (no workspace, or more than
 // kKvDealMost sequences) a CTA takes one problem. Few problems of caches that are not
 // long: a cluster of CTAs each, whose parts meet in shared memory, so there is one
 // launch and no workspace.
@@ -96,7 +98,7 @@ __device__ __forceinline__ bool paged_sync_or(bool x) {
 
 // What a problem weighs beside its units: queries, joining, output. Without it the CTA that
 // had the shortest sequences' problems ended 15 to 40 us behind the others: 64 sequences of
-// up to 8190 keys with 2 to 4 new tokens 204 us, 181 so; heads of 256 187 and 168.
+// up to 8190 keys with 2 to 4 new tokens 204 us, 176 so.
 template <int NB>
 constexpr int kPagedTokenOver = NB == 1 ? 3 : 5;
 
@@ -112,53 +114,50 @@ struct PagedDeal {
   }
 };
 
-// The weight before each sequence, in shared memory; all threads come here.
+// The weight before each sequence, in shared memory; all threads come here. (Sequences side
+// by side to threads side by side: 8 of them one after the other took a thread 3 us, one 1.5.)
 template <int NB>
 __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* before, int32_t* warp_sum,
                                                 PagedTimes* times) {
-  constexpr int PER = kKvDealMost / 128;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int u[PER], sum = 0, pre = 0;
+  constexpr int WARPS = kPagedTokenThreads / 32;
   PagedTimes t = {0, 0};
-  if (warp < kPagedWarps) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = tid * PER + i;
-      u[i] = 0;
-      if (b < p.s.B) {
-        const PagedSeq q = paged_seq(p.s, b);
-        if (paged_few(p, q)) u[i] = paged_span(p, q).units() + kPagedTokenOver<NB>;
-        if (p.shared) paged_time(p, q, &t);
-      }
-      sum += u[i];
+  int upto = 0;  // the weight of the sequences before b0
+  for (int b0 = 0; b0 < p.s.B; b0 += kPagedTokenThreads) {
+    const int b = b0 + tid;
+    int u = 0;
+    if (b < p.s.B) {
+      const PagedSeq q = paged_seq(p.s, b);
+      if (paged_few(p, q)) u = paged_span(p, q).units() + kPagedTokenOver<NB>;
+      if (p.shared) paged_time(p, q, &t);
     }
-    pre = sum;
+    int pre = u;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int x = __shfl_up_sync(0xffffffffu, pre, o);
       if (lane >= o) pre += x;
     }
     if (lane == 31) warp_sum[warp] = pre;
-    if (p.shared) {
-      if (t.tile) atomicAdd(&times->tile, t.tile);
-      if (t.token) atomicAdd(&times->token, t.token);
-    }
-  }
-  __syncthreads();
-  if (warp < kPagedWarps) {
-    int at = pre - sum;
-    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    __syncthreads();
+    int at = upto + pre - u;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (tid * PER + i <= p.s.B) before[tid * PER + i] = at;
-      at += u[i];
+    for (int w = 0; w < WARPS; ++w) {
+      const int x = warp_sum[w];
+      if (w < warp) at += x;
+      upto += x;
     }
-    if (tid == 127 && p.s.B == kKvDealMost) before[p.s.B] = at;
+    if (b < p.s.B) before[b] = at;
+    __syncthreads();  // the sums have been read
+  }
+  if (tid == 0) before[p.s.B] = upto;
+  if (p.shared) {
+    if (t.tile) atomicAdd(&times->tile, t.tile);
+    if (t.token) atomicAdd(&times->token, t.token);
   }
   __syncthreads();
   PagedDeal d;
   d.before = before;
-  d.total = before[p.s.B] * p.Nkv;
+  d.total = upto * p.Nkv;
   d.ctas = p.deal;
   if (p.shared) {  // those of the SMs that the other kernel leaves
     d.ctas = p.deal * (152 - paged_shares(*times)) / 152;
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   constexpr int KB = HD / 16;  // 16-dim blocks
   extern __shared__ uint8_t paged_smem[];
   __shared__ float s_m[kPagedWarps][NB * 8], s_l[kPagedWarps][NB * 8];
-  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kPagedWarps];
+  __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kPagedTokenThreads / 32];
   __shared__ float2 s_part[NB * 8];
   __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
   __shared__ PagedTimes s_times;
@@ -647,14 +646,84 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   if (p.shared && blockIdx.x == 0) pdl_wait();  // this kernel does not end before the other
 }
 
+// Loads that stay where they stand, ahead of what decides whether they count. Each value
+// is read once, so L1 is passed by.
+__device__ __forceinline__ float4 paged_load4(const float4* at) {
+  float4 x;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 paged_load2(const float2* at) {
+  float2 x;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(at) : "memory");
+  return x;
+}
+
+// A lane's dims (4 lane + 128 j) of row r from the parts n0, n0 + dn, .. of a problem: its
+// last segment's in CTA c0 (slot `last`), the first segments' of the CTAs behind. The loads of
+// 8 parts are in flight together, what they count beside them.
+__device__ __forceinline__ void paged_join_row(const PagedParams& p, int c0, int last, int parts, int n0, int dn, int r,
+                                               int lane, float* M, float* L, float4 (&acc)[kKvMaxHead / 128]) {
+  constexpr int NV = kKvMaxHead / 128, DEEP = 8;
+  float top = -CUDART_INF_F, sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int n1 = n0; n1 < parts; n1 += DEEP * dn) {
+    float2 ml[DEEP];
+    float4 o[DEEP][NV];
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) {
+      const int n = n1 + k * dn;
+      ml[k] = make_float2(-CUDART_INF_F, 0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) o[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (n < parts) {
+        const int at = (2 * (c0 + n) + (n == 0 ? last : 0)) * p.rt + r;
+        ml[k] = paged_load2(p.ws_ml + at);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (lane * 4 + 128 * j < p.H)
+            o[k][j] = paged_load4(reinterpret_cast<const float4*>(p.ws_o + at * p.H) + lane + 32 * j);
+      }
+    }
+    float m = top;
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) m = fmaxf(m, ml[k].x);
+    const float base = m == -CUDART_INF_F ? 0.0f : m, a = exp2f(top - base);
+    top = m;
+    sum *= a;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) acc[j].x *= a, acc[j].y *= a, acc[j].z *= a, acc[j].w *= a;
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) {
+      const float f = exp2f(ml[k].x - base);
+      sum = fmaf(ml[k].y, f, sum);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        // a CTA that had no units wrote nothing
+        if (ml[k].x == -CUDART_INF_F && ml[k].y == 0.0f) o[k][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        acc[j].x = fmaf(o[k][j].x, f, acc[j].x);
+        acc[j].y = fmaf(o[k][j].y, f, acc[j].y);
+        acc[j].z = fmaf(o[k][j].z, f, acc[j].z);
+        acc[j].w = fmaf(o[k][j].w, f, acc[j].w);
+      }
+    }
+  }
+  *M = top;
+  *L = sum;
+}
+
 // Joins the parts of the problems that paged_token_kernel_t dealt to several CTAs.
 // CTA (x, y): the problem that begins in CTA x there and goes on in others, if there
-// is one; its rows y, y + gridDim.y, ..; with more than 8 parts the four warps share
-// a row, else each takes rows of its own.
+// is one; its rows y, y + gridDim.y, ... Each warp takes rows of its own, or, where a
+// problem has more than 8 parts and each row a CTA, all four share it (8 sequences of up to
+// 8190 keys, 10 parts: all sharing one row after the other 38 us for the call, 30 so).
 template <class T>
 __global__ void __launch_bounds__(kKvTokenThreads) paged_join_kernel_t(const PagedParams p) {
   using bits = typename Elem<T>::bits;
-  __shared__ float s_o[kTokWarps][kKvMaxHead], s_l[kTokWarps];
+  constexpr int NV = kKvMaxHead / 128;
+  __shared__ float4 s_o[kTokWarps][kKvMaxHead / 4];
+  __shared__ float s_l[kTokWarps], s_m[kTokWarps];
   // It lets nothing start early: the next call's CTAs would take places unevenly. Behind
   // paged_tile_join_kernel_t, which begins after all parts are there, that one's end is
   // waited for at this one's.
@@ -665,67 +734,56 @@ __global__ void __launch_bounds__(kKvTokenThreads) paged_join_kernel_t(const Pag
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 what = p.ws_join[blockIdx.x];  // b, kvh, -, 2 * further CTAs + slot
   if (what.w < 2) return;
-  const int b = what.x, kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x;
-  // Part 0 is the last segment of CTA c0, the others the first segments of theirs.
-  const bool shared_row = parts > 8;
+  const int b = what.x, kvh = what.y, parts = (what.w >> 1) + 1, c0 = blockIdx.x, last = what.w & 1;
+  const bool shared_row = parts > 8 && gridDim.y > 1;
   const PagedSeq seq = paged_seq(p.s, b);
   const int rows = seq.n * p.G;
   const int dr = shared_row ? gridDim.y : gridDim.y * kTokWarps;
-  const int n0 = shared_row ? warp : 0, dn = shared_row ? kTokWarps : 1;
-  auto slot_of = [&](int n) -> int64_t { return 2 * (int64_t)(c0 + n) + (n == 0 ? what.w & 1 : 0); };
   for (int r = shared_row ? (int)blockIdx.y : (int)blockIdx.y * kTokWarps + warp; r < rows; r += dr) {
-    float M = -CUDART_INF_F;
-    for (int n = lane; n < parts; n += 32) M = fmaxf(M, p.ws_ml[slot_of(n) * p.rt + r].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -CUDART_INF_F ? 0.0f : M;
-    float L = 0.0f, acc[kKvMaxHead / 32];
-#pragma unroll
-    for (int j = 0; j < kKvMaxHead / 32; ++j) acc[j] = 0.0f;
-#pragma unroll 8
-    for (int n = n0; n < parts; n += dn) {
-      const int64_t s = slot_of(n);
-      const float2 ml = p.ws_ml[s * p.rt + r];
-      const float* o = p.ws_o + (s * p.rt + r) * p.H;
-      const float f = exp2f(ml.x - base);
-      L = fmaf(ml.y, f, L);
-#pragma unroll
-      for (int j = 0; j < kKvMaxHead / 128; ++j)
-        if (lane * 4 + 128 * j < p.H) {
-          float4 x = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * j);
-          if (ml.x == -CUDART_INF_F && ml.y == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // never written where a CTA had no units
-          acc[4 * j] = fmaf(x.x, f, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(x.y, f, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(x.z, f, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(x.w, f, acc[4 * j + 3]);
-        }
-    }
-    const int tok = kv_div(r, p.by_g);
-    bits* y = static_cast<bits*>(p.out) + ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+    float M, L;
+    float4 acc[NV];
+    paged_join_row(p, c0, last, parts, shared_row ? warp : 0, shared_row ? kTokWarps : 1, r, lane, &M, &L, acc);
     if (shared_row) {
       __syncthreads();  // the previous row's sums have been read
 #pragma unroll
-      for (int j = 0; j < kKvMaxHead / 128; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane * 4 + 128 * j < p.H) s_o[warp][lane * 4 + 128 * j + i] = acc[4 * j + i];
-      if (lane == 0) s_l[warp] = L;
+      for (int j = 0; j < NV; ++j) s_o[warp][lane + 32 * j] = acc[j];
+      if (lane == 0) s_m[warp] = M, s_l[warp] = L;
       __syncthreads();
-      L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      for (int d = threadIdx.x; d < p.H; d += kKvTokenThreads)
-        y[d] = Elem<T>::fromf(((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) * inv);
-    } else {
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      if (warp > 0) continue;
+      float top = s_m[0];
 #pragma unroll
-      for (int j = 0; j < kKvMaxHead / 128; ++j)
-        if (lane * 4 + 128 * j < p.H) {
-          VecT<T, 4> v;
+      for (int w = 1; w < kTokWarps; ++w) top = fmaxf(top, s_m[w]);
+      const float base = top == -CUDART_INF_F ? 0.0f : top;
+      L = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v.v[i] = Elem<T>::fromf(acc[4 * j + i] * inv);
-          *reinterpret_cast<VecT<T, 4>*>(y + lane * 4 + 128 * j) = v;
+      for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        const float f = exp2f(s_m[w] - base);
+        L = fmaf(s_l[w], f, L);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const float4 x = s_o[w][lane + 32 * j];
+          acc[j].x = fmaf(x.x, f, acc[j].x);
+          acc[j].y = fmaf(x.y, f, acc[j].y);
+          acc[j].z = fmaf(x.z, f, acc[j].z);
+          acc[j].w = fmaf(x.w, f, acc[j].w);
         }
+      }
     }
+    const int tok = kv_div(r, p.by_g);
+    bits* y = static_cast<bits*>(p.out) + ((seq.t0 + tok) * p.Nq + (int64_t)kvh * p.G + (r - tok * p.G)) * p.H;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane * 4 + 128 * j < p.H) {
+        VecT<T, 4> v;
+        v.v[0] = Elem<T>::fromf(acc[j].x * inv);
+        v.v[1] = Elem<T>::fromf(acc[j].y * inv);
+        v.v[2] = Elem<T>::fromf(acc[j].z * inv);
+        v.v[3] = Elem<T>::fromf(acc[j].w * inv);
+        *reinterpret_cast<VecT<T, 4>*>(y + lane * 4 + 128 * j) = v;
+      }
   }
 }
 
