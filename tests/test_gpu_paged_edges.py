@@ -223,11 +223,12 @@ def test_two_calls_at_a_time(lib, cuda):
             assert torch.equal(x, y)
 
 
-def test_the_next_kernel_sees_what_was_written(lib, cuda):
+@pytest.mark.parametrize("dtype,variant", [("f16", "auto"), ("f16", "simt"), ("f32", "auto")])
+def test_the_next_kernel_sees_what_was_written(lib, cuda, dtype, variant):
     """Append, attention, keep and append again with nothing between them: what each writes is there for the next,
     although each kernel starts before the one in front of it ends."""
     Nq, Nkv, H, ps, B = 8, 2, 128, 16, 40
-    b = _append_case(40, "f16", Nq, Nkv, H, ps, [11 * i % 300 for i in range(B)], [1] * (B - 1) + [200])
+    b = _append_case(40, dtype, Nq, Nkv, H, ps, [11 * i % 300 for i in range(B)], [1] * (B - 1) + [200])
     starts, past, table = (_i32(b[n], cuda) for n in ("starts", "past", "table"))
     q, cos, sin = (b[n].to(cuda) for n in ("q", "cos", "sin"))
     kept, lens = _i32([[0]] * (B - 1) + [[5]], cuda), _i32([1] * B, cuda)
@@ -247,10 +248,11 @@ def test_the_next_kernel_sees_what_was_written(lib, cuda):
             wait()
         return [*outs, k, v]
 
-    want = step(torch.cuda.synchronize)
-    for _ in range(5):
-        for x, y in zip(step(lambda: None), want):
-            assert torch.equal(x, y)
+    with lib.variant(variant):
+        want = step(torch.cuda.synchronize)
+        for _ in range(5):
+            for x, y in zip(step(lambda: None), want):
+                assert torch.equal(x, y)
 
 
 def test_append_kernels(lib, cuda):
@@ -259,3 +261,11 @@ def test_append_kernels(lib, cuda):
         a = _append_case(41, "bf16", *shape)
         _append(lib, a, cuda, a["k"].to(cuda), a["v"].to(cuda))
         assert lib.last_kernel() == kernel
+
+
+@pytest.mark.parametrize("H", [8, 16, 24, 40, 56, 104, 136, 200, 248])
+def test_head_sizes(lib, cuda, H):
+    """Multiples of 8 run padded on the tensor cores."""
+    for new, kernel in (([1, 2, 1], "token"), ([70, 1, 30], "tile")):
+        _check(lib, _make(H, "f16", 6, 3, H, 32, [150, 77, 40], new), cuda, f"{H} {new}")
+        assert lib.last_kernel() == f"paged_{kernel}_kernel"
