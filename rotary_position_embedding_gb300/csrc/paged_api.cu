@@ -2,6 +2,8 @@
 // kv_attention_paged and kv_keep_paged (include/rope.h). Argument checks, choice of
 // kernel, launch geometry. Nothing is allocated or kept, nothing waits, and every
 // check comes before any CUDA call.
+#include <algorithm>
+
 #include "kv_host.h"
 #include "paged_internal.h"
 #include "paged_maps.h"
@@ -349,7 +351,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
   PagedParams tile_p = p;
   const void* tile_join = nullptr;
   auto join_tiles = [&]() -> rope_status {
-    if (!tile_p.deal) return ROPE_OK;
+    if (!tile_p.deal || tile_p.entire) return ROPE_OK;
     int tr = kv_tile_rows(head_size);
     void* jargs[] = {&tile_p, &tr};
     return launch(tile_join, dim3(kSms * kPagedJoinCtas), kPagedJoinThreads, 0, stream, jargs,
@@ -360,7 +362,18 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     const int kind = softcap > 0.0f || !(scale > 0.0f) ? kKvAnyScore : alibi_slopes ? kKvBiased : kKvPlain;
     const PagedTileKernel k =
         dtype == ROPE_F16 ? paged_tile_kernel_f16((int)head_size, kind) : paged_tile_kernel_bf16((int)head_size, kind);
-    deal_of(pl, kv_tile_rows(head_size), 0);
+    // Ranges that end at whole items differ by the longest item at most. Where that weighs
+    // little more than joining is worth nothing is ever split: no workspace, and one launch
+    // less (5 prompts that see 512 keys 36.9 -> 34.8 us, 7 trees over up to 300 keys 17.6 ->
+    // 15.9; with 5 more in place of 3 no more gained).
+    const int64_t keys = kv_tile_keys(head_size);
+    int64_t units = (rows + keys - 1) / keys;
+    if (window > 0 && window <= kMaxLen) units = std::min(units, (window + p.tpi - 2) / keys + 2);
+    p.entire = pl.deal && !p.shared && units + p.over_item < p.over_join + 3;
+    if (p.entire)
+      p.deal = pl.deal;
+    else
+      deal_of(pl, kv_tile_rows(head_size), 0);
     p.items = p.deal ? (int32_t)pl.items : 0;
     void* targs[] = {&p, &tile_maps};
     KV_TRY(launch(k.fn, dim3((unsigned)(p.deal ? p.deal : pl.items * kv_num_heads)), kPagedTileBlock, k.smem, stream, targs,

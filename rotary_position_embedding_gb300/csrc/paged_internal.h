@@ -46,6 +46,7 @@ struct PagedParams {
   int32_t rt;              // and rows of a part in the workspace (8 or 16)
   int32_t tpi, items;      // paged_tile_kernel: tokens of an item; items of the batch, at most
   int32_t over_item, over_join;  // what an item weighs beside its key tiles, what joining parts is worth
+  int32_t entire;          // paged_tile_kernel: no item is split, whatever the lengths; no workspace
   int32_t shared;          // both kernels run at a time, each on its share of the SMs (see paged_shares)
   int32_t vec;             // 16-byte loads of Q, K and V are aligned
   KvDiv by_g;
@@ -73,7 +74,8 @@ PagedTokenKernel paged_token_kernel(int dtype, int H, bool few);
 
 // Any number of rows, the same types, G up to kv_tile_rows(H): items of PagedParams.tpi
 // tokens; the launch takes (PagedParams, PagedTileMaps), grid (deal), and is followed by
-// join with (PagedParams, kv_tile_rows(H)), grid (kPagedJoinCtas an SM); or, with more
+// join with (PagedParams, kv_tile_rows(H)), grid (kPagedJoinCtas an SM), unless
+// PagedParams.entire; or, with more
 // than kPagedItems items or no workspace, grid (items * Nkv).
 struct PagedTileKernel {
   const void* fn;

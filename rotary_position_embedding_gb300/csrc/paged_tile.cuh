@@ -31,7 +31,7 @@
 // 1476 Tflop/s); caps by the tanh between the products (2.5 us a key tile for 1.57); short
 // calls by what comes before the first product (6.5 us: lengths, items, table, K) and by
 // joining (one tree of 60 drafts behind 8000 keys 22 us, 32 trees over up to 4096 keys 79;
-// 5 prompts of 100 to 1531 tokens that see 512 keys 37).
+// 5 prompts of 100 to 1531 tokens that see 512 keys 35).
 //
 // Without a workspace, or with more than kPagedItems items, a CTA takes one item.
 #pragma once
@@ -366,15 +366,15 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
     s_ends[cta] = paged_nearest(p, (int)shares.first((uint32_t)cta), before, count);
     __syncthreads();
     const int load = s_ends[cta < (int)ctas ? cta + 1 : cta] - s_ends[cta];
-    const bool split = __syncthreads_or(load > (int)shares.per + p.over_join);
+    const bool split = __syncthreads_or(load > (int)shares.per + p.over_join) && !p.entire;
     if (blockIdx.x < ctas) {
       work.at = split ? (int)shares.first(blockIdx.x) : s_ends[blockIdx.x];
       work.last = split ? (int)shares.first(blockIdx.x + 1) : s_ends[blockIdx.x + 1];
     }
     // so far nothing begins here that goes on elsewhere, and nothing of this CTA's counts
     // where an item's CTAs lie on both sides of it
-    if (tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (work.at >= work.last && tid < ROWS) p.ws_ml[2 * (int64_t)blockIdx.x * ROWS + tid] = make_float2(-CUDART_INF_F, 0.0f);
+    if (!p.entire && tid == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!p.entire && work.at >= work.last && tid < ROWS) p.ws_ml[2 * (int64_t)blockIdx.x * ROWS + tid] = make_float2(-CUDART_INF_F, 0.0f);
   } else if (count > 0) {
     work.last = paged_item_tiles(items[0], N);
   }

@@ -269,3 +269,16 @@ def test_head_sizes(lib, cuda, H):
     for new, kernel in (([1, 2, 1], "token"), ([70, 1, 30], "tile")):
         _check(lib, _make(H, "f16", 6, 3, H, 32, [150, 77, 40], new), cuda, f"{H} {new}")
         assert lib.last_kernel() == f"paged_{kernel}_kernel"
+
+
+@pytest.mark.parametrize("width,window,cap", [(32, 0, 0.0), (34, 0, 0.0), (44, 0, 0.0), (46, 0, 0.0), (60, 0, 0.0), (200, 300, 0.0),
+                                              (200, 700, 0.0), (20, 0, 30.0), (32, 0, 30.0)])
+def test_split_or_not(lib, cuda, width, window, cap):
+    """On both sides of the table widths and windows up to which no item is split, with a workspace and without."""
+    a = _make(width + window, "f16", 4, 4, 64, 16, [150, 0, 200, 3, 190], [300, 17, 90, 1, 120], cap=cap, window=window)
+    for row in a["table"]:
+        row += [-3] * (width - len(row))
+    want = _check(lib, a, cuda, "planned")
+    none = torch.zeros(0, dtype=torch.uint8, device=cuda)
+    _check(lib, a, cuda, "none", workspace=none)
+    assert torch.equal(_call(lib, a, cuda), want)
