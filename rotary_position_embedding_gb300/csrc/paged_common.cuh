@@ -137,10 +137,25 @@ __device__ __forceinline__ void paged_time(const PagedParams& p, const PagedSeq&
     t->tile += (unsigned long long)(items * (span / keys + 1 + p.over_item)) * (unsigned)(p.cap > 0.0f ? step + 900 : step);
   }
 }
-__device__ __forceinline__ int paged_shares(const PagedTimes& t) {
-  const unsigned long long all = t.tile + t.token;
-  if (t.tile == 0 || all == 0) return 0;
-  int n = (int)(152.0 * ((double)t.tile / (double)all) + 0.5);
+// The times of a warp's threads, added up, to the warp's own place; paged_shares adds up
+// those of all warps. (96 threads' atomics on one place and a quotient of doubles took both
+// kernels 6 us.)
+__device__ __forceinline__ void paged_times(PagedTimes t, PagedTimes* of_warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t.tile += __shfl_xor_sync(0xffffffffu, t.tile, o);
+    t.token += __shfl_xor_sync(0xffffffffu, t.token, o);
+  }
+  if ((threadIdx.x & 31) == 0) *of_warp = t;
+}
+template <int WARPS>
+__device__ __forceinline__ int paged_shares(const PagedTimes* of_warp) {
+  PagedTimes t = {0, 0};
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) t.tile += of_warp[w].tile, t.token += of_warp[w].token;
+  const unsigned long long all = t.tile + t.token;  // below 2^50
+  if (t.tile == 0) return 0;
+  int n = (int)((2 * 152 * t.tile + all) / (2 * all));
   if (n < 1) n = 1;
   return t.token > 0 && n > 151 ? 151 : n > 152 ? 152 : n;
 }

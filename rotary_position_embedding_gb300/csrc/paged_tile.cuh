@@ -127,14 +127,11 @@ __device__ __forceinline__ int paged_items(const PagedParams& p, int only, int k
     count += all;
     if (p.deal == 0 && only < count) break;  // the same for all threads
   }
-  if (p.shared) {
-    if (t_all.tile) atomicAdd(&times->tile, t_all.tile);
-    if (t_all.token) atomicAdd(&times->token, t_all.token);
-  }
+  if (p.shared) paged_times(t_all, times + (tid >> 5));
   __syncthreads();
   *ctas = (uint32_t)p.deal;
   if (p.shared) {
-    const uint32_t n = (uint32_t)paged_shares(*times);
+    const uint32_t n = (uint32_t)paged_shares<kPagedTileThreads / 32>(times);
     *ctas = n < 1 ? 1 : n < *ctas ? n : *ctas;
     if (blockIdx.x >= *ctas) return 0;
   }
@@ -271,6 +268,31 @@ __device__ __forceinline__ void paged_turn(uint4 (&v)[8], int lane) {
   }
 }
 
+// tile_cap where tile_small holds: the polynomial alone, as tile_weights forms it. (Every
+// item has a tile or two with hidden keys, and all of tile_cap's tanh made them 9 us for 3.)
+template <int N>
+__device__ __forceinline__ void paged_cap_small(uint32_t ts, const TileRow& r) {
+  const float mult = r.mult * (0.5f / kLog2e), u = mult * mult, v = r.cap2 * mult;
+  const float2 k0 = make_float2(v, v), k1 = make_float2(v * u * kTanh1, v * u * kTanh1);
+  const float2 k2 = make_float2(v * u * u * kTanh2, v * u * u * kTanh2);
+  const float2 k3 = make_float2(v * u * u * u * kTanh3, v * u * u * u * kTanh3);
+#pragma unroll 1
+  for (int q = 0; q < N; q += 32) {
+    uint32_t c[32];
+    tc_ld32(c, ts + q);
+    tc_wait_ld32(c);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      float2 y = make_float2(__uint_as_float(c[k]), __uint_as_float(c[k + 1]));
+      const float2 z = __fmul2_rn(y, y);
+      y = __fmul2_rn(y, __ffma2_rn(z, __ffma2_rn(z, __ffma2_rn(z, k3, k2), k1), k0));
+      c[k] = __float_as_uint(y.x), c[k + 1] = __float_as_uint(y.y);
+    }
+    tc_st32(ts + q, c);
+  }
+  tc_wait_st();
+}
+
 // Scores of the tile at j0 that the row does not see become -inf.
 template <int N>
 __device__ __forceinline__ void paged_hide(float (&x)[N], int j0, int from, int lim, bool masks, int past, uint64_t word) {
@@ -300,7 +322,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   __shared__ PagedTileBars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_sum[kPagedTileThreads / 32];
-  __shared__ PagedTimes s_times;
+  __shared__ PagedTimes s_times[kPagedTileThreads / 32];
   __shared__ int s_ends[kPagedTileCtas + 1];
   uint8_t* base = kv_tiles + ((1024 - (kv_smem(kv_tiles) & 1023)) & 1023);
   const uint32_t sq = kv_smem(base), sk = sq + C::kQ, sv = sk + 2 * C::kStage;
@@ -310,7 +332,6 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
   auto bar = [&](uint64_t* b) { return kv_smem(b); };
 
   if (tid == 0) {
-    s_times.tile = s_times.token = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(&bars.k_full[i]), 1);
       mbar_init(bar(&bars.v_full[i]), 1);
@@ -346,7 +367,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
 
   tc_before();
   uint32_t ctas;  // that the work is dealt to
-  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), N, items, before, s_sum, &s_times, &ctas);
+  const int count = paged_items(p, (int)(blockIdx.x / (uint32_t)p.Nkv), N, items, before, s_sum, s_times, &ctas);
   tc_after();
   const uint32_t tmem = s_tmem;
   if (p.shared && blockIdx.x >= ctas) {  // an SM of the other kernel's
@@ -451,9 +472,13 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
         float x[N];
         tile_load<false, N>(x, ts, tr, true);
         bool done = general;  // x holds scores in log2, not raw ones
-        if (capped && (general || masked || !tile_small(x, tr))) {
+        const bool small = capped && tile_small(x, tr);
+        if (capped && (general || masked || !small)) {
           // (an infinite product is at an end of the cap from here on: -inf means hidden)
-          tile_cap<false, N>(ts, tr);
+          if (small)
+            paged_cap_small<N>(ts, tr);
+          else
+            tile_cap<false, N>(ts, tr);
           tile_load<false, N>(x, ts, tr, false);
           done = true;
         }

@@ -150,17 +150,14 @@ __device__ __forceinline__ PagedDeal paged_deal(const PagedParams& p, int32_t* b
     __syncthreads();  // the sums have been read
   }
   if (tid == 0) before[p.s.B] = upto;
-  if (p.shared) {
-    if (t.tile) atomicAdd(&times->tile, t.tile);
-    if (t.token) atomicAdd(&times->token, t.token);
-  }
+  if (p.shared) paged_times(t, times + warp);
   __syncthreads();
   PagedDeal d;
   d.before = before;
   d.total = upto * p.Nkv;
   d.ctas = p.deal;
   if (p.shared) {  // those of the SMs that the other kernel leaves
-    d.ctas = p.deal * (152 - paged_shares(*times)) / 152;
+    d.ctas = p.deal * (152 - paged_shares<WARPS>(times)) / 152;
     if (d.ctas < 1) d.ctas = 1;
   }
   return d;
@@ -232,13 +229,12 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   __shared__ int32_t s_before[kKvDealMost + 1], s_sum[kPagedTokenThreads / 32];
   __shared__ float2 s_part[NB * 8];
   __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];
-  __shared__ PagedTimes s_times;
+  __shared__ PagedTimes s_times[kPagedTokenThreads / 32];
   const uint32_t ring = (kv_smem(paged_smem) + 1023u) & ~1023u;
   float* const merge = reinterpret_cast<float*>(paged_smem + (ring - kv_smem(paged_smem)) + C::kRing);
   float* const part_smem = merge + C::kMerge / 4;  // in clusters
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    s_times.tile = s_times.token = 0;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(kv_smem(&s_full[i]), 2);
       mbar_init(kv_smem(&s_empty[i]), kPagedWarps);
@@ -262,7 +258,7 @@ __global__ void __launch_bounds__(kPagedTokenThreads, PagedTokenCfg<HD, NB>::kCt
   PagedWork<NB> work;
   work.at = work.last = 0;
   if (p.deal > 0) {
-    deal = paged_deal<NB>(p, s_before, s_sum, &s_times);
+    deal = paged_deal<NB>(p, s_before, s_sum, s_times);
     if (deal.total > 0) {
       work.at = deal.first(blockIdx.x);
       work.last = deal.first(blockIdx.x + 1);
