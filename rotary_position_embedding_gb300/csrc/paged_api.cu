@@ -288,8 +288,8 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
     memset(&tile_maps, 0, sizeof(tile_maps));
     const bool bf = dtype == ROPE_BF16;
     p.tpi = kv_tile_rows(head_size) / p.G;
-    // in key tiles, which take 1.6 us, capped 2.4 (and hidden keys of capped tiles 2 more):
-    // an item 4.5 to 6.5 us, joining 8 to 13 us where every SM has parts
+    // in key tiles, which take 1.1 to 1.6 us, capped 2.1 to 2.5: an item (Q, output, a tile
+    // or two with hidden keys) 4 to 6 us, joining 8 to 13 us where every SM has parts
     p.over_item = softcap > 0.0f ? 4 : 3;
     p.over_join = softcap > 0.0f ? 5 : 8;
     tile_maps.k = maps.k;

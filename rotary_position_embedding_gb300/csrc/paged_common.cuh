@@ -119,22 +119,24 @@ __device__ __forceinline__ bool paged_few(const PagedParams& p, const PagedSeq& 
 // paged_tile_kernel_t and paged_token_kernel_t run at a time, the first on `n` SMs, the
 // second on the others: about 100 of them take what the memory gives (62 GB/s an SM).
 // Both work n out of the lengths in whole numbers, each sequence's time (ns of an SM)
-// added up in any order. A mixed step of a capped prompt of 2048 tokens and 95 single
-// tokens over up to 4000 keys: one after the other 255 us, so 191.
+// added up in any order. The weights are what divided mixed batches best (12 of them, heads
+// of 64 to 256, capped or not; 4 ns a dim in place of 104 + 2.8 a dim: 4 to 8 % slower where
+// scores are not capped, the same where they are). A mixed step of a capped prompt of 2048 tokens and 95 single
+// tokens over up to 4000 keys: one after the other 255 us, so 175.
 struct PagedTimes {
   unsigned long long tile, token;
 };
 __device__ __forceinline__ void paged_time(const PagedParams& p, const PagedSeq& q, PagedTimes* t) {
   if (q.n == 0) return;
   if (paged_few(p, q)) {
-    t->token += (unsigned long long)paged_span(p, q).units() * (unsigned)p.H * 4u;
+    t->token += (unsigned long long)paged_span(p, q).units() * (104u + (unsigned)p.H * 28u / 10u);
   } else {
     const int keys = p.H <= 128 ? 128 : 64, step = p.H <= 64 ? 1400 : p.H <= 128 ? 1600 : 1000;
     int64_t span = (int64_t)q.past + q.n / 2;
     if (p.window > 0 && span > p.window + p.tpi) span = p.window + p.tpi;
     if (span < 0) span = 0;
     const int64_t items = (q.n + p.tpi - 1) / p.tpi;
-    t->tile += (unsigned long long)(items * (span / keys + 1 + p.over_item)) * (unsigned)(p.cap > 0.0f ? step + 900 : step);
+    t->tile += (unsigned long long)(items * (span / keys + 1 + p.over_item)) * (unsigned)(p.cap > 0.0f ? step + 650 : step);
   }
 }
 // The times of a warp's threads, added up, to the warp's own place; paged_shares adds up
