@@ -31,8 +31,7 @@ __global__ void __launch_bounds__(kPagedAppendThreads) paged_append_kernel_t(con
     const int hd = role == 0 ? n : role == 1 ? n - p.Nq : n - p.Nq - p.Nkv;
     int b;
     if (!paged_find(p.s, tok, &b)) continue;  // the same for the group
-    const int64_t s = tok - (p.s.starts ? (int64_t)__ldg(p.s.starts + b) : (int64_t)b * p.s.S);
-    const int64_t row = (int64_t)__ldg(p.s.past + b) + s;
+    const int64_t row = (int64_t)__ldg(p.s.past + b) + paged_nth(p.s, b, tok);
     const bits* x = p.packed ? static_cast<const bits*>(p.q) + (tok * N + n) * H
                              : static_cast<const bits*>(role == 0 ? p.q : role == 1 ? p.k : p.v) +
                                    (tok * (role == 0 ? p.Nq : p.Nkv) + hd) * H;

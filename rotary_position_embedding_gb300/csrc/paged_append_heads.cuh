@@ -126,8 +126,7 @@ __global__ void __maxnreg__(NORM ? 80 : 64) paged_append_heads_kernel_t(const Pa
     }
     int b;
     if (!paged_find(p.s, tok, &b)) continue;  // the same for a token's threads
-    const int64_t row =
-        (int64_t)__ldg(p.s.past + b) + (tok - (p.s.starts ? (int64_t)__ldg(p.s.starts + b) : (int64_t)b * p.s.S));
+    const int64_t row = (int64_t)__ldg(p.s.past + b) + paged_nth(p.s, b, tok);
     bool valid = false;
     RT c = zero, sn = zero;
     if (rotates) {

@@ -21,9 +21,8 @@ struct PagedSeq {
   int total;       // rows that exist, within [0, rows]
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b) {
-  PagedSeq q;
-  int64_t a, e;
+// The tokens [a, e) of sequence b: starts count as clipped to [0, T].
+__device__ __forceinline__ void paged_tokens(const PagedBatch& s, int b, int64_t& a, int64_t& e) {
   if (s.starts) {
     a = __ldg(s.starts + b);
     e = __ldg(s.starts + b + 1);
@@ -33,6 +32,12 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b) {
     a = s.S * b;
     e = a + s.S;
   }
+}
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b) {
+  PagedSeq q;
+  int64_t a, e;
+  paged_tokens(s, b, a, e);
   q.t0 = a;
   q.n = e - a > s.most ? 0 : (int)(e - a);
   int p = __ldg(s.past + b);
@@ -46,8 +51,9 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b) {
 // Once for each sequence: rows outside its page table, or more tokens than allowed.
 __device__ __forceinline__ void paged_flag_seq(const PagedBatch& s, int b, const PagedSeq& q) {
   if (!s.status) return;
-  const int64_t n = s.starts ? (int64_t)__ldg(s.starts + b + 1) - __ldg(s.starts + b) : s.S;
-  if (n > s.most || (q.n > 0 && (q.past < 0 || (int64_t)q.past + q.n > s.rows))) atomicOr(s.status, 4);
+  int64_t a, e;
+  paged_tokens(s, b, a, e);
+  if (e - a > s.most || (q.n > 0 && (q.past < 0 || (int64_t)q.past + q.n > s.rows))) atomicOr(s.status, 4);
 }
 
 // The page of row j, 0 <= j < rows, or -1.
@@ -84,6 +90,13 @@ __device__ __forceinline__ bool paged_find(const PagedBatch& s, int64_t t, int* 
   }
   *b = x;
   return __ldg(s.starts + x) <= t && t < __ldg(s.starts + x + 1);
+}
+
+// Which of sequence b's tokens `t` is, one of them: attention counts from the clipped start too.
+__device__ __forceinline__ int64_t paged_nth(const PagedBatch& s, int b, int64_t t) {
+  if (!s.starts) return t - s.S * b;
+  const int64_t a = __ldg(s.starts + b);
+  return t - (a < 0 ? 0 : a);
 }
 
 // Keys that the token at row i can see lie in [first, limit).

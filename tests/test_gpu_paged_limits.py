@@ -1,0 +1,55 @@
+"""The paged-cache operators where what a call allows ends: starts outside the tokens, rows below 0, bounds above the
+tokens, queries of nobody, pages of one tensor, heads that no other operator takes."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_util as pu
+from test_gpu_paged import MASKS, T, _append, _append_case, _call, _check, _i32, _keep, _make, _want
+from test_gpu_paged_edges import _tokens, _unaligned
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------
+# query_starts outside [0, tokens]: they count as clipped, for the append as for attention
+# --------------------------------------------------------------------------
+
+RAW, CLIPPED = [-3, 5, 5, 60], [0, 5, 5, 38]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H,norm", [(64, False), (64, True), (38, False), (38, True)])
+def test_append_clips_starts(lib, cuda, dtype, H, norm):
+    """Both append kernels (heads of 38 are the unaligned one's): rows, rotation and status of the clipped starts."""
+    a = _append_case(80, dtype, 8, 2, H, 16, [7, 3, 20], [5, 0, 33], norm=norm)
+    results = []
+    for starts in (CLIPPED, RAW):
+        k, v, status = a["k"].to(cuda), a["v"].to(cuda), torch.zeros(1, dtype=torch.int32, device=cuda)
+        q = _append(lib, dict(a, starts=starts), cuda, k, v, status=status)
+        results.append((q, k, v))
+        assert int(status) == 0, starts
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("new", [[5, 0, 33], [5, 0, 4], [40, 0, 50]])
+def test_append_and_attention_clip_alike(lib, cuda, dtype, new):
+    """What attention pairs with a token is what the append stored for it, and no sequence is flagged as too long."""
+    Nq, Nkv, H, ps, past = 8, 2, 64, 16, [7, 3, 20]
+    a = _append_case(81, dtype, Nq, Nkv, H, ps, past, new)
+    tokens, most = sum(new), max(new)
+    starts = [-3, new[0], new[0], tokens + 9]
+    k, v = a["k"].to(cuda), a["v"].to(cuda)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    q = _append(lib, dict(a, starts=starts), cuda, k, v, status=status)
+    b = dict(Nq=Nq, q=q, k=k, v=v, table=a["table"], past=past, starts=starts, cap=0.0, window=0, slopes=None, masks=None, most=most)
+    got = _call(lib, b, cuda, status=status)
+    assert int(status) == 0
+    k2, v2 = a["k"].to(cuda), a["v"].to(cuda)
+    q2 = _append(lib, a, cuda, k2, v2)
+    want, bound, owned = _want(dict(b, q=q2, k=k2, v=v2, starts=a["starts"]), cuda)
+    assert owned.all()
+    pu.close(got, want, bound)
