@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
       const int tok = kv_div(live ? tid : nrows - 1, p.by_g), head = (live ? tid : nrows - 1) - tok * p.G;
       const int pos = it.pos0 + tok;
       int lim = 0;
-      if (live && pos >= 0) lim = p.masks || pos + 1 > it.total ? it.total : pos + 1;
+      if (live) lim = p.masks || pos >= it.total ? it.total : pos < 0 ? 0 : pos + 1;
       const int from = paged_first(p, pos);
       const uint64_t word = p.masks && live ? (uint64_t)__ldg(p.masks + it.g0 + tok) : ~0ull;
       // keys in [below, full) are seen by every row of the warp

@@ -53,3 +53,25 @@ def test_append_and_attention_clip_alike(lib, cuda, dtype, new):
     want, bound, owned = _want(dict(b, q=q2, k=k2, v=v2, starts=a["starts"]), cuda)
     assert owned.all()
     pu.close(got, want, bound)
+
+
+# --------------------------------------------------------------------------
+# trees whose first rows lie below 0
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new", [[1, 1], [4, 2], [16, 2], [20, 9], [64, 3]])
+@pytest.mark.parametrize("below", [-1, -3, -19, -63])
+def test_trees_below_row_zero(lib, cuda, dtype, new, below):
+    """A draft at a row below 0 sees what its word says: key j, from 0 on, if bit j - past is set."""
+    rng = np.random.default_rng(90)
+    for cap in (0.0, 5.0):
+        a = _make(91, dtype, 8, 2, 64, 16, [60, 10], new, tree=True, cap=cap)
+        a["past"] = [below, 10]
+        a["table"][0] = rng.permutation(a["k"].shape[0])[:len(a["table"][0])].tolist()
+        a["masks"] = [int(x) for x in rng.integers(-2 ** 63, 2 ** 63 - 1, sum(new))]
+        status = torch.zeros(1, dtype=torch.int32, device=cuda)
+        got = _call(lib, a, cuda, status=status)
+        want, bound, owned = _want(a, cuda)
+        assert owned.all() and int(status) == 4
+        pu.close(got, want, bound, str(cap))
