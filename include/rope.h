@@ -645,9 +645,9 @@ rope_status rope_apply_qkv_paged(rope_dtype dtype, int64_t batch, int64_t tokens
  * row does not see, and rows from total on, may hold anything, NaN included.
  *
  * query     device T (tokens, num_heads*H): q_out of rope_apply_qkv_paged.
- * max_query_len  at least the new tokens of the longest sequence, at most tokens. The
- *           kernels and their split follow from it: 1 in a decode step. A longer
- *           sequence is left out (its rows stay as they were) and sets status bit 2.
+ * max_query_len  at least the new tokens of the longest sequence; more than tokens counts
+ *           as tokens. The kernels and their split follow from it: 1 in a decode step. A
+ *           longer sequence is left out (its rows stay as they were) and sets status bit 2.
  *           Without query_starts: tokens / batch.
  * window    0, or how many keys a token sees, itself among them (above 2^30: all).
  * tree_masks    NULL or device int64 (tokens): the new tokens are drafts, in any order,
@@ -672,7 +672,8 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
                                void* workspace, int64_t workspace_bytes, rope_stream_t stream);
 
 /* Bytes of workspace with which kv_attention_paged splits the keys of such a call as
-   planned; 0 where nothing is split, -1 for sizes that it refuses. A host function: no
+   planned; 0 where nothing is split, -1 for sizes that it refuses and for a
+   max_query_len above tokens. A host function: no
    CUDA call. */
 int64_t kv_attention_paged_workspace(rope_dtype dtype, int64_t batch, int64_t tokens,
                                      int64_t max_query_len, int32_t num_heads, int32_t kv_num_heads,

@@ -878,7 +878,7 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
 
 def kv_attention_paged_workspace(dtype, batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size,
                                  max_pages):
-    """Bytes of workspace that kv_attention_paged uses for such a call."""
+    """Bytes of workspace that kv_attention_paged uses for such a call (max_query_len at most tokens here)."""
     n = load_library().kv_attention_paged_workspace(_torch_code(dtype)[1], batch, tokens, max_query_len, num_heads,
                                                     kv_num_heads, head_size, page_size, max_pages)
     if n < 0:
@@ -893,9 +893,9 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
     include/rope.h), after rope_apply_qkv_paged with the same lengths and table.
 
     query is (tokens, num_heads*H) with query_starts (int32 (B + 1)), or (B, S, num_heads*H) without.
-    max_query_len: at least the longest sequence's new tokens; None: as many as there are tokens, which plans
-    worse (with 64 or more tokens tree_masks want it given). tree_masks: int64, one word a token, bit t: new token
-    t of its sequence is seen. scale: 1/sqrt(H) if None. workspace: uint8 device memory of
+    max_query_len: at least the longest sequence's new tokens; None, or more than there are tokens: as many as
+    there are, which plans worse (with more than 64 tokens tree_masks want it given). tree_masks: int64, one word a
+    token, bit t: new token t of its sequence is seen. scale: 1/sqrt(H) if None. workspace: uint8 device memory of
     ``kv_attention_paged_workspace`` bytes, or None to take it from PyTorch's allocator. Returns out."""
     T, at = query.dtype, query.get_device()
     torch, code = _torch_code(T)
@@ -919,6 +919,7 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
         if max_query_len not in (None, most):
             raise ValueError(f"max_query_len must be {most} without query_starts, got {max_query_len}")
         max_query_len = most
+    max_query_len = min(max_query_len, tokens)
     if alibi_slopes is not None:
         _shaped("alibi_slopes", alibi_slopes, query, (num_heads,), torch.float32)
     if tree_masks is not None:

@@ -177,8 +177,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(hidden == nq * g.H && nq > 0 && g.N > 0);
     fits(*q, index, g.type, (*q).sizes());
     const int64_t all = starts ? tokens : (*q).size(1);
-    const int64_t most = a[9] == Py_None ? all : whole(a[9]);
+    int64_t most = a[9] == Py_None ? all : whole(a[9]);
     need(starts || most == all);
+    if (most > all) most = all;
     if (slopes) fits(*slopes, index, at::kFloat, {nq});
     if (masks) fits(*masks, index, at::kLong, (*q).sizes().slice(0, (*q).dim() - 1));
     if (out) fits(*out, index, g.type, (*q).sizes());

@@ -214,6 +214,7 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
                                int32_t* status_flags, void* workspace, int64_t workspace_bytes, rope_stream_t stream) {
   set_last_error("");
   KV_TRY(check_dtype(dtype));
+  if (query_starts && max_query_len > tokens) max_query_len = tokens;  // a server's fixed bound, in a step with fewer
   KV_TRY(check_attention(batch, tokens, max_query_len, num_heads, kv_num_heads, head_size, page_size, max_pages));
   KV_TRY(check_pages(kv_num_heads, head_size, num_pages, page_size, page_stride));
   if (!query_starts && batch * max_query_len != tokens)

@@ -75,3 +75,27 @@ def test_trees_below_row_zero(lib, cuda, dtype, new, below):
         want, bound, owned = _want(a, cuda)
         assert owned.all() and int(status) == 4
         pu.close(got, want, bound, str(cap))
+
+
+# --------------------------------------------------------------------------
+# max_query_len as a bound of its own
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("short", [True, False])
+def test_a_bound_above_the_tokens(lib, cuda, dtype, short, monkeypatch):
+    """A server's fixed bound, in a step with fewer tokens: the call with as many as there are."""
+    if not short:
+        monkeypatch.setattr(lib, "_short", False)
+        monkeypatch.setattr(lib, "_short_way", lambda: False)
+    for new, tree in (([60], True), ([3, 1], True), ([1, 1, 1], False), ([70, 1], False), ([0, 0], False)):
+        a = _make(92, dtype, 8, 2, 64, 16, [100 + i for i in range(len(new))], new, tree=tree, behind=0)
+        want = _call(lib, a, cuda, max_query_len=sum(new))
+        for most in (64, 100, 8192, 2 ** 40):
+            if most >= sum(new):
+                status = torch.zeros(1, dtype=torch.int32, device=cuda)
+                assert torch.equal(_call(lib, a, cuda, max_query_len=most, status=status), want), most
+                assert int(status) == 0
+        if sum(new):
+            exact, bound, _ = _want(a, cuda)
+            pu.close(want, exact, bound)
