@@ -99,3 +99,26 @@ def test_a_bound_above_the_tokens(lib, cuda, dtype, short, monkeypatch):
         if sum(new):
             exact, bound, _ = _want(a, cuda)
             pu.close(want, exact, bound)
+
+
+# --------------------------------------------------------------------------
+# tokens of nobody
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64), (4, 2, 256), (12, 2, 64)])
+@pytest.mark.parametrize("masks", ["plain", "cap", "alibi", "window"])
+def test_queries_of_nobody_change_no_bit(lib, cuda, dtype, heads, masks):
+    """What lies in Q behind the last sequence and before the first (the padding of a captured step): zeros, large
+    numbers, infinities and NaN give the sequences the same bits."""
+    Nq, Nkv, H = heads
+    for new in ([61, 3], [90, 33], [17, 200]):
+        a = _make(93, dtype, Nq, Nkv, H, 16, [300, 777], new, lead=2, behind=70, **MASKS[masks])
+        lo, hi = a["starts"][0], a["starts"][-1]
+        a["q"][:lo], a["q"][hi:] = 0.0, 0.0
+        want = _check(lib, a, cuda, str(new))[lo:hi]
+        for bad in (60000.0, float("inf"), float("nan")):
+            a["q"][:lo], a["q"][hi:] = bad, bad
+            assert torch.equal(_call(lib, a, cuda)[lo:hi], want), (new, bad)
+        a["q"][hi:] = (torch.randn((70, Nq * H), generator=torch.Generator().manual_seed(1)) * 300).to(a["q"].dtype)
+        assert torch.equal(_call(lib, a, cuda)[lo:hi], want), new
