@@ -28,8 +28,9 @@ __global__ void __launch_bounds__(kPagedKeepThreads) paged_keep_kernel_t(const P
     const int64_t past = __ldg(p.s.past + b);
     const int n = __ldg(p.kept_lens + b);
     const int32_t* kept = p.kept + (int64_t)b * p.width;
-    // the sequence stays as it is unless every row is there and the indices ascend
-    bool ok = n >= 0 && n <= p.width && past >= 0;
+    // the sequence stays as it is unless every row is there, those that have their place already
+    // among them, and the indices ascend
+    bool ok = n >= 0 && n <= p.width && (n == 0 || past >= 0);
     int before = -1;
     for (int i0 = 0; ok && i0 < n; i0 += 32) {
       const int i = i0 + lane;
@@ -40,8 +41,7 @@ __global__ void __launch_bounds__(kPagedKeepThreads) paged_keep_kernel_t(const P
       bool mine = true;
       if (i < n) {
         mine = x > left && past + x < p.s.rows;
-        if (mine && x != i)
-          mine = paged_page(p.s, b, (int)past + x) >= 0 && paged_page(p.s, b, (int)past + i) >= 0;
+        if (mine) mine = paged_page(p.s, b, (int)past + x) >= 0 && (x == i || paged_page(p.s, b, (int)past + i) >= 0);
       }
       ok = __all_sync(0xffffffffu, mine);
     }

@@ -122,3 +122,35 @@ def test_queries_of_nobody_change_no_bit(lib, cuda, dtype, heads, masks):
             assert torch.equal(_call(lib, a, cuda)[lo:hi], want), (new, bad)
         a["q"][hi:] = (torch.randn((70, Nq * H), generator=torch.Generator().manual_seed(1)) * 300).to(a["q"].dtype)
         assert torch.equal(_call(lib, a, cuda)[lo:hi], want), new
+
+
+# --------------------------------------------------------------------------
+# keep
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 7])
+@pytest.mark.parametrize("path,spoiled", [([0, 2, 17], 0), ([0], 0), ([0, 1, 2, 3], 0), ([0, 1, 17], 1), ([1, 17], 1)])
+def test_keep_looks_at_rows_that_stay(lib, cuda, path, spoiled, bad):
+    """A kept row that has its place already counts like the others: its page has to be there."""
+    ps, past = 16, [20, 31]
+    table, pages = pu.table_for(np.random.default_rng(94), [90, 90], ps)
+    table[1][(31 + path[0]) // ps if spoiled == 0 else (31 + path[-1]) // ps] = bad
+    k, v = (torch.randn((pages, 2, ps, 64), device=cuda, dtype=torch.float16) for _ in range(2))
+    want = [x.clone() for x in (k, v)]
+    for x, y in zip((k, v), want):
+        y[table[0][21 // ps], :, 21 % ps] = x[table[0][25 // ps], :, 25 % ps]
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    _keep(lib, cuda, k, v, table, past, [[0, 5], path], status=status)
+    assert int(status) == 4
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+def test_keep_of_nothing_is_not_flagged(lib, cuda):
+    """No row is kept of a sequence whose length is not one, and whose pages are not there: nothing to flag."""
+    k, v = (torch.randn((4, 2, 16, 64), device=cuda, dtype=torch.float16) for _ in range(2))
+    want = [x.clone() for x in (k, v)]
+    for past in (-1, -2 ** 31, 2 ** 31 - 1, 500):
+        status = torch.zeros(1, dtype=torch.int32, device=cuda)
+        _keep(lib, cuda, k, v, [[-1, -1], [0, 1]], [past, 3], [[], []], width=2, status=status)
+        assert int(status) == 0, past
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
