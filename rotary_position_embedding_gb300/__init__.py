@@ -759,9 +759,9 @@ def kv_cache_paged(num_pages, kv_num_heads, page_size, head_size, dtype=None, de
     return tuple(torch.zeros(shape, dtype=dtype or torch.float16, device=device) for _ in range(2))
 
 
-def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32):
+def _paged(like, name, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32):
     """(shape of the pages, elements between them, sequences, entries of a row of the table), checked together
-    with the lengths."""
+    with the lengths; ``like``, the argument ``name``, says what device they have to be on."""
     plane, table = k_pages.shape, page_table.shape
     if not (at >= 0 and len(plane) == 4 and len(table) == 2 and k_pages.dtype is T and v_pages.dtype is T
             and page_table.dtype is i32 and past_seq_lens.dtype is i32 and v_pages.shape == plane
@@ -772,14 +772,15 @@ def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_star
             raise ValueError("k_pages must be (num_pages, kv_num_heads, page_size, head_size)")
         if len(table) != 2:
             raise ValueError("page_table must be (B, max_pages)")
-        _shaped("query", query, query, query.shape, T)
-        _shaped("page_table", page_table, query, table, i32)
-        _shaped("past_seq_lens", past_seq_lens, query, table[:1], i32)
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            if t.shape != plane or t.dtype != T or not t.is_cuda or t.device != query.device:
-                raise ValueError(f"{name} must be a {T} tensor of shape {tuple(plane)} on {query.device}")
+        if not like.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _shaped("page_table", page_table, like, table, i32)
+        _shaped("past_seq_lens", past_seq_lens, like, table[:1], i32)
+        for which, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.shape != plane or t.dtype != T or not t.is_cuda or t.device != like.device:
+                raise ValueError(f"{which} must be a {T} tensor of shape {tuple(plane)} on {like.device}")
             if t.numel() and not t[0].is_contiguous():
-                raise ValueError(f"{name} must be contiguous within a page")
+                raise ValueError(f"{which} must be contiguous within a page")
         if plane[0] > 1 and k_pages.stride(0) != v_pages.stride(0):
             raise ValueError("k_pages and v_pages must have the same stride between pages")
     within = plane[1] * plane[2] * plane[3]
@@ -789,7 +790,7 @@ def _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_star
     if query_starts is not None and not (
             query_starts.dtype is i32 and query_starts.shape == (table[0] + 1,) and query_starts.is_contiguous()
             and query_starts.get_device() == at):
-        _shaped("query_starts", query_starts, query, (table[0] + 1,), i32)
+        _shaped("query_starts", query_starts, like, (table[0] + 1,), i32)
     return plane, stride, table[0], table[1]
 
 
@@ -813,8 +814,8 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
 
     query is (tokens, num_heads*H) with query_starts (int32 (B + 1)), or (B, S, num_heads*H) without, packed
     [Q|K|V] where key and value are None; position_ids has its leading dimensions. k_pages and v_pages
-    (num_pages, kv_num_heads, page_size, H) are updated in place; page_table is int32 (B, max_pages). Returns
-    q_out."""
+    (num_pages, kv_num_heads, page_size, H) are updated in place; they may be views of one tensor that holds K and V
+    of each page side by side, for the other paged calls too. page_table is int32 (B, max_pages). Returns q_out."""
     T, at = query.dtype, query.get_device()
     torch, code = _torch_code(T)
     short = _short or _short_way()
@@ -828,7 +829,7 @@ def rope_apply_qkv_paged(query, cos_cache, sin_cache, position_ids=None, *, num_
             return done
     lib, dev = load_library(), query.device
     i32 = torch.int32
-    (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
+    (P, N, ps, H), stride, B, wide = _paged(query, "query", T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
     tokens, hidden = _tokens_of(query, query_starts, B)
     lead = query.shape[:-1]
     packed = key is None and value is None
@@ -910,7 +911,7 @@ def kv_attention_paged(query, k_pages, v_pages, page_table, past_seq_lens, *, nu
             return done
     lib, dev = load_library(), query.device
     i32 = torch.int32
-    (P, N, ps, H), stride, B, wide = _paged(query, T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
+    (P, N, ps, H), stride, B, wide = _paged(query, "query", T, at, k_pages, v_pages, page_table, past_seq_lens, query_starts, i32)
     tokens, hidden = _tokens_of(query, query_starts, B)
     if hidden != num_heads * H or not query.is_contiguous():
         _shaped("query", query, query, (*query.shape[:-1], num_heads * H), T)
@@ -970,7 +971,7 @@ def kv_keep_paged(k_pages, v_pages, page_table, past_seq_lens, kept, kept_lens, 
             return
     lib, dev = load_library(), k_pages.device
     i32 = torch.int32
-    (P, N, ps, H), stride, B, wide = _paged(k_pages, T, at, k_pages, v_pages, page_table, past_seq_lens, None, i32)
+    (P, N, ps, H), stride, B, wide = _paged(k_pages, "k_pages", T, at, k_pages, v_pages, page_table, past_seq_lens, None, i32)
     if kept.dim() != 2:
         raise ValueError("kept must be (B, max_kept)")
     most = kept.shape[1]

@@ -154,3 +154,34 @@ def test_keep_of_nothing_is_not_flagged(lib, cuda):
         _keep(lib, cuda, k, v, [[-1, -1], [0, 1]], [past, 3], [[], []], width=2, status=status)
         assert int(status) == 0, past
     assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H", [64, 19])
+def test_keep_and_append_in_pages_of_one_tensor(lib, cuda, dtype, H):
+    """K and V side by side in each page, for what writes pages as for what reads them."""
+    a = _append_case(95, dtype, 8, 2, H - H % 2, 16, [7, 3, 20], [25, 1, 33])
+    k, v = a["k"].to(cuda), a["v"].to(cuda)
+    both = torch.stack([k, v], 1).contiguous()
+    results = []
+    for x, y in ((k, v), (both[:, 0], both[:, 1])):
+        results.append(_append(lib, a, cuda, x, y))
+        status = torch.zeros(1, dtype=torch.int32, device=cuda)
+        _keep(lib, cuda, x, y, a["table"], a["past"], [[1, 4, 24], [0], [30, 32]], status=status)
+        assert int(status) == 0
+    assert torch.equal(*results) and torch.equal(both[:, 0], k) and torch.equal(both[:, 1], v)
+    if H % 2:
+        x, y = (torch.randn((5, 2, 16, H), device=cuda).to(k.dtype) for _ in range(2))
+        both = torch.stack([x, y], 1).contiguous()
+        for p, q in ((x, y), (both[:, 0], both[:, 1])):
+            _keep(lib, cuda, p, q, [[3, 1, 4]], [13], [[2, 5, 30]])
+        assert torch.equal(both[:, 0], x) and torch.equal(both[:, 1], y)
+
+
+def test_keep_says_what_is_wrong(lib, cuda):
+    k, v = (torch.zeros((5, 2, 16, 64), device=cuda) for _ in range(2))
+    both = torch.zeros((5, 2, 2, 16, 64), device=cuda)
+    for x, y, said in ((both[:, 0], v, "same stride"), (k, v.half(), "v_pages"), (k.transpose(1, 2), v.transpose(1, 2), "k_pages"),
+                       (k.cpu(), v, "k_pages"), (k[0], v[0], "k_pages")):
+        with pytest.raises(ValueError, match=said):
+            lib.kv_keep_paged(x, y, _i32([[3, 1, 4]], cuda), _i32([13], cuda), _i32([[2, 5, 30]], cuda), _i32([3], cuda))
