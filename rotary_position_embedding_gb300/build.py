@@ -6,6 +6,8 @@ loads on a machine without a GPU driver (every entry point then fails with
 ROPE_ERR_CUDA once it reaches a CUDA call; argument checks still run).
 """
 
+import glob
+import hashlib
 import importlib.metadata
 import importlib.util
 import os
@@ -40,8 +42,22 @@ def _torch_version():
         return "none"
 
 
-# what was compiled for another PyTorch is not loaded: its classes may be laid out differently
-BINDING_PATH = os.path.join(OUT_DIR, f"_binding-torch{_torch_version()}" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX") or ".so"
+
+
+def binding_path(sources, out_dir=OUT_DIR):
+    """Where the short way made of these sources lies. What was compiled of others is not found, and not loaded: of
+    another PyTorch its classes may be laid out differently, of another header the library's calls."""
+    h = hashlib.sha256()
+    for f in sources:
+        if os.path.exists(f):  # (a package without its sources has no short way)
+            with open(f, "rb") as s:
+                h.update(s.read())
+    return os.path.join(out_dir, f"_binding-torch{_torch_version()}-{h.hexdigest()[:16]}{_SUFFIX}")
+
+
+BINDING_SOURCES = (BINDING, os.path.join(INCLUDE, "rope.h"))
+BINDING_PATH = binding_path(BINDING_SOURCES)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -62,14 +78,13 @@ def _inputs():
 def build_binding(force=False):
     """Compile (if needed) the short way into the library for calls with PyTorch tensors, csrc/binding.cpp, and
     return its path; None where it cannot be compiled (calls then go through ctypes)."""
-    header = os.path.join(INCLUDE, "rope.h")
-    if not force and os.path.exists(BINDING_PATH) and all(
-            os.path.getmtime(f) <= os.path.getmtime(BINDING_PATH) for f in (BINDING, header)):
-        return BINDING_PATH
+    path = binding_path(BINDING_SOURCES, OUT_DIR)
+    if not force and os.path.exists(path):
+        return path
     try:
         torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
         os.makedirs(OUT_DIR, exist_ok=True)
-        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        tmp = path + f".tmp{os.getpid()}"
         cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
         cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1",
                "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include/torch/csrc/api/include"),
@@ -78,8 +93,11 @@ def build_binding(force=False):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr)
-        os.replace(tmp, BINDING_PATH)
-        return BINDING_PATH
+        os.replace(tmp, path)
+        for old in glob.glob(os.path.join(OUT_DIR, f"_binding-torch{_torch_version()}*{_SUFFIX}")):
+            if old != path:  # of sources that are gone
+                os.remove(old)
+        return path
     except Exception as e:  # no PyTorch, no Python.h, no g++: the library works without it
         sys.stderr.write(f"binding.cpp was not compiled, calls go through ctypes: {e}\n")
         return None
