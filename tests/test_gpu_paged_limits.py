@@ -185,3 +185,52 @@ def test_keep_says_what_is_wrong(lib, cuda):
                        (k.cpu(), v, "k_pages"), (k[0], v[0], "k_pages")):
         with pytest.raises(ValueError, match=said):
             lib.kv_keep_paged(x, y, _i32([[3, 1, 4]], cuda), _i32([13], cuda), _i32([[2, 5, 30]], cuda), _i32([3], cuda))
+
+
+# --------------------------------------------------------------------------
+# QK-Norm where no other operator has the bits to compare with
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,H,rd,inter,unaligned", [
+    ("f32", 256, 0, 0, False), ("f32", 256, 64, 1, False), ("f32", 140, 0, 0, False), ("f32", 256, 0, 0, True), ("f16", 96, 0, 0, True),
+    ("bf16", 96, 0, 1, True), ("f16", 96, 16, 0, False), ("bf16", 256, 0, 0, True), ("f16", 512, 0, 0, False), ("f16", 38, 0, 0, False)])
+def test_append_norm_by_definition(lib, cuda, dtype, H, rd, inter, unaligned):
+    """z = T(w T(x r)), r = 1 / sqrt(mean x^2 + eps), then the rotation, in 64 bits: heads of more than 32 units, with
+    lanes that take several, and 16-bit heads in loads of one element."""
+    Nq, Nkv, ps, past, new = 6, 2, 16, [7, 100], [33, 1]
+    a = _append_case(96, dtype, Nq, Nkv, H, ps, past, new, norm=True, inter=inter, rd=rd)
+    t = a["q"].dtype
+    k, v = a["k"].to(cuda), a["v"].to(cuda)
+    q = a["q"].to(cuda)
+    if unaligned:
+        q = _unaligned(q)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    got = _append(lib, dict(a, q=q), cuda, k, v, status=status)
+    assert int(status) == 0
+    b, s = _tokens(a)
+    row = torch.tensor(past)[b] + s
+    x = a["q"].double().view(-1, Nq + 2 * Nkv, H)
+    w = torch.cat([a["qw"].double().expand(Nq, H), a["kw"].double().expand(Nkv, H)])
+    z = x[:, :Nq + Nkv] / (x[:, :Nq + Nkv].square().mean(-1, keepdim=True) + 1e-6).sqrt() * w
+    half = (rd or H) // 2
+    c, sn = a["cos"].double()[row][:, None], a["sin"].double()[row][:, None]
+    if inter:
+        one, two = slice(0, 2 * half, 2), slice(1, 2 * half, 2)
+    else:
+        one, two = slice(0, half), slice(half, 2 * half)
+    y, size = z.clone(), z.abs()
+    y[..., one] = z[..., one] * c - z[..., two] * sn
+    y[..., two] = z[..., two] * c + z[..., one] * sn
+    size[..., one] = (z[..., one] * c).abs() + (z[..., two] * sn).abs()
+    size[..., two] = (z[..., two] * c).abs() + (z[..., one] * sn).abs()
+    # Three roundings to T of half a step each (x r, w times that, the result, whose size is at most `size`); in 32 bits
+    # the squares' sum of H terms (H 2^-24, half of that in r), the mean, root and quotient (4 2^-24) and the
+    # rotation (3 2^-24); 2 % for their products. Below float16's normal numbers a rounding is off by 2^-25 instead, which w
+    # (below 1.5) and the coefficients (below 6) carry on to less than 2^-20.
+    half_step = torch.finfo(t).eps / 2
+    most = 1.02 * (3 * half_step + (H / 2 + 7) * 2.0 ** -24) * size + (2.0 ** -20 if t == torch.float16 else 0.0)
+    assert a["cos"].abs().max() < 6 and a["sin"].abs().max() < 6
+    assert ((got.cpu().double().view(-1, Nq, H) - y[:, :Nq]).abs() <= most[:, :Nq]).all()
+    page = torch.tensor([a["table"][int(i)][int(r) // ps] for i, r in zip(b, row)])
+    assert ((k.cpu().double()[page, :, row % ps] - y[:, Nq:]).abs() <= most[:, Nq:]).all()
+    assert torch.equal(v.cpu()[page, :, row % ps], a["q"].view(-1, Nq + 2 * Nkv, H)[:, Nq + Nkv:])
