@@ -234,3 +234,88 @@ def test_append_norm_by_definition(lib, cuda, dtype, H, rd, inter, unaligned):
     page = torch.tensor([a["table"][int(i)][int(r) // ps] for i, r in zip(b, row)])
     assert ((k.cpu().double()[page, :, row % ps] - y[:, Nq:]).abs() <= most[:, Nq:]).all()
     assert torch.equal(v.cpu()[page, :, row % ps], a["q"].view(-1, Nq + 2 * Nkv, H)[:, Nq + Nkv:])
+
+
+# --------------------------------------------------------------------------
+# both kernels of a mixed batch at a time
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_mixed_batches_in_a_chain(lib, cuda, cap):
+    """Append, attention, keep and append again with nothing between them, in batches whose attention is two kernels at a
+    time, the second of which does not wait for what came before: the bits of the same calls with waits between them."""
+    Nq, Nkv, H, ps, B = 8, 2, 128, 16, 130
+    b = _append_case(97, "bf16", Nq, Nkv, H, ps, [11 * i % 300 for i in range(B)], [1] * (B - 2) + [200, 2])
+    starts, past, table = (_i32(b[n], cuda) for n in ("starts", "past", "table"))
+    q, cos, sin = (b[n].to(cuda) for n in ("q", "cos", "sin"))
+    kept, lens = _i32([[0]] * (B - 2) + [[5], [1]], cuda), _i32([1] * B, cuda)
+    calls = dict(num_heads=Nq, query_starts=starts, max_query_len=200, softcap=cap)
+
+    pages = [b[n].to(cuda) for n in ("k", "v")]
+
+    def step(wait):
+        k, v = (x.clone() for x in pages)
+        outs = []
+        for turn in range(3):
+            qo = lib.rope_apply_qkv_paged(q + turn, cos, sin, num_heads=Nq, kv_num_heads=Nkv, k_pages=k, v_pages=v, page_table=table,
+                                          past_seq_lens=past, query_starts=starts)
+            wait()
+            outs.append(lib.kv_attention_paged(qo, k, v, table, past, **calls))
+            wait()
+            lib.kv_keep_paged(k, v, table, past, kept, lens)
+            wait()
+            outs.append(lib.kv_attention_paged(qo, k, v, table, past, **calls))
+            wait()
+        return [*outs, k, v]
+
+    want = step(torch.cuda.synchronize)
+    assert lib.last_kernel() == "paged_token_kernel"
+    for _ in range(5):
+        for x, y in zip(step(lambda: None), want):
+            assert torch.equal(x, y)
+    assert lib.last_kernel() == "paged_token_kernel"
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(lambda: None)
+    for _ in range(3):
+        for x in got[:6]:
+            x.zero_()
+        graph.replay()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_mixed_batches_replayed_with_other_lengths(lib, cuda, dtype):
+    """One captured call for a mixed batch; the shares of both kernels follow the lengths of each replay."""
+    Nq, Nkv, H, ps, B, width, most = 8, 2, 128, 16, 120, 40, 300
+    tokens = 700
+    steps = [([0] * B, [1] * B), ([7 * b % 300 for b in range(B)], [1] * (B - 1) + [300]), ([5 * b for b in range(B)], [2, 0] * 60),
+             ([17] * B, [0] * B), ([3 * b for b in range(B)], [200, 300] + [1] * 60 + [0] * (B - 62)), ([630] + [4] * (B - 1), [5] * B)]
+    q = torch.zeros((tokens, Nq * H), dtype=T[dtype], device=cuda)
+    k, v = (torch.zeros((B * width, Nkv, ps, H), dtype=T[dtype], device=cuda) for _ in range(2))
+    table, past, starts = torch.zeros((B, width), dtype=torch.int32, device=cuda), _i32([0] * B, cuda), _i32([0] * (B + 1), cuda)
+    out = torch.zeros_like(q)
+
+    def run():
+        lib.kv_attention_paged(q, k, v, table, past, num_heads=Nq, query_starts=starts, max_query_len=most, out=out)
+
+    run()
+    assert lib.last_kernel() == "paged_token_kernel"
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i, (p, n) in enumerate(steps):
+        a = _make(98 + i, dtype, Nq, Nkv, H, ps, p, n, behind=tokens - sum(n))
+        pages = a["k"].shape[0]
+        q.copy_(a["q"])
+        k.fill_(float("nan"))[:pages] = a["k"].to(cuda)
+        v.fill_(float("nan"))[:pages] = a["v"].to(cuda)
+        table.copy_(_i32([row + [-7] * (width - len(row)) for row in a["table"]], cuda))
+        past.copy_(_i32(p, cuda))
+        starts.copy_(_i32(a["starts"], cuda))
+        out.fill_(7.0)
+        graph.replay()
+        want, bound, owned = _want(a, cuda)
+        pu.close(out[owned], want[owned], bound[owned], str(i))
+        assert torch.equal(out[~owned], torch.full_like(out[~owned], 7.0)), i
