@@ -246,17 +246,20 @@ __device__ __forceinline__ void tile_load(float (&x)[N], uint32_t ts, const Tile
   }
 }
 
-// Whether all raw scores of a warp's live rows have |y| <= 0.4: then the cap is a polynomial.
-// The bounds of mult keep the polynomial's powers normal numbers.
-template <int N>
-__device__ __forceinline__ bool tile_small(const float (&x)[N], const TileRow& r, bool live = true) {
+// Whether all of a warp's raw scores have |y| <= 0.4: then the cap is a polynomial.
+// The bounds of mult keep the polynomial's powers normal numbers. With SOME only rows that
+// `count` have a say, which is asked where the others' is not the same.
+template <bool SOME = false, int N>
+__device__ __forceinline__ bool tile_small(const float (&x)[N], const TileRow& r, bool count = true) {
   float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     a0 = fmaxf(a0, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
     a1 = fmaxf(a1, fmaxf(fabsf(x[i + 2]), fabsf(x[i + 3])));
   }
-  return __all_sync(0xffffffffu, (!live || fmaxf(a0, a1) * r.mult <= 2.0f * kTanhEnd * kLog2e) && r.mult > 1e-5f && r.mult < 1e4f);
+  const bool small = fmaxf(a0, a1) * r.mult <= 2.0f * kTanhEnd * kLog2e && r.mult > 1e-5f && r.mult < 1e4f;
+  if (SOME && !__all_sync(0xffffffffu, small)) return __all_sync(0xffffffffu, small || !count) && r.mult > 1e-5f && r.mult < 1e4f;
+  return SOME || __all_sync(0xffffffffu, small);
 }
 
 // Other scores, and those of tiles with hidden keys, are capped where they lie in

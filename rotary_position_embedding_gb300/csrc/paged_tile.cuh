@@ -455,8 +455,9 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
       const int below = __reduce_max_sync(0xffffffffu, live ? from : 0);
       tr.slope = 0.0f;
       if (p.slopes && live) tr.slope = __ldg(p.slopes + kvh * p.G + head) * kLog2e;
-      // Rows behind the last hold what TMA found there, tokens of other sequences or of nobody:
-      // their base stays 0, and they have no say in what the warp does.
+      // Rows behind the last (lim is 0) hold what TMA found there, tokens of other sequences or
+      // of nobody: they have no say in what the warp does. Whose say it was is asked only where
+      // somebody had one (asked at every key tile: 1 to 3 % of a prompt).
       float m = live ? -CUDART_INF_F : 0.0f, l = 0.0f;
       for (int step = 0; step < steps; ++step, ++done_steps) {
         const int j0 = lo + (steps - 1 - step) * N;
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
         float x[N];
         tile_load<false, N>(x, ts, tr, true);
         bool done = general;  // x holds scores in log2, not raw ones
-        const bool small = capped && tile_small(x, tr, live);
+        const bool small = capped && tile_small<true>(x, tr, lim > 0);
         if (capped && (general || masked || !small)) {
           // (an infinite product is at an end of the cap from here on: -inf means hidden)
           if (small)
@@ -499,13 +500,14 @@ __global__ void __launch_bounds__(kPagedTileThreads, 1)
         float sum = 0.0f;
         if (!move) {
           sum = weights();
-          move = __any_sync(0xffffffffu, live && !(sum <= 32768.0f));
+          move = __any_sync(0xffffffffu, !(sum <= 32768.0f));
+          if (move) move = __any_sync(0xffffffffu, lim > 0 && !(sum <= 32768.0f));
         }
         if (move) {
           const float top = tile_max(x);
           float mx = top * (done ? 1.0f : mult);
           if (capped && !done) mx = kv_tanh_of(mx) * tr.cap2;
-          const float mn = live ? fmaxf(m, mx) : 0.0f;
+          const float mn = fmaxf(m, mx);
           float a = mn == -CUDART_INF_F ? 1.0f : kv_exp2(m - mn);
           m = mn;
           l *= a;
