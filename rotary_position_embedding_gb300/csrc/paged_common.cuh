@@ -101,7 +101,8 @@ __device__ __forceinline__ int64_t paged_nth(const PagedBatch& s, int b, int64_t
 
 // Keys that the token at row i can see lie in [first, limit).
 __device__ __forceinline__ int paged_limit(const PagedParams& p, const PagedSeq& q, int64_t i) {
-  const int64_t l = p.masks ? q.total : i < 0 ? 0 : i + 1;
+  if (i < 0 && !p.masks) return 0;
+  const int64_t l = p.masks ? q.total : i + 1;
   return l < q.total ? (int)l : q.total;
 }
 __device__ __forceinline__ int paged_first(const PagedParams& p, int64_t i) {
