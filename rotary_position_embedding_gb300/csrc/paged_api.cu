@@ -146,7 +146,7 @@ PagedPlan plan_tile(int64_t B, int64_t T, int64_t most, bool ragged, int64_t Nq,
 
 // The matrix kernels take 16-bit types whose rows are 16-byte aligned, in pages that
 // TMA copies in boxes of 8 rows and more. Up to 16 rows of a problem go to the kernel
-// for few rows. Where some sequences may have no more than that and others do, both
+// for few rows. Where some sequences may have up to kMixedRows and others have more, both
 // kernels run, unless the short ones are so few that their CTAs of the kernel for many
 // rows fit beside the others', or the tokens are drafts, whose trees are much alike.
 PagedFamily choose_paged(bool matrix, int64_t B, int64_t T, int64_t most, bool ragged, bool trees, int64_t G, int64_t Nkv,
@@ -314,8 +314,8 @@ rope_status kv_attention_paged(rope_dtype dtype, int64_t batch, int64_t tokens, 
       p.ws_join = reinterpret_cast<int4*>(p.ws_ml + n);  // 16-byte aligned: n is a multiple of 16
     }
   };
-  // The two kernels of a mixed batch run at a time where both are dealt to with a
-  // workspace of their own.
+  // The two kernels of a mixed batch run at a time where both are dealt to every SM with a
+  // workspace of their own, else one after the other.
   int64_t token_at = 0;  // where paged_token_kernel's begins
   const int64_t token_most = p.mixed ? kMixedRows / p.G : max_query_len;
   if (p.mixed) {

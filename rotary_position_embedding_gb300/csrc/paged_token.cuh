@@ -19,6 +19,10 @@
 // where a score passes it by 8 (in log2), so weights stay below 2^8 and the common
 // unit costs one vote.
 //
+// Weights are rounded to T, the product's type, and their sum is of the unrounded ones: in
+// bfloat16 outputs are off by 1.9e-3 where one rounding at the end gives 1.7e-3, in float16
+// by 2.6e-4 for 2.1e-4.
+//
 // A value that no row sees is zeroed before the product. Where one that only some
 // rows see is not finite, its zero weight in the others would make a NaN of it: the
 // rows are then done over again one by one (paged_careful_row).
